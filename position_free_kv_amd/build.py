@@ -5,7 +5,9 @@
 The library is the C ABI of include/kamera.h: host validation and packing
 (csrc/kamera_host.cpp) plus the gfx950 kernels: the operator
 (csrc/kamera_kernels.hip), the patch builder (csrc/kamera_builder.hip) and the
-streaming probes used for measurement (csrc/kamera_probe.hip).
+streaming probes used for measurement (csrc/kamera_probe.hip); and the serving step of
+include/kamera_step.h: its host part (csrc/kamera_step_host.cpp) and kernels
+(csrc/kamera_step.hip).
 """
 from __future__ import annotations
 
@@ -27,6 +29,8 @@ ARCH = os.environ.get("KAMERA_OFFLOAD_ARCH", "gfx950")
 # instead of being funnelled through one set of accumulation registers.
 HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
+
+STEP_KERNELS = ["kamera_step"]
 
 
 def hipcc() -> str:
@@ -57,8 +61,16 @@ def build(verbose_asm: bool = False) -> str:
           os.path.join(CSRC, "kamera_probe.hip"), "-o", pobj])
     _run([cc, "-x", "c++", *COMMON, "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", "-c",
           os.path.join(CSRC, "kamera_host.cpp"), "-o", hobj])
+    step_objs = []
+    for name in STEP_KERNELS:
+        step_objs.append(os.path.join(objdir, name + ".o"))
+        _run([cc, f"--offload-arch={ARCH}", *COMMON, *HIP_FLAGS, "-c", os.path.join(CSRC, name + ".hip"),
+              "-o", step_objs[-1]])
+    step_objs.append(os.path.join(objdir, "kamera_step_host.o"))
+    _run([cc, "-x", "c++", *COMMON, "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", "-c",
+          os.path.join(CSRC, "kamera_step_host.cpp"), "-o", step_objs[-1]])
     tmp = LIB + ".tmp"
-    _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", kobj, bobj, pobj, hobj, "-o", tmp])
+    _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", kobj, bobj, pobj, hobj, *step_objs, "-o", tmp])
     os.replace(tmp, LIB)
     if verbose_asm:
         _run([cc, f"--offload-arch={ARCH}", *COMMON, *HIP_FLAGS, "--cuda-device-only", "-S",

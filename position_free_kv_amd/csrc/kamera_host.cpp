@@ -677,6 +677,25 @@ bool launch_inline(const kamera_layout* L, const kamera_chunk* chunks, int32_t n
 
 }  // namespace
 
+// Shared with the serving step's host part (kamera_step_host.cpp).
+namespace kamera {
+kamera_status host_fail(kamera_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+void host_clear_error() { g_last_error.clear(); }
+kamera_status host_check_layout(const kamera_layout* L) { return check_layout(L); }
+kamera_status host_stage(const void* src, size_t bytes, void* dst, hipStream_t stream) {
+  // the copy-in kernel moves whole 16-byte words: a shorter tail would stay behind
+  if (bytes % 16) return fail(KAMERA_E_SHAPE, "staged blocks are multiples of 16 bytes (got %zu)", bytes);
+  return upload(src, bytes, dst, stream);
+}
+}  // namespace kamera
+
 extern "C" {
 
 size_t kamera_workspace_bytes(int32_t num_chunks, int64_t total_block_table_entries) {

@@ -1,0 +1,415 @@
+// Kernels of the serving step (include/kamera_step.h) for gfx950: cos/sin table, append,
+// plain attention, the join of partial attention results, page copies.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kamera_step_desc.h"
+
+namespace kamera {
+
+#define KGLOBAL __attribute__((address_space(1)))
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWave = 64;
+constexpr int kThreads = 256;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Element types by their storage: uint16_t holds bf16 bits, float itself.
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<uint16_t>(uint16_t x) {
+  return __uint_as_float((uint32_t)x << 16);
+}
+template <>
+__device__ __forceinline__ float to_float<float>(float x) {
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ uint16_t from_float<uint16_t>(float x) {
+  return __builtin_bit_cast(uint16_t, (__bf16)x);  // round to nearest even
+}
+template <>
+__device__ __forceinline__ float from_float<float>(float x) {
+  return x;
+}
+
+// N consecutive elements as floats
+template <typename T, int N>
+__device__ __forceinline__ void load_floats(const KGLOBAL T* p, float* x) {
+  if constexpr (N == 1) {
+    x[0] = to_float<T>(p[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    const u32x2 w = *(const KGLOBAL u32x2*)p;
+    x[0] = __uint_as_float(w.x << 16);
+    x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16);
+    x[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+    const f32x4 w = *(const KGLOBAL f32x4*)p;
+    for (int e = 0; e < 4; ++e) x[e] = w[e];
+  }
+}
+
+// Pool row (page * page_size + offset) of slot `slot` of a page table.
+__device__ __forceinline__ int64_t pool_row(const StepArgs& a, const KGLOBAL int32_t* pages, int slot) {
+  if (a.page_shift >= 0)
+    return ((int64_t)pages[slot >> a.page_shift] << a.page_shift) + (slot & (a.page_size - 1));
+  const int pg = slot / a.page_size;
+  return (int64_t)pages[pg] * a.page_size + (slot - pg * a.page_size);
+}
+
+// ============================================================================
+// cos/sin of the appended tokens: phi = position * base^(-2i/d_rot) in fp64, rounded once to
+// fp32 (as the rehydrate operator's tables). Once a step, read by every layer: 4 d_rot bytes
+// a token, against 2 (Hq + 2 Hkv) d bytes of rows.
+// ============================================================================
+__global__ __launch_bounds__(kThreads) void step_phase(StepArgs a) {
+  const int half = a.d_rot >> 1;
+  const int64_t n = (int64_t)a.num_tokens * half;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const int64_t t = i / half;
+  const int p = (int)(i - t * half);
+  int32_t at;
+  if (a.pos) {
+    at = a.pos[t];
+  } else {
+    const int sections = a.mrope[0] + a.mrope[1] + a.mrope[2];
+    const int c = sections == 0 || p < a.mrope[0] ? 0 : (p < a.mrope[0] + a.mrope[1] ? 1 : 2);
+    at = a.positions[3 * t + c];
+  }
+  const double phi = (double)at * pow(a.rope_base, (-2.0 * (double)p) / (double)a.d_rot);
+  double sd, cd;
+  sincos(phi, &sd, &cd);
+  a.phase[t * a.d_rot + p] = (float)cd;
+  a.phase[t * a.d_rot + half + p] = (float)sd;
+}
+
+// ============================================================================
+// Append, any layout: one wave per (token, unit); units are the query heads, the key heads
+// (MLA: the one row), and for GQA the V row. Lanes walk the unit's pairs; a pair is read and
+// written by one lane, so in-place queries are safe.
+// ============================================================================
+__device__ __forceinline__ float wave_sum(float x) {
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, kWave);
+  return x;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void append_plain(StepArgs a, int64_t layer0, kamera_append_rows r) {
+  const int lane = threadIdx.x & 63;
+  const int nq = r.q ? a.num_q_heads : 0;
+  const int units = nq + a.heads + (a.family == KAMERA_GQA ? 1 : 0);
+  const int64_t task = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t t = task / units;
+  if (t >= a.num_tokens) return;
+  const int u = (int)(task - t * units);
+  const int64_t slot = a.slots[t];
+  const T* x;
+  T* y;
+  const T* w = nullptr;
+  int norm_cols = 0, band0 = 0;
+  if (u < nq) {
+    x = (const T*)r.q + t * r.q_stride + (int64_t)u * a.dk;
+    y = (T*)r.q_out + t * r.q_out_stride + (int64_t)u * a.dk;
+    band0 = a.latent;
+    w = (const T*)r.q_weight;
+    norm_cols = w ? a.dk : 0;
+  } else if (u < nq + a.heads) {
+    const int h = u - nq;
+    x = (const T*)r.k + t * r.k_stride + (int64_t)h * a.dk;
+    y = (T*)a.k_pool + layer0 + slot * a.row + (int64_t)h * a.dk;
+    band0 = a.latent;
+    w = (const T*)r.k_weight;
+    norm_cols = w ? (a.family == KAMERA_MLA ? a.latent : a.dk) : 0;
+  } else {
+    x = (const T*)r.v + t * r.v_stride;
+    y = (T*)a.v_pool + layer0 + slot * a.row;
+    for (int c = lane; c < a.row; c += kWave) y[c] = x[c];
+    return;
+  }
+  float scale = 1.0f;
+  if (norm_cols) {
+    float ss = 0.0f;
+    for (int c = lane; c < norm_cols; c += kWave) {
+      const float f = to_float<T>(x[c]);
+      ss += f * f;
+    }
+    scale = 1.0f / sqrtf(wave_sum(ss) / (float)norm_cols + r.eps);
+  }
+  for (int c = lane; c < band0; c += kWave)
+    y[c] = norm_cols ? from_float<T>(to_float<T>(x[c]) * scale * to_float<T>(w[c])) : x[c];
+  const int half = a.d_rot >> 1;
+  const float* cs = a.phase + t * a.d_rot;
+  const bool normed = norm_cols > band0;  // the norm covers the band (GQA)
+  for (int p = lane; p < half; p += kWave) {
+    const int ia = band0 + (a.pairing == KAMERA_NEOX ? p : 2 * p);
+    const int ib = a.pairing == KAMERA_NEOX ? ia + half : ia + 1;
+    float xa = to_float<T>(x[ia]), xb = to_float<T>(x[ib]);
+    if (normed) {
+      xa = xa * scale * to_float<T>(w[ia]);
+      xb = xb * scale * to_float<T>(w[ib]);
+    }
+    const float c = cs[p], s = cs[half + p];
+    y[ia] = from_float<T>(xa * c - xb * s);
+    y[ib] = from_float<T>(xa * s + xb * c);
+  }
+}
+
+// ============================================================================
+// Attention, any layout (head widths and alignments the matrix-core kernel does not take): one
+// wave per row of the tile. A wave reads 4 tokens at a time, 16 lanes to a token, each lane
+// holding VEC * NJ of the key's columns; every 16-lane group runs its own online softmax
+// (running maximum m and sum l in base-2 logarithms, o scaled by exp2(m_old - m)) and the four
+// are joined at the end.
+// ============================================================================
+struct AttendIo {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride, out_stride, layer0;
+  float scale2;  // scale * log2(e)
+};
+
+// exp2(m - to) where m may still be -inf: nothing seen yet counts as zero
+__device__ __forceinline__ float shrink(float m, float to) { return m == to ? 1.0f : exp2f(m - to); }
+
+template <typename T, int VEC, int NJ>
+__global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io) {
+  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const AttendItem it = a.items[item];
+  const AttendRun run = a.runs[it.run];
+  const int lane = threadIdx.x & 63, dl = lane & 15, tg = lane >> 4;
+  const int row = it.row0 + (threadIdx.x >> 6);
+  if (row >= run.ntok * a.group) return;
+  const int j = row / a.group, g = row - j * a.group;
+  const int token = run.listed ? a.tok[run.tok0 + j] : run.tok0 + j;
+  const int qh = head * a.group + g;
+  const int end = min(it.kv1, max(run.len_a - 1, run.lim0 + j * run.lstep) + 1);
+  const KGLOBAL T* kp = (const KGLOBAL T*)a.k_pool + io.layer0 + (int64_t)head * a.dk;
+  const KGLOBAL T* vp = (const KGLOBAL T*)a.v_pool + io.layer0 + (int64_t)head * a.dk;
+  const KGLOBAL int32_t* pages = (const KGLOBAL int32_t*)a.pages;
+  const KGLOBAL T* qp = (const KGLOBAL T*)io.q + (int64_t)token * io.q_stride + (int64_t)qh * a.dk;
+  float q[NJ * VEC], o[NJ * VEC];
+#pragma unroll
+  for (int i = 0; i < NJ; ++i) {
+    const int d = (i * 16 + dl) * VEC;
+    for (int e = 0; e < VEC; ++e) q[i * VEC + e] = o[i * VEC + e] = 0.0f;
+    if (d < a.dk) load_floats<T, VEC>(qp + d, q + i * VEC);
+    for (int e = 0; e < VEC; ++e) q[i * VEC + e] *= io.scale2;
+  }
+  float m = -INFINITY, l = 0.0f;
+  for (int t0 = it.kv0; t0 < end; t0 += 4) {
+    const int t = t0 + tg;
+    const bool seen = t < end;
+    int64_t at = 0;
+    float s = 0.0f;
+    if (seen) {
+      at = (t < run.len_a ? pool_row(a, pages + run.pg_a, run.slot_a + t)
+                          : pool_row(a, pages + run.pg_b, run.slot_b + (t - run.len_a))) * a.row;
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) {
+        const int d = (i * 16 + dl) * VEC;
+        if (d >= a.dk) continue;
+        float k[VEC];
+        load_floats<T, VEC>(kp + at + d, k);
+        for (int e = 0; e < VEC; ++e) s += q[i * VEC + e] * k[e];
+      }
+    }
+    for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d, 16);
+    if (!seen) continue;
+    const float to = fmaxf(m, s);
+    const float alpha = shrink(m, to), p = shrink(s, to);
+    const bool nothing = to == -INFINITY && s == -INFINITY;  // only -inf so far: weight 0, not exp(-inf + inf)
+    l = l * alpha + (nothing ? 0.0f : p);
+    m = to;
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) {
+      const int d = (i * 16 + dl) * VEC;
+      if (d >= a.dv) continue;
+      float v[VEC];
+      load_floats<T, VEC>(vp + at + d, v);
+      for (int e = 0; e < VEC; ++e) o[i * VEC + e] = nothing ? 0.0f : o[i * VEC + e] * alpha + p * v[e];
+    }
+  }
+  float top = m;
+  for (int d = 16; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+  const float w = l == 0.0f ? 0.0f : shrink(m, top);
+  float sum = l * w;
+  for (int d = 16; d < 64; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+#pragma unroll
+  for (int i = 0; i < NJ * VEC; ++i) {
+    float x = l == 0.0f ? 0.0f : o[i] * w;
+    for (int d = 16; d < 64; d <<= 1) x += __shfl_xor(x, d, kWave);
+    o[i] = x;
+  }
+  if (tg) return;
+  if (run.direct) {
+    T* out = (T*)io.out + (int64_t)token * io.out_stride + (int64_t)qh * a.dv;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int i = 0; i < NJ; ++i)
+      for (int e = 0; e < VEC; ++e) {
+        const int d = (i * 16 + dl) * VEC + e;
+        if (d < a.dv) out[d] = from_float<T>(o[i * VEC + e] * inv);
+      }
+    if (io.lse && dl == 0)
+      io.lse[(int64_t)token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  } else {
+    const int64_t pr = run.part0 + ((int64_t)it.split * a.heads + head) * ((int64_t)run.ntok * a.group) + row;
+    for (int i = 0; i < NJ; ++i)
+      for (int e = 0; e < VEC; ++e) {
+        const int d = (i * 16 + dl) * VEC + e;
+        if (d < a.dv) a.part_o[pr * a.dv + d] = o[i * VEC + e];
+      }
+    if (dl == 0) a.part_ml[pr] = make_float2(top, sum);
+  }
+}
+
+// ============================================================================
+// Join of partial results: one wave per (token, query head). Parts are taken in a fixed order,
+// so the result does not depend on which workgroup finished first.
+// ============================================================================
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io) {
+  const int64_t task = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t i = task / a.num_q_heads;
+  if (i >= a.num_merge) return;
+  const int qh = (int)(task - i * a.num_q_heads), head = qh / a.group, g = qh - head * a.group;
+  const int lane = threadIdx.x & 63;
+  const MergeToken mt = a.merge[i];
+  float top = -INFINITY, sum = 0.0f;
+  for (int s = 0; s < 2; ++s)
+    for (int k = lane; k < mt.splits[s]; k += kWave) {
+      const float2 ml = a.part_ml[mt.part[s] + ((int64_t)k * a.heads + head) * mt.rows[s] + mt.row0[s] + g];
+      if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+    }
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+  for (int c0 = 0; c0 < a.dv; c0 += kWave) {
+    const int c = c0 + lane;
+    float o = 0.0f;
+    sum = 0.0f;
+    for (int s = 0; s < 2; ++s)
+      for (int k = 0; k < mt.splits[s]; ++k) {
+        const int64_t pr = mt.part[s] + ((int64_t)k * a.heads + head) * mt.rows[s] + mt.row0[s] + g;
+        const float2 ml = a.part_ml[pr];
+        if (ml.y == 0.0f) continue;
+        const float w = shrink(ml.x, top);
+        sum += ml.y * w;
+        if (c < a.dv) o += a.part_o[pr * a.dv + c] * w;
+      }
+    if (c < a.dv)
+      ((T*)io.out)[(int64_t)mt.token * io.out_stride + (int64_t)qh * a.dv + c] =
+          from_float<T>(sum == 0.0f ? 0.0f : o / sum);
+  }
+  if (io.lse && lane == 0)
+    io.lse[(int64_t)mt.token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// ============================================================================
+// Page copies: each thread owns a few columns of the page in one layer of one tensor and
+// carries its chain's copies out in order, so a page is never overwritten before its columns
+// were read, without any ordering between threads.
+// ============================================================================
+template <typename U>
+__global__ __launch_bounds__(kThreads) void copy_pages(CopyArgs a, InlineCopies in, int staged) {
+  const int64_t cols = a.page_bytes / (int64_t)sizeof(U);
+  const int64_t blocks = (cols + kThreads - 1) / kThreads;
+  int64_t b = blockIdx.x;
+  const int64_t col = (b % blocks) * kThreads + threadIdx.x;
+  b /= blocks;
+  const int chain = (int)(b % a.chains);
+  b /= a.chains;
+  const int layer = (int)(b % a.layers), tensor = (int)(b / a.layers);
+  if (col >= cols) return;
+  U* base = (U*)(a.pool[tensor] + layer * a.layer_bytes) + col;
+  U kept = {};
+  const int c0 = staged ? a.chain[chain] : chain, c1 = staged ? a.chain[chain + 1] : chain + 1;
+  for (int c = c0; c < c1; ++c) {
+    const PageCopy p = staged ? a.copies[c] : in.c[c];
+    const U x = p.src < 0 ? kept : base[p.src * cols];
+    if (p.dst < 0) kept = x;
+    else base[p.dst * cols] = x;
+  }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T, int VEC>
+hipError_t plain_attend(const StepArgs& a, const AttendIo& io, int64_t grid, hipStream_t stream) {
+  const int nj = (a.dk + 16 * VEC - 1) / (16 * VEC);
+  const dim3 g((unsigned)grid), b(kThreads);
+  if (nj * VEC <= 8) hipLaunchKernelGGL((attend_plain<T, VEC, 8 / VEC>), g, b, 0, stream, a, io);
+  else if (nj * VEC <= 16) hipLaunchKernelGGL((attend_plain<T, VEC, 16 / VEC>), g, b, 0, stream, a, io);
+  else if (nj * VEC <= 40) hipLaunchKernelGGL((attend_plain<T, VEC, 40 / VEC>), g, b, 0, stream, a, io);
+  else hipLaunchKernelGGL((attend_plain<T, VEC, 64 / VEC>), g, b, 0, stream, a, io);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
+  const int64_t grid = (int64_t)a.num_items * a.heads;
+  if (grid > 0) {
+    // four columns at a time where every row and head starts on a four-column boundary
+    const size_t al = 4 * sizeof(T);
+    const bool vec = a.dk % 4 == 0 && a.dv % 4 == 0 && a.row % 4 == 0 && io.q_stride % 4 == 0 && io.layer0 % 4 == 0 &&
+                     (uintptr_t)io.q % al == 0 && (uintptr_t)a.k_pool % al == 0 && (uintptr_t)a.v_pool % al == 0;
+    const hipError_t e = vec ? plain_attend<T, 4>(a, io, grid, stream) : plain_attend<T, 1>(a, io, grid, stream);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t join = ceil_div((int64_t)a.num_merge * a.num_q_heads, kThreads / kWave);
+  if (join > 0) hipLaunchKernelGGL((attend_join<T>), dim3((unsigned)join), dim3(kThreads), 0, stream, a, io);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream) {
+  const int64_t blocks = ceil_div((int64_t)a.num_tokens * (a.d_rot / 2), kThreads);
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(step_phase, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream) {
+  const int64_t units = (rows.q ? a.num_q_heads : 0) + a.heads + (a.family == KAMERA_GQA ? 1 : 0);
+  const int64_t blocks = ceil_div(a.num_tokens * units, kThreads / kWave);
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  const int64_t layer0 = layer * a.layer_stride;
+  const dim3 g((unsigned)blocks), b(kThreads);
+  if (a.dtype == KAMERA_BF16) hipLaunchKernelGGL((append_plain<uint16_t>), g, b, 0, stream, a, layer0, rows);
+  else hipLaunchKernelGGL((append_plain<float>), g, b, 0, stream, a, layer0, rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_step_attend(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out,
+                              int64_t out_stride, float* lse, float scale, hipStream_t stream) {
+  const AttendIo io{q, out, lse, q_stride, out_stride, layer * a.layer_stride, scale * kLog2e};
+  if (a.dtype == KAMERA_BF16) return attend_typed<uint16_t>(a, io, stream);
+  return attend_typed<float>(a, io, stream);
+}
+
+hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStream_t stream) {
+  const int64_t cols = a.page_bytes / a.unit;
+  const int64_t blocks = ceil_div(cols, kThreads) * a.chains * a.layers * a.tensors;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  static const InlineCopies kNone = {};
+  const InlineCopies& in = inl ? *inl : kNone;
+  const dim3 g((unsigned)blocks), b(kThreads);
+  const int staged = inl ? 0 : 1;
+  if (a.unit == 16) hipLaunchKernelGGL((copy_pages<u32x4>), g, b, 0, stream, a, in, staged);
+  else if (a.unit == 4) hipLaunchKernelGGL((copy_pages<uint32_t>), g, b, 0, stream, a, in, staged);
+  else hipLaunchKernelGGL((copy_pages<uint16_t>), g, b, 0, stream, a, in, staged);
+  return hipGetLastError();
+}
+
+}  // namespace kamera

@@ -1,0 +1,111 @@
+// Internal records of the serving step, shared by its host part (kamera_step_host.cpp) and
+// its kernels. The public interface is include/kamera_step.h.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kamera_step.h"
+
+namespace kamera {
+
+// ---------------------------------------------------------------- host helpers (kamera_host.cpp)
+kamera_status host_fail(kamera_status st, const char* fmt, ...);
+void host_clear_error();
+kamera_status host_check_layout(const kamera_layout* L);
+// `bytes` (a multiple of 16) of `src` into device memory through the pinned staging ring, stream-ordered
+kamera_status host_stage(const void* src, size_t bytes, void* dst, hipStream_t stream);
+
+// ---------------------------------------------------------------- attention work list
+// A run is a set of query tokens that read the same keys: the members of a shared prefix
+// (keys: the prefix), or one request (keys: its own tokens, or its prefix and its own tokens
+// one after the other). Its rows are (token j of the run, query head g of a KV head's group):
+// row = j * G + g, for every KV head.
+struct alignas(16) AttendRun {
+  int32_t pg_a, slot_a, len_a;  // first segment: tables entry, slot of its token 0, tokens
+  int32_t pg_b, slot_b;         // second segment, its tokens numbered from len_a on
+  int32_t kv;                   // tokens of both
+  int32_t tok0;                 // first query token (or its index in the token list)
+  int32_t ntok;
+  int32_t listed;               // query tokens are tok[tok0 + j] rather than tok0 + j
+  int32_t lim0, lstep;          // token j sees keys t <= max(len_a - 1, lim0 + j * lstep)
+  int32_t direct;               // the only part of its tokens' results: written to the output
+  int64_t part0;                // first partial row: part0 + (split * H + head) * (ntok * G) + row
+  int32_t splits;               // ranges its keys are cut into
+  int32_t pad;
+};
+static_assert(sizeof(AttendRun) == 64, "run record");
+
+// A workgroup's work for each KV head: rows [row0, row0 + tile) of a run, keys [kv0, kv1).
+struct alignas(16) AttendItem {
+  int32_t run, row0, kv0, kv1;
+  int32_t split, kind, pad[2];
+};
+
+// Query token whose result is joined from partial rows of up to two runs.
+struct alignas(16) MergeToken {
+  int64_t part[2];
+  int32_t rows[2];    // rows of the run per (split, head)
+  int32_t row0[2];    // the token's first row in the run
+  int32_t splits[2];
+  int32_t token, pad;
+};
+static_assert(sizeof(MergeToken) == 48, "merge record");
+
+// Kernel arguments of a step (held in the plan).
+struct StepArgs {
+  uint16_t* k_pool;
+  uint16_t* v_pool;     // MLA: the same rows
+  int64_t layer_stride; // elements
+  const int32_t* pages;
+  const AttendRun* runs;
+  const AttendItem* items;
+  const int32_t* tok;
+  const MergeToken* merge;
+  float* part_o;        // [partial rows][dv]
+  float2* part_ml;      // [partial rows]: running maximum (base-2 logarithms) and sum
+  const int64_t* slots; // [N] pool slot of every appended token
+  float* phase;         // [N][2][d_rot / 2]: cosines, then sines
+  const int32_t* pos;   // [N] positions (NULL: `positions`)
+  const int32_t* positions;
+  double rope_base;
+  int32_t family, dtype, pairing, row;  // row = F
+  int32_t heads, group, dk, dv;         // KV heads, query heads per KV head, key and value widths
+  int32_t num_q_heads, d_rot, latent, page_size;
+  int32_t page_shift, num_items, num_merge, num_tokens;
+  int32_t mrope[3];
+  int32_t kernel;       // attention kernel of the items (AttendKernel)
+};
+static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
+
+enum AttendKernel { ATTEND_PLAIN = 0 };
+constexpr int kPlainRows = 4;  // plain kernel: rows per workgroup, one wave each
+constexpr int attend_tile(int kernel) { return kernel == ATTEND_PLAIN ? kPlainRows : 0; }
+
+hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream);
+hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream);
+hipError_t launch_step_attend(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out,
+                              int64_t out_stride, float* lse, float scale, hipStream_t stream);
+
+// ---------------------------------------------------------------- page copies
+// A chain is a list of copies one thread carries out in order for its columns of the page:
+// entry (src, dst); src < 0: from the register saved by an entry with dst < 0.
+struct PageCopy {
+  int32_t src, dst;
+};
+struct CopyArgs {
+  char* pool[2];
+  int64_t layer_bytes;      // between layers
+  int64_t page_bytes;
+  const int32_t* chain;     // [chains + 1] first copy of each chain
+  const PageCopy* copies;
+  int32_t chains, layers, tensors, unit;  // unit: bytes per access (16, 4 or 2)
+};
+constexpr int kInlineCopies = 400;
+struct InlineCopies {
+  PageCopy c[kInlineCopies];  // independent copies: chain i is copy i
+};
+hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStream_t stream);
+
+}  // namespace kamera

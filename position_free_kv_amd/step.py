@@ -1,0 +1,188 @@
+"""ctypes binding of the serving step (include/kamera_step.h): same names, argument marshalling only.
+
+Every computation runs in the library's HIP kernels. A `Step` is marshalled once and may be
+kept between steps: its `num_tokens`, `num_queries`, `slot0`, `position0` and block tables are
+read by each upload, so a decode loop changes them in place.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import numpy as np
+
+from . import abi
+from .abi import Layout, Pool, _check, _ptr, _stream, _ws
+
+APPEND, ATTEND = 1, 2
+REQUEST_ALL = 1
+ATTEND_MAX_DIM = 1024
+
+EXPORTED = ["kamera_step_workspace_bytes", "kamera_step_upload", "kamera_step_append", "kamera_step_attend",
+            "kamera_copy_pages_workspace_bytes", "kamera_copy_pages", "kamera_compact_pages"]
+
+
+class Prefix(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("slot0", ctypes.c_int32), ("num_tokens", ctypes.c_int32)]
+
+
+class Request(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("slot0", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("num_queries", ctypes.c_int32), ("prefix", ctypes.c_int32), ("position0", ctypes.c_int64),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_void_p), ("prefixes", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("num_requests", ctypes.c_int32), ("num_prefixes", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32 * 2)]
+
+
+class Plan(ctypes.Structure):
+    _fields_ = [("workspace", ctypes.c_void_p), ("num_tokens", ctypes.c_int32), ("num_layers", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32), ("detail", ctypes.c_uint64 * 40)]
+
+
+class AppendRows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+_REQUEST = np.dtype({"names": [n for n, _ in Request._fields_],
+                     "formats": [np.uint64, np.int32, np.int32, np.int32, np.int32, np.int64, np.uint32, np.int32],
+                     "offsets": [getattr(Request, n).offset for n, _ in Request._fields_],
+                     "itemsize": ctypes.sizeof(Request)})
+_PREFIX = np.dtype({"names": [n for n, _ in Prefix._fields_], "formats": [np.uint64, np.int32, np.int32],
+                    "offsets": [getattr(Prefix, n).offset for n, _ in Prefix._fields_],
+                    "itemsize": ctypes.sizeof(Prefix)})
+
+_bound = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _bound
+    if _bound is None:
+        L = abi.lib()
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        lay, pool, plan = ctypes.POINTER(Layout), ctypes.POINTER(Pool), ctypes.POINTER(Plan)
+        L.kamera_step_workspace_bytes.argtypes = [lay, ctypes.POINTER(StepDesc)]
+        L.kamera_step_upload.argtypes = [lay, ctypes.POINTER(StepDesc), pool, vp, sz, vp, plan]
+        L.kamera_step_append.argtypes = [plan, i32, ctypes.POINTER(AppendRows), vp]
+        L.kamera_step_attend.argtypes = [plan, i32, vp, i64, vp, i64, vp, ctypes.c_float, vp]
+        L.kamera_copy_pages_workspace_bytes.argtypes = [i32]
+        L.kamera_copy_pages.argtypes = [lay, pool, vp, vp, i32, vp, sz, vp]
+        L.kamera_compact_pages.argtypes = [lay, pool, ctypes.POINTER(vp), vp, i32, ctypes.POINTER(i32), vp, sz, vp]
+        for name in EXPORTED:
+            getattr(L, name).restype = sz if name.endswith("_bytes") else ctypes.c_int
+        _bound = L
+    return _bound
+
+
+def _tables(block_tables, n: int):
+    """Host int32 tables, one a request: a 2-D array (a row each) or a sequence of arrays. Returns
+    (addresses, objects to keep alive)."""
+    if isinstance(block_tables, np.ndarray) and block_tables.ndim == 2:
+        if block_tables.dtype != np.int32 or not block_tables.flags.c_contiguous:
+            block_tables = np.ascontiguousarray(block_tables, dtype=np.int32)
+        if block_tables.shape[0] != n:
+            raise ValueError(f"{block_tables.shape[0]} block tables for {n} requests")
+        return block_tables.ctypes.data + np.arange(n, dtype=np.uint64) * np.uint64(block_tables.strides[0]), block_tables
+    keep = [np.zeros(1, np.int32) if t is None else np.ascontiguousarray(t, dtype=np.int32) for t in block_tables]
+    if len(keep) != n:
+        raise ValueError(f"{len(keep)} block tables for {n} requests")
+    return np.array([t.ctypes.data for t in keep], dtype=np.uint64), keep
+
+
+class Step:
+    """A kamera_step and the host arrays it points into.
+
+    block_tables: a 2-D int32 array or a sequence of 1-D ones, a row a request. The other
+    request fields are scalars or one value a request. prefixes: dicts with block_table,
+    num_tokens and (optionally) slot0. `requests` is the structured array the library reads.
+    """
+
+    def __init__(self, *, num_q_heads: int, block_tables, num_tokens, num_queries, slot0=0, prefix=-1,
+                 prefixes: Sequence[dict] = (), position0=0, request_flags=0, positions=None, flags: int = APPEND | ATTEND):
+        n = len(block_tables)
+        addresses, self._keep = _tables(block_tables, n)
+        self.requests = np.zeros(n, _REQUEST)
+        self.requests["block_table"] = addresses
+        for name, value in (("slot0", slot0), ("num_tokens", num_tokens), ("num_queries", num_queries),
+                            ("prefix", prefix), ("position0", position0), ("flags", request_flags)):
+            self.requests[name] = value
+        self._prefix_tables = [np.ascontiguousarray(p["block_table"], dtype=np.int32) for p in prefixes]
+        self.prefixes = np.zeros(len(prefixes), _PREFIX)
+        for i, p in enumerate(prefixes):
+            self.prefixes[i] = (self._prefix_tables[i].ctypes.data, p.get("slot0", 0), p["num_tokens"])
+        self._positions = positions
+        self.c = StepDesc(self.requests.ctypes.data if n else None, self.prefixes.ctypes.data if len(prefixes) else None,
+                          _ptr(positions), n, len(prefixes), int(num_q_heads), int(flags))
+
+
+def workspace_bytes(layout: Layout, step: Step) -> int:
+    return int(_lib().kamera_step_workspace_bytes(ctypes.byref(layout), ctypes.byref(step.c)))
+
+
+def upload(layout: Layout, step: Step, pool: Pool, workspace, stream=None) -> Plan:
+    """Validate a step and put its description into the workspace; the plan serves every layer.
+    It points into the workspace and keeps that tensor alive."""
+    wp, wb = _ws(workspace)
+    plan = Plan()
+    _check(_lib().kamera_step_upload(ctypes.byref(layout), ctypes.byref(step.c), ctypes.byref(pool), wp, wb,
+                                     _stream(stream), ctypes.byref(plan)))
+    plan._workspace = workspace
+    return plan
+
+
+def _stride(x, stride: Optional[int]) -> int:
+    """Elements between tokens: as given, or the first stride of a tensor (0, packed, if it has one row)."""
+    if stride is not None:
+        return int(stride)
+    return int(x.stride(0)) if hasattr(x, "stride") and x.shape[0] > 1 else 0
+
+
+def append(plan: Plan, layer: int, *, k, v=None, q=None, q_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+           q_stride: Optional[int] = None, k_stride: Optional[int] = None, v_stride: Optional[int] = None,
+           q_out_stride: Optional[int] = None, stream=None) -> None:
+    """Norm and rotate the step's queries and keys; write its K and V rows into layer `layer`."""
+    rows = AppendRows(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _stride(q, q_stride), _stride(k, k_stride), _stride(v, v_stride),
+                      _stride(q_out, q_out_stride), _ptr(q_weight), _ptr(k_weight), float(eps), 0)
+    _check(_lib().kamera_step_append(ctypes.byref(plan), int(layer), ctypes.byref(rows), _stream(stream)))
+
+
+def attend(plan: Plan, layer: int, q, out, scale: float, lse=None, *, q_stride: Optional[int] = None,
+           out_stride: Optional[int] = None, stream=None) -> None:
+    """Attention of the step's query tokens over layer `layer` of the pool."""
+    _check(_lib().kamera_step_attend(ctypes.byref(plan), int(layer), _ptr(q), _stride(q, q_stride), _ptr(out),
+                                     _stride(out, out_stride), _ptr(lse), float(scale), _stream(stream)))
+
+
+def copy_pages_workspace_bytes(num_copies: int) -> int:
+    return int(_lib().kamera_copy_pages_workspace_bytes(int(num_copies)))
+
+
+def copy_pages(layout: Layout, pool: Pool, src, dst, workspace, stream=None) -> None:
+    """Page dst[i] becomes what page src[i] was, for all i at once, in every layer."""
+    s, d = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
+    if s.shape != d.shape or s.ndim != 1:
+        raise ValueError("src and dst are one-dimensional and of one length")
+    wp, wb = _ws(workspace)
+    _check(_lib().kamera_copy_pages(ctypes.byref(layout), ctypes.byref(pool), s.ctypes.data, d.ctypes.data, s.size, wp, wb,
+                                    _stream(stream)))
+
+
+def compact_pages(layout: Layout, pool: Pool, tables: Sequence[np.ndarray], workspace, stream=None) -> int:
+    """Move the pages that `tables` (int32 host arrays, rewritten in place) name to the pool's start; their number."""
+    for t in tables:
+        if t.dtype != np.int32 or not t.flags.c_contiguous or not t.flags.writeable:
+            raise ValueError("tables are writable, contiguous int32 arrays")
+    n = len(tables)
+    ptrs = (ctypes.c_void_p * max(n, 1))(*[t.ctypes.data for t in tables])
+    lengths = np.array([t.size for t in tables] or [0], dtype=np.int32)
+    live = ctypes.c_int32()
+    wp, wb = _ws(workspace)
+    _check(_lib().kamera_compact_pages(ctypes.byref(layout), ctypes.byref(pool), ptrs, lengths.ctypes.data, n,
+                                       ctypes.byref(live), wp, wb, _stream(stream)))
+    return int(live.value)
