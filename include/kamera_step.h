@@ -94,8 +94,9 @@ typedef struct kamera_step_plan {
   uint64_t detail[40];
 } kamera_step_plan;
 
-/* Bytes of device workspace a step needs (packed tables, cos/sin of the appended tokens,
- * partial results of the attention); 0 if the arguments are invalid. */
+/* Bytes of device workspace a step needs, whatever the pool's alignment (packed tables,
+ * cos/sin of the appended tokens, partial results of the attention); 0 if the arguments are
+ * invalid. */
 size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_step* step);
 
 /* Validate a step and put its description into the workspace (256-byte aligned), on `stream`,

@@ -173,14 +173,6 @@ __global__ __launch_bounds__(kThreads) void append_plain(StepArgs a, int64_t lay
 // (running maximum m and sum l in base-2 logarithms, o scaled by exp2(m_old - m)) and the four
 // are joined at the end.
 // ============================================================================
-struct AttendIo {
-  const void* q;
-  void* out;
-  float* lse;
-  int64_t q_stride, out_stride, layer0;
-  float scale2;  // scale * log2(e)
-};
-
 // exp2(m - to) where m may still be -inf: nothing seen yet counts as zero
 __device__ __forceinline__ float shrink(float m, float to) { return m == to ? 1.0f : exp2f(m - to); }
 
@@ -206,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
     const int d = (i * 16 + dl) * VEC;
     for (int e = 0; e < VEC; ++e) q[i * VEC + e] = o[i * VEC + e] = 0.0f;
     if (d < a.dk) load_floats<T, VEC>(qp + d, q + i * VEC);
-    for (int e = 0; e < VEC; ++e) q[i * VEC + e] *= io.scale2;
+    for (int e = 0; e < VEC; ++e) q[i * VEC + e] *= io.negate ? -io.scale2 : io.scale2;
   }
   float m = -INFINITY, l = 0.0f;
   for (int t0 = it.kv0; t0 < end; t0 += 4) {
@@ -363,7 +355,9 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
     const size_t al = 4 * sizeof(T);
     const bool vec = a.dk % 4 == 0 && a.dv % 4 == 0 && a.row % 4 == 0 && io.q_stride % 4 == 0 && io.layer0 % 4 == 0 &&
                      (uintptr_t)io.q % al == 0 && (uintptr_t)a.k_pool % al == 0 && (uintptr_t)a.v_pool % al == 0;
-    const hipError_t e = vec ? plain_attend<T, 4>(a, io, grid, stream) : plain_attend<T, 1>(a, io, grid, stream);
+    const hipError_t e = a.kernel == ATTEND_MFMA ? launch_attend_mfma(a, io, stream)
+                         : vec                   ? plain_attend<T, 4>(a, io, grid, stream)
+                                                 : plain_attend<T, 1>(a, io, grid, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t join = ceil_div((int64_t)a.num_merge * a.num_q_heads, kThreads / kWave);
@@ -393,7 +387,11 @@ hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_
 
 hipError_t launch_step_attend(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out,
                               int64_t out_stride, float* lse, float scale, hipStream_t stream) {
-  const AttendIo io{q, out, lse, q_stride, out_stride, layer * a.layer_stride, scale * kLog2e};
+  AttendIo io{q, out, lse, q_stride, out_stride, layer * a.layer_stride, fabsf(scale) * kLog2e, scale < 0.0f, 0, 0};
+  // -inf marks a masked score: a scale of zero would make it NaN, the smallest one keeps it
+  if (a.kernel == ATTEND_MFMA) io.scale2 = fmaxf(io.scale2, 1.17549435e-38f);
+  io.q_vec = q_stride % 8 == 0 && (uintptr_t)q % 16 == 0;
+  io.out_vec = out_stride % 4 == 0 && (uintptr_t)out % 8 == 0;
   if (a.dtype == KAMERA_BF16) return attend_typed<uint16_t>(a, io, stream);
   return attend_typed<float>(a, io, stream);
 }

@@ -76,12 +76,33 @@ struct StepArgs {
   int32_t page_shift, num_items, num_merge, num_tokens;
   int32_t mrope[3];
   int32_t kernel;       // attention kernel of the items (AttendKernel)
+  uint32_t page_magic;  // slot / page_size = slot * page_magic >> page_bits, slot < 2^31
+  int32_t page_bits;
+  int32_t num_narrow;   // ATTEND_MFMA: the first items are tiles of kNarrowRows, the rest of kWideRows
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
 
-enum AttendKernel { ATTEND_PLAIN = 0 };
-constexpr int kPlainRows = 4;  // plain kernel: rows per workgroup, one wave each
-constexpr int attend_tile(int kernel) { return kernel == ATTEND_PLAIN ? kPlainRows : 0; }
+enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_MFMA = 1 };
+constexpr int kPlainRows = 4;    // plain kernel: rows per workgroup, one wave each
+constexpr int kNarrowRows = 32;  // matrix-core kernels: rows per workgroup
+constexpr int kWideRows = 128;
+// rows per workgroup of item `item`
+inline int attend_tile(const StepArgs& a, int item) {
+  if (a.kernel == ATTEND_PLAIN) return kPlainRows;
+  return item < a.num_narrow ? kNarrowRows : kWideRows;
+}
+
+// One attention launch: what kamera_step_attend was given.
+struct AttendIo {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride, out_stride, layer0;
+  float scale2;            // |scale| * log2(e)
+  int32_t negate;          // the scale is negative: scores of -q
+  int32_t q_vec, out_vec;  // rows of q (16 bytes) and out (8 bytes) aligned for vector access
+};
+hipError_t launch_attend_mfma(const StepArgs& a, const AttendIo& io, hipStream_t stream);
 
 hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream);
 hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream);

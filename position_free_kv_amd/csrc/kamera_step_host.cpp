@@ -40,6 +40,9 @@ struct Counts {
   int64_t tokens = 0, entries = 0;
 };
 
+// slots and key numbers are 32-bit in the kernels, with room for a tile beyond the last
+constexpr int64_t kMaxSlot = (int64_t(1) << 31) - 4096;
+
 int64_t table_entries(int32_t slot0, int64_t tokens, int P) { return tokens > 0 ? ceil_div(slot0 + tokens, P) : 0; }
 
 kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n) {
@@ -70,6 +73,7 @@ kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n
     if (p.num_tokens == 0) continue;
     if (!p.block_table) return host_fail(KAMERA_E_NULL, "prefix %d: block_table is NULL", i);
     if (p.slot0 < 0 || p.slot0 >= P) return host_fail(KAMERA_E_PAGE, "prefix %d: slot0 must be in [0, page_size)", i);
+    if ((int64_t)p.slot0 + p.num_tokens >= kMaxSlot) return host_fail(KAMERA_E_SHAPE, "prefix %d: too many tokens", i);
     n.entries += table_entries(p.slot0, p.num_tokens, P);
   }
   for (int i = 0; i < s->num_requests; ++i) {
@@ -87,7 +91,8 @@ kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n
         return host_fail(KAMERA_E_DELTA, "request %d: positions must stay within 2^31", i);
     }
     const int64_t kv = (int64_t)r.num_tokens + (r.prefix >= 0 ? s->prefixes[r.prefix].num_tokens : 0);
-    if (kv >= (int64_t(1) << 31) - 4096) return host_fail(KAMERA_E_SHAPE, "request %d: too many tokens", i);
+    if (kv >= kMaxSlot || (int64_t)r.slot0 + r.num_tokens >= kMaxSlot)
+      return host_fail(KAMERA_E_SHAPE, "request %d: too many tokens", i);
     n.tokens += r.num_queries;
     if (r.num_tokens == 0) continue;
     if (!r.block_table) return host_fail(KAMERA_E_NULL, "request %d: block_table is NULL", i);
@@ -133,6 +138,7 @@ struct Work {
   std::vector<int32_t> tok;
   std::vector<MergeToken> merge;
   int64_t part_rows = 0;
+  int32_t narrow = 0;
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -140,9 +146,19 @@ struct Tables {
   std::vector<int32_t> prefix, request;
 };
 
+// Rows per workgroup: the matrix-core kernel takes 128, or 32 where a run has no more.
 int tile_rows(int kernel, int64_t rows) {
-  (void)kernel, (void)rows;
-  return kPlainRows;
+  if (kernel == ATTEND_PLAIN) return kPlainRows;
+  return rows <= kNarrowRows ? kNarrowRows : kWideRows;
+}
+
+// The matrix-core kernel reads the pool in 16-byte pieces of 64- or 128-wide bf16 heads.
+bool mfma_layout(const kamera_layout* L) {
+  return L->dtype == KAMERA_BF16 && L->family == KAMERA_GQA && (L->head_dim == 64 || L->head_dim == 128);
+}
+int pick_kernel(const kamera_layout* L, const kamera_pool* pool) {
+  return mfma_layout(L) && aligned(pool->k_pool, 16) && aligned(pool->v_pool, 16) && pool->layer_stride % 8 == 0 ? ATTEND_MFMA
+                                                                                                                : ATTEND_PLAIN;
 }
 
 void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Work& w) {
@@ -210,7 +226,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     w.runs.push_back(r);
   }
   // keys per item: short enough for the items to fill the chip
-  const int64_t gran = 32, target = 2048;
+  const int64_t gran = kernel == ATTEND_PLAIN ? 32 : 128, target = kernel == ATTEND_PLAIN ? 2048 : 1024;
   auto blocks = [&](int64_t chunk) {
     int64_t n = 0;
     for (const AttendRun& r : w.runs) {
@@ -255,6 +271,12 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
         w.items.push_back(it);
       }
     }
+  }
+  // the kernels' items apart
+  w.narrow = 0;
+  if (kernel == ATTEND_MFMA) {
+    auto narrow = [&](const AttendItem& it) { return (int64_t)w.runs[(size_t)it.run].ntok * G <= kNarrowRows; };
+    w.narrow = (int32_t)(std::stable_partition(w.items.begin(), w.items.end(), narrow) - w.items.begin());
   }
   // tokens joined from parts (or that see no key at all)
   std::vector<int32_t> listed((size_t)s->num_prefixes, 0);  // tokens of each prefix run so far
@@ -396,7 +418,7 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   thread_local Tables tb;
   thread_local Work w;
   place_tables(L, s, tb);
-  const int kernel = ATTEND_PLAIN;
+  const int kernel = pick_kernel(L, pool);
   if (attend) plan_attention(L, s, tb, kernel, w);
   else w = Work();
   const Offsets f = carve(L, s, n, w);
@@ -463,11 +485,17 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   a.latent = L->family == KAMERA_MLA ? L->latent_dim : 0;
   a.page_size = P;
   a.page_shift = (P & (P - 1)) == 0 ? __builtin_ctz((unsigned)P) : -1;
+  // with b = ceil(log2 P): floor(2^(31 + b) / P) + 1 exceeds 2^(31 + b) / P by at most 2^b / (P 2^b),
+  // which the 31 bits of a slot cannot raise to a whole
+  a.page_bits = 31;
+  while ((int64_t(1) << (a.page_bits - 31)) < P) ++a.page_bits;
+  a.page_magic = (uint32_t)((uint64_t(1) << a.page_bits) / (uint64_t)P + 1);
   a.num_items = (int32_t)w.items.size();
   a.num_merge = (int32_t)w.merge.size();
   a.num_tokens = (int32_t)n.tokens;
   for (int k = 0; k < 3; ++k) a.mrope[k] = L->mrope_section[k];
   a.kernel = kernel;
+  a.num_narrow = w.narrow;
 
   if (n.tokens > 0) {
     st = host_stage(blob.data(), f.upload, ws, stream);
@@ -646,8 +674,15 @@ size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_ste
     Tables tb;
     Work w;
     place_tables(layout, step, tb);
-    if (step->flags & KAMERA_STEP_ATTEND) plan_attention(layout, step, tb, ATTEND_PLAIN, w);
-    bytes = carve(layout, step, n, w).total;
+    const bool attend = step->flags & KAMERA_STEP_ATTEND;
+    // the pool's alignment decides between the kernels: enough for either
+    if (attend) plan_attention(layout, step, tb, ATTEND_PLAIN, w);
+    size_t need = carve(layout, step, n, w).total;
+    if (attend && mfma_layout(layout)) {
+      plan_attention(layout, step, tb, ATTEND_MFMA, w);
+      need = std::max(need, carve(layout, step, n, w).total);
+    }
+    bytes = need;
     return KAMERA_OK;
   });
   return bytes;

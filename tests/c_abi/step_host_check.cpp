@@ -72,7 +72,6 @@ hipError_t launch_step_append(const StepArgs& a, int, const kamera_append_rows&,
 // Walks the items as the kernels do; marks which partial rows exist and which keys each token met.
 hipError_t launch_step_attend(const StepArgs& a, int, const void*, int64_t, void*, int64_t, float*, float, hipStream_t) {
   const kamera_step* s = g_seen->step;
-  const int tile = attend_tile(a.kernel);
   std::map<int64_t, int> part;      // partial row -> times written (head 0)
   std::map<int64_t, int> direct;    // (token, g) -> times written
   std::map<int64_t, std::vector<int64_t>> part_keys;  // partial row -> pool slots met
@@ -81,6 +80,7 @@ hipError_t launch_step_attend(const StepArgs& a, int, const void*, int64_t, void
     const AttendItem& it = a.items[i];
     const AttendRun& run = a.runs[it.run];
     const int64_t rows = (int64_t)run.ntok * a.group;
+    const int tile = attend_tile(a, i);
     CHECK(it.row0 >= 0 && it.row0 < rows && it.kv0 >= 0 && it.kv1 <= run.kv && it.split < run.splits);
     for (int64_t row = it.row0; row < std::min<int64_t>(it.row0 + tile, rows); ++row) {
       const int64_t j = row / a.group, g = row % a.group;

@@ -125,15 +125,18 @@ def test_null_pointers_pools_and_workspaces_refused():
     s = make(prefix=0, prefixes=PRE)
     s.prefixes["block_table"] = 0
     refused("KAMERA_E_NULL", upload, s)
+    refused("KAMERA_E_SHAPE", upload, make(num_tokens=(1 << 31) - 4000, num_queries=0))
     s = make()
     s.requests["reserved"] = 1
     refused("KAMERA_E_SHAPE", upload, s)
     for name, p in (("KAMERA_E_NULL", pool(k=None)), ("KAMERA_E_NULL", pool(v=None)), ("KAMERA_E_SHAPE", pool(num_pages=0)),
                     ("KAMERA_E_ALIGN", pool(k=FAKE + 1)), ("KAMERA_E_SHAPE", pool(layer_stride=100))):
         refused(name, upload, make(), p=p)
-    need = step.workspace_bytes(layout(), make())
+    f32 = abi.make_layout(abi.GQA, abi.F32, **GQA_LAY)  # (a bf16 layout's size covers two kernels)
+    need = step.workspace_bytes(f32, make())
     assert need > 0
-    refused("KAMERA_E_WORKSPACE", upload, make(), ws=(FAKE, need - 1))
+    refused("KAMERA_E_WORKSPACE", upload, make(), lay=f32, ws=(FAKE, need - 1))
+    refused("KAMERA_E_WORKSPACE", upload, make(), ws=(FAKE, 256))
     refused("KAMERA_E_WORKSPACE", upload, make(), ws=None)
     refused("KAMERA_E_ALIGN", upload, make(), ws=(FAKE + 64, need))
     refused("KAMERA_E_SHAPE", upload, make(), lay=layout(head_dim=7))
