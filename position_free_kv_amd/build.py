@@ -7,7 +7,7 @@ The library is the C ABI of include/kamera.h: host validation and packing
 (csrc/kamera_kernels.hip), the patch builder (csrc/kamera_builder.hip) and the
 streaming probes used for measurement (csrc/kamera_probe.hip); and the serving step of
 include/kamera_step.h: its host part (csrc/kamera_step_host.cpp) and kernels
-(csrc/kamera_step.hip, csrc/kamera_attend.hip).
+(csrc/kamera_step.hip, csrc/kamera_attend*.hip).
 """
 from __future__ import annotations
 
@@ -30,7 +30,7 @@ ARCH = os.environ.get("KAMERA_OFFLOAD_ARCH", "gfx950")
 HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
 
-STEP_KERNELS = ["kamera_step", "kamera_attend"]
+STEP_KERNELS = ["kamera_step", "kamera_attend", "kamera_attend_latent"]
 
 
 def hipcc() -> str:

@@ -1,0 +1,182 @@
+// Attention over MLA rows on the matrix cores: bf16 rows of a 512-wide latent and a 64-wide rope
+// band, one row a token for all query heads; keys are the whole row, values its latent (method and
+// register layouts: kamera_attend.h; work list: kamera_step_desc.h).
+//
+// The row is staged once and read from LDS twice, as K and as V^T. A wave keeps 16 query rows: 72
+// registers of queries and 128 of output, so that two waves share a SIMD and one's softmax runs under
+// the other's products. LDS bounds the wide kernel: per 32 keys each of its 8 waves issues 68 products
+// (1088 cycles; two waves a SIMD) and reads 68 KB, 544 KB together at 128 bytes a cycle: 4250 cycles,
+// 1.29 PFLOP/s. 32 rows a wave would halve that traffic, but its 400 registers did not compile
+// without spills.
+#include "kamera_attend.h"
+
+namespace kamera {
+
+namespace {
+
+constexpr int kLatent = 512, kRope = 64, kKey = kLatent + kRope;
+constexpr int kLatentRow = 2 * kLatent, kRopeRow = 2 * kRope;
+constexpr int kKeys = 32;  // keys per stage
+constexpr int kLatents = kKeys * kLatentRow, kBands = kKeys * kRopeRow;  // 32 KB and 4 KB
+typedef State<kKey, kLatent, 16> LatentState;
+
+// Pool rows of a stage's keys: lane i holds that of key first + i % n. The page id is asked for one
+// stage ahead and used when the stage is loaded.
+struct LatentRows {
+  int page, place;
+  __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int n, int last) {
+    const int t = min(t0 + first + (int)(threadIdx.x & 63 & (n - 1)), last);
+    page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, t, place)];
+  }
+  // N keys of the stage from `first` on (a multiple of N): one instruction a latent, one for 8 bands
+  template <int N>
+  __device__ __forceinline__ void load(const StepArgs& a, const uint16_t* k, KLDS char* latents, KLDS char* bands, int first) const {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // what follows from it is made anew each stage: kept, it would cost the products registers
+    const int row = page * a.page_size + place;  // rows of 1152 bytes: their number fits 32 bits
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint16_t* p = k + (int64_t)__builtin_amdgcn_readlane(row, i) * kKey;
+      const int piece = lane ^ (N >= 8 ? swz(i) : swz(first + i));
+      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8), (KLDS void*)(latents + (first + i) * kLatentRow), 16, 0, 0);
+    }
+    constexpr int M = N < 8 ? N : 8;  // bands an instruction brings in, 8 pieces each
+    const int piece = (lane & 7) ^ swz(first + lane / 8);
+#pragma unroll
+    for (int i = 0; i < N; i += M) {
+      const uint16_t* p = k + (int64_t)__shfl(row, i + lane / 8, 64) * kKey + kLatent;
+      if (lane < 8 * M)
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8),
+                                         (KLDS void*)(bands + (first + i) * kRopeRow), 16, 0, 0);
+    }
+  }
+};
+
+// A wave's result: normalised into the output, or as partial rows.
+__device__ __forceinline__ void put_state(const StepArgs& a, const AttendIo& io, const AttendRun& run, const AttendItem& it, const Lane& r,
+                                          const LatentState& st, float l) {
+  if (!r.owned) return;
+  const int64_t part = part_row(a, run, it, 0, r.row);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int b = 0; b < LatentState::kBlocks; ++b) {
+    const float x[4] = {st.o[b][0], st.o[b][1], st.o[b][2], st.o[b][3]};
+    put<4>(a, io, run, part, r.token, r.qh, LatentState::column(b, 0), x, inv);
+  }
+  if (LatentState::group() == 0) put_stats(a, io, run, part, r.token, r.qh, st.m, l);
+}
+
+// ============================================================================
+// Tiles of 128 rows: 8 waves of 16 rows share stages of 32 keys.
+// ============================================================================
+constexpr int kWideWaves = 8;
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char k0[kLatents], k1[kLatents], r0[kBands], r1[kBands];
+  const AttendItem it = a.items[a.num_narrow + blockIdx.x];
+  const AttendRun run = a.runs[it.run];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const Lane r = lane_row(a, run, it, 0, it.row0 + wave * 16 + (lane & 15));
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
+  bf16x8 q[LatentState::kKSteps];
+  LatentState::load_q(io, r, q);
+  LatentState st;
+  st.clear();
+  const uint16_t* kp = a.k_pool + io.layer0;
+  constexpr int PER = kKeys / kWideWaves;  // rows a wave brings in
+  const int first = wave * PER, last = it.kv1 - 1;
+  if (it.kv1 > it.kv0) {
+    LatentRows rows;
+    rows.find(a, run, it.kv0, first, PER, last);
+    rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
+    rows.find(a, run, it.kv0 + kKeys, first, PER, last);
+    for (int t = it.kv0;;) {
+      __syncthreads();  // this stage has arrived, the other buffer has been read
+      if (t + kKeys < it.kv1) {
+        rows.load<PER>(a, kp, (KLDS char*)k1, (KLDS char*)r1, first);
+        rows.find(a, run, t + 2 * kKeys, first, PER, last);
+      }
+      walk<kKeys>(st, q, (const KLDS char*)k0, (const KLDS char*)r0, (const KLDS char*)k0, t, r.end, end_min, end_max, io.scale2);
+      if ((t += kKeys) >= it.kv1) break;
+      __syncthreads();
+      if (t + kKeys < it.kv1) {
+        rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
+        rows.find(a, run, t + 2 * kKeys, first, PER, last);
+      }
+      walk<kKeys>(st, q, (const KLDS char*)k1, (const KLDS char*)r1, (const KLDS char*)k1, t, r.end, end_min, end_max, io.scale2);
+      if ((t += kKeys) >= it.kv1) break;
+    }
+  }
+  const float l = row_sum<16>(st.l);
+  int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
+  asm volatile("" : "+v"(tid));
+  put_state(a, io, run, it, lane_row(a, run, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
+}
+
+// ============================================================================
+// Tiles of up to 16 rows: each wave walks stages of its own (one buffer each: LDS holds no more),
+// the four out of step with each other, and the results are joined pairwise through LDS.
+// ============================================================================
+__global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char buf[kWaves][kLatents], bands[kWaves][kBands];
+  __shared__ float ml[2][kWaves][64];
+  const AttendItem it = a.items[blockIdx.x];
+  const AttendRun run = a.runs[it.run];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const Lane r = lane_row(a, run, it, 0, it.row0 + (lane & 15));
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
+  bf16x8 q[LatentState::kKSteps];
+  LatentState::load_q(io, r, q);
+  LatentState st;
+  st.clear();
+  const uint16_t* kp = a.k_pool + io.layer0;
+  const int last = it.kv1 - 1;
+  int t = it.kv0 + wave * kKeys;
+  if (t < it.kv1) {
+    KLDS char *mine = (KLDS char*)buf[wave], *band = (KLDS char*)bands[wave];
+    LatentRows rows;
+    rows.find(a, run, t, 0, kKeys, last);
+    for (; t < it.kv1; t += kWaves * kKeys) {
+      rows.load<kKeys>(a, kp, mine, band, 0);
+      rows.find(a, run, t + kWaves * kKeys, 0, kKeys, last);
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's stage has arrived
+      __builtin_amdgcn_wave_barrier();
+      walk<kKeys>(st, q, (const KLDS char*)mine, (const KLDS char*)band, (const KLDS char*)mine, t, r.end, end_min, end_max, io.scale2);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  // 2 and 3 into 0 and 1, then 1 into 0: registers of like lanes, 32 KB a wave
+  float l = row_sum<16>(st.l);
+  f32x4* place = (f32x4*)&buf[0][0];
+#pragma unroll
+  for (int step = 2; step; step >>= 1) {
+    __syncthreads();
+    if (wave >= step && wave < 2 * step) {
+#pragma unroll
+      for (int b = 0; b < LatentState::kBlocks; ++b) place[((wave - step) * LatentState::kBlocks + b) * 64 + lane] = st.o[b];
+      ml[0][wave][lane] = st.m;
+      ml[1][wave][lane] = l;
+    }
+    __syncthreads();
+    if (wave < step) {
+      const float m = ml[0][wave + step][lane], top = fmaxf(st.m, m);
+      const float f0 = st.m == top ? 1.0f : __builtin_amdgcn_exp2f(st.m - top), f1 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      st.m = top;
+      l = l * f0 + ml[1][wave + step][lane] * f1;
+#pragma unroll
+      for (int b = 0; b < LatentState::kBlocks; ++b) st.o[b] = st.o[b] * f0 + place[(wave * LatentState::kBlocks + b) * 64 + lane] * f1;
+    }
+  }
+  if (wave == 0) put_state(a, io, run, it, r, st, l);
+}
+
+}  // namespace
+
+hipError_t launch_attend_latent(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
+  const int wide = a.num_items - a.num_narrow, narrow = a.num_narrow;
+  if (wide > 0) hipLaunchKernelGGL(attend_latent_wide, dim3((unsigned)wide), dim3(64 * kWideWaves), 0, stream, a, io);
+  if (narrow > 0) hipLaunchKernelGGL(attend_latent_narrow, dim3((unsigned)narrow), dim3(kThreads), 0, stream, a, io);
+  return hipGetLastError();
+}
+
+}  // namespace kamera

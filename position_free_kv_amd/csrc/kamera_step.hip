@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
   const AttendItem it = a.items[item];
   const AttendRun run = a.runs[it.run];
   const int lane = threadIdx.x & 63, dl = lane & 15, tg = lane >> 4;
-  const int row = it.row0 + (threadIdx.x >> 6);
+  const int row = it.row0 + (threadIdx.x >> 6);  // narrow_rows(ATTEND_PLAIN) waves
   if (row >= run.ntok * a.group) return;
   const int j = row / a.group, g = row - j * a.group;
   const int token = run.listed ? a.tok[run.tok0 + j] : run.tok0 + j;
@@ -355,9 +355,10 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
     const size_t al = 4 * sizeof(T);
     const bool vec = a.dk % 4 == 0 && a.dv % 4 == 0 && a.row % 4 == 0 && io.q_stride % 4 == 0 && io.layer0 % 4 == 0 &&
                      (uintptr_t)io.q % al == 0 && (uintptr_t)a.k_pool % al == 0 && (uintptr_t)a.v_pool % al == 0;
-    const hipError_t e = a.kernel == ATTEND_MFMA ? launch_attend_mfma(a, io, stream)
-                         : vec                   ? plain_attend<T, 4>(a, io, grid, stream)
-                                                 : plain_attend<T, 1>(a, io, grid, stream);
+    const hipError_t e = a.kernel == ATTEND_HEADS    ? launch_attend_heads(a, io, stream)
+                         : a.kernel == ATTEND_LATENT ? launch_attend_latent(a, io, stream)
+                         : vec                       ? plain_attend<T, 4>(a, io, grid, stream)
+                                                     : plain_attend<T, 1>(a, io, grid, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t join = ceil_div((int64_t)a.num_merge * a.num_q_heads, kThreads / kWave);
@@ -389,7 +390,7 @@ hipError_t launch_step_attend(const StepArgs& a, int layer, const void* q, int64
                               int64_t out_stride, float* lse, float scale, hipStream_t stream) {
   AttendIo io{q, out, lse, q_stride, out_stride, layer * a.layer_stride, fabsf(scale) * kLog2e, scale < 0.0f, 0, 0};
   // -inf marks a masked score: a scale of zero would make it NaN, the smallest one keeps it
-  if (a.kernel == ATTEND_MFMA) io.scale2 = fmaxf(io.scale2, 1.17549435e-38f);
+  if (a.kernel != ATTEND_PLAIN) io.scale2 = fmaxf(io.scale2, 1.17549435e-38f);
   io.q_vec = q_stride % 8 == 0 && (uintptr_t)q % 16 == 0;
   io.out_vec = out_stride % 4 == 0 && (uintptr_t)out % 8 == 0;
   if (a.dtype == KAMERA_BF16) return attend_typed<uint16_t>(a, io, stream);

@@ -78,18 +78,18 @@ struct StepArgs {
   int32_t kernel;       // attention kernel of the items (AttendKernel)
   uint32_t page_magic;  // slot / page_size = slot * page_magic >> page_bits, slot < 2^31
   int32_t page_bits;
-  int32_t num_narrow;   // ATTEND_MFMA: the first items are tiles of kNarrowRows, the rest of kWideRows
+  int32_t num_narrow;   // matrix-core kernels: the first items are narrow tiles, the rest wide ones
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
 
-enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_MFMA = 1 };
-constexpr int kPlainRows = 4;    // plain kernel: rows per workgroup, one wave each
-constexpr int kNarrowRows = 32;  // matrix-core kernels: rows per workgroup
+// PLAIN: any layout. HEADS: bf16 GQA/MHA heads of 64 or 128 columns; LATENT: bf16 MLA rows of 512 + 64
+// columns, both on the matrix cores.
+enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2 };
+// Rows per workgroup: a run that fits the narrow tile takes that, others the wide one.
 constexpr int kWideRows = 128;
-// rows per workgroup of item `item`
-inline int attend_tile(const StepArgs& a, int item) {
-  if (a.kernel == ATTEND_PLAIN) return kPlainRows;
-  return item < a.num_narrow ? kNarrowRows : kWideRows;
+constexpr int narrow_rows(int kernel) { return kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32; }
+constexpr int tile_rows(int kernel, int64_t rows) {
+  return kernel == ATTEND_PLAIN || rows <= narrow_rows(kernel) ? narrow_rows(kernel) : kWideRows;
 }
 
 // One attention launch: what kamera_step_attend was given.
@@ -102,7 +102,8 @@ struct AttendIo {
   int32_t negate;          // the scale is negative: scores of -q
   int32_t q_vec, out_vec;  // rows of q (16 bytes) and out (8 bytes) aligned for vector access
 };
-hipError_t launch_attend_mfma(const StepArgs& a, const AttendIo& io, hipStream_t stream);
+hipError_t launch_attend_heads(const StepArgs& a, const AttendIo& io, hipStream_t stream);
+hipError_t launch_attend_latent(const StepArgs& a, const AttendIo& io, hipStream_t stream);
 
 hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream);
 hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream);

@@ -146,19 +146,18 @@ struct Tables {
   std::vector<int32_t> prefix, request;
 };
 
-// Rows per workgroup: the matrix-core kernel takes 128, or 32 where a run has no more.
-int tile_rows(int kernel, int64_t rows) {
-  if (kernel == ATTEND_PLAIN) return kPlainRows;
-  return rows <= kNarrowRows ? kNarrowRows : kWideRows;
-}
-
-// The matrix-core kernel reads the pool in 16-byte pieces of 64- or 128-wide bf16 heads.
-bool mfma_layout(const kamera_layout* L) {
-  return L->dtype == KAMERA_BF16 && L->family == KAMERA_GQA && (L->head_dim == 64 || L->head_dim == 128);
+// Layouts of the matrix-core kernels; they also need the pool in 16-byte pieces, and the MLA one
+// row numbers of 32 bits.
+int matrix_kernel(const kamera_layout* L) {
+  if (L->dtype != KAMERA_BF16) return ATTEND_PLAIN;
+  if (L->family == KAMERA_GQA) return L->head_dim == 64 || L->head_dim == 128 ? ATTEND_HEADS : ATTEND_PLAIN;
+  return L->latent_dim == 512 && L->rope_dim == 64 ? ATTEND_LATENT : ATTEND_PLAIN;
 }
 int pick_kernel(const kamera_layout* L, const kamera_pool* pool) {
-  return mfma_layout(L) && aligned(pool->k_pool, 16) && aligned(pool->v_pool, 16) && pool->layer_stride % 8 == 0 ? ATTEND_MFMA
-                                                                                                                : ATTEND_PLAIN;
+  const int kernel = matrix_kernel(L);
+  if (!aligned(pool->k_pool, 16) || (L->family == KAMERA_GQA && !aligned(pool->v_pool, 16)) || pool->layer_stride % 8) return ATTEND_PLAIN;
+  if (kernel == ATTEND_LATENT && (int64_t)pool->num_pages * L->page_size >= (int64_t(1) << 31)) return ATTEND_PLAIN;
+  return kernel;
 }
 
 void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Work& w) {
@@ -274,8 +273,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   }
   // the kernels' items apart
   w.narrow = 0;
-  if (kernel == ATTEND_MFMA) {
-    auto narrow = [&](const AttendItem& it) { return (int64_t)w.runs[(size_t)it.run].ntok * G <= kNarrowRows; };
+  if (kernel != ATTEND_PLAIN) {
+    auto narrow = [&](const AttendItem& it) { return (int64_t)w.runs[(size_t)it.run].ntok * G <= narrow_rows(kernel); };
     w.narrow = (int32_t)(std::stable_partition(w.items.begin(), w.items.end(), narrow) - w.items.begin());
   }
   // tokens joined from parts (or that see no key at all)
@@ -678,8 +677,8 @@ size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_ste
     // the pool's alignment decides between the kernels: enough for either
     if (attend) plan_attention(layout, step, tb, ATTEND_PLAIN, w);
     size_t need = carve(layout, step, n, w).total;
-    if (attend && mfma_layout(layout)) {
-      plan_attention(layout, step, tb, ATTEND_MFMA, w);
+    if (attend && matrix_kernel(layout) != ATTEND_PLAIN) {
+      plan_attention(layout, step, tb, matrix_kernel(layout), w);
       need = std::max(need, carve(layout, step, n, w).total);
     }
     bytes = need;

@@ -80,7 +80,8 @@ hipError_t launch_step_attend(const StepArgs& a, int, const void*, int64_t, void
     const AttendItem& it = a.items[i];
     const AttendRun& run = a.runs[it.run];
     const int64_t rows = (int64_t)run.ntok * a.group;
-    const int tile = attend_tile(a, i);
+    const int tile = tile_rows(a.kernel, rows);
+    CHECK(a.kernel == ATTEND_PLAIN || (i < a.num_narrow) == (tile < kWideRows));
     CHECK(it.row0 >= 0 && it.row0 < rows && it.kv0 >= 0 && it.kv1 <= run.kv && it.split < run.splits);
     for (int64_t row = it.row0; row < std::min<int64_t>(it.row0 + tile, rows); ++row) {
       const int64_t j = row / a.group, g = row % a.group;

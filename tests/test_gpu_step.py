@@ -101,6 +101,31 @@ def test_attend_ignores_what_is_unseen(dim, dtype, bad):
     assert torch.equal(o0[:, keep], o1[:, keep]) and torch.equal(z0[:, keep], z1[:, keep])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("heads", [4, 16, 40])
+def test_attend_on_latent_rows_ignores_what_is_unseen(heads, bad):
+    c = Case(family=MLA, heads=heads, latent=512, rope=64, garbage=bad, prefixes=[35], seed=9,
+             requests=[(0, 20, 4), (-1, 70, 40), (0, 3, 1), (0, 50, 30), (-1, 3, 5)])
+    o0, z0 = c.check_attend(scale_of(c))
+    for r in range(len(c.requests)):  # each request's last token: only its last query sees it
+        c.pools[0][:, int(c.rows[1 + r][-1])] = bad
+    o1, z1 = c.attend(scale_of(c))
+    torch.cuda.synchronize()
+    keep = torch.ones(c.n, dtype=torch.bool, device="cuda")
+    keep[torch.cumsum(torch.tensor([r[2] for r in c.requests]), 0) - 1] = False
+    assert torch.equal(o0[:, keep], o1[:, keep]) and torch.equal(z0[:, keep], z1[:, keep])
+
+
+@pytest.mark.parametrize("heads,dim,family", [(8, 128, GQA), (8, 64, GQA), (16, 64, MLA), (48, 64, MLA)])
+def test_attend_splits_long_keys(heads, dim, family):
+    """Few rows over many keys: split over workgroups and joined, own tokens and prefix alike."""
+    more = dict(heads=heads, kv_heads=1, head_dim=dim) if family == GQA else dict(family=MLA, heads=heads, latent=512, rope=dim)
+    c = Case(layers=1, prefixes=[9000, 700], requests=[(0, 1, 1), (0, 5000, 1), (1, 20, 1), (-1, 7001, 3), (1, 3, 2)], seed=dim, **more)
+    c.check_attend(scale_of(c))
+    c.check_attend(-scale_of(c))
+    c.check_attend(0.0)
+
+
 @pytest.mark.parametrize("dim,dtype", [(128, BF16), (64, F32), (10, BF16)])
 def test_attend_scores_of_every_size(dim, dtype):
     """Scores of thousands, equal scores, scores of the type's lowest value."""
