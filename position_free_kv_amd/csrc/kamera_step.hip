@@ -268,43 +268,139 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
 }
 
 // ============================================================================
-// Join of partial results: one wave per (token, query head). Parts are taken in a fixed order,
-// so the result does not depend on which workgroup finished first.
+// Join of partial results: TPR threads (a wave, or a workgroup where a row has many parts) for each
+// (token, query head). First every part's maximum and sum become its weight, all parts at once; then
+// the weighted rows are added, 16 bytes a thread, several parts side by side where a row is shorter
+// than the threads. Parts are taken in a fixed order, so the result does not depend on which
+// workgroup finished first.
 // ============================================================================
-template <typename T>
+constexpr int kJoinParts = 2 * kMaxSplits;
+
+struct Parts {
+  MergeToken mt;
+  int heads, head, g;
+  __device__ __forceinline__ int count() const { return mt.splits[0] + mt.splits[1]; }
+  __device__ __forceinline__ int64_t row(int k) const {
+    const int s = k >= mt.splits[0];
+    return mt.part[s] + ((int64_t)(s ? k - mt.splits[0] : k) * heads + head) * mt.rows[s] + mt.row0[s] + g;
+  }
+};
+
+// TPR threads' maximum or sum, every thread receiving it (a workgroup's through `red`)
+template <int TPR, bool MAX>
+__device__ __forceinline__ float over_threads(float x, float* red) {
+  for (int d = 32; d; d >>= 1) {
+    const float y = __shfl_xor(x, d, kWave);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  if constexpr (TPR == kWave) return x;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = red[0];
+  for (int i = 1; i < TPR / kWave; ++i) x = MAX ? fmaxf(x, red[i]) : x + red[i];
+  return x;
+}
+
+template <typename T, int TPR>
 __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io) {
+  constexpr int ROWS = kThreads / TPR;  // rows of a workgroup
+  constexpr int MAXP = TPR == kWave ? kWave : kJoinParts;
+  __shared__ float weight[ROWS][MAXP];
+  __shared__ f32x4 held[ROWS][TPR];
+  __shared__ float red[ROWS][4];
+  const int sub = threadIdx.x / TPR, tid = threadIdx.x - sub * TPR;
+  const int64_t task = (int64_t)blockIdx.x * ROWS + sub;
+  const int64_t i = min(task / a.num_q_heads, (int64_t)a.num_merge - 1);
+  const int qh = (int)(task % a.num_q_heads);
+  const bool live = task < (int64_t)a.num_merge * a.num_q_heads;
+  const Parts p{a.merge[i], a.heads, qh / a.group, qh % a.group};
+  const int n = p.count();
+  float top = -INFINITY, sum = 0.0f, m[MAXP / TPR], l[MAXP / TPR];
+#pragma unroll
+  for (int j = 0; j < MAXP / TPR; ++j) {
+    const int k = j * TPR + tid;
+    const float2 ml = k < n ? a.part_ml[p.row(k)] : make_float2(-INFINITY, 0.0f);
+    m[j] = ml.x;
+    l[j] = ml.y;
+    if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+  }
+  top = over_threads<TPR, true>(top, red[sub]);
+#pragma unroll
+  for (int j = 0; j < MAXP / TPR; ++j) {
+    const int k = j * TPR + tid;
+    const float w = l[j] == 0.0f ? 0.0f : shrink(m[j], top);
+    if (k < n) weight[sub][k] = w;
+    sum += l[j] * w;
+  }
+  sum = over_threads<TPR, false>(sum, red[sub]);
+  __syncthreads();
+  const int quads = a.dv / 4;
+  T* out = (T*)io.out + (int64_t)a.merge[i].token * io.out_stride + (int64_t)qh * a.dv;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const KGLOBAL f32x4* rows = (const KGLOBAL f32x4*)a.part_o;
+  // side by side: `side` parts, `quads` threads each; rows longer than the threads in turns
+  const int side = quads < TPR ? TPR / quads : 1, lane = quads < TPR ? tid % quads : tid, first = quads < TPR ? tid / quads : 0;
+  for (int c = lane; c < quads; c += TPR) {
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (first < side) {
+#pragma unroll 4
+      for (int k = first; k < n; k += side) {
+        const float w = weight[sub][k];
+        const f32x4 x = rows[p.row(k) * quads + c];
+        if (w != 0.0f)  // (an empty part's row may hold anything)
+          for (int e = 0; e < 4; ++e) o[e] += x[e] * w;
+      }
+    }
+    if (side > 1) {  // (one turn only: every thread is here)
+      held[sub][tid] = o;
+      if (TPR == kWave) __builtin_amdgcn_wave_barrier();
+      else __syncthreads();
+      if (first == 0)
+        for (int s = 1; s < side; ++s) {
+          const f32x4 x = held[sub][s * quads + c];
+          for (int e = 0; e < 4; ++e) o[e] += x[e];
+        }
+    }
+    if (live && first == 0)
+      for (int e = 0; e < 4; ++e) out[4 * c + e] = from_float<T>(o[e] * inv);
+  }
+  if (live && io.lse && tid == 0)
+    io.lse[(int64_t)a.merge[i].token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// Rows that are not whole 16-byte pieces: a wave a row, one part after the other.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attend_join_any(StepArgs a, AttendIo io) {
   const int64_t task = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
   const int64_t i = task / a.num_q_heads;
   if (i >= a.num_merge) return;
-  const int qh = (int)(task - i * a.num_q_heads), head = qh / a.group, g = qh - head * a.group;
+  const int qh = (int)(task - i * a.num_q_heads);
   const int lane = threadIdx.x & 63;
-  const MergeToken mt = a.merge[i];
+  const Parts p{a.merge[i], a.heads, qh / a.group, qh % a.group};
+  const int n = p.count();
   float top = -INFINITY, sum = 0.0f;
-  for (int s = 0; s < 2; ++s)
-    for (int k = lane; k < mt.splits[s]; k += kWave) {
-      const float2 ml = a.part_ml[mt.part[s] + ((int64_t)k * a.heads + head) * mt.rows[s] + mt.row0[s] + g];
-      if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-    }
+  for (int k = lane; k < n; k += kWave) {
+    const float2 ml = a.part_ml[p.row(k)];
+    if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+  }
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-  for (int c0 = 0; c0 < a.dv; c0 += kWave) {
-    const int c = c0 + lane;
+  for (int c = lane; c - lane < a.dv; c += kWave) {
     float o = 0.0f;
     sum = 0.0f;
-    for (int s = 0; s < 2; ++s)
-      for (int k = 0; k < mt.splits[s]; ++k) {
-        const int64_t pr = mt.part[s] + ((int64_t)k * a.heads + head) * mt.rows[s] + mt.row0[s] + g;
-        const float2 ml = a.part_ml[pr];
-        if (ml.y == 0.0f) continue;
-        const float w = shrink(ml.x, top);
-        sum += ml.y * w;
-        if (c < a.dv) o += a.part_o[pr * a.dv + c] * w;
-      }
+    for (int k = 0; k < n; ++k) {
+      const int64_t pr = p.row(k);
+      const float2 ml = a.part_ml[pr];
+      if (ml.y == 0.0f) continue;
+      const float w = shrink(ml.x, top);
+      sum += ml.y * w;
+      if (c < a.dv) o += a.part_o[pr * a.dv + c] * w;
+    }
     if (c < a.dv)
-      ((T*)io.out)[(int64_t)mt.token * io.out_stride + (int64_t)qh * a.dv + c] =
-          from_float<T>(sum == 0.0f ? 0.0f : o / sum);
+      ((T*)io.out)[(int64_t)p.mt.token * io.out_stride + (int64_t)qh * a.dv + c] = from_float<T>(sum == 0.0f ? 0.0f : o / sum);
   }
   if (io.lse && lane == 0)
-    io.lse[(int64_t)mt.token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    io.lse[(int64_t)p.mt.token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ============================================================================
@@ -361,8 +457,13 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
                                                      : plain_attend<T, 1>(a, io, grid, stream);
     if (e != hipSuccess) return e;
   }
-  const int64_t join = ceil_div((int64_t)a.num_merge * a.num_q_heads, kThreads / kWave);
-  if (join > 0) hipLaunchKernelGGL((attend_join<T>), dim3((unsigned)join), dim3(kThreads), 0, stream, a, io);
+  const int64_t rows = (int64_t)a.num_merge * a.num_q_heads;
+  if (rows == 0) return hipSuccess;
+  const dim3 b(kThreads);
+  const unsigned by_wave = (unsigned)ceil_div(rows, kThreads / kWave);
+  if (a.dv % 4) hipLaunchKernelGGL((attend_join_any<T>), dim3(by_wave), b, 0, stream, a, io);
+  else if (a.max_parts <= kJoinByWave) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave), b, 0, stream, a, io);
+  else hipLaunchKernelGGL((attend_join<T, kThreads>), dim3((unsigned)rows), b, 0, stream, a, io);
   return hipGetLastError();
 }
 

@@ -78,6 +78,7 @@ struct StepArgs {
   int32_t kernel;       // attention kernel of the items (AttendKernel)
   uint32_t page_magic;  // slot / page_size = slot * page_magic >> page_bits, slot < 2^31
   int32_t page_bits;
+  int32_t max_parts;    // most parts of a joined row
   int32_t num_narrow;   // matrix-core kernels: the first items are narrow tiles, the rest wide ones
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
@@ -91,6 +92,9 @@ constexpr int narrow_rows(int kernel) { return kernel == ATTEND_PLAIN ? 4 : kern
 constexpr int tile_rows(int kernel, int64_t rows) {
   return kernel == ATTEND_PLAIN || rows <= narrow_rows(kernel) ? narrow_rows(kernel) : kWideRows;
 }
+
+constexpr int kMaxSplits = 512;  // ranges a run's keys are cut into, at most
+constexpr int kJoinByWave = 8;   // parts up to which a wave joins a row, rather than a workgroup
 
 // One attention launch: what kamera_step_attend was given.
 struct AttendIo {

@@ -138,7 +138,7 @@ struct Work {
   std::vector<int32_t> tok;
   std::vector<MergeToken> merge;
   int64_t part_rows = 0;
-  int32_t narrow = 0;
+  int32_t narrow = 0, max_parts = 0;
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -168,6 +168,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   w.tok.clear();
   w.merge.clear();
   w.part_rows = 0;
+  w.max_parts = 0;
   // members of each prefix whose rows are few enough to share its reads
   std::vector<int32_t> members((size_t)s->num_prefixes, 0);
   auto few = [&](const kamera_request& r) {
@@ -224,58 +225,69 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
-  // keys per item: short enough for the items to fill the chip
-  const int64_t gran = kernel == ATTEND_PLAIN ? 32 : 128, target = kernel == ATTEND_PLAIN ? 2048 : 1024;
-  auto blocks = [&](int64_t chunk) {
-    int64_t n = 0;
-    for (const AttendRun& r : w.runs) {
-      const int64_t rows = (int64_t)r.ntok * G;
-      n += ceil_div(rows, tile_rows(kernel, rows)) * ceil_div(r.kv, chunk);
+  // Keys per item: each kernel's items (narrow, wide) should fill the chip once. Items wait for a
+  // few reads one after the other (item, run, page ids, rows) before their first product, so more
+  // and shorter ones cost: `least` keys at least.
+  const bool plain = kernel == ATTEND_PLAIN;
+  const int64_t gran = plain ? 32 : 128, least = plain ? 32 : 128;
+  int64_t chunk_of[2];
+  w.narrow = 0;
+  for (int wide = 0; wide < 2; ++wide) {
+    const int64_t target = plain ? 2048 : 512;
+    auto is = [&](const AttendRun& r) { return (tile_rows(kernel, (int64_t)r.ntok * G) == kWideRows) == (wide == 1); };
+    auto blocks = [&](int64_t chunk) {
+      int64_t n = 0;
+      for (const AttendRun& r : w.runs) {
+        const int64_t rows = (int64_t)r.ntok * G;
+        if (is(r)) n += ceil_div(rows, tile_rows(kernel, rows)) * ceil_div(r.kv, chunk);
+      }
+      return n * h.heads;
+    };
+    int64_t longest = least;
+    for (const AttendRun& r : w.runs)
+      if (is(r)) longest = std::max<int64_t>(longest, r.kv);
+    int64_t lo = ceil_div(std::max(least, ceil_div(longest, kMaxSplits)), gran), hi = std::max(lo, ceil_div(longest, gran));  // in units of gran
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (blocks(mid * gran) <= target) hi = mid;
+      else lo = mid + 1;
     }
-    return n * h.heads;
-  };
-  int64_t longest = gran;
-  for (const AttendRun& r : w.runs) longest = std::max<int64_t>(longest, r.kv);
-  int64_t lo = 1, hi = ceil_div(longest, gran);  // chunk in units of gran
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (blocks(mid * gran) <= target) hi = mid;
-    else lo = mid + 1;
+    chunk_of[wide] = lo * gran;
   }
-  const int64_t chunk0 = lo * gran;
-  for (size_t k = 0; k < w.runs.size(); ++k) {
-    AttendRun& r = w.runs[k];
-    const int64_t rows = (int64_t)r.ntok * G;
-    const int tile = tile_rows(kernel, rows);
-    const int64_t splits = ceil_div(r.kv, chunk0);
-    const int64_t chunk = (int64_t)round_up((size_t)ceil_div(r.kv, splits), (size_t)gran);
-    const int64_t n = ceil_div(r.kv, chunk);
-    r.splits = (int32_t)n;
-    if (n > 1) r.direct = 0;
-    if (!r.direct) {
-      r.part0 = w.part_rows;
-      w.part_rows += n * h.heads * rows;
-    }
-    for (int64_t row0 = 0; row0 < rows; row0 += tile) {
-      const int64_t last = (std::min(row0 + tile, rows) - 1) / G;  // the tile's last token
-      const int64_t end = std::min<int64_t>(r.kv, std::max<int64_t>(r.len_a - 1, r.lim0 + last * r.lstep) + 1);
-      for (int64_t sp = 0; sp < n; ++sp) {
-        AttendItem it;
-        std::memset(&it, 0, sizeof(it));
-        it.run = (int32_t)k;
-        it.row0 = (int32_t)row0;
-        it.kv0 = (int32_t)(sp * chunk);
-        it.kv1 = (int32_t)std::max<int64_t>(it.kv0, std::min(end, (sp + 1) * chunk));
-        it.split = (int32_t)sp;
-        w.items.push_back(it);
+  for (int wide = 0; wide < 2; ++wide) {
+    for (size_t k = 0; k < w.runs.size(); ++k) {
+      AttendRun& r = w.runs[k];
+      const int64_t rows = (int64_t)r.ntok * G;
+      const int tile = tile_rows(kernel, rows);
+      if ((tile == kWideRows) != (wide == 1)) continue;
+      const int64_t splits = ceil_div(r.kv, chunk_of[wide]);
+      const int64_t chunk = (int64_t)round_up((size_t)ceil_div(r.kv, splits), (size_t)gran);
+      const int64_t n = ceil_div(r.kv, chunk);
+      r.splits = (int32_t)n;
+      if (n > 1) r.direct = 0;
+      if (!r.direct) {
+        r.part0 = w.part_rows;
+        w.part_rows += n * h.heads * rows;
+      }
+      for (int64_t row0 = 0; row0 < rows; row0 += tile) {
+        const int64_t last = (std::min(row0 + tile, rows) - 1) / G;  // the tile's last token
+        const int64_t end = std::min<int64_t>(r.kv, std::max<int64_t>(r.len_a - 1, r.lim0 + last * r.lstep) + 1);
+        for (int64_t sp = 0; sp < n; ++sp) {
+          AttendItem it;
+          std::memset(&it, 0, sizeof(it));
+          it.run = (int32_t)k;
+          it.row0 = (int32_t)row0;
+          it.kv0 = (int32_t)(sp * chunk);
+          it.kv1 = (int32_t)std::max<int64_t>(it.kv0, std::min(end, (sp + 1) * chunk));
+          it.split = (int32_t)sp;
+          w.items.push_back(it);
+        }
       }
     }
-  }
-  // the kernels' items apart
-  w.narrow = 0;
-  if (kernel != ATTEND_PLAIN) {
-    auto narrow = [&](const AttendItem& it) { return (int64_t)w.runs[(size_t)it.run].ntok * G <= narrow_rows(kernel); };
-    w.narrow = (int32_t)(std::stable_partition(w.items.begin(), w.items.end(), narrow) - w.items.begin());
+    // the longest first: the short ones fill the gaps at the end
+    auto longer = [](const AttendItem& x, const AttendItem& y) { return x.kv1 - x.kv0 > y.kv1 - y.kv0; };
+    if (!plain) std::stable_sort(w.items.begin() + (wide ? w.narrow : 0), w.items.end(), longer);
+    if (!wide) w.narrow = (int32_t)w.items.size();
   }
   // tokens joined from parts (or that see no key at all)
   std::vector<int32_t> listed((size_t)s->num_prefixes, 0);  // tokens of each prefix run so far
@@ -298,6 +310,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       m.token = (int32_t)(tok + j);
       if (sh) part(m, 0, prefix_run[(size_t)q.prefix], listed[(size_t)q.prefix]++);
       if (run >= 0) part(m, 1, run, j);
+      w.max_parts = std::max(w.max_parts, m.splits[0] + m.splits[1]);
       w.merge.push_back(m);
     }
   }
@@ -495,6 +508,7 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   for (int k = 0; k < 3; ++k) a.mrope[k] = L->mrope_section[k];
   a.kernel = kernel;
   a.num_narrow = w.narrow;
+  a.max_parts = w.max_parts;
 
   if (n.tokens > 0) {
     st = host_stage(blob.data(), f.upload, ws, stream);
