@@ -16,10 +16,8 @@
 // 2^8, which neither bf16 nor the fp32 sums mind.
 //
 // K and V go from the pool's pages straight into LDS (global_load_lds, 16 bytes a lane, every
-// lane its own row address: pages may be of any size and order), double-buffered. 16-byte
-// pieces of a token's row are stored at position piece ^ swz(token): the row reads of K (32
-// tokens, one piece each) and the transposing reads of V (4 tokens x 32 bytes) then touch all
-// banks evenly. Rows past the range's end repeat its last row and are masked.
+// lane its own row address: pages may be of any size and order). Rows past the range's end repeat
+// its last row and are masked. Steps whose keys every row sees (nearly all) carry no mask.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,7 +83,15 @@ __device__ __forceinline__ float row_sum(float x) {
   return p.a + p.b;
 }
 
-__device__ __forceinline__ int swz(int token) { return ((token & 3) << 1) | ((token >> 2) & 1); }
+// Where a token's 16-byte pieces lie in its LDS row: piece ^ swz(token). LDS serves 256 bytes at a
+// time over 64 banks: 16 lanes of a row read (16 tokens, one piece each) and 32 lanes of a transposing
+// read (32 query rows: 4 tokens x 64 bytes, 16 rows: 8 tokens x 32 bytes) must fall into 16 different
+// pieces of 256 bytes. BYTES: the LDS row, 128 (two tokens to 256 bytes) or a multiple of 256.
+template <int ROWS, int BYTES>
+__device__ __forceinline__ constexpr int swz(int token) {
+  return BYTES % 256 == 0 ? (ROWS == 32 ? ((token & 3) << 2) | ((token >> 2) & 3) : ((token & 7) << 1) | ((token >> 3) & 1))
+                          : (ROWS == 32 ? ((token & 2) << 1) | ((token >> 2) & 3) : (token & 6) | ((token >> 3) & 1));
+}
 
 // One lane's view of its query row and of the range of keys.
 struct Lane {
@@ -133,9 +139,7 @@ struct State {
   static constexpr int kScores = ROWS == 32 ? 16 : 4;  // values of a lane in one result tile
   static constexpr int kBlocks = DV / ROWS;            // output tiles
   static constexpr int kPSteps = 32 / kDepth;          // products a block takes of a step: 2 or 1
-  static constexpr int kTurns = 128 / (16 * kGroups);  // products between bases 128 bytes apart: 4 or 2
-  static constexpr int kVTurns = 128 / (2 * ROWS);     // output tiles likewise: 2 or 4
-  static constexpr int kAhead = DV > 128 ? 2 : 4;            // operands read ahead of their products
+  static constexpr bool kTight = DV > 128;             // registers are short: operands are read in small groups
   typedef float Acc __attribute__((ext_vector_type(kScores)));
   Acc o[kBlocks];
   float m, l;  // l: this lane's keys only (a row's lanes are added at the end)
@@ -180,36 +184,47 @@ struct State {
     }
   }
 
-  // Lane's byte offsets of V^T operands: output tile b, step u: base[b % kVTurns] + ...
-  static __device__ __forceinline__ void v_base(int (&at)[kVTurns]) {
+  // V^T operand of output tile b and product u: the lane reads 4 columns of key 4 g + (lane & 15) / 4, and of
+  // the key 8 (or 16) further on
+  static __device__ __forceinline__ bf16x8 v_operand(const KLDS char* v, int u, int b) {
     const int lane = threadIdx.x & 63;
     const int token = 4 * group() + ((lane & 15) >> 2);
+    constexpr int next = ROWS == 32 ? 8 : 16;
     const int piece = (ROWS == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((lane >> 1) & 1);
-    const int v0 = token * kRow + ((piece ^ swz(token)) << 4) + (lane & 1) * 8;
-#pragma unroll
-    for (int i = 0; i < kVTurns; ++i) at[i] = v0 ^ (i * 2 * ROWS);
-  }
-  static __device__ __forceinline__ bf16x8 v_operand(const KLDS char* v, const int (&v_at)[kVTurns], int u, int b) {
-    const KLDS char* p = v + v_at[b % kVTurns] + u * 16 * kRow + (b / kVTurns) * 128;
+    const int at = token * kRow + ((piece ^ swz<ROWS, kRow>(token)) << 4) + (lane & 1) * 8;
+    constexpr int kSpan = kRow % 256 == 0 ? 256 : 128;  // what the pieces' places are permuted in
+    const int c = b * 2 * ROWS;
+    const KLDS char* p = v + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + u * 16 * kRow);
+    const KLDS char* p2 = v + ((at ^ (c % kSpan) ^ (ROWS == 32 ? 32 : 0)) + (c / kSpan) * kSpan + u * 16 * kRow + next * kRow);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KLDS s16x4*)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KLDS s16x4*)(p + (ROWS == 32 ? 8 : 16) * kRow));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KLDS s16x4*)p2);
     typedef short s16x8 __attribute__((ext_vector_type(8)));
     const s16x8 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, both);
+  }
+  // K operand: key n (+ ROWS tile), columns kDepth ks + 8 g on
+  static __device__ __forceinline__ bf16x8 k_operand(const KLDS char* k, const KLDS char* rest, int tile, int ks) {
+    if (ks * kDepth < DV) {
+      constexpr int kSpan = kRow % 256 == 0 ? 256 : 128;
+      const int at = row() * kRow + ((group() ^ swz<ROWS, kRow>(row())) << 4), c = ks * 2 * kDepth;
+      return *(const KLDS bf16x8*)(k + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + tile * ROWS * kRow));
+    }
+    const int at = row() * kRestRow + ((group() ^ swz<ROWS, 128>(row())) << 4), c = ks * 2 * kDepth - 2 * DV;
+    return *(const KLDS bf16x8*)(rest + ((at ^ (c % 128)) + (c / 128) * 128 + tile * ROWS * kRestRow));
   }
 
   // O += P V for a step whose keys some row does not see: a value that is not finite must reach the
   // rows that see its key (weight > 0) and no other, where a product would make 0 * inf = NaN. Such
   // values are left out of the product; where there is one, products of the same weights with marks
   // (1 for inf, -inf; both for NaN) tell which results it reaches.
-  __device__ __forceinline__ void careful(const bf16x8 (&p)[kPSteps], const KLDS char* v, const int (&v_at)[kVTurns]) {
+  __device__ __forceinline__ void careful(const bf16x8 (&p)[kPSteps], const KLDS char* v) {
 #pragma nounroll
     for (int u = 0; u < kPSteps; ++u) {
       const bf16x8 pw = kPSteps == 2 && u ? p[kPSteps - 1] : p[0];
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
         __builtin_amdgcn_sched_barrier(0);
-        u32x4 w = __builtin_bit_cast(u32x4, v_operand(v, v_at, u, b));
+        u32x4 w = __builtin_bit_cast(u32x4, v_operand(v, u, b));
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max((w[i] >> 16) & 0x7f80u, w[i] & 0x7f80u));
@@ -248,66 +263,58 @@ struct State {
     return __builtin_bit_cast(bf16x8, w);
   }
 
-  // 32 keys from t0 on, in LDS at k (rest: the columns from DV on) and v.
-  __device__ __forceinline__ void step(const bf16x8 (&q)[kKSteps], const KLDS char* k, const KLDS char* rest, const KLDS char* v, int t0, int end, int end_min,
-                                       float scale2) {
-    // K: key n (+ ROWS), piece (kGroups ks + g) ^ swz(key)
-    const int k0 = row() * kRow + ((group() ^ swz(row())) << 4);
-    int k_at[kTurns], v_at[kVTurns];
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i) k_at[i] = k0 ^ (i * 16 * kGroups);
-    v_base(v_at);
-    Acc s[kTiles];
+  // scores of 32 keys
+  __device__ __forceinline__ void score(Acc (&s)[kTiles], const bf16x8 (&q)[kKSteps], const KLDS char* k, const KLDS char* rest) const {
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) s[n] = (Acc)(0.0f);
-    // operands a few products ahead: all at once they would not fit the registers
     constexpr int kProducts = kKSteps * kTiles;  // product c: step c / kTiles, tile c % kTiles
-    static_assert(kProducts % kAhead == 0 && kPSteps * kBlocks % kAhead == 0, "whole groups");
-    bf16x8 a[2][kAhead];
-    const int r0 = row() * kRestRow + ((group() ^ swz(row())) << 4);
-    auto key = [&](int c) {
-      const int ks = c / kTiles, ks_rest = ks - DV / kDepth;
-      if (ks_rest >= 0)
-        return *(const KLDS bf16x8*)(rest + (c % kTiles) * ROWS * kRestRow + (r0 ^ (ks_rest % kTurns * 16 * kGroups)) + (ks_rest / kTurns) * 128);
-      return *(const KLDS bf16x8*)(k + (c % kTiles) * ROWS * kRow + k_at[ks % kTurns] + (ks / kTurns) * 128);
-    };
+    constexpr int A = kTight ? 2 : kProducts;    // operands read ahead of their products
+    static_assert(kProducts % A == 0, "whole groups");
+    bf16x8 a[2][A];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) a[0][i] = key(i);
+    for (int i = 0; i < A; ++i) a[0][i] = k_operand(k, rest, i % kTiles, i / kTiles);
 #pragma unroll
-    for (int c = 0; c < kProducts; c += kAhead) {
-      if (c + kAhead < kProducts) {
+    for (int c = 0; c < kProducts; c += A) {
+      if (c + A < kProducts) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) a[(c / kAhead + 1) & 1][i] = key(c + kAhead + i);
+        for (int i = 0; i < A; ++i) a[(c / A + 1) & 1][i] = k_operand(k, rest, (c + A + i) % kTiles, (c + A + i) / kTiles);
       }
-      __builtin_amdgcn_sched_barrier(0);
+      if (kTight) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) s[(c + i) % kTiles] = mfma(a[(c / kAhead) & 1][i], q[(c + i) / kTiles], s[(c + i) % kTiles]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < A; ++i) s[(c + i) % kTiles] = mfma(a[(c / A) & 1][i], q[(c + i) / kTiles], s[(c + i) % kTiles]);
+      if (kTight) __builtin_amdgcn_sched_barrier(0);
     }
-    const bool edge = t0 + 32 > end_min;  // a key some row of the wave does not see
-    if (edge) {
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-        for (int i = 0; i < kScores; ++i)
-          if (t0 + slot_key(n, i) >= end) s[n][i] = -INFINITY;
+  }
+
+  // O += P V for 32 keys
+  template <bool EDGE>
+  __device__ __forceinline__ void add(const bf16x8 (&p)[kPSteps], const KLDS char* v) {
+    if constexpr (EDGE && kRestRow == 0) {
+      careful(p, v);
+      return;
     }
-    float top = s[0][0];
+    constexpr int kProducts = kPSteps * kBlocks, A = kTight ? 2 : kProducts;
+    bf16x8 a[2][A];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n)
+    for (int i = 0; i < A; ++i) a[0][i] = v_operand(v, i / kBlocks, i % kBlocks);
 #pragma unroll
-      for (int i = 0; i < kScores; ++i) top = fmaxf(top, s[n][i]);
-    top = row_max<ROWS>(top) * scale2;
-    if (__any(top > m + kGrow)) {
-      const float to = fmaxf(m, top);
-      const float alpha = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      l *= alpha;
+    for (int c = 0; c < kProducts; c += A) {
+      if (c + A < kProducts) {
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) o[b] *= alpha;
+        for (int i = 0; i < A; ++i) a[(c / A + 1) & 1][i] = v_operand(v, (c + A + i) / kBlocks, (c + A + i) % kBlocks);
+      }
+      if (kTight) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const bf16x8 x = EDGE ? finite(a[(c / A) & 1][i]) : a[(c / A) & 1][i];
+        o[(c + i) % kBlocks] = mfma(x, p[(c + i) / kBlocks], o[(c + i) % kBlocks]);
+      }
+      if (kTight) __builtin_amdgcn_sched_barrier(0);
     }
-    const float base = m == -INFINITY ? 0.0f : m;
-    bf16x8 p[kPSteps];
+  }
+
+  // weights of 32 keys from their scores
+  __device__ __forceinline__ void weigh(bf16x8 (&p)[kPSteps], const Acc (&s)[kTiles], float scale2, float base) {
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < kPSteps; ++u) {
@@ -327,39 +334,57 @@ struct State {
       p[u] = __builtin_bit_cast(bf16x8, w);
     }
     l += sum;
-    if (kRestRow == 0 && edge) {
-      careful(p, v, v_at);
-      return;
+  }
+
+  // NT x 32 keys from t0 on, in LDS at k (rest: the columns from DV on) and v. EDGE: some row does not see
+  // some of them.
+  template <int NT, bool EDGE>
+  __device__ __forceinline__ void step(const bf16x8 (&q)[kKSteps], const KLDS char* k, const KLDS char* rest, const KLDS char* v, int t0,
+                                       int end, float scale2) {
+    Acc s[NT][kTiles];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) score(s[n], q, k + n * 32 * kRow, rest + n * 32 * kRestRow);
+    float top = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+        for (int i = 0; i < kScores; ++i) {
+          if (EDGE && t0 + n * 32 + slot_key(x, i) >= end) s[n][x][i] = -INFINITY;
+          top = fmaxf(top, s[n][x][i]);
+        }
+    top = row_max<ROWS>(top) * scale2;
+    if (__any(top > m + kGrow)) {
+      const float to = fmaxf(m, top);
+      const float alpha = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= alpha;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[b] *= alpha;
     }
+    const float base = m == -INFINITY ? 0.0f : m;
+    bf16x8 p[NT][kPSteps];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) a[0][i] = v_operand(v, v_at, i / kBlocks, i % kBlocks);
+    for (int n = 0; n < NT; ++n) weigh(p[n], s[n], scale2, base);
 #pragma unroll
-    for (int c = 0; c < kPSteps * kBlocks; c += kAhead) {
-      if (c + kAhead < kPSteps * kBlocks) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) a[(c / kAhead + 1) & 1][i] = v_operand(v, v_at, (c + kAhead + i) / kBlocks, (c + kAhead + i) % kBlocks);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (kRestRow != 0 && edge) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) a[(c / kAhead) & 1][i] = finite(a[(c / kAhead) & 1][i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) o[(c + i) % kBlocks] = mfma(a[(c / kAhead) & 1][i], p[(c + i) / kBlocks], o[(c + i) % kBlocks]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int n = 0; n < NT; ++n) add<EDGE>(p[n], v + n * 32 * kRow);
   }
 
   // column of values 4 i on of output tile b
   static __device__ __forceinline__ int column(int b, int i) { return b * ROWS + (ROWS == 32 ? 8 * i : 0) + 4 * group(); }
 };
 
-// A stage of TS keys, 32 at a time, as far as a row of the wave sees.
-template <int TS, int DK, int DV, int ROWS>
+// A stage of TS keys, as far as a row of the wave sees: NT x 32 at a time while every row sees them all.
+template <int TS, int NT, int DK, int DV, int ROWS>
 __device__ __forceinline__ void walk(State<DK, DV, ROWS>& st, const bf16x8 (&q)[State<DK, DV, ROWS>::kKSteps], const KLDS char* k,
                                      const KLDS char* rest, const KLDS char* v, int t, int end, int end_min, int end_max, float scale2) {
+  int s = 0;
 #pragma nounroll
-  for (int s = 0; s < TS && t + s < end_max; s += 32) st.step(q, k + s * 2 * DV, rest + s * 2 * (DK - DV), v + s * 2 * DV, t + s, end, end_min, scale2);
+  for (; s < TS && t + s + 32 * NT <= end_min; s += 32 * NT)
+    st.template step<NT, false>(q, k + s * 2 * DV, rest + s * 2 * (DK - DV), v + s * 2 * DV, t + s, end, scale2);
+#pragma nounroll
+  for (; s < TS && t + s < end_max; s += 32) st.template step<1, true>(q, k + s * 2 * DV, rest + s * 2 * (DK - DV), v + s * 2 * DV, t + s, end, scale2);
 }
 
 // N consecutive columns of a row's result: normalised into the output, or as a partial row.
@@ -395,6 +420,61 @@ __device__ __forceinline__ void put_stats(const StepArgs& a, const AttendIo& io,
 
 __device__ __forceinline__ int64_t part_row(const StepArgs& a, const AttendRun& run, const AttendItem& it, int head, int row) {
   return run.part0 + ((int64_t)it.split * a.heads + head) * ((int64_t)run.ntok * a.group) + row;
+}
+
+// A wave's result: normalised into the output, or as partial rows.
+template <typename S>
+__device__ __forceinline__ void put_state(const StepArgs& a, const AttendIo& io, const AttendRun& run, const AttendItem& it, int head,
+                                          const Lane& r, const S& st, float l) {
+  if (!r.owned) return;
+  const int64_t part = part_row(a, run, it, head, r.row);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+    for (int i = 0; i < S::kScores / 4; ++i) {
+      const float x[4] = {st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
+      put<4>(a, io, run, part, r.token, r.qh, S::column(b, i), x, inv);
+    }
+  if (S::group() == 0) put_stats(a, io, run, part, r.token, r.qh, st.m, l);
+}
+
+// Four waves' results for the same rows into wave 0's: 2 and 3 into 0 and 1, then 1 into 0; like lanes
+// hold like values. place: LDS of two waves' results, whose former use has ended in every wave only
+// after the first barrier here. l: sums over whole rows.
+template <typename S>
+__device__ __forceinline__ void join_waves(S& st, float& l, f32x4* place, float (&ml)[2][kWaves][64]) {
+  constexpr int kQuads = S::kScores / 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+  for (int step = kWaves / 2; step; step >>= 1) {
+    __syncthreads();
+    if (wave >= step && wave < 2 * step) {
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+          place[(((wave - step) * S::kBlocks + b) * kQuads + i) * 64 + lane] =
+              (f32x4){st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
+      ml[0][wave][lane] = st.m;
+      ml[1][wave][lane] = l;
+    }
+    __syncthreads();
+    if (wave < step) {
+      const float m = ml[0][wave + step][lane], top = fmaxf(st.m, m);
+      const float f0 = st.m == top ? 1.0f : __builtin_amdgcn_exp2f(st.m - top), f1 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      st.m = top;
+      l = l * f0 + ml[1][wave + step][lane] * f1;
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const f32x4 y = place[((wave * S::kBlocks + b) * kQuads + i) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.o[b][4 * i + e] = st.o[b][4 * i + e] * f0 + y[e] * f1;
+        }
+    }
+  }
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ constexpr int kRowsPerLoad = 1024 / (2 * D);  // tokens one wave instruction bri
 // NI wave instructions bring rows `first`, `first` + kRowsPerLoad, ... of a stage into LDS. The
 // page ids are asked for one stage ahead (find) and used only when the stage is loaded: loads
 // return in order, so using them at once would wait for the stage in flight as well.
-template <int D, int NI>
+template <int D, int NI, int ROWS>
 struct Rows {
   int page[NI], place[NI];
   __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int last) {
@@ -31,7 +31,7 @@ struct Rows {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int piece = (lane & (LPR - 1)) ^ swz(first + i * RPL + lane / LPR);
+      const int piece = (lane & (LPR - 1)) ^ swz<ROWS, 2 * D>(first + i * RPL + lane / LPR);
       const int64_t at = ((int64_t)page[i] * a.page_size + place[i]) * a.row + piece * 8;
       __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(k + at), (KLDS void*)(kbuf + (first + i * RPL) * 2 * D), 16, 0, 0);
       __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(v + at), (KLDS void*)(vbuf + (first + i * RPL) * 2 * D), 16, 0, 0);
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo 
   const uint16_t* vp = a.v_pool + io.layer0 + head * D;
   const int first = wave * NI * kRowsPerLoad<D>, last = it.kv1 - 1;
   if (it.kv1 > it.kv0) {
-    Rows<D, NI> rows;
+    Rows<D, NI, 32> rows;
     rows.find(a, run, it.kv0, first, last);
     rows.load(a, kp, vp, (KLDS char*)k0, (KLDS char*)v0, first);
     rows.find(a, run, it.kv0 + TS, first, last);
@@ -71,129 +71,79 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo 
         rows.load(a, kp, vp, (KLDS char*)k1, (KLDS char*)v1, first);
         rows.find(a, run, t + 2 * TS, first, last);
       }
-      walk<TS>(st, q, (const KLDS char*)k0, (const KLDS char*)k0, (const KLDS char*)v0, t, r.end, end_min, end_max, io.scale2);
+      walk<TS, 2>(st, q, (const KLDS char*)k0, (const KLDS char*)k0, (const KLDS char*)v0, t, r.end, end_min, end_max, io.scale2);
       if ((t += TS) >= it.kv1) break;
       __syncthreads();
       if (t + TS < it.kv1) {
         rows.load(a, kp, vp, (KLDS char*)k0, (KLDS char*)v0, first);
         rows.find(a, run, t + 2 * TS, first, last);
       }
-      walk<TS>(st, q, (const KLDS char*)k1, (const KLDS char*)k1, (const KLDS char*)v1, t, r.end, end_min, end_max, io.scale2);
+      walk<TS, 2>(st, q, (const KLDS char*)k1, (const KLDS char*)k1, (const KLDS char*)v1, t, r.end, end_min, end_max, io.scale2);
       if ((t += TS) >= it.kv1) break;
     }
   }
-  const float l = row_sum<32>(st.l);
-  if (!r.owned) return;
-  const int64_t part = part_row(a, run, it, head, r.row);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int h = lane >> 5;
-#pragma unroll
-  for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x[4] = {st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
-      put<4>(a, io, run, part, r.token, r.qh, b * 32 + 8 * i + 4 * h, x, inv);
-    }
-  if (h == 0) put_stats(a, io, run, part, r.token, r.qh, st.m, l);
+  put_state(a, io, run, it, head, r, st, row_sum<32>(st.l));
 }
 
 // ============================================================================
-// Tiles of up to 32 rows (few queries on a KV head: reading the keys is what takes time): each of
-// the 4 waves walks stages of its own, of 32 (128-wide) or 64 keys, at its own pace, and the four
-// results are joined in LDS.
+// Tiles of up to 32 rows (few queries on a KV head: reading the keys is what takes time). Each of the
+// 4 waves walks stages of its own, of 32 (128-wide) or 64 keys, at its own pace, and the four results
+// are joined in LDS. One buffer a wave (16 KB): two workgroups share a CU, so that the other seven
+// waves' reads are in flight while one computes. Up to 16 rows take the products of 16 rows.
 // ============================================================================
 template <int D>
-__global__ __launch_bounds__(kThreads, 1) void attend_narrow(StepArgs a, AttendIo io) {
-  constexpr int TS = 4096 / D, NI = TS / kRowsPerLoad<D>, STAGE = TS * 2 * D;
-  constexpr int OS = D + 4;  // floats between rows of a wave's result
-  __shared__ __align__(1024) char b0[kWaves][2][STAGE], b1[kWaves][2][STAGE];
-  __shared__ float ml[kWaves][2][32];
-  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
-  const AttendItem it = a.items[item];
-  const AttendRun run = a.runs[it.run];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Lane r = lane_row(a, run, it, head, it.row0 + (lane & 31));
-  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 31);
-  typedef State<D, D, 32> S;
+constexpr int kStageKeys = 4096 / D;
+template <int D>
+constexpr int kStageBytes = kStageKeys<D> * 2 * D;
+
+template <int D, int ROWS>
+__device__ __forceinline__ void narrow_rows_of(const StepArgs& a, const AttendIo& io, const AttendRun& run, const AttendItem& it, int head,
+                                               KLDS char* kbuf, KLDS char* vbuf, f32x4* place, float (&ml)[2][kWaves][64]) {
+  typedef State<D, D, ROWS> S;
+  constexpr int TS = kStageKeys<D>, NI = TS / kRowsPerLoad<D>, STEP = kWaves * TS;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Lane r = lane_row(a, run, it, head, it.row0 + S::row());
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, ROWS - 1);
+  const uint16_t* kp = a.k_pool + io.layer0 + head * D;
+  const uint16_t* vp = a.v_pool + io.layer0 + head * D;
+  const int last = it.kv1 - 1;
+  int t = it.kv0 + wave * TS;
+  Rows<D, NI, ROWS> rows;
+  if (t < it.kv1) {
+    rows.find(a, run, t, 0, last);
+    rows.load(a, kp, vp, kbuf, vbuf, 0);
+  }
   bf16x8 q[S::kKSteps];
   S::load_q(io, r, q);
   S st;
   st.clear();
-  const uint16_t* kp = a.k_pool + io.layer0 + head * D;
-  const uint16_t* vp = a.v_pool + io.layer0 + head * D;
-  const int last = it.kv1 - 1;
-  constexpr int STEP = kWaves * TS;
-  int t = it.kv0 + wave * TS;
-  if (t < it.kv1) {
-    KLDS char *ka = (KLDS char*)b0[wave][0], *va = (KLDS char*)b0[wave][1];
-    KLDS char *kb = (KLDS char*)b1[wave][0], *vb = (KLDS char*)b1[wave][1];
-    Rows<D, NI> rows;
-    rows.find(a, run, t, 0, last);
-    rows.load(a, kp, vp, ka, va, 0);
+  while (t < it.kv1) {
     rows.find(a, run, t + STEP, 0, last);
-    for (;;) {
-      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's stage has arrived
-      __builtin_amdgcn_wave_barrier();
-      if (t + STEP < it.kv1) {
-        rows.load(a, kp, vp, kb, vb, 0);
-        rows.find(a, run, t + 2 * STEP, 0, last);
-      }
-      walk<TS>(st, q, (const KLDS char*)ka, (const KLDS char*)ka, (const KLDS char*)va, t, r.end, end_min, end_max, io.scale2);
-      if ((t += STEP) >= it.kv1) break;
-      __builtin_amdgcn_s_waitcnt(0x0f70);
-      __builtin_amdgcn_wave_barrier();
-      if (t + STEP < it.kv1) {
-        rows.load(a, kp, vp, ka, va, 0);
-        rows.find(a, run, t + 2 * STEP, 0, last);
-      }
-      walk<TS>(st, q, (const KLDS char*)kb, (const KLDS char*)kb, (const KLDS char*)vb, t, r.end, end_min, end_max, io.scale2);
-      if ((t += STEP) >= it.kv1) break;
-    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's stage has arrived
+    __builtin_amdgcn_wave_barrier();
+    walk<TS, 1>(st, q, (const KLDS char*)kbuf, (const KLDS char*)kbuf, (const KLDS char*)vbuf, t, r.end, end_min, end_max, io.scale2);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
+    __builtin_amdgcn_wave_barrier();
+    if ((t += STEP) < it.kv1) rows.load(a, kp, vp, kbuf, vbuf, 0);
   }
-  // every wave's rows, then their join: thread = (row, D / 8 columns)
-  const float l = row_sum<32>(st.l);
-  __syncthreads();  // the stages have been read: their place holds the results
-  static_assert(kWaves / 2 * 32 * OS * 4 <= (int)sizeof(b0), "results fit where the stages were");
-  auto result = [&](int i, int row) { return (float*)(i < kWaves / 2 ? &b0[0][0][0] : &b1[0][0][0]) + ((i & 1) * 32 + row) * OS; };
-  const int h = lane >> 5;
-#pragma unroll
-  for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *(f32x4*)(result(wave, lane & 31) + b * 32 + 8 * i + 4 * h) =
-          (f32x4){st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
-  if (h == 0) {
-    ml[wave][0][lane] = st.m;
-    ml[wave][1][lane] = l;
-  }
-  __syncthreads();
-  const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
-  const Lane w = lane_row(a, run, it, head, it.row0 + row);
-  if (!w.owned) return;
-  float top = -INFINITY, sum = 0.0f, f[kWaves], x[D / 8];
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) top = fmaxf(top, ml[i][0][row]);
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    const float mi = ml[i][0][row];
-    f[i] = mi == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : (mi == top ? 1.0f : __builtin_amdgcn_exp2f(mi - top));
-    sum += ml[i][1][row] * f[i];
-  }
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c) x[c] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    if (f[i] == 0.0f) continue;
-#pragma unroll
-    for (int c = 0; c < D / 8; c += 4) {
-      const f32x4 y = *(const f32x4*)(result(i, row) + d0 + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[c + e] += y[e] * f[i];
-    }
-  }
-  const int64_t part = part_row(a, run, it, head, w.row);
-  put<D / 8>(a, io, run, part, w.token, w.qh, d0, x, sum == 0.0f ? 0.0f : 1.0f / sum);
-  if ((threadIdx.x & 7) == 0) put_stats(a, io, run, part, w.token, w.qh, top, sum);
+  float l = row_sum<ROWS>(st.l);
+  join_waves(st, l, place, ml);
+  if (wave == 0) put_state(a, io, run, it, head, r, st, l);
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attend_narrow(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char buf[kWaves][2][kStageBytes<D>];
+  __shared__ float ml[2][kWaves][64];
+  static_assert(sizeof(buf) >= 2 * 64 * 4 * D / 2, "two waves' results fit where the stages were");
+  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const AttendItem it = a.items[item];
+  const AttendRun run = a.runs[it.run];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  KLDS char *k = (KLDS char*)buf[wave][0], *v = (KLDS char*)buf[wave][1];
+  f32x4* place = (f32x4*)&buf[0][0][0];
+  if (run.ntok * a.group <= 16) narrow_rows_of<D, 16>(a, io, run, it, head, k, v, place, ml);
+  else narrow_rows_of<D, 32>(a, io, run, it, head, k, v, place, ml);
 }
 
 template <int D>

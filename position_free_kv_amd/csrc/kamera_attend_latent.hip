@@ -37,13 +37,13 @@ struct LatentRows {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint16_t* p = k + (int64_t)__builtin_amdgcn_readlane(row, i) * kKey;
-      const int piece = lane ^ (N >= 8 ? swz(i) : swz(first + i));
+      const int piece = lane ^ (N >= 16 ? swz<16, kLatentRow>(i) : swz<16, kLatentRow>(first + i));
       __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8), (KLDS void*)(latents + (first + i) * kLatentRow), 16, 0, 0);
     }
     constexpr int M = N < 8 ? N : 8;  // bands an instruction brings in, 8 pieces each
-    const int piece = (lane & 7) ^ swz(first + lane / 8);
 #pragma unroll
     for (int i = 0; i < N; i += M) {
+      const int piece = (lane & 7) ^ swz<16, kRopeRow>(first + i + lane / 8);
       const uint16_t* p = k + (int64_t)__shfl(row, i + lane / 8, 64) * kKey + kLatent;
       if (lane < 8 * M)
         __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8),
@@ -51,20 +51,6 @@ struct LatentRows {
     }
   }
 };
-
-// A wave's result: normalised into the output, or as partial rows.
-__device__ __forceinline__ void put_state(const StepArgs& a, const AttendIo& io, const AttendRun& run, const AttendItem& it, const Lane& r,
-                                          const LatentState& st, float l) {
-  if (!r.owned) return;
-  const int64_t part = part_row(a, run, it, 0, r.row);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int b = 0; b < LatentState::kBlocks; ++b) {
-    const float x[4] = {st.o[b][0], st.o[b][1], st.o[b][2], st.o[b][3]};
-    put<4>(a, io, run, part, r.token, r.qh, LatentState::column(b, 0), x, inv);
-  }
-  if (LatentState::group() == 0) put_stats(a, io, run, part, r.token, r.qh, st.m, l);
-}
 
 // ============================================================================
 // Tiles of 128 rows: 8 waves of 16 rows share stages of 32 keys.
@@ -95,21 +81,21 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArg
         rows.load<PER>(a, kp, (KLDS char*)k1, (KLDS char*)r1, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
       }
-      walk<kKeys>(st, q, (const KLDS char*)k0, (const KLDS char*)r0, (const KLDS char*)k0, t, r.end, end_min, end_max, io.scale2);
+      walk<kKeys, 1>(st, q, (const KLDS char*)k0, (const KLDS char*)r0, (const KLDS char*)k0, t, r.end, end_min, end_max, io.scale2);
       if ((t += kKeys) >= it.kv1) break;
       __syncthreads();
       if (t + kKeys < it.kv1) {
         rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
       }
-      walk<kKeys>(st, q, (const KLDS char*)k1, (const KLDS char*)r1, (const KLDS char*)k1, t, r.end, end_min, end_max, io.scale2);
+      walk<kKeys, 1>(st, q, (const KLDS char*)k1, (const KLDS char*)r1, (const KLDS char*)k1, t, r.end, end_min, end_max, io.scale2);
       if ((t += kKeys) >= it.kv1) break;
     }
   }
   const float l = row_sum<16>(st.l);
   int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
   asm volatile("" : "+v"(tid));
-  put_state(a, io, run, it, lane_row(a, run, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
+  put_state(a, io, run, it, 0, lane_row(a, run, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
 }
 
 // ============================================================================
@@ -140,34 +126,15 @@ __global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, 
       rows.find(a, run, t + kWaves * kKeys, 0, kKeys, last);
       __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's stage has arrived
       __builtin_amdgcn_wave_barrier();
-      walk<kKeys>(st, q, (const KLDS char*)mine, (const KLDS char*)band, (const KLDS char*)mine, t, r.end, end_min, end_max, io.scale2);
+      walk<kKeys, 1>(st, q, (const KLDS char*)mine, (const KLDS char*)band, (const KLDS char*)mine, t, r.end, end_min, end_max, io.scale2);
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
       __builtin_amdgcn_wave_barrier();
     }
   }
-  // 2 and 3 into 0 and 1, then 1 into 0: registers of like lanes, 32 KB a wave
   float l = row_sum<16>(st.l);
-  f32x4* place = (f32x4*)&buf[0][0];
-#pragma unroll
-  for (int step = 2; step; step >>= 1) {
-    __syncthreads();
-    if (wave >= step && wave < 2 * step) {
-#pragma unroll
-      for (int b = 0; b < LatentState::kBlocks; ++b) place[((wave - step) * LatentState::kBlocks + b) * 64 + lane] = st.o[b];
-      ml[0][wave][lane] = st.m;
-      ml[1][wave][lane] = l;
-    }
-    __syncthreads();
-    if (wave < step) {
-      const float m = ml[0][wave + step][lane], top = fmaxf(st.m, m);
-      const float f0 = st.m == top ? 1.0f : __builtin_amdgcn_exp2f(st.m - top), f1 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
-      st.m = top;
-      l = l * f0 + ml[1][wave + step][lane] * f1;
-#pragma unroll
-      for (int b = 0; b < LatentState::kBlocks; ++b) st.o[b] = st.o[b] * f0 + place[(wave * LatentState::kBlocks + b) * 64 + lane] * f1;
-    }
-  }
-  if (wave == 0) put_state(a, io, run, it, r, st, l);
+  static_assert(sizeof(buf) >= 2 * 64 * LatentState::kBlocks * 16, "two waves' results fit where the stages were");
+  join_waves(st, l, (f32x4*)&buf[0][0], ml);
+  if (wave == 0) put_state(a, io, run, it, 0, r, st, l);
 }
 
 }  // namespace
