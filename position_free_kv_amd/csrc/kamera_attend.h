@@ -101,7 +101,8 @@ struct Lane {
   int end;           // keys [kv0, end) are seen
 };
 
-__device__ __forceinline__ Lane lane_row(const StepArgs& a, const AttendRun& run, const AttendItem& it, int head, int row) {
+__device__ __forceinline__ Lane lane_row(const StepArgs& a, const AttendItem& it, int head, int row) {
+  const AttendRun& run = it.run;
   Lane r;
   const int rows = run.ntok * a.group;
   r.owned = row < rows;
@@ -162,18 +163,24 @@ struct State {
     l = 0.0f;
   }
 
-  // the row's queries: operand ks holds columns kDepth ks + 8 g on
+  // First column of operand ks. With 32 rows they follow each other; with 16 two operands share 64
+  // columns, group g taking 16 g on: LDS serves a 16-byte row read in groups of 16 lanes that mix two
+  // g (lanes 0-3, 12-15, 20-23, 24-27, ...), which 8 g on would send to the same banks.
+  static __device__ __forceinline__ constexpr int k_column(int ks) {
+    return ROWS == 32 ? kDepth * ks + 8 * group() : 64 * (ks >> 1) + 16 * group() + 8 * (ks & 1);
+  }
+  // the row's queries
   static __device__ __forceinline__ void load_q(const AttendIo& io, const Lane& r, bf16x8 (&q)[kKSteps]) {
-    const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * DK + 8 * group();
+    const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * DK;
     u32x4 w[kKSteps];
     if (io.q_vec) {
 #pragma unroll
-      for (int ks = 0; ks < kKSteps; ++ks) w[ks] = *(const KGLOBAL u32x4*)(p + kDepth * ks);
+      for (int ks = 0; ks < kKSteps; ++ks) w[ks] = *(const KGLOBAL u32x4*)(p + k_column(ks));
     } else {
 #pragma unroll
       for (int ks = 0; ks < kKSteps; ++ks)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[ks][i] = (uint32_t)p[kDepth * ks + 2 * i] | ((uint32_t)p[kDepth * ks + 2 * i + 1] << 16);
+        for (int i = 0; i < 4; ++i) w[ks][i] = (uint32_t)p[k_column(ks) + 2 * i] | ((uint32_t)p[k_column(ks) + 2 * i + 1] << 16);
     }
     const uint32_t sign = io.negate ? 0x80008000u : 0u;
 #pragma unroll
@@ -202,15 +209,17 @@ struct State {
     const s16x8 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, both);
   }
-  // K operand: key n (+ ROWS tile), columns kDepth ks + 8 g on
+  // K operand ks: key n (+ ROWS tile)
   static __device__ __forceinline__ bf16x8 k_operand(const KLDS char* k, const KLDS char* rest, int tile, int ks) {
-    if (ks * kDepth < DV) {
+    constexpr int kLaneBytes = ROWS == 32 ? 16 : 32;           // between groups
+    const int c = ROWS == 32 ? 32 * ks : 128 * (ks >> 1) + 16 * (ks & 1);  // bytes of operand ks in the row
+    if (c < kRow) {
       constexpr int kSpan = kRow % 256 == 0 ? 256 : 128;
-      const int at = row() * kRow + ((group() ^ swz<ROWS, kRow>(row())) << 4), c = ks * 2 * kDepth;
+      const int at = row() * kRow + ((group() * kLaneBytes) ^ (swz<ROWS, kRow>(row()) << 4));
       return *(const KLDS bf16x8*)(k + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + tile * ROWS * kRow));
     }
-    const int at = row() * kRestRow + ((group() ^ swz<ROWS, 128>(row())) << 4), c = ks * 2 * kDepth - 2 * DV;
-    return *(const KLDS bf16x8*)(rest + ((at ^ (c % 128)) + (c / 128) * 128 + tile * ROWS * kRestRow));
+    const int at = row() * kRestRow + ((group() * kLaneBytes) ^ (swz<ROWS, 128>(row()) << 4)), c2 = c - kRow;
+    return *(const KLDS bf16x8*)(rest + ((at ^ (c2 % 128)) + (c2 / 128) * 128 + tile * ROWS * kRestRow));
   }
 
   // O += P V for a step whose keys some row does not see: a value that is not finite must reach the
@@ -375,6 +384,13 @@ struct State {
   static __device__ __forceinline__ int column(int b, int i) { return b * ROWS + (ROWS == 32 ? 8 * i : 0) + 4 * group(); }
 };
 
+// Every wave's part of a stage has arrived in LDS, and every wave has read the stage before. (The
+// barrier alone orders LDS instructions; loads into LDS are counted with the memory ones.)
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __syncthreads();
+}
+
 // A stage of TS keys, as far as a row of the wave sees: NT x 32 at a time while every row sees them all.
 template <int TS, int NT, int DK, int DV, int ROWS>
 __device__ __forceinline__ void walk(State<DK, DV, ROWS>& st, const bf16x8 (&q)[State<DK, DV, ROWS>::kKSteps], const KLDS char* k,
@@ -418,63 +434,68 @@ __device__ __forceinline__ void put_stats(const StepArgs& a, const AttendIo& io,
   else if (io.lse) io.lse[(int64_t)token * a.num_q_heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-__device__ __forceinline__ int64_t part_row(const StepArgs& a, const AttendRun& run, const AttendItem& it, int head, int row) {
-  return run.part0 + ((int64_t)it.split * a.heads + head) * ((int64_t)run.ntok * a.group) + row;
+__device__ __forceinline__ int64_t part_row(const StepArgs& a, const AttendItem& it, int head, int row) {
+  return it.run.part0 + ((int64_t)it.split * a.heads + head) * ((int64_t)it.run.ntok * a.group) + row;
 }
 
 // A wave's result: normalised into the output, or as partial rows.
 template <typename S>
-__device__ __forceinline__ void put_state(const StepArgs& a, const AttendIo& io, const AttendRun& run, const AttendItem& it, int head,
+__device__ __forceinline__ void put_state(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head,
                                           const Lane& r, const S& st, float l) {
   if (!r.owned) return;
-  const int64_t part = part_row(a, run, it, head, r.row);
+  const int64_t part = part_row(a, it, head, r.row);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
     for (int i = 0; i < S::kScores / 4; ++i) {
       const float x[4] = {st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
-      put<4>(a, io, run, part, r.token, r.qh, S::column(b, i), x, inv);
+      put<4>(a, io, it.run, part, r.token, r.qh, S::column(b, i), x, inv);
     }
-  if (S::group() == 0) put_stats(a, io, run, part, r.token, r.qh, st.m, l);
+  if (S::group() == 0) put_stats(a, io, it.run, part, r.token, r.qh, st.m, l);
 }
 
-// Four waves' results for the same rows into wave 0's: 2 and 3 into 0 and 1, then 1 into 0; like lanes
-// hold like values. place: LDS of two waves' results, whose former use has ended in every wave only
-// after the first barrier here. l: sums over whole rows.
+// Joins two waves' results for the same rows: `giver` waves put theirs into LDS at `place` (like lanes
+// hold like values), the others take slot `pair`'s. place's former use has ended in every wave only
+// after the first barrier here; every wave of the workgroup comes along. l: sums over whole rows.
+template <typename S>
+__device__ __forceinline__ void join_two(S& st, float& l, bool giver, int pair, f32x4* place, float (&ml)[2][kWaves][64], bool idle = false) {
+  constexpr int kQuads = S::kScores / 4;
+  const int lane = threadIdx.x & 63;
+  __syncthreads();
+  if (giver && !idle) {
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+        place[(b * kQuads + i) * 64 + lane] = (f32x4){st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
+    ml[0][pair][lane] = st.m;
+    ml[1][pair][lane] = l;
+  }
+  __syncthreads();
+  if (!giver && !idle) {
+    const float m = ml[0][pair][lane], top = fmaxf(st.m, m);
+    const float f0 = st.m == top ? 1.0f : __builtin_amdgcn_exp2f(st.m - top), f1 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    st.m = top;
+    l = l * f0 + ml[1][pair][lane] * f1;
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const f32x4 y = place[(b * kQuads + i) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[b][4 * i + e] = st.o[b][4 * i + e] * f0 + y[e] * f1;
+      }
+  }
+}
+
+// Four waves' results for the same rows into wave 0's: 2 and 3 into 0 and 1, then 1 into 0. place: LDS
+// of two waves' results.
 template <typename S>
 __device__ __forceinline__ void join_waves(S& st, float& l, f32x4* place, float (&ml)[2][kWaves][64]) {
-  constexpr int kQuads = S::kScores / 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-#pragma unroll
-  for (int step = kWaves / 2; step; step >>= 1) {
-    __syncthreads();
-    if (wave >= step && wave < 2 * step) {
-#pragma unroll
-      for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i)
-          place[(((wave - step) * S::kBlocks + b) * kQuads + i) * 64 + lane] =
-              (f32x4){st.o[b][4 * i], st.o[b][4 * i + 1], st.o[b][4 * i + 2], st.o[b][4 * i + 3]};
-      ml[0][wave][lane] = st.m;
-      ml[1][wave][lane] = l;
-    }
-    __syncthreads();
-    if (wave < step) {
-      const float m = ml[0][wave + step][lane], top = fmaxf(st.m, m);
-      const float f0 = st.m == top ? 1.0f : __builtin_amdgcn_exp2f(st.m - top), f1 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
-      st.m = top;
-      l = l * f0 + ml[1][wave + step][lane] * f1;
-#pragma unroll
-      for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const f32x4 y = place[((wave * S::kBlocks + b) * kQuads + i) * 64 + lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st.o[b][4 * i + e] = st.o[b][4 * i + e] * f0 + y[e] * f1;
-        }
-    }
-  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  join_two(st, l, wave >= 2, wave & 1, place + (wave & 1) * (S::kBlocks * S::kScores / 4) * 64, ml);
+  join_two(st, l, wave == 1, 0, place, ml, wave >= 2);
 }
 
 }  // namespace

@@ -59,9 +59,9 @@ constexpr int kWideWaves = 8;
 __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArgs a, AttendIo io) {
   __shared__ __align__(1024) char k0[kLatents], k1[kLatents], r0[kBands], r1[kBands];
   const AttendItem it = a.items[a.num_narrow + blockIdx.x];
-  const AttendRun run = a.runs[it.run];
+  const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Lane r = lane_row(a, run, it, 0, it.row0 + wave * 16 + (lane & 15));
+  const Lane r = lane_row(a, it, 0, it.row0 + wave * 16 + (lane & 15));
   const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
   bf16x8 q[LatentState::kKSteps];
   LatentState::load_q(io, r, q);
@@ -76,14 +76,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArg
     rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
     rows.find(a, run, it.kv0 + kKeys, first, PER, last);
     for (int t = it.kv0;;) {
-      __syncthreads();  // this stage has arrived, the other buffer has been read
+      stage_barrier();
       if (t + kKeys < it.kv1) {
         rows.load<PER>(a, kp, (KLDS char*)k1, (KLDS char*)r1, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
       }
       walk<kKeys, 1>(st, q, (const KLDS char*)k0, (const KLDS char*)r0, (const KLDS char*)k0, t, r.end, end_min, end_max, io.scale2);
       if ((t += kKeys) >= it.kv1) break;
-      __syncthreads();
+      stage_barrier();
       if (t + kKeys < it.kv1) {
         rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArg
   const float l = row_sum<16>(st.l);
   int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
   asm volatile("" : "+v"(tid));
-  put_state(a, io, run, it, 0, lane_row(a, run, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
+  put_state(a, io, it, 0, lane_row(a, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
 }
 
 // ============================================================================
@@ -106,9 +106,9 @@ __global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, 
   __shared__ __align__(1024) char buf[kWaves][kLatents], bands[kWaves][kBands];
   __shared__ float ml[2][kWaves][64];
   const AttendItem it = a.items[blockIdx.x];
-  const AttendRun run = a.runs[it.run];
+  const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Lane r = lane_row(a, run, it, 0, it.row0 + (lane & 15));
+  const Lane r = lane_row(a, it, 0, it.row0 + (lane & 15));
   const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
   bf16x8 q[LatentState::kKSteps];
   LatentState::load_q(io, r, q);
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, 
   float l = row_sum<16>(st.l);
   static_assert(sizeof(buf) >= 2 * 64 * LatentState::kBlocks * 16, "two waves' results fit where the stages were");
   join_waves(st, l, (f32x4*)&buf[0][0], ml);
-  if (wave == 0) put_state(a, io, run, it, 0, r, st, l);
+  if (wave == 0) put_state(a, io, it, 0, r, st, l);
 }
 
 }  // namespace

@@ -180,7 +180,7 @@ template <typename T, int VEC, int NJ>
 __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io) {
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const AttendItem it = a.items[item];
-  const AttendRun run = a.runs[it.run];
+  const AttendRun& run = it.run;
   const int lane = threadIdx.x & 63, dl = lane & 15, tg = lane >> 4;
   const int row = it.row0 + (threadIdx.x >> 6);  // narrow_rows(ATTEND_PLAIN) waves
   if (row >= run.ntok * a.group) return;

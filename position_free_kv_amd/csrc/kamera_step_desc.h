@@ -39,9 +39,11 @@ static_assert(sizeof(AttendRun) == 64, "run record");
 
 // A workgroup's work for each KV head: rows [row0, row0 + tile) of a run, keys [kv0, kv1).
 struct alignas(16) AttendItem {
-  int32_t run, row0, kv0, kv1;
-  int32_t split, kind, pad[2];
+  AttendRun run;  // a copy: one read less before a workgroup knows its work
+  int32_t row0, kv0, kv1;
+  int32_t split;
 };
+static_assert(sizeof(AttendItem) == 80, "item record");
 
 // Query token whose result is joined from partial rows of up to two runs.
 struct alignas(16) MergeToken {
@@ -59,7 +61,6 @@ struct StepArgs {
   uint16_t* v_pool;     // MLA: the same rows
   int64_t layer_stride; // elements
   const int32_t* pages;
-  const AttendRun* runs;
   const AttendItem* items;
   const int32_t* tok;
   const MergeToken* merge;
@@ -79,18 +80,26 @@ struct StepArgs {
   uint32_t page_magic;  // slot / page_size = slot * page_magic >> page_bits, slot < 2^31
   int32_t page_bits;
   int32_t max_parts;    // most parts of a joined row
-  int32_t num_narrow;   // matrix-core kernels: the first items are narrow tiles, the rest wide ones
+  int32_t num_narrow, num_pairs;  // matrix-core kernels: the items' order: narrow, pairs, wide
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
 
 // PLAIN: any layout. HEADS: bf16 GQA/MHA heads of 64 or 128 columns; LATENT: bf16 MLA rows of 512 + 64
 // columns, both on the matrix cores.
 enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2 };
-// Rows per workgroup: a run that fits the narrow tile takes that, others the wide one.
-constexpr int kWideRows = 128;
+// Tiles, by the rows of a run: narrow where they fit it, wide ones of 128 rows; in between HEADS has
+// one of 64 rows (pairs).
+enum TileClass { TILE_NARROW = 0, TILE_PAIRS = 1, TILE_WIDE = 2 };
+constexpr int kWideRows = 128, kPairRows = 64;
 constexpr int narrow_rows(int kernel) { return kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32; }
+constexpr int tile_class(int kernel, int64_t rows) {
+  return kernel == ATTEND_PLAIN || rows <= narrow_rows(kernel) ? TILE_NARROW
+         : kernel == ATTEND_HEADS && rows <= kPairRows         ? TILE_PAIRS
+                                                               : TILE_WIDE;
+}
 constexpr int tile_rows(int kernel, int64_t rows) {
-  return kernel == ATTEND_PLAIN || rows <= narrow_rows(kernel) ? narrow_rows(kernel) : kWideRows;
+  const int c = tile_class(kernel, rows);
+  return c == TILE_NARROW ? narrow_rows(kernel) : c == TILE_PAIRS ? kPairRows : kWideRows;
 }
 
 constexpr int kMaxSplits = 512;  // ranges a run's keys are cut into, at most

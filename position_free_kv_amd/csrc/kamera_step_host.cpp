@@ -132,13 +132,18 @@ kamera_status check_workspace(const void* ws, size_t have, size_t need) {
 // reads the prefix and its own tokens as one sequence, and its result needs no joining.
 constexpr int64_t kShareRows = 64;
 
+// What the choice of an item's length goes by: the time of a workgroup before its first product (its
+// item, page ids, rows and queries are read one after the other), of one key of a tile while the chip
+// is full, and of a partial row's column written and read again.
+constexpr double kStartNs = 5000, kKeyNs = 30, kPartNs = 0.0016;
+
 struct Work {
   std::vector<AttendRun> runs;
   std::vector<AttendItem> items;
   std::vector<int32_t> tok;
   std::vector<MergeToken> merge;
   int64_t part_rows = 0;
-  int32_t narrow = 0, max_parts = 0;
+  int32_t narrow = 0, pairs = 0, max_parts = 0;
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -194,6 +199,12 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       if (s->requests[i].prefix == p && shares(s->requests[i]))
         for (int j = 0; j < s->requests[i].num_queries; ++j) w.tok.push_back((int32_t)(t + j));
     r.ntok = (int32_t)w.tok.size() - r.tok0;
+    const int32_t t0 = w.tok[(size_t)r.tok0];
+    if (w.tok.back() - t0 == r.ntok - 1) {  // ascending and without gaps: no list needed
+      w.tok.resize((size_t)r.tok0);
+      r.listed = 0;
+      r.tok0 = t0;
+    }
     prefix_run[(size_t)p] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
@@ -225,42 +236,44 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
-  // Keys per item: each kernel's items (narrow, wide) should fill the chip once. Items wait for a
-  // few reads one after the other (item, run, page ids, rows) before their first product, so more
-  // and shorter ones cost: `least` keys at least.
+  // Keys per item (a multiple of gran), for each class of tiles, each of which should
+  // fill the chip: the least estimate of the time that `slots` workgroups at once take for it.
   const bool plain = kernel == ATTEND_PLAIN;
-  const int64_t gran = plain ? 32 : 128, least = plain ? 32 : 128;
-  int64_t chunk_of[2];
-  w.narrow = 0;
-  for (int wide = 0; wide < 2; ++wide) {
-    const int64_t target = plain ? 2048 : 512;
-    auto is = [&](const AttendRun& r) { return (tile_rows(kernel, (int64_t)r.ntok * G) == kWideRows) == (wide == 1); };
-    auto blocks = [&](int64_t chunk) {
-      int64_t n = 0;
-      for (const AttendRun& r : w.runs) {
-        const int64_t rows = (int64_t)r.ntok * G;
-        if (is(r)) n += ceil_div(rows, tile_rows(kernel, rows)) * ceil_div(r.kv, chunk);
-      }
-      return n * h.heads;
-    };
-    int64_t longest = least;
+  const int64_t gran = plain ? 32 : 128, slots = plain ? 2048 : kernel == ATTEND_LATENT ? 256 : 512;
+  int64_t chunk_of[3] = {gran, gran, gran};
+  for (int c = 0; c < 3; ++c) {
+    int64_t longest = 0;
+    auto is = [&](const AttendRun& r) { return tile_class(kernel, (int64_t)r.ntok * G) == c; };
     for (const AttendRun& r : w.runs)
       if (is(r)) longest = std::max<int64_t>(longest, r.kv);
-    int64_t lo = ceil_div(std::max(least, ceil_div(longest, kMaxSplits)), gran), hi = std::max(lo, ceil_div(longest, gran));  // in units of gran
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (blocks(mid * gran) <= target) hi = mid;
-      else lo = mid + 1;
+    double best = 0;
+    const int64_t lowest = (int64_t)round_up((size_t)std::max(gran, ceil_div(longest, kMaxSplits)), (size_t)gran);
+    for (int64_t chunk = lowest;; chunk = std::min(longest, (int64_t)round_up((size_t)(chunk + chunk / 3), (size_t)gran))) {
+      double keys = 0, items = 0, parts = 0;
+      for (const AttendRun& r : w.runs) {
+        if (!is(r)) continue;
+        const int64_t rows = (int64_t)r.ntok * G, tiles = ceil_div(rows, tile_rows(kernel, rows)), n = ceil_div(r.kv, chunk);
+        keys += (double)tiles * r.kv;
+        items += (double)tiles * n;
+        if (n > 1 || !r.direct) parts += (double)rows * n;
+      }
+      const double one = kStartNs + kKeyNs * chunk, all = h.heads * (kKeyNs * keys + kStartNs * items) / slots;
+      const double ns = std::max(one, all) + one / 4 + kPartNs * h.dv * h.heads * parts;
+      if (best == 0 || ns < best) {
+        best = ns;
+        chunk_of[c] = chunk;
+      }
+      if (chunk >= longest) break;
     }
-    chunk_of[wide] = lo * gran;
   }
-  for (int wide = 0; wide < 2; ++wide) {
+  int32_t start[4] = {0, 0, 0, 0};  // each class's first item
+  for (int c = 0; c < 3; ++c) {
     for (size_t k = 0; k < w.runs.size(); ++k) {
       AttendRun& r = w.runs[k];
       const int64_t rows = (int64_t)r.ntok * G;
       const int tile = tile_rows(kernel, rows);
-      if ((tile == kWideRows) != (wide == 1)) continue;
-      const int64_t splits = ceil_div(r.kv, chunk_of[wide]);
+      if (tile_class(kernel, rows) != c) continue;
+      const int64_t splits = ceil_div(r.kv, chunk_of[c]);
       const int64_t chunk = (int64_t)round_up((size_t)ceil_div(r.kv, splits), (size_t)gran);
       const int64_t n = ceil_div(r.kv, chunk);
       r.splits = (int32_t)n;
@@ -275,7 +288,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
         for (int64_t sp = 0; sp < n; ++sp) {
           AttendItem it;
           std::memset(&it, 0, sizeof(it));
-          it.run = (int32_t)k;
+          it.run = r;
           it.row0 = (int32_t)row0;
           it.kv0 = (int32_t)(sp * chunk);
           it.kv1 = (int32_t)std::max<int64_t>(it.kv0, std::min(end, (sp + 1) * chunk));
@@ -286,9 +299,11 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     }
     // the longest first: the short ones fill the gaps at the end
     auto longer = [](const AttendItem& x, const AttendItem& y) { return x.kv1 - x.kv0 > y.kv1 - y.kv0; };
-    if (!plain) std::stable_sort(w.items.begin() + (wide ? w.narrow : 0), w.items.end(), longer);
-    if (!wide) w.narrow = (int32_t)w.items.size();
+    if (!plain) std::stable_sort(w.items.begin() + start[c], w.items.end(), longer);
+    start[c + 1] = (int32_t)w.items.size();
   }
+  w.narrow = start[1];
+  w.pairs = start[2] - start[1];
   // tokens joined from parts (or that see no key at all)
   std::vector<int32_t> listed((size_t)s->num_prefixes, 0);  // tokens of each prefix run so far
   auto part = [&](MergeToken& m, int slot, int run, int64_t j) {
@@ -318,7 +333,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 
 // ------------------------------------------------------------------ workspace
 struct Offsets {
-  size_t pages, runs, items, tok, merge, slots, pos, upload, phase, ml, o, total;
+  size_t pages, items, tok, merge, slots, pos, upload, phase, ml, o, total;
 };
 Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Work& w) {
   Offsets f;
@@ -331,7 +346,6 @@ Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, con
   const bool append = s->flags & KAMERA_STEP_APPEND;
   const Shape h = shape_of(L, s->num_q_heads);
   f.pages = take((size_t)n.entries * 4);
-  f.runs = take(w.runs.size() * sizeof(AttendRun));
   f.items = take(w.items.size() * sizeof(AttendItem));
   f.tok = take(w.tok.size() * 4);
   f.merge = take(w.merge.size() * sizeof(MergeToken));
@@ -448,7 +462,6 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
     put(tb.prefix[(size_t)i], s->prefixes[i].block_table, table_entries(s->prefixes[i].slot0, s->prefixes[i].num_tokens, P));
   for (int i = 0; i < s->num_requests; ++i)
     put(tb.request[(size_t)i], s->requests[i].block_table, table_entries(s->requests[i].slot0, s->requests[i].num_tokens, P));
-  if (!w.runs.empty()) std::memcpy(blob.data() + f.runs, w.runs.data(), w.runs.size() * sizeof(AttendRun));
   if (!w.items.empty()) std::memcpy(blob.data() + f.items, w.items.data(), w.items.size() * sizeof(AttendItem));
   if (!w.tok.empty()) std::memcpy(blob.data() + f.tok, w.tok.data(), w.tok.size() * 4);
   if (!w.merge.empty()) std::memcpy(blob.data() + f.merge, w.merge.data(), w.merge.size() * sizeof(MergeToken));
@@ -474,7 +487,6 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   a.row = row_width(L);
   a.layer_stride = pool->layer_stride ? pool->layer_stride : (int64_t)pool->num_pages * P * a.row;
   a.pages = reinterpret_cast<const int32_t*>(base + f.pages);
-  a.runs = reinterpret_cast<const AttendRun*>(base + f.runs);
   a.items = reinterpret_cast<const AttendItem*>(base + f.items);
   a.tok = reinterpret_cast<const int32_t*>(base + f.tok);
   a.merge = reinterpret_cast<const MergeToken*>(base + f.merge);
@@ -508,6 +520,7 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   for (int k = 0; k < 3; ++k) a.mrope[k] = L->mrope_section[k];
   a.kernel = kernel;
   a.num_narrow = w.narrow;
+  a.num_pairs = w.pairs;
   a.max_parts = w.max_parts;
 
   if (n.tokens > 0) {

@@ -78,10 +78,11 @@ hipError_t launch_step_attend(const StepArgs& a, int, const void*, int64_t, void
   std::vector<std::vector<int64_t>> met((size_t)a.num_tokens);
   for (int i = 0; i < a.num_items; ++i) {
     const AttendItem& it = a.items[i];
-    const AttendRun& run = a.runs[it.run];
+    const AttendRun& run = it.run;
     const int64_t rows = (int64_t)run.ntok * a.group;
     const int tile = tile_rows(a.kernel, rows);
-    CHECK(a.kernel == ATTEND_PLAIN || (i < a.num_narrow) == (tile < kWideRows));
+    const int cls = i < a.num_narrow ? TILE_NARROW : i < a.num_narrow + a.num_pairs ? TILE_PAIRS : TILE_WIDE;
+    CHECK(tile_class(a.kernel, rows) == cls);
     CHECK(it.row0 >= 0 && it.row0 < rows && it.kv0 >= 0 && it.kv1 <= run.kv && it.split < run.splits);
     for (int64_t row = it.row0; row < std::min<int64_t>(it.row0 + tile, rows); ++row) {
       const int64_t j = row / a.group, g = row % a.group;

@@ -126,6 +126,16 @@ def test_attend_splits_long_keys(heads, dim, family):
     c.check_attend(0.0)
 
 
+@pytest.mark.parametrize("heads,dim,family", [(4, 128, GQA), (4, 64, GQA), (16, 64, MLA)])
+@pytest.mark.parametrize("members", [2, 5, 8, 9, 16, 17, 40])
+def test_attend_tiles_of_every_size_over_long_prefixes(heads, dim, family, members):
+    """A prefix of many stages a workgroup, its members' rows filling each kind of tile."""
+    more = dict(heads=heads, kv_heads=1, head_dim=dim) if family == GQA else dict(family=MLA, heads=heads, latent=512, rope=dim)
+    c = Case(layers=1, prefixes=[20000], requests=[(0, 1 + i % 3, 1) for i in range(members)], seed=members, **more)
+    c.q *= 4  # a few keys stand out: a lost or doubled stage shows
+    c.check_attend(scale_of(c))
+
+
 @pytest.mark.parametrize("dim,dtype", [(128, BF16), (64, F32), (10, BF16)])
 def test_attend_scores_of_every_size(dim, dtype):
     """Scores of thousands, equal scores, scores of the type's lowest value."""
