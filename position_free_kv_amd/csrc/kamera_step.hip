@@ -167,6 +167,187 @@ __global__ __launch_bounds__(kThreads) void append_plain(StepArgs a, int64_t lay
 }
 
 // ============================================================================
+// Append, bf16 heads of 16 * 2^k columns in whole 16-byte pieces (HBM-bound: rows are read and written
+// once). A lane holds 16 columns of a head, the two partners of each of its 8 pairs among them
+// (NeoX: 8 of each half; GPT-J: 16 in a row), so `lanes` = d / 16 lanes make a head and the sum of
+// squares is a few exchanges. A wave takes heads of one token in turn and keeps the token's cosines and
+// sines; a token's heads are spread over `parts` waves when there are few tokens.
+// ============================================================================
+__device__ __forceinline__ void widen(u32x4 w, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ u32x4 narrow(const float* x) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bf16x2 r;
+    r.x = (__bf16)x[2 * i];  // round to nearest even
+    r.y = (__bf16)x[2 * i + 1];
+    w[i] = __builtin_bit_cast(uint32_t, r);
+  }
+  return w;
+}
+// 8 pairs: NeoX (x[j], x[8 + j]), GPT-J (x[2 j], x[2 j + 1])
+template <bool NEOX>
+__device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float& a = x[NEOX ? j : 2 * j];
+    float& b = x[NEOX ? 8 + j : 2 * j + 1];
+    const float y = a * c[j] - b * s[j];
+    b = a * s[j] + b * c[j];
+    a = y;
+  }
+}
+// the lane's columns of a band of 16 * lanes: two pieces of 8
+template <bool NEOX>
+__device__ __forceinline__ int piece(int lane, int lanes, int half) {
+  return NEOX ? 8 * lane + (half ? 8 * lanes : 0) : 16 * lane + 8 * half;
+}
+__device__ __forceinline__ void load_phase(const StepArgs& a, int64_t t, int lane, float (&c)[8], float (&s)[8]) {
+  const KGLOBAL f32x4* p = (const KGLOBAL f32x4*)(a.phase + t * a.d_rot) + 2 * lane;
+  const KGLOBAL f32x4* q = (const KGLOBAL f32x4*)(a.phase + t * a.d_rot + a.d_rot / 2) + 2 * lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = p[j >> 2][j & 3];
+    s[j] = q[j >> 2][j & 3];
+  }
+}
+
+template <bool NEOX>
+__global__ __launch_bounds__(kThreads) void append_heads(StepArgs a, int64_t layer0, kamera_append_rows r, int lanes, int parts) {
+  const int64_t wave = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t t = wave / parts;
+  if (t >= a.num_tokens) return;
+  const int lane = threadIdx.x & (lanes - 1), seat = (threadIdx.x & 63) / lanes, seats = kWave / lanes;
+  const int nq = r.q ? a.num_q_heads : 0, heads = nq + 2 * a.heads;
+  const int first = piece<NEOX>(lane, lanes, 0), second = piece<NEOX>(lane, lanes, 1);
+  const int64_t slot = a.slots[t];
+  float c[8], s[8];
+  load_phase(a, t, lane, c, s);
+  float wq[16], wk[16];
+  if (r.q_weight) {
+    widen(*(const KGLOBAL u32x4*)((const KGLOBAL uint16_t*)r.q_weight + first), wq);
+    widen(*(const KGLOBAL u32x4*)((const KGLOBAL uint16_t*)r.q_weight + second), wq + 8);
+  }
+  if (r.k_weight) {
+    widen(*(const KGLOBAL u32x4*)((const KGLOBAL uint16_t*)r.k_weight + first), wk);
+    widen(*(const KGLOBAL u32x4*)((const KGLOBAL uint16_t*)r.k_weight + second), wk + 8);
+  }
+  for (int u = (int)(wave - t * parts) * seats + seat; u < heads; u += parts * seats) {
+    const bool is_q = u < nq, is_v = u >= nq + a.heads;
+    const int h = is_q ? u : is_v ? u - nq - a.heads : u - nq;
+    const KGLOBAL uint16_t* x = is_q   ? (const KGLOBAL uint16_t*)r.q + t * r.q_stride + (int64_t)h * a.dk
+                                : is_v ? (const KGLOBAL uint16_t*)r.v + t * r.v_stride + (int64_t)h * a.dk
+                                       : (const KGLOBAL uint16_t*)r.k + t * r.k_stride + (int64_t)h * a.dk;
+    KGLOBAL uint16_t* y = is_q ? (KGLOBAL uint16_t*)r.q_out + t * r.q_out_stride + (int64_t)h * a.dk
+                               : (KGLOBAL uint16_t*)(is_v ? a.v_pool : a.k_pool) + layer0 + slot * a.row + (int64_t)h * a.dk;
+    u32x4 lo = *(const KGLOBAL u32x4*)(x + first), hi = *(const KGLOBAL u32x4*)(x + second);
+    float f[16];
+    widen(lo, f);
+    widen(hi, f + 8);
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) ss += f[j] * f[j];
+    for (int d = 1; d < lanes; d <<= 1) ss += __shfl_xor(ss, d, kWave);  // (a head's lanes are here together)
+    if (!is_v) {
+      if (is_q ? r.q_weight != nullptr : r.k_weight != nullptr) {
+        const float g = 1.0f / sqrtf(ss / (float)a.dk + r.eps);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = f[j] * g * (is_q ? wq[j] : wk[j]);
+      }
+      turn<NEOX>(f, c, s);
+      lo = narrow(f);
+      hi = narrow(f + 8);
+    }
+    *(KGLOBAL u32x4*)(y + first) = lo;
+    *(KGLOBAL u32x4*)(y + second) = hi;
+  }
+}
+
+// ============================================================================
+// Append, bf16 MLA rows in whole 16-byte pieces. Three kinds of waves for a token: the rotary bands of
+// its query heads and of its KV row (16 columns a lane, as above), the norm of the KV row's latent (8
+// columns a lane and turn), and, unless queries are turned in place, their latents' copy.
+// ============================================================================
+constexpr int kLatentTurns = 4;  // latents of at most 4 * 512 columns
+constexpr int kCopyTurns = 4;    // pieces a lane copies
+
+template <bool NEOX>
+__global__ __launch_bounds__(kThreads) void append_latent(StepArgs a, int64_t layer0, kamera_append_rows r, int lanes, int bands, int copies) {
+  const int waves = bands + 1 + copies;
+  const int64_t wave = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t t = wave / waves;
+  if (t >= a.num_tokens) return;
+  const int j = (int)(wave - t * waves), tid = threadIdx.x & 63;
+  const int nq = r.q ? a.num_q_heads : 0;
+  const KGLOBAL uint16_t* q = (const KGLOBAL uint16_t*)r.q + t * r.q_stride;
+  KGLOBAL uint16_t* qo = (KGLOBAL uint16_t*)r.q_out + t * r.q_out_stride;
+  const KGLOBAL uint16_t* k = (const KGLOBAL uint16_t*)r.k + t * r.k_stride;
+  KGLOBAL uint16_t* ko = (KGLOBAL uint16_t*)a.k_pool + layer0 + a.slots[t] * a.row;
+  if (j < bands) {
+    const int lane = tid & (lanes - 1), h = j * (kWave / lanes) + tid / lanes;
+    if (h > nq) return;
+    const KGLOBAL uint16_t* x = (h < nq ? q + (int64_t)h * a.dk : k) + a.latent;
+    KGLOBAL uint16_t* y = (h < nq ? qo + (int64_t)h * a.dk : ko) + a.latent;
+    const int first = piece<NEOX>(lane, lanes, 0), second = piece<NEOX>(lane, lanes, 1);
+    float c[8], s[8], f[16];
+    load_phase(a, t, lane, c, s);
+    widen(*(const KGLOBAL u32x4*)(x + first), f);
+    widen(*(const KGLOBAL u32x4*)(x + second), f + 8);
+    turn<NEOX>(f, c, s);
+    *(KGLOBAL u32x4*)(y + first) = narrow(f);
+    *(KGLOBAL u32x4*)(y + second) = narrow(f + 8);
+  } else if (j == bands) {
+    u32x4 w[kLatentTurns];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLatentTurns; ++i) {
+      const int c = (i * kWave + tid) * 8;
+      if (c >= a.latent) continue;
+      w[i] = *(const KGLOBAL u32x4*)(k + c);
+      float f[8];
+      widen(w[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
+    }
+    const float g = r.k_weight ? 1.0f / sqrtf(wave_sum(ss) / (float)a.latent + r.eps) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < kLatentTurns; ++i) {
+      const int c = (i * kWave + tid) * 8;
+      if (c >= a.latent) continue;
+      if (r.k_weight) {
+        float f[8], v[8];
+        widen(w[i], f);
+        widen(*(const KGLOBAL u32x4*)((const KGLOBAL uint16_t*)r.k_weight + c), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * g * v[e];
+        w[i] = narrow(f);
+      }
+      *(KGLOBAL u32x4*)(ko + c) = w[i];
+    }
+  } else {
+    const int per = a.latent / 8, total = nq * per;  // pieces of a head, of the token
+    u32x4 w[kCopyTurns];
+    int at[kCopyTurns];
+#pragma unroll
+    for (int i = 0; i < kCopyTurns; ++i) {
+      const int p = ((j - bands - 1) * kCopyTurns + i) * kWave + tid, h = p / per;
+      at[i] = p < total ? h * a.dk + (p - h * per) * 8 : -1;
+      if (at[i] >= 0) w[i] = *(const KGLOBAL u32x4*)(q + at[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyTurns; ++i)
+      if (at[i] >= 0) *(KGLOBAL u32x4*)(qo + at[i]) = w[i];
+  }
+}
+
+// ============================================================================
 // Attention, any layout (head widths and alignments the matrix-core kernel does not take): one
 // wave per row of the tile. A wave reads 4 tokens at a time, 16 lanes to a token, each lane
 // holding VEC * NJ of the key's columns; every 16-lane group runs its own online softmax
@@ -477,13 +658,45 @@ hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream) {
-  const int64_t units = (rows.q ? a.num_q_heads : 0) + a.heads + (a.family == KAMERA_GQA ? 1 : 0);
-  const int64_t blocks = ceil_div(a.num_tokens * units, kThreads / kWave);
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   const int64_t layer0 = layer * a.layer_stride;
-  const dim3 g((unsigned)blocks), b(kThreads);
-  if (a.dtype == KAMERA_BF16) hipLaunchKernelGGL((append_plain<uint16_t>), g, b, 0, stream, a, layer0, rows);
-  else hipLaunchKernelGGL((append_plain<float>), g, b, 0, stream, a, layer0, rows);
+  const dim3 b(kThreads);
+  const bool gqa = a.family == KAMERA_GQA;
+  // whole 16-byte pieces everywhere?
+  auto pieces = [](const void* p, int64_t stride) { return p == nullptr || ((uintptr_t)p % 16 == 0 && stride % 8 == 0); };
+  const int lanes = a.d_rot / 16;
+  const bool vec = a.dtype == KAMERA_BF16 && a.d_rot % 16 == 0 && (lanes & (lanes - 1)) == 0 && a.row % 8 == 0 && layer0 % 8 == 0 &&
+                   pieces(rows.q, rows.q_stride) && pieces(rows.q_out, rows.q_out_stride) && pieces(rows.k, rows.k_stride) &&
+                   (!gqa || pieces(rows.v, rows.v_stride)) && pieces(rows.q_weight, 0) && pieces(rows.k_weight, 0) && pieces(a.k_pool, 0) &&
+                   (!gqa || pieces(a.v_pool, 0)) && (gqa || (a.latent % 8 == 0 && a.latent <= kLatentTurns * kWave * 8));
+  const int nq = rows.q ? a.num_q_heads : 0;
+  auto grid = [&](int64_t waves) { return ceil_div(waves, kThreads / kWave); };
+  int64_t blocks;
+  if (vec && gqa) {
+    // a wave for each group of heads it holds at once while there are few tokens; beyond 4096 waves,
+    // heads in turn save reading the token's cosines and sines again
+    const int turns = (int)ceil_div(nq + 2 * a.heads, kWave / lanes);
+    int parts = turns;
+    while (parts > 1 && (int64_t)a.num_tokens * (parts / 2) >= 4096) parts /= 2;
+    blocks = grid((int64_t)a.num_tokens * parts);
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks);
+    if (a.pairing == KAMERA_NEOX) hipLaunchKernelGGL((append_heads<true>), g, b, 0, stream, a, layer0, rows, lanes, parts);
+    else hipLaunchKernelGGL((append_heads<false>), g, b, 0, stream, a, layer0, rows, lanes, parts);
+  } else if (vec) {
+    const int bands = (int)ceil_div(nq + 1, kWave / lanes);
+    const int copies = nq == 0 || rows.q == rows.q_out ? 0 : (int)ceil_div((int64_t)nq * (a.latent / 8), kCopyTurns * kWave);
+    blocks = grid((int64_t)a.num_tokens * (bands + 1 + copies));
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks);
+    if (a.pairing == KAMERA_NEOX) hipLaunchKernelGGL((append_latent<true>), g, b, 0, stream, a, layer0, rows, lanes, bands, copies);
+    else hipLaunchKernelGGL((append_latent<false>), g, b, 0, stream, a, layer0, rows, lanes, bands, copies);
+  } else {
+    blocks = grid((int64_t)a.num_tokens * (nq + a.heads + (gqa ? 1 : 0)));
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    const dim3 g((unsigned)blocks);
+    if (a.dtype == KAMERA_BF16) hipLaunchKernelGGL((append_plain<uint16_t>), g, b, 0, stream, a, layer0, rows);
+    else hipLaunchKernelGGL((append_plain<float>), g, b, 0, stream, a, layer0, rows);
+  }
   return hipGetLastError();
 }
 
