@@ -489,13 +489,13 @@ __device__ __forceinline__ void join_two(S& st, float& l, bool giver, int pair, 
   }
 }
 
-// Four waves' results for the same rows into wave 0's: 2 and 3 into 0 and 1, then 1 into 0. place: LDS
-// of two waves' results.
+// Four waves' results for the same rows into wave 0's: 2 and 3 into 0 and 1, then 1 into 0. even, odd:
+// LDS of a wave's result each.
 template <typename S>
-__device__ __forceinline__ void join_waves(S& st, float& l, f32x4* place, float (&ml)[2][kWaves][64]) {
+__device__ __forceinline__ void join_waves(S& st, float& l, f32x4* even, f32x4* odd, float (&ml)[2][kWaves][64]) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  join_two(st, l, wave >= 2, wave & 1, place + (wave & 1) * (S::kBlocks * S::kScores / 4) * 64, ml);
-  join_two(st, l, wave == 1, 0, place, ml, wave >= 2);
+  join_two(st, l, wave >= 2, wave & 1, wave & 1 ? odd : even, ml);
+  join_two(st, l, wave == 1, 0, even, ml, wave >= 2);
 }
 
 }  // namespace

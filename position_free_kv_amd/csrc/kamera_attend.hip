@@ -39,18 +39,21 @@ struct Rows {
   }
 };
 
+// LDS of a workgroup: four places of 64 rows (keys or values) each.
+constexpr int kStageKeys = 64;
+template <int D>
+constexpr int kPlace = kStageKeys * 2 * D;
+
 // ============================================================================
 // Tiles of 128 rows: 4 waves share stages of 64 keys, 32 rows each. A run of at most 64 rows gives its
 // rows to two waves, which take the first half of a stage's keys, and again to the other two, which
 // take the second half (PAIRS); the pairs' results are joined at the end.
 // ============================================================================
 template <int D, bool PAIRS>
-__global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo io, int item0) {
-  constexpr int TS = 64, NI = TS / kRowsPerLoad<D> / kWaves, BYTES = TS * 2 * D;
+__device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* k0, KLDS char* v0,
+                                          KLDS char* k1, KLDS char* v1, float (&ml)[2][kWaves][64]) {
+  constexpr int TS = kStageKeys, NI = TS / kRowsPerLoad<D> / kWaves;
   typedef State<D, D, 32> S;
-  __shared__ __align__(1024) char k0[BYTES], v0[BYTES], k1[BYTES], v1[BYTES];
-  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
-  const AttendItem it = a.items[item0 + item];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint16_t* kp = a.k_pool + io.layer0 + head * D;
   const uint16_t* vp = a.v_pool + io.layer0 + head * D;
@@ -59,7 +62,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo 
   Rows<D, NI, 32> rows;
   if (any) {
     rows.find(a, it.run, it.kv0, first, last);
-    rows.load(a, kp, vp, (KLDS char*)k0, (KLDS char*)v0, first);
+    rows.load(a, kp, vp, k0, v0, first);
     rows.find(a, it.run, it.kv0 + TS, first, last);
   }
   const int block = PAIRS ? wave & 1 : wave, part = PAIRS ? wave >> 1 : 0;  // rows, and keys of a stage
@@ -78,24 +81,22 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo 
     for (int t = it.kv0;;) {
       stage_barrier();
       if (t + TS < it.kv1) {
-        rows.load(a, kp, vp, (KLDS char*)k1, (KLDS char*)v1, first);
+        rows.load(a, kp, vp, k1, v1, first);
         rows.find(a, it.run, t + 2 * TS, first, last);
       }
-      stage((const KLDS char*)k0, (const KLDS char*)v0, t);
+      stage(k0, v0, t);
       if ((t += TS) >= it.kv1) break;
       stage_barrier();
       if (t + TS < it.kv1) {
-        rows.load(a, kp, vp, (KLDS char*)k0, (KLDS char*)v0, first);
+        rows.load(a, kp, vp, k0, v0, first);
         rows.find(a, it.run, t + 2 * TS, first, last);
       }
-      stage((const KLDS char*)k1, (const KLDS char*)v1, t);
+      stage(k1, v1, t);
       if ((t += TS) >= it.kv1) break;
     }
   }
   float l = row_sum<32>(st.l);
   if constexpr (PAIRS) {
-    static_assert(BYTES >= 64 * 4 * D / 2, "a wave's result fits in a buffer");
-    __shared__ float ml[2][kWaves][64];
     join_two(st, l, wave >= 2, wave & 1, wave & 1 ? (f32x4*)v0 : (f32x4*)k0, ml);
     if (wave >= 2) return;
   }
@@ -104,23 +105,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide(StepArgs a, AttendIo 
 
 // ============================================================================
 // Tiles of up to 32 rows (few queries on a KV head: reading the keys is what takes time). Each of the
-// 4 waves walks stages of its own, of 32 (128-wide) or 64 keys, at its own pace, and the four results
-// are joined in LDS. One buffer a wave (16 KB): two workgroups share a CU, so that the other seven
-// waves' reads are in flight while one computes. Up to 16 rows take the products of 16 rows.
+// 4 waves walks stages of 32 keys of its own, at its own pace, and the four results are joined in LDS.
+// One buffer a wave: two workgroups share a CU, so that the other waves' reads are in flight while one
+// computes. Up to 16 rows take the products of 16 rows.
 // ============================================================================
-template <int D>
-constexpr int kStageKeys = 4096 / D;
-template <int D>
-constexpr int kStageBytes = kStageKeys<D> * 2 * D;
-
 template <int D, int ROWS>
-__device__ __forceinline__ void narrow_rows_of(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head,
-                                               KLDS char* kbuf, KLDS char* vbuf, f32x4* place, float (&ml)[2][kWaves][64]) {
+__device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* mine,
+                                            KLDS char* place0, KLDS char* place1, float (&ml)[2][kWaves][64]) {
   typedef State<D, D, ROWS> S;
-  constexpr int TS = kStageKeys<D>, NI = TS / kRowsPerLoad<D>, STEP = kWaves * TS;
+  constexpr int TS = 32, NI = TS / kRowsPerLoad<D>, STEP = kWaves * TS;
+  KLDS char *kbuf = mine, *vbuf = mine + TS * 2 * D;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Lane r = lane_row(a, it, head, it.row0 + S::row());
-  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, ROWS - 1);
   const uint16_t* kp = a.k_pool + io.layer0 + head * D;
   const uint16_t* vp = a.v_pool + io.layer0 + head * D;
   const int last = it.kv1 - 1;
@@ -130,6 +125,8 @@ __device__ __forceinline__ void narrow_rows_of(const StepArgs& a, const AttendIo
     rows.find(a, it.run, t, 0, last);
     rows.load(a, kp, vp, kbuf, vbuf, 0);
   }
+  const Lane r = lane_row(a, it, head, it.row0 + S::row());
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, ROWS - 1);
   bf16x8 q[S::kKSteps];
   S::load_q(io, r, q);
   S st;
@@ -144,32 +141,34 @@ __device__ __forceinline__ void narrow_rows_of(const StepArgs& a, const AttendIo
     if ((t += STEP) < it.kv1) rows.load(a, kp, vp, kbuf, vbuf, 0);
   }
   float l = row_sum<ROWS>(st.l);
-  join_waves(st, l, place, ml);
+  join_waves(st, l, (f32x4*)place0, (f32x4*)place1, ml);
   if (wave == 0) put_state(a, io, it, head, r, st, l);
 }
 
+// One launch for all tiles, the wide ones first: what they compute runs beside what the narrow ones read.
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attend_narrow(StepArgs a, AttendIo io) {
-  __shared__ __align__(1024) char buf[kWaves][2][kStageBytes<D>];
+__global__ __launch_bounds__(kThreads, 2) void attend_heads(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char p0[kPlace<D>], p1[kPlace<D>], p2[kPlace<D>], p3[kPlace<D>];
   __shared__ float ml[2][kWaves][64];
-  static_assert(sizeof(buf) >= 2 * 64 * 4 * D / 2, "two waves' results fit where the stages were");
+  static_assert(kPlace<D> >= 64 * 4 * D / 2, "a wave's result fits in a place");
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const AttendItem it = a.items[item];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  KLDS char *k = (KLDS char*)buf[wave][0], *v = (KLDS char*)buf[wave][1];
-  f32x4* place = (f32x4*)&buf[0][0][0];
-  if (it.run.ntok * a.group <= 16) narrow_rows_of<D, 16>(a, io, it, head, k, v, place, ml);
-  else narrow_rows_of<D, 32>(a, io, it, head, k, v, place, ml);
+  if (item < a.num_wide) {
+    wide_tile<D, false>(a, io, it, head, (KLDS char*)p0, (KLDS char*)p1, (KLDS char*)p2, (KLDS char*)p3, ml);
+  } else if (item < a.num_wide + a.num_pairs) {
+    wide_tile<D, true>(a, io, it, head, (KLDS char*)p0, (KLDS char*)p1, (KLDS char*)p2, (KLDS char*)p3, ml);
+  } else {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    KLDS char* mine = wave < 2 ? (wave ? (KLDS char*)p1 : (KLDS char*)p0) : (wave == 2 ? (KLDS char*)p2 : (KLDS char*)p3);
+    if (it.run.ntok * a.group <= 16) narrow_tile<D, 16>(a, io, it, head, mine, (KLDS char*)p0, (KLDS char*)p1, ml);
+    else narrow_tile<D, 32>(a, io, it, head, mine, (KLDS char*)p0, (KLDS char*)p1, ml);
+  }
 }
 
 template <int D>
 hipError_t launch(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
-  const dim3 b(kThreads);
-  auto grid = [&](int items) { return dim3((unsigned)((int64_t)items * a.heads)); };
-  const int wide0 = a.num_narrow + a.num_pairs, wide = a.num_items - wide0;
-  if (wide > 0) hipLaunchKernelGGL((attend_wide<D, false>), grid(wide), b, 0, stream, a, io, wide0);
-  if (a.num_pairs > 0) hipLaunchKernelGGL((attend_wide<D, true>), grid(a.num_pairs), b, 0, stream, a, io, a.num_narrow);
-  if (a.num_narrow > 0) hipLaunchKernelGGL((attend_narrow<D>), grid(a.num_narrow), b, 0, stream, a, io);
+  const int64_t blocks = (int64_t)a.num_items * a.heads;
+  if (blocks > 0) hipLaunchKernelGGL((attend_heads<D>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, io);
   return hipGetLastError();
 }
 

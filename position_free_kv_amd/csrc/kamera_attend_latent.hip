@@ -25,7 +25,9 @@ typedef State<kKey, kLatent, 16> LatentState;
 struct LatentRows {
   int page, place;
   __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int n, int last) {
-    const int t = min(t0 + first + (int)(threadIdx.x & 63 & (n - 1)), last);
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // (see load)
+    const int t = min(t0 + first + (lane & (n - 1)), last);
     page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, t, place)];
   }
   // N keys of the stage from `first` on (a multiple of N): one instruction a latent, one for 8 bands
@@ -34,13 +36,16 @@ struct LatentRows {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is made anew each stage: kept, it would cost the products registers
     const int row = page * a.page_size + place;  // rows of 1152 bytes: their number fits 32 bits
+    constexpr int M = N < 8 ? N : 8;  // latents a turn (each with an address in scalar registers), bands an instruction
+#pragma nounroll
+    for (int i0 = 0; i0 < N; i0 += M)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint16_t* p = k + (int64_t)__builtin_amdgcn_readlane(row, i) * kKey;
-      const int piece = lane ^ (N >= 16 ? swz<16, kLatentRow>(i) : swz<16, kLatentRow>(first + i));
-      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8), (KLDS void*)(latents + (first + i) * kLatentRow), 16, 0, 0);
-    }
-    constexpr int M = N < 8 ? N : 8;  // bands an instruction brings in, 8 pieces each
+      for (int i1 = 0; i1 < M; ++i1) {
+        const int i = i0 + i1;
+        const uint16_t* p = k + (int64_t)__builtin_amdgcn_readlane(row, i) * kKey;
+        const int piece = lane ^ swz<16, kLatentRow>(first + i);
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(p + piece * 8), (KLDS void*)(latents + (first + i) * kLatentRow), 16, 0, 0);
+      }
 #pragma unroll
     for (int i = 0; i < N; i += M) {
       const int piece = (lane & 7) ^ swz<16, kRopeRow>(first + i + lane / 8);
@@ -56,9 +61,8 @@ struct LatentRows {
 // Tiles of 128 rows: 8 waves of 16 rows share stages of 32 keys.
 // ============================================================================
 constexpr int kWideWaves = 8;
-__global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArgs a, AttendIo io) {
-  __shared__ __align__(1024) char k0[kLatents], k1[kLatents], r0[kBands], r1[kBands];
-  const AttendItem it = a.items[a.num_narrow + blockIdx.x];
+__device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, KLDS char* k0, KLDS char* k1,
+                                          KLDS char* r0, KLDS char* r1) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Lane r = lane_row(a, it, 0, it.row0 + wave * 16 + (lane & 15));
@@ -73,19 +77,19 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArg
   if (it.kv1 > it.kv0) {
     LatentRows rows;
     rows.find(a, run, it.kv0, first, PER, last);
-    rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
+    rows.load<PER>(a, kp, k0, r0, first);
     rows.find(a, run, it.kv0 + kKeys, first, PER, last);
     for (int t = it.kv0;;) {
       stage_barrier();
       if (t + kKeys < it.kv1) {
-        rows.load<PER>(a, kp, (KLDS char*)k1, (KLDS char*)r1, first);
+        rows.load<PER>(a, kp, k1, r1, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
       }
       walk<kKeys, 1>(st, q, (const KLDS char*)k0, (const KLDS char*)r0, (const KLDS char*)k0, t, r.end, end_min, end_max, io.scale2);
       if ((t += kKeys) >= it.kv1) break;
       stage_barrier();
       if (t + kKeys < it.kv1) {
-        rows.load<PER>(a, kp, (KLDS char*)k0, (KLDS char*)r0, first);
+        rows.load<PER>(a, kp, k0, r0, first);
         rows.find(a, run, t + 2 * kKeys, first, PER, last);
       }
       walk<kKeys, 1>(st, q, (const KLDS char*)k1, (const KLDS char*)r1, (const KLDS char*)k1, t, r.end, end_min, end_max, io.scale2);
@@ -102,10 +106,8 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent_wide(StepArg
 // Tiles of up to 16 rows: each wave walks stages of its own (one buffer each: LDS holds no more),
 // the four out of step with each other, and the results are joined pairwise through LDS.
 // ============================================================================
-__global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, AttendIo io) {
-  __shared__ __align__(1024) char buf[kWaves][kLatents], bands[kWaves][kBands];
-  __shared__ float ml[2][kWaves][64];
-  const AttendItem it = a.items[blockIdx.x];
+__device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, KLDS char* mine, KLDS char* band,
+                                            KLDS char* place0, KLDS char* place1, float (&ml)[2][kWaves][64]) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Lane r = lane_row(a, it, 0, it.row0 + (lane & 15));
@@ -118,7 +120,6 @@ __global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, 
   const int last = it.kv1 - 1;
   int t = it.kv0 + wave * kKeys;
   if (t < it.kv1) {
-    KLDS char *mine = (KLDS char*)buf[wave], *band = (KLDS char*)bands[wave];
     LatentRows rows;
     rows.find(a, run, t, 0, kKeys, last);
     for (; t < it.kv1; t += kWaves * kKeys) {
@@ -132,17 +133,34 @@ __global__ __launch_bounds__(kThreads, 1) void attend_latent_narrow(StepArgs a, 
     }
   }
   float l = row_sum<16>(st.l);
-  static_assert(sizeof(buf) >= 2 * 64 * LatentState::kBlocks * 16, "two waves' results fit where the stages were");
-  join_waves(st, l, (f32x4*)&buf[0][0], ml);
-  if (wave == 0) put_state(a, io, it, 0, r, st, l);
+  static_assert(kLatents >= 64 * LatentState::kBlocks * 16, "a wave's result fits where a stage was");
+  join_waves(st, l, (f32x4*)place0, (f32x4*)place1, ml);
+  int tid = threadIdx.x;  // (as in the wide tile)
+  asm volatile("" : "+v"(tid));
+  if (wave == 0) put_state(a, io, it, 0, lane_row(a, it, 0, it.row0 + (tid & 15)), st, l);
+}
+
+// One launch for both kinds of tiles, the wide ones first. Narrow tiles have work for 4 of the 8 waves.
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char k0[kLatents], k1[kLatents], k2[kLatents], k3[kLatents];
+  __shared__ __align__(1024) char r0[kBands], r1[kBands], r2[kBands], r3[kBands];
+  __shared__ float ml[2][kWaves][64];
+  const AttendItem it = a.items[blockIdx.x];
+  if ((int)blockIdx.x < a.num_wide) {
+    wide_tile(a, io, it, (KLDS char*)k0, (KLDS char*)k1, (KLDS char*)r0, (KLDS char*)r1);
+  } else {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= kWaves) return;  // (barriers count the waves that are left)
+    KLDS char* mine = wave < 2 ? (wave ? (KLDS char*)k1 : (KLDS char*)k0) : (wave == 2 ? (KLDS char*)k2 : (KLDS char*)k3);
+    KLDS char* band = wave < 2 ? (wave ? (KLDS char*)r1 : (KLDS char*)r0) : (wave == 2 ? (KLDS char*)r2 : (KLDS char*)r3);
+    narrow_tile(a, io, it, mine, band, (KLDS char*)k0, (KLDS char*)k1, ml);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_attend_latent(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
-  const int wide = a.num_items - a.num_narrow, narrow = a.num_narrow;
-  if (wide > 0) hipLaunchKernelGGL(attend_latent_wide, dim3((unsigned)wide), dim3(64 * kWideWaves), 0, stream, a, io);
-  if (narrow > 0) hipLaunchKernelGGL(attend_latent_narrow, dim3((unsigned)narrow), dim3(kThreads), 0, stream, a, io);
+  if (a.num_items > 0) hipLaunchKernelGGL(attend_latent, dim3((unsigned)a.num_items), dim3(64 * kWideWaves), 0, stream, a, io);
   return hipGetLastError();
 }
 

@@ -80,7 +80,7 @@ struct StepArgs {
   uint32_t page_magic;  // slot / page_size = slot * page_magic >> page_bits, slot < 2^31
   int32_t page_bits;
   int32_t max_parts;    // most parts of a joined row
-  int32_t num_narrow, num_pairs;  // matrix-core kernels: the items' order: narrow, pairs, wide
+  int32_t num_wide, num_pairs;  // the items' order: wide, pairs, narrow
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
 
@@ -89,7 +89,7 @@ static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step argume
 enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2 };
 // Tiles, by the rows of a run: narrow where they fit it, wide ones of 128 rows; in between HEADS has
 // one of 64 rows (pairs).
-enum TileClass { TILE_NARROW = 0, TILE_PAIRS = 1, TILE_WIDE = 2 };
+enum TileClass { TILE_WIDE = 0, TILE_PAIRS = 1, TILE_NARROW = 2 };
 constexpr int kWideRows = 128, kPairRows = 64;
 constexpr int narrow_rows(int kernel) { return kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32; }
 constexpr int tile_class(int kernel, int64_t rows) {

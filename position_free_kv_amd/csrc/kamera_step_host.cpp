@@ -132,10 +132,15 @@ kamera_status check_workspace(const void* ws, size_t have, size_t need) {
 // reads the prefix and its own tokens as one sequence, and its result needs no joining.
 constexpr int64_t kShareRows = 64;
 
-// What the choice of an item's length goes by: the time of a workgroup before its first product (its
-// item, page ids, rows and queries are read one after the other), of one key of a tile while the chip
-// is full, and of a partial row's column written and read again.
-constexpr double kStartNs = 5000, kKeyNs = 30, kPartNs = 0.0016;
+// What the choice of an item's length goes by, measured: the time of a workgroup around its keys (its
+// item, page ids, rows and queries are read one after the other, its results joined and written), of
+// one key of a tile while the chip is full, and of a partial row's column written and read again.
+constexpr double kStartNs = 6000, kPartNs = 0.001;
+double key_ns(int kernel, int tile) {
+  if (kernel == ATTEND_LATENT) return tile == TILE_WIDE ? 60 : 20;
+  if (kernel == ATTEND_HEADS) return tile == TILE_WIDE ? 30 : tile == TILE_PAIRS ? 38 : 25;
+  return 40;
+}
 
 struct Work {
   std::vector<AttendRun> runs;
@@ -143,7 +148,7 @@ struct Work {
   std::vector<int32_t> tok;
   std::vector<MergeToken> merge;
   int64_t part_rows = 0;
-  int32_t narrow = 0, pairs = 0, max_parts = 0;
+  int32_t wide = 0, pairs = 0, max_parts = 0;
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -247,6 +252,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     for (const AttendRun& r : w.runs)
       if (is(r)) longest = std::max<int64_t>(longest, r.kv);
     double best = 0;
+    const double per_key = key_ns(kernel, c);
     const int64_t lowest = (int64_t)round_up((size_t)std::max(gran, ceil_div(longest, kMaxSplits)), (size_t)gran);
     for (int64_t chunk = lowest;; chunk = std::min(longest, (int64_t)round_up((size_t)(chunk + chunk / 3), (size_t)gran))) {
       double keys = 0, items = 0, parts = 0;
@@ -257,7 +263,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
         items += (double)tiles * n;
         if (n > 1 || !r.direct) parts += (double)rows * n;
       }
-      const double one = kStartNs + kKeyNs * chunk, all = h.heads * (kKeyNs * keys + kStartNs * items) / slots;
+      const double one = kStartNs + per_key * chunk, all = h.heads * (per_key * keys + kStartNs * items) / slots;
       const double ns = std::max(one, all) + one / 4 + kPartNs * h.dv * h.heads * parts;
       if (best == 0 || ns < best) {
         best = ns;
@@ -302,7 +308,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     if (!plain) std::stable_sort(w.items.begin() + start[c], w.items.end(), longer);
     start[c + 1] = (int32_t)w.items.size();
   }
-  w.narrow = start[1];
+  w.wide = start[1];
   w.pairs = start[2] - start[1];
   // tokens joined from parts (or that see no key at all)
   std::vector<int32_t> listed((size_t)s->num_prefixes, 0);  // tokens of each prefix run so far
@@ -519,7 +525,7 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   a.num_tokens = (int32_t)n.tokens;
   for (int k = 0; k < 3; ++k) a.mrope[k] = L->mrope_section[k];
   a.kernel = kernel;
-  a.num_narrow = w.narrow;
+  a.num_wide = w.wide;
   a.num_pairs = w.pairs;
   a.max_parts = w.max_parts;
 
