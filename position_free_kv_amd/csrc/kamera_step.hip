@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
   for (int c = lane; c < quads; c += TPR) {
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     if (first < side) {
-#pragma unroll 4
+#pragma unroll 8
       for (int k = first; k < n; k += side) {
         const float w = weight[sub][k];
         const f32x4 x = rows[p.row(k) * quads + c];

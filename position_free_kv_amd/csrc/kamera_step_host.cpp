@@ -156,8 +156,8 @@ struct Tables {
   std::vector<int32_t> prefix, request;
 };
 
-// Layouts of the matrix-core kernels; they also need the pool in 16-byte pieces, and the MLA one
-// row numbers of 32 bits.
+// Layouts of the matrix-core kernels; they also need the pool in 16-byte pieces, and row numbers of
+// 32 bits.
 int matrix_kernel(const kamera_layout* L) {
   if (L->dtype != KAMERA_BF16) return ATTEND_PLAIN;
   if (L->family == KAMERA_GQA) return L->head_dim == 64 || L->head_dim == 128 ? ATTEND_HEADS : ATTEND_PLAIN;
@@ -166,7 +166,7 @@ int matrix_kernel(const kamera_layout* L) {
 int pick_kernel(const kamera_layout* L, const kamera_pool* pool) {
   const int kernel = matrix_kernel(L);
   if (!aligned(pool->k_pool, 16) || (L->family == KAMERA_GQA && !aligned(pool->v_pool, 16)) || pool->layer_stride % 8) return ATTEND_PLAIN;
-  if (kernel == ATTEND_LATENT && (int64_t)pool->num_pages * L->page_size >= (int64_t(1) << 31)) return ATTEND_PLAIN;
+  if ((int64_t)pool->num_pages * L->page_size >= (int64_t(1) << 31)) return ATTEND_PLAIN;
   return kernel;
 }
 
@@ -241,35 +241,56 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
-  // Keys per item (a multiple of gran), for each class of tiles, each of which should
-  // fill the chip: the least estimate of the time that `slots` workgroups at once take for it.
+  // Keys per item (a multiple of gran), for each class of tiles: the least estimate of the launch's
+  // time. All classes share `slots` places; a class whose items are alike takes whole rounds of them
+  // (8 heads of a 131072-key prefix in 69 ranges, 552 workgroups on 512 places: 137 us; in 64: 109 us).
   const bool plain = kernel == ATTEND_PLAIN;
   const int64_t gran = plain ? 32 : 128, slots = plain ? 2048 : kernel == ATTEND_LATENT ? 256 : 512;
-  int64_t chunk_of[3] = {gran, gran, gran};
-  for (int c = 0; c < 3; ++c) {
+  struct Class {
     int64_t longest = 0;
-    auto is = [&](const AttendRun& r) { return tile_class(kernel, (int64_t)r.ntok * G) == c; };
-    for (const AttendRun& r : w.runs)
-      if (is(r)) longest = std::max<int64_t>(longest, r.kv);
+    double tiles = 0, keys = 0;
+  } cls[3];
+  for (const AttendRun& r : w.runs) {
+    const int64_t rows = (int64_t)r.ntok * G;
+    Class& c = cls[tile_class(kernel, rows)];
+    const double tiles = (double)ceil_div(rows, tile_rows(kernel, rows));
+    c.longest = std::max<int64_t>(c.longest, r.kv);
+    c.tiles += tiles;
+    c.keys += tiles * r.kv;
+  }
+  double whole = 0;  // the launch's time if the places were always full and nothing split
+  for (int k = 0; k < 3; ++k) whole += h.heads * (key_ns(kernel, k) * cls[k].keys + kStartNs * cls[k].tiles) / slots;
+  int64_t chunk_of[3] = {gran, gran, gran};
+  for (int k = 0; k < 3; ++k) {
+    const Class& c = cls[k];
+    const double per_key = key_ns(kernel, k);
+    const bool alike = c.keys > 0.9 * c.tiles * c.longest;
     double best = 0;
-    const double per_key = key_ns(kernel, c);
-    const int64_t lowest = (int64_t)round_up((size_t)std::max(gran, ceil_div(longest, kMaxSplits)), (size_t)gran);
-    for (int64_t chunk = lowest;; chunk = std::min(longest, (int64_t)round_up((size_t)(chunk + chunk / 3), (size_t)gran))) {
-      double keys = 0, items = 0, parts = 0;
+    auto consider = [&](int64_t chunk) {
+      double items = 0, parts = 0;
       for (const AttendRun& r : w.runs) {
-        if (!is(r)) continue;
-        const int64_t rows = (int64_t)r.ntok * G, tiles = ceil_div(rows, tile_rows(kernel, rows)), n = ceil_div(r.kv, chunk);
-        keys += (double)tiles * r.kv;
-        items += (double)tiles * n;
+        const int64_t rows = (int64_t)r.ntok * G, n = ceil_div(r.kv, chunk);
+        if (tile_class(kernel, rows) != k) continue;
+        items += (double)ceil_div(rows, tile_rows(kernel, rows)) * n;
         if (n > 1 || !r.direct) parts += (double)rows * n;
       }
-      const double one = kStartNs + per_key * chunk, all = h.heads * (per_key * keys + kStartNs * items) / slots;
-      const double ns = std::max(one, all) + one / 4 + kPartNs * h.dv * h.heads * parts;
+      items *= h.heads;
+      const double one = kStartNs + per_key * std::min(chunk, c.longest), more = kStartNs * (items - c.tiles * h.heads) / slots;
+      const double rounds = alike ? std::ceil(items / slots) * one : one * 5 / 4;
+      const double ns = std::max(rounds, whole + more + (alike ? 0 : one / 4)) + kPartNs * h.dv * h.heads * parts;
       if (best == 0 || ns < best) {
         best = ns;
-        chunk_of[c] = chunk;
+        chunk_of[k] = chunk;
       }
-      if (chunk >= longest) break;
+    };
+    const int64_t lowest = (int64_t)round_up((size_t)std::max(gran, ceil_div(c.longest, kMaxSplits)), (size_t)gran);
+    for (int64_t chunk = lowest;; chunk = (int64_t)round_up((size_t)(chunk + chunk / 3), (size_t)gran)) {
+      consider(chunk);
+      if (chunk >= c.longest) break;
+    }
+    for (int64_t round = 1; alike && round <= 4; ++round) {  // ranges that fill whole rounds
+      const int64_t n = (int64_t)(round * slots / (c.tiles * h.heads));
+      if (n > 0) consider(std::max(lowest, (int64_t)round_up((size_t)ceil_div(c.longest, n), (size_t)gran)));
     }
   }
   int32_t start[4] = {0, 0, 0, 0};  // each class's first item

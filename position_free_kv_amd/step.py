@@ -12,7 +12,7 @@ from typing import Optional, Sequence
 import numpy as np
 
 from . import abi
-from .abi import Layout, Pool, _check, _ptr, _stream, _ws
+from .abi import Layout, Pool, _check, _ptr, _ws
 
 APPEND, ATTEND = 1, 2
 REQUEST_ALL = 1
@@ -80,6 +80,23 @@ def _lib() -> ctypes.CDLL:
     return _bound
 
 
+_cuda = None  # torch.cuda where there is a GPU, else False
+
+
+def _stream(stream) -> Optional[int]:
+    """Handle of a stream: torch's current one by default (None, the null stream, without a GPU)."""
+    global _cuda
+    if stream is None:
+        if _cuda is None:
+            try:
+                import torch
+                _cuda = torch.cuda if torch.cuda.is_available() else False
+            except ImportError:
+                _cuda = False
+        return _cuda.current_stream().cuda_stream if _cuda else None
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
 def _tables(block_tables, n: int):
     """Host int32 tables, one a request: a 2-D array (a row each) or a sequence of arrays. Returns
     (addresses, objects to keep alive)."""
@@ -136,27 +153,39 @@ def upload(layout: Layout, step: Step, pool: Pool, workspace, stream=None) -> Pl
     return plan
 
 
-def _stride(x, stride: Optional[int]) -> int:
-    """Elements between tokens: as given, or the first stride of a tensor (0, packed, if it has one row)."""
-    if stride is not None:
-        return int(stride)
-    return int(x.stride(0)) if hasattr(x, "stride") and x.shape[0] > 1 else 0
+def _rows(x, stride: Optional[int]):
+    """(address, elements between tokens) of a tensor or an address; one row has no stride (0: packed)."""
+    if x is None:
+        return None, 0 if stride is None else stride
+    if isinstance(x, int):
+        return x, 0 if stride is None else stride
+    if stride is None:
+        stride = x.stride(0) if x.size(0) > 1 else 0
+    return x.data_ptr(), stride
 
 
 def append(plan: Plan, layer: int, *, k, v=None, q=None, q_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
            q_stride: Optional[int] = None, k_stride: Optional[int] = None, v_stride: Optional[int] = None,
            q_out_stride: Optional[int] = None, stream=None) -> None:
     """Norm and rotate the step's queries and keys; write its K and V rows into layer `layer`."""
-    rows = AppendRows(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _stride(q, q_stride), _stride(k, k_stride), _stride(v, v_stride),
-                      _stride(q_out, q_out_stride), _ptr(q_weight), _ptr(k_weight), float(eps), 0)
-    _check(_lib().kamera_step_append(ctypes.byref(plan), int(layer), ctypes.byref(rows), _stream(stream)))
+    qp, qs = _rows(q, q_stride)
+    kp, ks = _rows(k, k_stride)
+    vp, vs = _rows(v, v_stride)
+    op, os_ = _rows(q_out, q_out_stride)
+    rows = AppendRows(qp, kp, vp, op, qs, ks, vs, os_, _ptr(q_weight), _ptr(k_weight), eps, 0)
+    status = (_bound or _lib()).kamera_step_append(ctypes.byref(plan), layer, ctypes.byref(rows), _stream(stream))
+    if status:
+        _check(status)
 
 
 def attend(plan: Plan, layer: int, q, out, scale: float, lse=None, *, q_stride: Optional[int] = None,
            out_stride: Optional[int] = None, stream=None) -> None:
     """Attention of the step's query tokens over layer `layer` of the pool."""
-    _check(_lib().kamera_step_attend(ctypes.byref(plan), int(layer), _ptr(q), _stride(q, q_stride), _ptr(out),
-                                     _stride(out, out_stride), _ptr(lse), float(scale), _stream(stream)))
+    qp, qs = _rows(q, q_stride)
+    op, os_ = _rows(out, out_stride)
+    status = (_bound or _lib()).kamera_step_attend(ctypes.byref(plan), layer, qp, qs, op, os_, _ptr(lse), scale, _stream(stream))
+    if status:
+        _check(status)
 
 
 def copy_pages_workspace_bytes(num_copies: int) -> int:
