@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void step_phase(StepArgs a) {
     const int c = sections == 0 || p < a.mrope[0] ? 0 : (p < a.mrope[0] + a.mrope[1] ? 1 : 2);
     at = a.positions[3 * t + c];
   }
-  const double phi = (double)at * pow(a.rope_base, (-2.0 * (double)p) / (double)a.d_rot);
+  const double phi = (double)at * a.theta[p];
   double sd, cd;
   sincos(phi, &sd, &cd);
   a.phase[t * a.d_rot + p] = (float)cd;
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
   const AttendItem it = a.items[item];
   const AttendRun& run = it.run;
   const int lane = threadIdx.x & 63, dl = lane & 15, tg = lane >> 4;
-  const int row = it.row0 + (threadIdx.x >> 6);  // narrow_rows(ATTEND_PLAIN) waves
+  const int row = it.row0 + (threadIdx.x >> 6);  // (a tile's rows are the workgroup's waves)
   if (row >= run.ntok * a.group) return;
   const int j = row / a.group, g = row - j * a.group;
   const int token = run.listed ? a.tok[run.tok0 + j] : run.tok0 + j;
@@ -643,7 +643,7 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
   const dim3 b(kThreads);
   const unsigned by_wave = (unsigned)ceil_div(rows, kThreads / kWave);
   if (a.dv % 4) hipLaunchKernelGGL((attend_join_any<T>), dim3(by_wave), b, 0, stream, a, io);
-  else if (a.max_parts <= kJoinByWave) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave), b, 0, stream, a, io);
+  else if (join_by_wave(rows, a.max_parts)) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave), b, 0, stream, a, io);
   else hipLaunchKernelGGL((attend_join<T, kThreads>), dim3((unsigned)rows), b, 0, stream, a, io);
   return hipGetLastError();
 }

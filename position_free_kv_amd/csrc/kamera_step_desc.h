@@ -33,7 +33,7 @@ struct alignas(16) AttendRun {
   int32_t direct;               // the only part of its tokens' results: written to the output
   int64_t part0;                // first partial row: part0 + (split * H + head) * (ntok * G) + row
   int32_t splits;               // ranges its keys are cut into
-  int32_t pad;
+  int32_t tile;                 // TileClass
 };
 static_assert(sizeof(AttendRun) == 64, "run record");
 
@@ -68,9 +68,9 @@ struct StepArgs {
   float2* part_ml;      // [partial rows]: running maximum (base-2 logarithms) and sum
   const int64_t* slots; // [N] pool slot of every appended token
   float* phase;         // [N][2][d_rot / 2]: cosines, then sines
-  const int32_t* pos;   // [N] positions (NULL: `positions`)
+  const int32_t* pos;   // [N] positions (NULL: `positions`, the caller's [N][3])
   const int32_t* positions;
-  double rope_base;
+  const double* theta;  // [d_rot / 2] rope_base^(-2 i / d_rot)
   int32_t family, dtype, pairing, row;  // row = F
   int32_t heads, group, dk, dv;         // KV heads, query heads per KV head, key and value widths
   int32_t num_q_heads, d_rot, latent, page_size;
@@ -87,23 +87,16 @@ static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step argume
 // PLAIN: any layout. HEADS: bf16 GQA/MHA heads of 64 or 128 columns; LATENT: bf16 MLA rows of 512 + 64
 // columns, both on the matrix cores.
 enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2 };
-// Tiles, by the rows of a run: narrow where they fit it, wide ones of 128 rows; in between HEADS has
-// one of 64 rows (pairs).
+// Tiles of rows. HEADS: narrow 32, pairs 64, wide 128 rows; LATENT: narrow 16, wide 128; PLAIN: narrow 4.
 enum TileClass { TILE_WIDE = 0, TILE_PAIRS = 1, TILE_NARROW = 2 };
-constexpr int kWideRows = 128, kPairRows = 64;
-constexpr int narrow_rows(int kernel) { return kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32; }
-constexpr int tile_class(int kernel, int64_t rows) {
-  return kernel == ATTEND_PLAIN || rows <= narrow_rows(kernel) ? TILE_NARROW
-         : kernel == ATTEND_HEADS && rows <= kPairRows         ? TILE_PAIRS
-                                                               : TILE_WIDE;
-}
-constexpr int tile_rows(int kernel, int64_t rows) {
-  const int c = tile_class(kernel, rows);
-  return c == TILE_NARROW ? narrow_rows(kernel) : c == TILE_PAIRS ? kPairRows : kWideRows;
+constexpr int tile_rows(int kernel, int tile) {
+  return tile == TILE_WIDE ? 128 : tile == TILE_PAIRS ? 64 : kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32;
 }
 
 constexpr int kMaxSplits = 512;  // ranges a run's keys are cut into, at most
-constexpr int kJoinByWave = 8;   // parts up to which a wave joins a row, rather than a workgroup
+// A wave joins a row where rows abound (2048 rows of 10 parts: 7.6 us, 9.3 us by workgroups; 1024 rows of
+// 11: 6.7 us and 6.0) or parts are few, a workgroup otherwise.
+constexpr bool join_by_wave(int64_t rows, int parts) { return parts <= 8 || (parts <= 64 && rows >= 2048); }
 
 // One attention launch: what kamera_step_attend was given.
 struct AttendIo {

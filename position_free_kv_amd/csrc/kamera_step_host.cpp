@@ -241,19 +241,25 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
+  const bool plain = kernel == ATTEND_PLAIN;
+  const int64_t gran = plain ? 32 : 128, slots = plain ? 2048 : kernel == ATTEND_LATENT ? 256 : 512;
+  // Tiles: the smallest that a run's rows fit, wide ones where they fit none.
+  for (AttendRun& r : w.runs) {
+    const int64_t rows = (int64_t)r.ntok * G;
+    if (plain || rows <= tile_rows(kernel, TILE_NARROW)) r.tile = TILE_NARROW;
+    else r.tile = kernel == ATTEND_HEADS && rows <= tile_rows(kernel, TILE_PAIRS) ? TILE_PAIRS : TILE_WIDE;
+  }
   // Keys per item (a multiple of gran), for each class of tiles: the least estimate of the launch's
   // time. All classes share `slots` places; a class whose items are alike takes whole rounds of them
   // (8 heads of a 131072-key prefix in 69 ranges, 552 workgroups on 512 places: 137 us; in 64: 109 us).
-  const bool plain = kernel == ATTEND_PLAIN;
-  const int64_t gran = plain ? 32 : 128, slots = plain ? 2048 : kernel == ATTEND_LATENT ? 256 : 512;
   struct Class {
     int64_t longest = 0;
     double tiles = 0, keys = 0;
   } cls[3];
   for (const AttendRun& r : w.runs) {
     const int64_t rows = (int64_t)r.ntok * G;
-    Class& c = cls[tile_class(kernel, rows)];
-    const double tiles = (double)ceil_div(rows, tile_rows(kernel, rows));
+    Class& c = cls[r.tile];
+    const double tiles = (double)ceil_div(rows, tile_rows(kernel, r.tile));
     c.longest = std::max<int64_t>(c.longest, r.kv);
     c.tiles += tiles;
     c.keys += tiles * r.kv;
@@ -270,8 +276,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       double items = 0, parts = 0;
       for (const AttendRun& r : w.runs) {
         const int64_t rows = (int64_t)r.ntok * G, n = ceil_div(r.kv, chunk);
-        if (tile_class(kernel, rows) != k) continue;
-        items += (double)ceil_div(rows, tile_rows(kernel, rows)) * n;
+        if (r.tile != k) continue;
+        items += (double)ceil_div(rows, tile_rows(kernel, k)) * n;
         if (n > 1 || !r.direct) parts += (double)rows * n;
       }
       items *= h.heads;
@@ -298,8 +304,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     for (size_t k = 0; k < w.runs.size(); ++k) {
       AttendRun& r = w.runs[k];
       const int64_t rows = (int64_t)r.ntok * G;
-      const int tile = tile_rows(kernel, rows);
-      if (tile_class(kernel, rows) != c) continue;
+      const int tile = tile_rows(kernel, c);
+      if (r.tile != c) continue;
       const int64_t splits = ceil_div(r.kv, chunk_of[c]);
       const int64_t chunk = (int64_t)round_up((size_t)ceil_div(r.kv, splits), (size_t)gran);
       const int64_t n = ceil_div(r.kv, chunk);
@@ -360,7 +366,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 
 // ------------------------------------------------------------------ workspace
 struct Offsets {
-  size_t pages, items, tok, merge, slots, pos, upload, phase, ml, o, total;
+  size_t pages, items, tok, merge, slots, pos, theta, upload, phase, ml, o, total;
 };
 Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Work& w) {
   Offsets f;
@@ -378,6 +384,7 @@ Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, con
   f.merge = take(w.merge.size() * sizeof(MergeToken));
   f.slots = take(append ? (size_t)n.tokens * 8 : 0);
   f.pos = take(append && !s->positions ? (size_t)n.tokens * 4 : 0);
+  f.theta = take(append ? (size_t)h.d_rot / 2 * 8 : 0);
   f.upload = at;
   f.phase = take(append ? (size_t)n.tokens * h.d_rot * 4 : 0);
   f.ml = take((size_t)w.part_rows * 8);
@@ -504,6 +511,8 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
         if (!s->positions) pos[t] = (int32_t)(r.position0 + own);
       }
     }
+    double* theta = reinterpret_cast<double*>(blob.data() + f.theta);
+    for (int i = 0; i < h.d_rot / 2; ++i) theta[i] = std::pow(L->rope_base, -2.0 * i / h.d_rot);
   }
 
   StepArgs a;
@@ -523,7 +532,7 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   a.phase = reinterpret_cast<float*>(base + f.phase);
   a.pos = s->positions ? nullptr : reinterpret_cast<const int32_t*>(base + f.pos);
   a.positions = s->positions;
-  a.rope_base = L->rope_base;
+  a.theta = reinterpret_cast<const double*>(base + f.theta);
   a.family = L->family;
   a.dtype = L->dtype;
   a.pairing = L->pairing;

@@ -80,9 +80,9 @@ hipError_t launch_step_attend(const StepArgs& a, int, const void*, int64_t, void
     const AttendItem& it = a.items[i];
     const AttendRun& run = it.run;
     const int64_t rows = (int64_t)run.ntok * a.group;
-    const int tile = tile_rows(a.kernel, rows);
+    const int tile = tile_rows(a.kernel, run.tile);
     const int cls = i < a.num_wide ? TILE_WIDE : i < a.num_wide + a.num_pairs ? TILE_PAIRS : TILE_NARROW;
-    CHECK(tile_class(a.kernel, rows) == cls);
+    CHECK(run.tile == cls);
     CHECK(it.row0 >= 0 && it.row0 < rows && it.kv0 >= 0 && it.kv1 <= run.kv && it.split < run.splits);
     for (int64_t row = it.row0; row < std::min<int64_t>(it.row0 + tile, rows); ++row) {
       const int64_t j = row / a.group, g = row % a.group;
