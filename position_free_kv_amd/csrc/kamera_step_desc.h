@@ -126,13 +126,17 @@ struct CopyArgs {
   char* pool[2];
   int64_t layer_bytes;      // between layers
   int64_t page_bytes;
-  const int32_t* chain;     // [chains + 1] first copy of each chain
-  const PageCopy* copies;
+  const int32_t* chain;     // [chains + 1] first copy of each chain; NULL: each copy is a chain of its own
+  const PageCopy* copies;   // NULL: they travel as the kernel's argument
   int32_t chains, layers, tensors, unit;  // unit: bytes per access (16, 4 or 2)
+  // After the chains: rings, lists of kLongChain or more copies in which each copy reads the page that
+  // the next one writes (the last one possibly what the first writes), and no page is read twice.
+  int32_t rings;
 };
+constexpr int kLongChain = 64;
 constexpr int kInlineCopies = 400;
 struct InlineCopies {
-  PageCopy c[kInlineCopies];  // independent copies: chain i is copy i
+  PageCopy c[kInlineCopies];
 };
 hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStream_t stream);
 

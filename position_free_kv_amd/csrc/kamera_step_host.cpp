@@ -598,15 +598,18 @@ kamera_status check_rows(const char* what, const void* p, int64_t& stride, int64
 struct CopyPlan {
   std::vector<int32_t> chain;
   std::vector<PageCopy> copies;
+  int32_t rings = 0;        // the last chains: see CopyArgs
   bool independent = true;  // every chain is one copy
 };
 
 // Orders the copies so that each page is read for the last time before it is written. A copy
 // whose pages no other copy writes or reads stands alone; the others form groups joined by
-// the pages they share, each carried out in order, a cycle through a saved page.
+// the pages they share, each carried out in order, a cycle through a saved page. A long group in which
+// each page is read once (one path or one cycle) is left in the order of its pages as a ring.
 void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num_pages, CopyPlan& out) {
   out.chain.clear();
   out.copies.clear();
+  out.rings = 0;
   out.independent = true;
   std::vector<int32_t> by_dst((size_t)num_pages, -1), readers((size_t)num_pages, 0);
   std::vector<int32_t> todo;
@@ -638,7 +641,13 @@ void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num
     for (int32_t i : bound)
       if (by_dst[(size_t)src[i]] >= 0) up[(size_t)root(i)] = root(by_dst[(size_t)src[i]]);
     std::vector<std::vector<PageCopy>> group((size_t)n);
-    std::vector<uint8_t> done((size_t)n, 0);
+    std::vector<uint8_t> done((size_t)n, 0), single((size_t)n, 1);  // single: each page of the group is read once
+    std::vector<int32_t> size((size_t)n, 0);
+    for (int32_t i : bound) {
+      ++size[(size_t)root(i)];
+      if (readers[(size_t)src[i]] > 1) single[(size_t)root(i)] = 0;
+    }
+    auto ring = [&](int32_t i) { return single[(size_t)root(i)] && size[(size_t)root(i)] >= kLongChain; };
     for (int32_t i : bound)  // from pages nobody reads: write, then the page read becomes free to be written
       for (int32_t j = i; j >= 0 && !done[(size_t)j] && readers[(size_t)dst[j]] == 0;) {
         done[(size_t)j] = 1;
@@ -648,17 +657,20 @@ void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num
     for (int32_t i : bound) {  // what is left are cycles
       if (done[(size_t)i]) continue;
       std::vector<PageCopy>& g = group[(size_t)root(i)];
-      g.push_back(PageCopy{dst[i], -1});  // keep the page written first
+      if (!ring(i)) g.push_back(PageCopy{dst[i], -1});  // keep the page written first
       for (int32_t j = i; !done[(size_t)j]; j = by_dst[(size_t)src[j]]) {
         done[(size_t)j] = 1;
-        g.push_back(PageCopy{src[j] == dst[i] ? -1 : src[j], dst[j]});
+        g.push_back(PageCopy{src[j] == dst[i] && !ring(i) ? -1 : src[j], dst[j]});
       }
     }
-    for (const std::vector<PageCopy>& g : group) {
-      if (g.empty()) continue;
-      out.chain.push_back((int32_t)out.copies.size());
-      out.copies.insert(out.copies.end(), g.begin(), g.end());
-    }
+    for (int rings = 0; rings < 2; ++rings)
+      for (int32_t i = 0; i < n; ++i) {
+        const std::vector<PageCopy>& g = group[(size_t)i];
+        if (g.empty() || ring(i) != (rings == 1)) continue;
+        out.chain.push_back((int32_t)out.copies.size());
+        out.copies.insert(out.copies.end(), g.begin(), g.end());
+        out.rings += rings;
+      }
   }
   out.chain.push_back((int32_t)out.copies.size());
 }
@@ -682,7 +694,8 @@ kamera_status enqueue_copies(const kamera_layout* L, const kamera_pool* pool, co
   a.layers = L->num_layers;
   a.page_bytes = (int64_t)L->page_size * row_width(L) * (int64_t)es;
   a.layer_bytes = pool->layer_stride ? pool->layer_stride * (int64_t)es : (int64_t)pool->num_pages * a.page_bytes;
-  a.chains = (int32_t)p.chain.size() - 1;
+  a.chains = (int32_t)p.chain.size() - 1 - p.rings;
+  a.rings = p.rings;
   auto fits = [&](int unit) {
     return a.page_bytes % unit == 0 && a.layer_bytes % unit == 0 && aligned(a.pool[0], (size_t)unit) &&
            (a.tensors == 1 || aligned(a.pool[1], (size_t)unit));
@@ -702,7 +715,7 @@ kamera_status enqueue_copies(const kamera_layout* L, const kamera_pool* pool, co
     std::memcpy(blob.data() + at, p.copies.data(), p.copies.size() * sizeof(PageCopy));
     const kamera_status st = host_stage(blob.data(), bytes, ws, stream);
     if (st != KAMERA_OK) return st;
-    a.chain = static_cast<const int32_t*>(ws);
+    a.chain = p.independent ? nullptr : static_cast<const int32_t*>(ws);
     a.copies = reinterpret_cast<const PageCopy*>(static_cast<char*>(ws) + at);
     e = launch_copy_pages(a, nullptr, stream);
   }

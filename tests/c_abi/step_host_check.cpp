@@ -145,13 +145,23 @@ hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* in, hipStrea
       char* base = a.pool[tensor] + layer * a.layer_bytes;
       for (int chain = a.chains - 1; chain >= 0; --chain) {  // chains do not depend on each other's order
         std::vector<char> kept((size_t)a.page_bytes), x((size_t)a.page_bytes);
-        const int c0 = in ? chain : a.chain[chain], c1 = in ? chain + 1 : a.chain[chain + 1];
+        const int c0 = a.chain ? a.chain[chain] : chain, c1 = a.chain ? a.chain[chain + 1] : chain + 1;
+        CHECK(!(in && a.chain));
         for (int c = c0; c < c1; ++c) {
           const PageCopy p = in ? in->c[c] : a.copies[c];
           if (p.src < 0) x = kept;
           else std::memcpy(x.data(), base + p.src * a.page_bytes, (size_t)a.page_bytes);
           if (p.dst < 0) kept = x;
           else std::memcpy(base + p.dst * a.page_bytes, x.data(), (size_t)a.page_bytes);
+        }
+      }
+      for (int ring = a.chains; ring < a.chains + a.rings; ++ring) {  // as a list, the first page written kept for the last
+        const int c0 = a.chain[ring], c1 = a.chain[ring + 1];
+        CHECK(c1 - c0 >= kLongChain);
+        std::vector<char> last(base + a.copies[c1 - 1].src * a.page_bytes, base + (a.copies[c1 - 1].src + 1) * a.page_bytes);
+        for (int c = c0; c < c1; ++c) {
+          CHECK(a.copies[c].src >= 0 && a.copies[c].dst >= 0 && (c + 1 == c1 || a.copies[c].src == a.copies[c + 1].dst));
+          std::memcpy(base + a.copies[c].dst * a.page_bytes, c + 1 == c1 ? last.data() : base + a.copies[c].src * a.page_bytes, (size_t)a.page_bytes);
         }
       }
     }

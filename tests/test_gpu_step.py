@@ -442,6 +442,21 @@ def test_copy_pages_random(seed):
     check_copies(src, rng.permutation(pages)[:n], family=GQA, dtype=BF16, layers=2, pages=pages, page=4, kv_heads=1, head_dim=16)
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 79, 80, 81, 127, 255, 256, 257, 300, 900])
+@pytest.mark.parametrize("closed", [False, True])
+def test_copy_pages_long_paths_and_cycles(n, closed):
+    """Paths and cycles around the length from which they are shared out, alone and beside other copies."""
+    order = np.random.default_rng(n).permutation(1000)
+    ring = order[:n]
+    src, dst = (np.roll(ring, -1), ring) if closed else (ring[1:], ring[:-1])
+    for more in (0, 5):
+        s, d = np.concatenate([src, order[n:n + more]]), np.concatenate([dst, order[n + more:n + 2 * more]])
+        check_copies(s, d, family=GQA, dtype=BF16, layers=2, pages=1000, page=4, kv_heads=1, head_dim=16 if n % 2 else 10)
+    if not closed:  # a page of the path read twice: no ring any more
+        s, d = np.concatenate([src, src[5:6]]), np.concatenate([dst, order[-1:]])
+        check_copies(s, d, family=MLA, dtype=F32, layers=2, pages=1000, page=3)
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_compact_pages(seed):
     rng = np.random.default_rng(seed)
