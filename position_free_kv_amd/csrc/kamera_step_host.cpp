@@ -607,21 +607,27 @@ struct CopyPlan {
 // the pages they share, each carried out in order, a cycle through a saved page. A long group in which
 // each page is read once (one path or one cycle) is left in the order of its pages as a ring.
 void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num_pages, CopyPlan& out) {
+  thread_local std::vector<int32_t> by_dst, readers, bound, up, size, start;
+  thread_local std::vector<uint8_t> done, single;
+  struct Entry {
+    int32_t group;
+    PageCopy copy;
+  };
+  thread_local std::vector<Entry> order;
   out.chain.clear();
   out.copies.clear();
   out.rings = 0;
   out.independent = true;
-  std::vector<int32_t> by_dst((size_t)num_pages, -1), readers((size_t)num_pages, 0);
-  std::vector<int32_t> todo;
-  todo.reserve((size_t)n);
+  by_dst.assign((size_t)num_pages, -1);
+  readers.assign((size_t)num_pages, 0);
   for (int32_t i = 0; i < n; ++i) {
     if (src[i] == dst[i]) continue;
     by_dst[(size_t)dst[i]] = i;
     ++readers[(size_t)src[i]];
-    todo.push_back(i);
   }
-  std::vector<int32_t> bound;  // copies that share a page with another's destination
-  for (int32_t i : todo) {
+  bound.clear();  // copies that share a page with another's destination
+  for (int32_t i = 0; i < n; ++i) {
+    if (src[i] == dst[i]) continue;
     if (readers[(size_t)dst[i]] == 0 && by_dst[(size_t)src[i]] < 0) {
       out.chain.push_back((int32_t)out.copies.size());
       out.copies.push_back(PageCopy{src[i], dst[i]});
@@ -632,7 +638,7 @@ void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num
   if (!bound.empty()) {
     out.independent = false;
     // groups: copies connected through a page that one writes and another reads
-    std::vector<int32_t> up((size_t)n);
+    up.resize((size_t)n);
     for (int32_t i = 0; i < n; ++i) up[(size_t)i] = i;
     auto root = [&](int32_t i) {
       while (up[(size_t)i] != i) i = up[(size_t)i] = up[(size_t)up[(size_t)i]];
@@ -640,37 +646,48 @@ void order_copies(const int32_t* src, const int32_t* dst, int32_t n, int32_t num
     };
     for (int32_t i : bound)
       if (by_dst[(size_t)src[i]] >= 0) up[(size_t)root(i)] = root(by_dst[(size_t)src[i]]);
-    std::vector<std::vector<PageCopy>> group((size_t)n);
-    std::vector<uint8_t> done((size_t)n, 0), single((size_t)n, 1);  // single: each page of the group is read once
-    std::vector<int32_t> size((size_t)n, 0);
+    done.assign((size_t)n, 0);
+    single.assign((size_t)n, 1);  // each page of the group is read once (and, below, there are enough of them)
+    size.assign((size_t)n, 0);    // its copies
     for (int32_t i : bound) {
-      ++size[(size_t)root(i)];
-      if (readers[(size_t)src[i]] > 1) single[(size_t)root(i)] = 0;
+      const int32_t g = root(i);
+      ++size[(size_t)g];
+      if (readers[(size_t)src[i]] > 1) single[(size_t)g] = 0;
     }
-    auto ring = [&](int32_t i) { return single[(size_t)root(i)] && size[(size_t)root(i)] >= kLongChain; };
+    for (int32_t g = 0; g < n; ++g) single[(size_t)g] = single[(size_t)g] && size[(size_t)g] >= kLongChain;
+    auto ring = [&](int32_t g) { return single[(size_t)g] != 0; };
+    order.clear();
     for (int32_t i : bound)  // from pages nobody reads: write, then the page read becomes free to be written
       for (int32_t j = i; j >= 0 && !done[(size_t)j] && readers[(size_t)dst[j]] == 0;) {
         done[(size_t)j] = 1;
-        group[(size_t)root(j)].push_back(PageCopy{src[j], dst[j]});
+        order.push_back(Entry{root(j), PageCopy{src[j], dst[j]}});
         j = --readers[(size_t)src[j]] == 0 ? by_dst[(size_t)src[j]] : -1;
       }
     for (int32_t i : bound) {  // what is left are cycles
       if (done[(size_t)i]) continue;
-      std::vector<PageCopy>& g = group[(size_t)root(i)];
-      if (!ring(i)) g.push_back(PageCopy{dst[i], -1});  // keep the page written first
+      const int32_t g = root(i);
+      if (!ring(g)) {
+        order.push_back(Entry{g, PageCopy{dst[i], -1}});  // keep the page written first
+        ++size[(size_t)g];
+      }
       for (int32_t j = i; !done[(size_t)j]; j = by_dst[(size_t)src[j]]) {
         done[(size_t)j] = 1;
-        g.push_back(PageCopy{src[j] == dst[i] && !ring(i) ? -1 : src[j], dst[j]});
+        order.push_back(Entry{g, PageCopy{src[j] == dst[i] && !ring(g) ? -1 : src[j], dst[j]}});
       }
     }
+    // group after group, the rings last
+    start.assign((size_t)n, 0);
+    int32_t at = (int32_t)out.copies.size();
     for (int rings = 0; rings < 2; ++rings)
-      for (int32_t i = 0; i < n; ++i) {
-        const std::vector<PageCopy>& g = group[(size_t)i];
-        if (g.empty() || ring(i) != (rings == 1)) continue;
-        out.chain.push_back((int32_t)out.copies.size());
-        out.copies.insert(out.copies.end(), g.begin(), g.end());
+      for (int32_t g = 0; g < n; ++g) {
+        if (size[(size_t)g] == 0 || ring(g) != (rings == 1)) continue;
+        out.chain.push_back(at);
+        start[(size_t)g] = at;
+        at += size[(size_t)g];
         out.rings += rings;
       }
+    out.copies.resize((size_t)at);
+    for (const Entry& e : order) out.copies[(size_t)start[(size_t)e.group]++] = e.copy;
   }
   out.chain.push_back((int32_t)out.copies.size());
 }

@@ -260,7 +260,7 @@ void one_step(Rng& r) {
   }
 }
 
-void one_copy(Rng& r) {
+void one_copy(Rng& r, int exactly = 0) {
   kamera_layout L;
   std::memset(&L, 0, sizeof(L));
   L.family = KAMERA_GQA;
@@ -269,14 +269,14 @@ void one_copy(Rng& r) {
   L.num_kv_heads = 1;
   L.head_dim = 2;
   L.page_size = 2;
-  const int n = (int)draw(r, 1, draw(r, 0, 1) ? 12 : 1500), copies = (int)draw(r, 0, n);
+  const int n = exactly ? exactly : (int)draw(r, 1, draw(r, 0, 1) ? 12 : 1500), copies = exactly ? n : (int)draw(r, 0, n);
   std::vector<int32_t> src((size_t)n), dst((size_t)n);
   for (int i = 0; i < n; ++i) src[(size_t)i] = dst[(size_t)i] = i;
   std::shuffle(dst.begin(), dst.end(), r);
   std::shuffle(src.begin(), src.end(), r);
   if (draw(r, 0, 1))
     for (int32_t& x : src) x = (int32_t)draw(r, 0, n - 1);
-  if (draw(r, 0, 2) == 0)  // long chains
+  if (exactly || draw(r, 0, 2) == 0)  // long chains
     for (int i = 0; i < n; ++i) src[(size_t)i] = (dst[(size_t)i] + 1) % n;
   std::vector<float> k((size_t)(2 * n * 4)), v(k.size());
   for (float& x : k) x = (float)draw(r, 0, 1 << 20);
@@ -304,6 +304,7 @@ int main() {
   Rng r(12345);
   for (int i = 0; i < 150; ++i) one_step(r);
   for (int i = 0; i < 300; ++i) one_copy(r);
+  for (int n = kLongChain - 3; n < kLongChain + 3; ++n) one_copy(r, n);  // one cycle
   std::printf("ok\n");
   return 0;
 }
