@@ -685,22 +685,30 @@ __global__ __launch_bounds__(kThreads) void copy_rings(CopyArgs a) {
   const int ring = a.chains + (int)(b % a.rings);
   b /= a.rings;
   const int layer = (int)(b % a.layers), tensor = (int)(b / a.layers);
+  const KGLOBAL int32_t* copies = (const KGLOBAL int32_t*)a.copies;  // source, destination, source, ...
   const int r0 = a.chain[ring], n = a.chain[ring + 1] - r0, each = (n + kSegments - 1) / kSegments;
   const int c0 = r0 + min((int)(threadIdx.x / kColumns) * each, n), c1 = min(c0 + each, r0 + n);
-  U* base = (U*)(a.pool[tensor] + layer * a.layer_bytes) + col;
+  KGLOBAL U* base = (KGLOBAL U*)(a.pool[tensor] + layer * a.layer_bytes) + col;
   const bool mine = col < cols && c0 < c1;
-  U last = {};
-  if (mine) last = base[a.copies[c1 - 1].src * cols];
-  __syncthreads();  // (waits for the reads)
+  U last = {}, x[kBatch] = {};
+  auto read = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (c + i < c1 - 1) x[i] = base[copies[2 * (c + i)] * cols];
+  };
+  if (mine) {
+    last = base[copies[2 * (c1 - 1)] * cols];
+    read(c0);  // (the first batch's as well)
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
   if (!mine) return;
-  for (int c = c0; c < c1; c += kBatch) {
-    U x[kBatch];
+  for (int c = c0;;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (c + i < c1 - 1) x[i] = base[a.copies[c + i].src * cols];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (c + i < c1) base[a.copies[c + i].dst * cols] = c + i == c1 - 1 ? last : x[i];
+      if (c + i < c1) base[copies[2 * (c + i) + 1] * cols] = c + i == c1 - 1 ? last : x[i];
+    if ((c += kBatch) >= c1) break;
+    read(c);
   }
 }
 
