@@ -65,6 +65,10 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
                                           KLDS char* r0, KLDS char* r1) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int PER = kKeys / kWideWaves;  // rows a wave brings in
+  const int first = wave * PER, last = it.kv1 - 1;
+  LatentRows rows;  // (asked for ahead of the queries, as loads return in order)
+  if (it.kv1 > it.kv0) rows.find(a, run, it.kv0, first, PER, last);
   const Lane r = lane_row(a, it, 0, it.row0 + wave * 16 + (lane & 15));
   const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
   bf16x8 q[LatentState::kKSteps];
@@ -72,11 +76,7 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
   LatentState st;
   st.clear();
   const uint16_t* kp = a.k_pool + io.layer0;
-  constexpr int PER = kKeys / kWideWaves;  // rows a wave brings in
-  const int first = wave * PER, last = it.kv1 - 1;
   if (it.kv1 > it.kv0) {
-    LatentRows rows;
-    rows.find(a, run, it.kv0, first, PER, last);
     rows.load<PER>(a, kp, k0, r0, first);
     rows.find(a, run, it.kv0 + kKeys, first, PER, last);
     for (int t = it.kv0;;) {
@@ -110,6 +110,10 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
                                             KLDS char* place0, KLDS char* place1, float (&ml)[2][kWaves][64]) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int last = it.kv1 - 1;
+  int t = it.kv0 + wave * kKeys;
+  LatentRows rows;  // (as in the wide tile)
+  if (t < it.kv1) rows.find(a, run, t, 0, kKeys, last);
   const Lane r = lane_row(a, it, 0, it.row0 + (lane & 15));
   const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 15);
   bf16x8 q[LatentState::kKSteps];
@@ -117,11 +121,7 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   LatentState st;
   st.clear();
   const uint16_t* kp = a.k_pool + io.layer0;
-  const int last = it.kv1 - 1;
-  int t = it.kv0 + wave * kKeys;
   if (t < it.kv1) {
-    LatentRows rows;
-    rows.find(a, run, t, 0, kKeys, last);
     for (; t < it.kv1; t += kWaves * kKeys) {
       rows.load<kKeys>(a, kp, mine, band, 0);
       rows.find(a, run, t + kWaves * kKeys, 0, kKeys, last);

@@ -452,10 +452,12 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
 // Join of partial results: TPR threads (a wave, or a workgroup where a row has many parts) for each
 // (token, query head). First every part's maximum and sum become its weight, all parts at once; then
 // the weighted rows are added, 16 bytes a thread, several parts side by side where a row is shorter
-// than the threads. Parts are taken in a fixed order, so the result does not depend on which
+// than the threads; rows of more than 256 columns are shared by workgroups, which fills the chip where
+// rows are few (512 MLA rows of 36 parts: 12.9 us with one workgroup a row, 9.7 with two). Parts are taken in a fixed order, so the result does not depend on which
 // workgroup finished first.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
+constexpr int kJoinQuads = kWave;  // quads of columns a workgroup takes (grid.y): a wave's parts side by side
 
 struct Parts {
   MergeToken mt;
@@ -516,37 +518,34 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
   }
   sum = over_threads<TPR, false>(sum, red[sub]);
   __syncthreads();
-  const int quads = a.dv / 4;
+  const int quads = a.dv / 4, c0 = blockIdx.y * kJoinQuads, wide = min(quads - c0, kJoinQuads);
   T* out = (T*)io.out + (int64_t)a.merge[i].token * io.out_stride + (int64_t)qh * a.dv;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const KGLOBAL f32x4* rows = (const KGLOBAL f32x4*)a.part_o;
-  // side by side: `side` parts, `quads` threads each; rows longer than the threads in turns
-  const int side = quads < TPR ? TPR / quads : 1, lane = quads < TPR ? tid % quads : tid, first = quads < TPR ? tid / quads : 0;
-  for (int c = lane; c < quads; c += TPR) {
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (first < side) {
+  const int side = TPR / wide, first = tid / wide, c = c0 + tid % wide;  // `side` parts at a time, `wide` threads each
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (first < side) {
 #pragma unroll 8
-      for (int k = first; k < n; k += side) {
-        const float w = weight[sub][k];
-        const f32x4 x = rows[p.row(k) * quads + c];
-        if (w != 0.0f)  // (an empty part's row may hold anything)
-          for (int e = 0; e < 4; ++e) o[e] += x[e] * w;
-      }
+    for (int k = first; k < n; k += side) {
+      const float w = weight[sub][k];
+      const f32x4 x = rows[p.row(k) * quads + c];
+      if (w != 0.0f)  // (an empty part's row may hold anything)
+        for (int e = 0; e < 4; ++e) o[e] += x[e] * w;
     }
-    if (side > 1) {  // (one turn only: every thread is here)
-      held[sub][tid] = o;
-      if (TPR == kWave) __builtin_amdgcn_wave_barrier();
-      else __syncthreads();
-      if (first == 0)
-        for (int s = 1; s < side; ++s) {
-          const f32x4 x = held[sub][s * quads + c];
-          for (int e = 0; e < 4; ++e) o[e] += x[e];
-        }
-    }
-    if (live && first == 0)
-      for (int e = 0; e < 4; ++e) out[4 * c + e] = from_float<T>(o[e] * inv);
   }
-  if (live && io.lse && tid == 0)
+  if (side > 1) {
+    held[sub][tid] = o;
+    if (TPR == kWave) __builtin_amdgcn_wave_barrier();
+    else __syncthreads();
+    if (first == 0)
+      for (int s = 1; s < side; ++s) {
+        const f32x4 x = held[sub][s * wide + tid];
+        for (int e = 0; e < 4; ++e) o[e] += x[e];
+      }
+  }
+  if (live && first == 0)
+    for (int e = 0; e < 4; ++e) out[4 * c + e] = from_float<T>(o[e] * inv);
+  if (live && io.lse && tid == 0 && blockIdx.y == 0)
     io.lse[(int64_t)a.merge[i].token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
@@ -743,10 +742,11 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
   if (rows == 0) return hipSuccess;
   const dim3 b(kThreads);
   const unsigned by_wave = (unsigned)ceil_div(rows, kThreads / kWave);
+  const unsigned blocks = (unsigned)ceil_div(a.dv / 4, kJoinQuads);
   if (a.dv % 4) hipLaunchKernelGGL((attend_join_any<T>), dim3(by_wave), b, 0, stream, a, io);
   else if (a.max_parts <= kFewParts) hipLaunchKernelGGL((attend_join_few<T>), dim3((unsigned)ceil_div(rows * (a.dv / 4), kThreads)), b, 0, stream, a, io);
-  else if (join_by_wave(rows, a.max_parts)) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave), b, 0, stream, a, io);
-  else hipLaunchKernelGGL((attend_join<T, kThreads>), dim3((unsigned)rows), b, 0, stream, a, io);
+  else if (join_by_wave(rows, a.max_parts)) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave, blocks), b, 0, stream, a, io);
+  else hipLaunchKernelGGL((attend_join<T, kThreads>), dim3((unsigned)rows, blocks), b, 0, stream, a, io);
   return hipGetLastError();
 }
 
