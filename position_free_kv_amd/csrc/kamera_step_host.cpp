@@ -128,9 +128,12 @@ kamera_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 // ------------------------------------------------------------------ attention work list
-// A request whose rows alone fill a tile gains nothing from sharing its prefix's reads: it
-// reads the prefix and its own tokens as one sequence, and its result needs no joining.
-constexpr int64_t kShareRows = 64;
+// A request whose rows alone fill a tile gains little from sharing its prefix's reads: it reads the
+// prefix and its own tokens as one sequence, and its result needs no joining. (32 requests over an
+// 8192-token prefix, 2 layers, us shared and alone. 28 + 4 heads: 28 rows a KV head 79 and 94, 84 rows
+// 147 and 178, 119 rows 205 and 188. MLA, 16 heads: 32 rows 131 and 188, 64 rows 170 and 199, 128 rows
+// 249 and 220.)
+constexpr int64_t kShareRows = 96;
 
 // What the choice of an item's length goes by, measured: the time of a workgroup around its keys (its
 // item, page ids, rows and queries are read one after the other, its results joined and written), of
