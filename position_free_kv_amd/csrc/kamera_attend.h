@@ -322,8 +322,8 @@ struct State {
     }
   }
 
-  // weights of 32 keys from their scores: rounded to bf16 for the product (2^-9 of each on average, at most
-  // 2^-8), as the matrix cores take them at eight times fp32's rate; their sum is that of the unrounded ones
+  // weights of 32 keys from their scores: rounded to bf16 for the product (off by at most 2^-8 of each), as
+  // the matrix cores take them; their sum is that of the unrounded ones, in fp32
   __device__ __forceinline__ void weigh(bf16x8 (&p)[kPSteps], const Acc (&s)[kTiles], float scale2, float base) {
     float sum = 0.0f;
 #pragma unroll
