@@ -136,6 +136,26 @@ def test_attend_tiles_of_every_size_over_long_prefixes(heads, dim, family, membe
     c.check_attend(scale_of(c))
 
 
+@pytest.mark.parametrize("latent,rope", [(260, 4), (300, 8), (512, 64), (516, 4), (1000, 24)])
+@pytest.mark.parametrize("tokens", [150, 400, 900, 6000])
+def test_attend_joins_rows_wider_than_a_workgroups_share(latent, rope, tokens):
+    """Rows of 65 to 250 pieces of 16 bytes, joined from few parts and from many."""
+    for dtype in (BF16, F32):
+        c = Case(family=MLA, dtype=dtype, heads=3, latent=latent, rope=rope, layers=1, prefixes=[tokens, tokens // 2], seed=latent + tokens,
+                 requests=[(0, 1, 1), (0, tokens, 1), (1, 5, 1), (-1, tokens + 1, 2)])
+        c.check_attend(scale_of(c))
+
+
+@pytest.mark.parametrize("heads,queries", [(8, 11), (8, 12), (5, 19), (5, 20), (97, 1)])
+@pytest.mark.parametrize("family", [GQA, MLA])
+def test_attend_rows_around_the_limit_of_sharing(heads, queries, family):
+    """Requests that just share their prefix's reads beside ones that just do not."""
+    more = dict(heads=heads, kv_heads=1, head_dim=128) if family == GQA else dict(family=MLA, heads=heads, latent=512, rope=64)
+    c = Case(layers=1, prefixes=[1500], seed=heads + queries, **more,
+             requests=[(0, queries, queries), (0, queries + 40, queries), (0, queries + 3, queries + 1), (0, 200, max(queries - 1, 1))])
+    c.check_attend(scale_of(c))
+
+
 @pytest.mark.parametrize("dim,dtype", [(128, BF16), (64, F32), (10, BF16)])
 def test_attend_scores_of_every_size(dim, dtype):
     """Scores of thousands, equal scores, scores of the type's lowest value."""
