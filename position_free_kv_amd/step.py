@@ -98,24 +98,51 @@ def _stream(stream) -> Optional[int]:
 
 
 def _tables(block_tables, n: int):
-    """Host int32 tables, one a request: a 2-D array (a row each) or a sequence of arrays. Returns
-    (addresses, objects to keep alive)."""
+    """Host int32 tables, one a request: a 2-D array (a row each) or a sequence of arrays (None: no table).
+    Returns (addresses, entries, objects to keep alive)."""
     if isinstance(block_tables, np.ndarray) and block_tables.ndim == 2:
         if block_tables.dtype != np.int32 or not block_tables.flags.c_contiguous:
             block_tables = np.ascontiguousarray(block_tables, dtype=np.int32)
         if block_tables.shape[0] != n:
             raise ValueError(f"{block_tables.shape[0]} block tables for {n} requests")
-        return block_tables.ctypes.data + np.arange(n, dtype=np.uint64) * np.uint64(block_tables.strides[0]), block_tables
-    keep = [np.zeros(1, np.int32) if t is None else np.ascontiguousarray(t, dtype=np.int32) for t in block_tables]
+        return (block_tables.ctypes.data + np.arange(n, dtype=np.uint64) * np.uint64(block_tables.strides[0]),
+                np.full(n, block_tables.shape[1], dtype=np.int64), block_tables)
+    keep = [None if t is None else np.ascontiguousarray(t, dtype=np.int32) for t in block_tables]
     if len(keep) != n:
         raise ValueError(f"{len(keep)} block tables for {n} requests")
-    return np.array([t.ctypes.data for t in keep], dtype=np.uint64), keep
+    return (np.array([0 if t is None else t.ctypes.data for t in keep], dtype=np.uint64),
+            np.array([0 if t is None else t.size for t in keep], dtype=np.int64), keep)
+
+
+class _Entries:
+    """How many tokens each record's table holds entries for. The library takes a table by its address alone and reads
+    what the tokens need, so a shorter one is refused here. Records that the library refuses before it reads any table
+    (no address, slot0 outside a page, tokens beyond 2^31 - 4096) are left to it."""
+
+    def __init__(self, what: str, records: np.ndarray, entries: np.ndarray):
+        self._what, self._records, self._entries = what, records, entries
+        self._slot0, self._tokens = records["slot0"], records["num_tokens"]
+        self._page_size, self._limit = 0, entries
+
+    def check(self, page_size: int) -> None:
+        if page_size != self._page_size:
+            self._page_size, self._limit = page_size, self._entries * max(page_size, 1)
+        # (a sum that wraps belongs to a record that the library refuses)
+        if not np.count_nonzero(self._slot0 + self._tokens > self._limit) or page_size < 1:
+            return
+        slot0, tokens = self._slot0.astype(np.int64), self._tokens.astype(np.int64)
+        short = (tokens > 0) & (slot0 + tokens > self._limit) & (slot0 + tokens < (1 << 31) - 4096)
+        short &= (self._records["block_table"] != 0) & (slot0 >= 0) & (slot0 < page_size)
+        for i in np.flatnonzero(short)[:1]:
+            raise ValueError(f"{self._what} {i}: {self._entries[i]} block table entries of {page_size} tokens "
+                             f"for {tokens[i]} tokens from slot {slot0[i]} on")
 
 
 class Step:
     """A kamera_step and the host arrays it points into.
 
-    block_tables: a 2-D int32 array or a sequence of 1-D ones, a row a request. The other
+    block_tables: a 2-D int32 array or a sequence of 1-D ones (None: a request without tokens of
+    its own), a row a request; a table is as long as slot0 + num_tokens needs at every upload. The other
     request fields are scalars or one value a request. prefixes: dicts with block_table,
     num_tokens and (optionally) slot0. `requests` is the structured array the library reads.
     """
@@ -123,7 +150,7 @@ class Step:
     def __init__(self, *, num_q_heads: int, block_tables, num_tokens, num_queries, slot0=0, prefix=-1,
                  prefixes: Sequence[dict] = (), position0=0, request_flags=0, positions=None, flags: int = APPEND | ATTEND):
         n = len(block_tables)
-        addresses, self._keep = _tables(block_tables, n)
+        addresses, entries, self._keep = _tables(block_tables, n)
         self.requests = np.zeros(n, _REQUEST)
         self.requests["block_table"] = addresses
         for name, value in (("slot0", slot0), ("num_tokens", num_tokens), ("num_queries", num_queries),
@@ -133,6 +160,9 @@ class Step:
         self.prefixes = np.zeros(len(prefixes), _PREFIX)
         for i, p in enumerate(prefixes):
             self.prefixes[i] = (self._prefix_tables[i].ctypes.data, p.get("slot0", 0), p["num_tokens"])
+        self._entries = [_Entries("request", self.requests, entries)] if n else []
+        if len(prefixes):
+            self._entries.append(_Entries("prefix", self.prefixes, np.array([t.size for t in self._prefix_tables], dtype=np.int64)))
         self._positions = positions
         self.c = StepDesc(self.requests.ctypes.data if n else None, self.prefixes.ctypes.data if len(prefixes) else None,
                           _ptr(positions), n, len(prefixes), int(num_q_heads), int(flags))
@@ -145,6 +175,8 @@ def workspace_bytes(layout: Layout, step: Step) -> int:
 def upload(layout: Layout, step: Step, pool: Pool, workspace, stream=None) -> Plan:
     """Validate a step and put its description into the workspace; the plan serves every layer.
     It points into the workspace and keeps that tensor alive."""
+    for tables in step._entries:
+        tables.check(layout.page_size)
     wp, wb = _ws(workspace)
     plan = Plan()
     _check(_lib().kamera_step_upload(ctypes.byref(layout), ctypes.byref(step.c), ctypes.byref(pool), wp, wb,

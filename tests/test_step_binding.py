@@ -1,0 +1,78 @@
+"""What the serving step's Python binding refuses before the library is called. No GPU is needed: device pointers
+are fake addresses that nothing dereferences."""
+
+import numpy as np
+import pytest
+
+from position_free_kv_amd import abi, step
+
+
+def _gpu_present() -> bool:
+    try:
+        import torch
+        return torch.cuda.device_count() > 0
+    except Exception:  # noqa: BLE001
+        return False
+
+
+pytestmark = pytest.mark.skipif(_gpu_present(), reason="fake device addresses")
+
+FAKE = 0x10_0000_0000
+PAGE = 16
+
+
+def layout(**kw):
+    return abi.make_layout(abi.GQA, kw.pop("dtype", abi.BF16), 2, **{**dict(num_kv_heads=2, head_dim=64, page_size=PAGE), **kw})
+
+
+def upload(s, lay=None):
+    return step.upload(lay or layout(), s, abi.make_pool(FAKE, FAKE, 100), (FAKE, 1 << 30))
+
+
+def accepted(s):
+    """All checks passed: what is left is the first call of the GPU."""
+    with pytest.raises(abi.KameraError) as e:
+        upload(s)
+    assert e.value.name == "KAMERA_E_HIP"
+
+
+def refused(s):
+    with pytest.raises(ValueError):
+        upload(s)
+
+
+# ------------------------------------------------------------------ tables as long as their tokens
+@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("slot0,tokens,entries", [(0, 16, 1), (0, 17, 2), (5, 11, 1), (5, 12, 2), (15, 1, 1), (15, 2, 2), (3, 160, 11)])
+def test_tables_shorter_than_their_tokens_are_refused(rows, slot0, tokens, entries):
+    """One entry less would be read from the next request's table, or past the array's end."""
+    def make(n):
+        t = np.arange(2 * n, dtype=np.int32).reshape(2, n)
+        return step.Step(num_q_heads=4, block_tables=t if rows else list(t), slot0=slot0, num_tokens=[tokens, 1], num_queries=1)
+    accepted(make(entries))
+    refused(make(entries - 1))
+
+
+def test_a_step_that_outgrows_its_tables_in_place_is_refused():
+    s = step.Step(num_q_heads=4, block_tables=np.array([[1], [2]], np.int32), num_tokens=[16, 3], num_queries=1)
+    accepted(s)
+    s.requests["num_tokens"] += 1
+    refused(s)
+
+
+def test_prefix_tables_shorter_than_their_tokens_are_refused():
+    def make(tokens, slot0):
+        return step.Step(num_q_heads=4, block_tables=[np.array([1], np.int32)], num_tokens=1, num_queries=1, prefix=0,
+                         prefixes=[dict(block_table=np.array([3, 4], np.int32), num_tokens=tokens, slot0=slot0)])
+    accepted(make(32, 0))
+    accepted(make(28, 4))
+    refused(make(33, 0))
+    refused(make(29, 4))
+
+
+def test_requests_without_a_table_have_no_tokens():
+    with pytest.raises(abi.KameraError) as e:
+        upload(step.Step(num_q_heads=4, block_tables=[None], num_tokens=1, num_queries=1))
+    assert e.value.name == "KAMERA_E_NULL"
+    refused(step.Step(num_q_heads=4, block_tables=[np.zeros(0, np.int32)], num_tokens=1, num_queries=1))
+    accepted(step.Step(num_q_heads=4, block_tables=[None, np.zeros(0, np.int32)], num_tokens=0, num_queries=[1, 0], flags=step.ATTEND))
