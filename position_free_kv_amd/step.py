@@ -97,17 +97,26 @@ def _stream(stream) -> Optional[int]:
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
+def _table(t) -> np.ndarray:
+    """A host int32 table, shared with the caller: what it holds at an upload is what the upload reads."""
+    a = None if isinstance(t, (list, tuple)) else np.asarray(t)
+    if a is None or a.dtype != np.int32 or a.ndim != 1 or not a.flags.c_contiguous:
+        raise ValueError("block tables are int32 arrays of one dimension, contiguous (the library reads them in place)")
+    return a
+
+
 def _tables(block_tables, n: int):
     """Host int32 tables, one a request: a 2-D array (a row each) or a sequence of arrays (None: no table).
     Returns (addresses, entries, objects to keep alive)."""
     if isinstance(block_tables, np.ndarray) and block_tables.ndim == 2:
-        if block_tables.dtype != np.int32 or not block_tables.flags.c_contiguous:
-            block_tables = np.ascontiguousarray(block_tables, dtype=np.int32)
-        if block_tables.shape[0] != n:
-            raise ValueError(f"{block_tables.shape[0]} block tables for {n} requests")
-        return (block_tables.ctypes.data + np.arange(n, dtype=np.uint64) * np.uint64(block_tables.strides[0]),
-                np.full(n, block_tables.shape[1], dtype=np.int64), block_tables)
-    keep = [None if t is None else np.ascontiguousarray(t, dtype=np.int32) for t in block_tables]
+        rows, width = block_tables.shape
+        if rows != n:
+            raise ValueError(f"{rows} block tables for {n} requests")
+        if block_tables.dtype != np.int32 or (width > 1 and block_tables.strides[1] != 4):
+            raise ValueError("rows of block tables are contiguous and int32 (the library reads them in place)")
+        addresses = block_tables.ctypes.data + np.arange(n, dtype=np.int64) * block_tables.strides[0]
+        return addresses.astype(np.uint64), np.full(n, width, dtype=np.int64), block_tables
+    keep = [None if t is None else _table(t) for t in block_tables]
     if len(keep) != n:
         raise ValueError(f"{len(keep)} block tables for {n} requests")
     return (np.array([0 if t is None else t.ctypes.data for t in keep], dtype=np.uint64),
@@ -142,7 +151,8 @@ class Step:
     """A kamera_step and the host arrays it points into.
 
     block_tables: a 2-D int32 array or a sequence of 1-D ones (None: a request without tokens of
-    its own), a row a request; a table is as long as slot0 + num_tokens needs at every upload. The other
+    its own), a row a request, read in place by every upload (rows may be part of a wider array; other
+    types are refused, as a copy would not follow the caller's changes) and as long as slot0 + num_tokens needs. The other
     request fields are scalars or one value a request. prefixes: dicts with block_table,
     num_tokens and (optionally) slot0. `requests` is the structured array the library reads.
     """
@@ -156,7 +166,7 @@ class Step:
         for name, value in (("slot0", slot0), ("num_tokens", num_tokens), ("num_queries", num_queries),
                             ("prefix", prefix), ("position0", position0), ("flags", request_flags)):
             self.requests[name] = value
-        self._prefix_tables = [np.ascontiguousarray(p["block_table"], dtype=np.int32) for p in prefixes]
+        self._prefix_tables = [_table(p["block_table"]) for p in prefixes]
         self.prefixes = np.zeros(len(prefixes), _PREFIX)
         for i, p in enumerate(prefixes):
             self.prefixes[i] = (self._prefix_tables[i].ctypes.data, p.get("slot0", 0), p["num_tokens"])

@@ -76,3 +76,41 @@ def test_requests_without_a_table_have_no_tokens():
     assert e.value.name == "KAMERA_E_NULL"
     refused(step.Step(num_q_heads=4, block_tables=[np.zeros(0, np.int32)], num_tokens=1, num_queries=1))
     accepted(step.Step(num_q_heads=4, block_tables=[None, np.zeros(0, np.int32)], num_tokens=0, num_queries=[1, 0], flags=step.ATTEND))
+
+
+# ------------------------------------------------------------------ tables read in place
+def entry(s, record, i):
+    """The page id that the library would read as entry i of a record's table."""
+    import ctypes
+    return ctypes.cast(int(record["block_table"]), ctypes.POINTER(ctypes.c_int32))[i]
+
+
+@pytest.mark.parametrize("of", [lambda b: b[:, :4], lambda b: b, lambda b: b[::-1], lambda b: b[::2, 3:], lambda b: b[:, 2:3], list,
+                                lambda b: [r[1:3] for r in b]])
+def test_tables_follow_changes_in_place(of):
+    """Column slices, rows in another order and single columns are read where they lie."""
+    big = np.zeros((4, 8), np.int32)
+    tables = of(big)
+    s = step.Step(num_q_heads=4, block_tables=tables, num_tokens=1, num_queries=1)
+    big[:] = np.arange(32).reshape(4, 8)
+    for r, t in zip(s.requests, tables):
+        assert [entry(s, r, i) for i in range(len(t))] == t.tolist()
+
+
+def test_prefix_tables_follow_changes_in_place():
+    pages = np.zeros(6, np.int32)
+    s = step.Step(num_q_heads=4, block_tables=[np.array([1], np.int32)], num_tokens=1, num_queries=1, prefix=0,
+                  prefixes=[dict(block_table=pages[1:], num_tokens=80)])
+    pages[:] = np.arange(6) + 40
+    assert [entry(s, s.prefixes[0], i) for i in range(5)] == [41, 42, 43, 44, 45]
+
+
+@pytest.mark.parametrize("table", [np.zeros((2, 4), np.int64), np.zeros((4, 2), np.int32).T, np.zeros((2, 8), np.int32)[:, ::2],
+                                   np.zeros((2, 4), np.uint32), [np.zeros(4, np.int64)] * 2, [np.zeros(8, np.int32)[::2]] * 2,
+                                   [[0, 1], [2, 3]], [np.zeros((2, 2), np.int32)] * 2])
+def test_tables_that_would_have_to_be_copied_are_refused(table):
+    with pytest.raises(ValueError):
+        step.Step(num_q_heads=4, block_tables=table, num_tokens=1, num_queries=1)
+    for t in table if not isinstance(table, np.ndarray) else []:
+        with pytest.raises(ValueError):
+            step.Step(num_q_heads=4, block_tables=[], num_tokens=1, num_queries=1, prefixes=[dict(block_table=t, num_tokens=1)])
