@@ -166,6 +166,8 @@ class Step:
         for name, value in (("slot0", slot0), ("num_tokens", num_tokens), ("num_queries", num_queries),
                             ("prefix", prefix), ("position0", position0), ("flags", request_flags)):
             self.requests[name] = value
+            if (self.requests[name] != value).any():
+                raise ValueError(f"{name}: a value does not fit its field")
         self._prefix_tables = [_table(p["block_table"]) for p in prefixes]
         self.prefixes = np.zeros(len(prefixes), _PREFIX)
         for i, p in enumerate(prefixes):
@@ -234,9 +236,20 @@ def copy_pages_workspace_bytes(num_copies: int) -> int:
     return int(_lib().kamera_copy_pages_workspace_bytes(int(num_copies)))
 
 
+def _page_ids(x) -> np.ndarray:
+    """Page ids as contiguous int32; ids that int32 does not hold are refused, not wrapped into others."""
+    a = np.asarray(x)
+    if a.size and a.dtype.kind not in "iu":
+        raise ValueError(f"page ids are whole numbers, not {a.dtype}")
+    ids = np.ascontiguousarray(a, dtype=np.int32)
+    if a.dtype != np.int32 and (ids != a).any():
+        raise ValueError("a page id does not fit 32 bits")
+    return ids
+
+
 def copy_pages(layout: Layout, pool: Pool, src, dst, workspace, stream=None) -> None:
     """Page dst[i] becomes what page src[i] was, for all i at once, in every layer."""
-    s, d = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
+    s, d = _page_ids(src), _page_ids(dst)
     if s.shape != d.shape or s.ndim != 1:
         raise ValueError("src and dst are one-dimensional and of one length")
     wp, wb = _ws(workspace)

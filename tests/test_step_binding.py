@@ -114,3 +114,23 @@ def test_tables_that_would_have_to_be_copied_are_refused(table):
     for t in table if not isinstance(table, np.ndarray) else []:
         with pytest.raises(ValueError):
             step.Step(num_q_heads=4, block_tables=[], num_tokens=1, num_queries=1, prefixes=[dict(block_table=t, num_tokens=1)])
+
+
+# ------------------------------------------------------------------ page ids
+@pytest.mark.parametrize("bad", [np.array([2 ** 32 + 1]), np.array([2 ** 31], np.uint32), np.array([-2 ** 32]), np.array([1.0]), [1.5], ["1"],
+                                 np.array([True])])
+def test_page_ids_that_would_become_others_are_refused(bad):
+    ws = (FAKE, 1 << 20)
+    for src, dst in ((bad, [1]), ([1], bad)):
+        with pytest.raises((ValueError, OverflowError)):
+            step.copy_pages(layout(), abi.make_pool(FAKE, FAKE, 100), src, dst, ws)
+    for good in ([4], np.array([4], np.int64), np.array([4], np.uint8), np.array([4, 0], np.int32)[::2]):
+        step.copy_pages(layout(), abi.make_pool(FAKE, FAKE, 100), good, [4], ws)  # (nothing to do)
+
+
+@pytest.mark.parametrize("kw", [dict(num_tokens=np.array([2 ** 32 + 5])), dict(num_queries=np.array([2 ** 32 + 1])), dict(slot0=np.array([2 ** 32])),
+                                dict(prefix=np.array([2 ** 32 - 1])), dict(num_tokens=5.5), dict(position0=0.5), dict(request_flags=np.array([2 ** 32])),
+                                dict(num_tokens=2 ** 32 + 5)])
+def test_request_fields_that_would_become_others_are_refused(kw):
+    with pytest.raises((ValueError, OverflowError)):
+        step.Step(num_q_heads=4, block_tables=[np.array([1], np.int32)], **{**dict(num_tokens=5, num_queries=1), **kw})
