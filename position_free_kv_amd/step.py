@@ -41,6 +41,7 @@ class StepDesc(ctypes.Structure):
 class Plan(ctypes.Structure):
     _fields_ = [("workspace", ctypes.c_void_p), ("num_tokens", ctypes.c_int32), ("num_layers", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32), ("detail", ctypes.c_uint64 * 40)]
+    _like = None  # what the launches' tensors have to be (set by upload)
 
 
 class AppendRows(ctypes.Structure):
@@ -80,20 +81,24 @@ def _lib() -> ctypes.CDLL:
     return _bound
 
 
-_cuda = None  # torch.cuda where there is a GPU, else False
+_current = None  # () -> handle of torch's current stream where there is a GPU, else False
 
 
 def _stream(stream) -> Optional[int]:
     """Handle of a stream: torch's current one by default (None, the null stream, without a GPU)."""
-    global _cuda
+    global _current
     if stream is None:
-        if _cuda is None:
+        if _current is None:
+            _current = False
             try:
                 import torch
-                _cuda = torch.cuda if torch.cuda.is_available() else False
+                if torch.cuda.is_available():
+                    torch.cuda.init()
+                    raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice  # (current_stream() makes an object a call)
+                    _current = lambda: raw(device())
             except ImportError:
-                _cuda = False
-        return _cuda.current_stream().cuda_stream if _cuda else None
+                pass
+        return _current() if _current else None
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
@@ -184,27 +189,88 @@ def workspace_bytes(layout: Layout, step: Step) -> int:
     return int(_lib().kamera_step_workspace_bytes(ctypes.byref(layout), ctypes.byref(step.c)))
 
 
+class _Like:
+    """What the tensors of a step's launches have to be: the layout's element type and widths. The library takes
+    addresses and strides between tokens alone, so anything else would be read as something that it is not."""
+
+    def __init__(self, torch, layout: Layout, num_q_heads: int):
+        self.gqa = gqa = layout.family == abi.GQA
+        self.dtype = torch.bfloat16 if layout.dtype == abi.BF16 else torch.float32
+        self.k = layout.num_kv_heads * layout.head_dim if gqa else layout.latent_dim + layout.rope_dim
+        self.dk = layout.head_dim if gqa else self.k
+        self.normed = layout.head_dim if gqa else layout.latent_dim  # columns of the keys' norm
+        self.heads = num_q_heads
+        self.q, self.out = num_q_heads * self.dk, num_q_heads * (self.dk if gqa else layout.latent_dim)
+        self.stats, self.positions = torch.float32, torch.int32
+
+
+def _on_gpu(what: str, x) -> None:
+    if not x.is_cuda and not x.is_pinned():
+        raise ValueError(f"{what}: a tensor of {x.device}, which the GPU does not read")
+
+
+def _flat(what: str, x, dtype, size: int, exactly: bool = False) -> Optional[int]:
+    """Address of a packed tensor of `size` elements (or more)."""
+    if x is None or isinstance(x, int):
+        return x
+    have = x.numel()
+    if x.dtype is not dtype or not x.is_contiguous() or have < size or (exactly and have != size):
+        raise ValueError(f"{what}: {tuple(x.shape)} of {x.dtype}, strides {x.stride()}; {size} packed elements of {dtype} are needed")
+    _on_gpu(what, x)
+    return x.data_ptr()
+
+
 def upload(layout: Layout, step: Step, pool: Pool, workspace, stream=None) -> Plan:
     """Validate a step and put its description into the workspace; the plan serves every layer.
     It points into the workspace and keeps that tensor alive."""
     for tables in step._entries:
         tables.check(layout.page_size)
+    like = None
+    try:
+        import torch
+        like = _Like(torch, layout, step.c.num_q_heads)
+    except ImportError:  # addresses alone
+        pass
+    if like is not None and step._positions is not None and step.c.flags & APPEND:
+        _flat("positions", step._positions, like.positions, 3 * int(step.requests["num_queries"].sum(dtype=np.int64)))
     wp, wb = _ws(workspace)
     plan = Plan()
     _check(_lib().kamera_step_upload(ctypes.byref(layout), ctypes.byref(step.c), ctypes.byref(pool), wp, wb,
                                      _stream(stream), ctypes.byref(plan)))
     plan._workspace = workspace
+    plan._like = like
     return plan
 
 
-def _rows(x, stride: Optional[int]):
-    """(address, elements between tokens) of a tensor or an address; one row has no stride (0: packed)."""
-    if x is None:
-        return None, 0 if stride is None else stride
-    if isinstance(x, int):
+def _rows(what: str, x, stride: Optional[int], n: int, width: int, like: Optional[_Like]):
+    """(address, elements between tokens) of n rows: a tensor, a row a token and each row packed, or an address.
+    A tensor of one row has no stride (0: packed). With a stride given, a tensor is where the rows begin."""
+    if x is None or isinstance(x, int):
         return x, 0 if stride is None else stride
+    if like is None:
+        return x.data_ptr(), (x.stride(0) if x.size(0) > 1 else 0) if stride is None else stride
+    shape, strides, fits = x.shape, x.stride(), True
     if stride is None:
-        stride = x.stride(0) if x.size(0) > 1 else 0
+        have = 1  # elements of a token, if they follow one another
+        if len(shape) == 2:  # (the usual case)
+            have = shape[1]
+            fits = strides[1] == 1 or have == 1
+        else:
+            for d in range(len(shape) - 1, 0, -1):
+                if strides[d] != have and shape[d] != 1:
+                    fits = False
+                have *= shape[d]
+        stride = strides[0] if shape and shape[0] > 1 else 0
+        # (a stride of 0, one row for all tokens, would mean packed to the library)
+        if n and (not shape or shape[0] < n or have < width or (stride == 0 and n > 1)):
+            fits = False
+    elif n and stride >= 0:
+        reach = x.storage_offset() + (stride or width) * (n - 1) + width
+        fits = reach * x.element_size() <= x.untyped_storage().nbytes()
+    if not fits or x.dtype is not like.dtype:
+        raise ValueError(f"{what}: {tuple(shape)} of {x.dtype}, strides {strides}; {n} rows of {width} packed elements of {like.dtype} are needed")
+    if not x.is_cuda:
+        _on_gpu(what, x)
     return x.data_ptr(), stride
 
 
@@ -212,10 +278,16 @@ def append(plan: Plan, layer: int, *, k, v=None, q=None, q_out=None, q_weight=No
            q_stride: Optional[int] = None, k_stride: Optional[int] = None, v_stride: Optional[int] = None,
            q_out_stride: Optional[int] = None, stream=None) -> None:
     """Norm and rotate the step's queries and keys; write its K and V rows into layer `layer`."""
-    qp, qs = _rows(q, q_stride)
-    kp, ks = _rows(k, k_stride)
-    vp, vs = _rows(v, v_stride)
-    op, os_ = _rows(q_out, q_out_stride)
+    n, like = plan.num_tokens, plan._like
+    wq = wk = 0
+    if like is not None:
+        wq, wk = like.q, like.k
+        q_weight = _flat("q_weight", q_weight, like.dtype, like.dk, True)
+        k_weight = _flat("k_weight", k_weight, like.dtype, like.normed, True)
+    qp, qs = _rows("q", q, q_stride, n, wq, like)
+    kp, ks = _rows("k", k, k_stride, n, wk, like)
+    vp, vs = _rows("v", v, v_stride, n, wk, like if like is not None and like.gqa else None)  # (MLA: not read)
+    op, os_ = _rows("q_out", q_out, q_out_stride, n, wq, like)
     rows = AppendRows(qp, kp, vp, op, qs, ks, vs, os_, _ptr(q_weight), _ptr(k_weight), eps, 0)
     status = (_bound or _lib()).kamera_step_append(ctypes.byref(plan), layer, ctypes.byref(rows), _stream(stream))
     if status:
@@ -225,8 +297,13 @@ def append(plan: Plan, layer: int, *, k, v=None, q=None, q_out=None, q_weight=No
 def attend(plan: Plan, layer: int, q, out, scale: float, lse=None, *, q_stride: Optional[int] = None,
            out_stride: Optional[int] = None, stream=None) -> None:
     """Attention of the step's query tokens over layer `layer` of the pool."""
-    qp, qs = _rows(q, q_stride)
-    op, os_ = _rows(out, out_stride)
+    n, like = plan.num_tokens, plan._like
+    wq = wo = 0
+    if like is not None:
+        wq, wo = like.q, like.out
+        lse = _flat("lse", lse, like.stats, n * like.heads)
+    qp, qs = _rows("q", q, q_stride, n, wq, like)
+    op, os_ = _rows("out", out, out_stride, n, wo, like)
     status = (_bound or _lib()).kamera_step_attend(ctypes.byref(plan), layer, qp, qs, op, os_, _ptr(lse), scale, _stream(stream))
     if status:
         _check(status)

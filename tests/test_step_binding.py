@@ -134,3 +134,119 @@ def test_page_ids_that_would_become_others_are_refused(bad):
 def test_request_fields_that_would_become_others_are_refused(kw):
     with pytest.raises((ValueError, OverflowError)):
         step.Step(num_q_heads=4, block_tables=[np.array([1], np.int32)], **{**dict(num_tokens=5, num_queries=1), **kw})
+
+
+# ------------------------------------------------------------------ tensors of the launches
+@pytest.fixture
+def tensors(monkeypatch):
+    """Tensors of the host stand for the GPU's: what is left of the checks are types, shapes and strides."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(step, "_on_gpu", lambda what, x: None, raising=False)
+    return torch
+
+
+def a_plan(tokens=3, family=abi.GQA, dtype=abi.BF16, heads=4, flags=step.APPEND | step.ATTEND):
+    lay = layout(dtype=dtype) if family == abi.GQA else abi.make_layout(abi.MLA, dtype, 2, latent_dim=64, rope_dim=16)
+    plan = step.upload(lay, step.Step(num_q_heads=heads, block_tables=[np.array([1], np.int32)], num_tokens=1, num_queries=0, flags=flags),
+                       abi.make_pool(FAKE, FAKE, 100), (FAKE, 1 << 30))  # no tokens: nothing is enqueued
+    plan.num_tokens = tokens
+    return plan
+
+
+def launched(fn, *args, **kw):
+    """Every check passed: what is left is the launch, for which there is no GPU (or nothing to launch)."""
+    try:
+        fn(*args, **kw)
+    except abi.KameraError as e:
+        assert e.name == "KAMERA_E_HIP", str(e)
+
+
+def good_rows(torch, n=3):
+    fused = torch.zeros(n, 4 * 64 + 2 * 128, dtype=torch.bfloat16)
+    return dict(q=fused[:, :256], k=fused[:, 256:384], v=fused[:, 384:], q_out=torch.zeros(n, 4, 64, dtype=torch.bfloat16),
+                q_weight=torch.ones(64, dtype=torch.bfloat16), k_weight=torch.ones(64, dtype=torch.bfloat16))
+
+
+def test_append_takes_rows_as_they_lie(tensors):
+    torch, plan = tensors, a_plan()
+    launched(step.append, plan, 0, **good_rows(torch))
+    launched(step.append, plan, 0, **good_rows(torch, 5))  # buffers for more tokens than the step has
+    wide = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    launched(step.append, plan, 0, **dict(good_rows(torch), q=wide[:, 2:6], k=wide[:, :2], v=wide[:, 6:]))
+    flat = torch.zeros(3 * 256, dtype=torch.bfloat16)  # where rows begin, their stride given
+    launched(step.append, plan, 0, **dict(good_rows(torch), q=flat, q_stride=256))
+    launched(step.append, a_plan(1), 0, **{k: v[:1] if v.dim() > 1 else v for k, v in good_rows(torch).items()})
+    one = torch.zeros(1, 128, dtype=torch.bfloat16)
+    launched(step.append, a_plan(1), 0, **dict(good_rows(torch), k=one.expand(4, 128)))
+    mla = torch.zeros(3, 4, 80, dtype=torch.bfloat16)
+    launched(step.append, a_plan(family=abi.MLA), 0, q=mla, q_out=mla, k=torch.zeros(3, 80, dtype=torch.bfloat16),
+             k_weight=torch.ones(64, dtype=torch.bfloat16), v=flat.float())  # (no V rows here)
+
+
+def bad_rows(torch):
+    z = dict(dtype=torch.bfloat16)
+    yield "q", torch.zeros(3, 256)                                            # another type
+    yield "q", torch.zeros(3, 256, dtype=torch.float16)
+    yield "k", torch.zeros(3, 2, 96, **z)[:, :, :64]                          # the first columns of wider heads
+    yield "k", torch.zeros(2, 3, 64, **z).transpose(0, 1)                     # heads before tokens
+    yield "v", torch.zeros(128, 3, **z).t()
+    yield "v", torch.zeros(3, 256, **z)[:, ::2]
+    yield "k", torch.zeros(2, 128, **z)                                       # fewer rows than tokens
+    yield "k", torch.zeros(3, 120, **z)                                       # narrower
+    yield "k", torch.zeros(3, 200, **z)[:, :100]
+    yield "q_out", torch.zeros(1, 256, **z).expand(3, 256)                    # one row for all tokens
+    yield "v", torch.zeros(1, 128, **z).expand(3, 128)
+    yield "q", torch.zeros(256, **z)
+    yield "q", torch.zeros((), **z)
+    yield "q_weight", torch.ones(64)
+    yield "q_weight", torch.ones(256, **z)
+    yield "k_weight", torch.ones(128, **z)[::2]
+    yield "k_weight", torch.ones(32, **z)
+
+
+def test_append_refuses_rows_it_would_misread(tensors):
+    plan = a_plan()
+    for name, x in bad_rows(tensors):
+        with pytest.raises(ValueError) as e:
+            step.append(plan, 0, **dict(good_rows(tensors), **{name: x}))
+        assert str(e.value).startswith(name + ":")
+    with pytest.raises(ValueError):  # the last row would end past the buffer
+        step.append(plan, 0, **dict(good_rows(tensors), q=tensors.zeros(3 * 256, dtype=tensors.bfloat16)[1:], q_stride=256))
+    with pytest.raises(ValueError):
+        step.append(a_plan(dtype=abi.F32), 0, **good_rows(tensors))
+
+
+def test_attend_checks_queries_outputs_and_statistics(tensors):
+    torch, plan = tensors, a_plan()
+    q, out = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 256, dtype=torch.bfloat16)
+    launched(step.attend, plan, 0, q, out, 1.0)
+    launched(step.attend, plan, 0, q, out, 1.0, lse=torch.zeros(3, 4))
+    launched(step.attend, plan, 0, q, torch.zeros(3, 300, dtype=torch.bfloat16)[:, 8:], 1.0, out_stride=300)
+    launched(step.attend, a_plan(family=abi.MLA), 0, torch.zeros(3, 4, 80, dtype=torch.bfloat16), out, 1.0)
+    for bad in (dict(q=q.float()), dict(q=q[:2]), dict(q=torch.zeros(3, 4, 80, dtype=torch.bfloat16)[:, :, :64]), dict(out=out.float()),
+                dict(out=out[:, :255]), dict(lse=torch.zeros(3, 4, dtype=torch.float64)), dict(lse=torch.zeros(4, 3).t()), dict(lse=torch.zeros(3, 3)),
+                dict(lse=torch.zeros(3, 4, dtype=torch.bfloat16)), dict(out=torch.zeros(3 * 300 - 45, dtype=torch.bfloat16), out_stride=300)):
+        args = dict(q=q, out=out, lse=None, **{k: v for k, v in bad.items() if k.endswith("stride")})
+        args.update(bad)
+        with pytest.raises(ValueError):
+            step.attend(plan, 0, args.pop("q"), args.pop("out"), 1.0, **args)
+
+
+def test_positions_are_packed_int32(tensors):
+    torch = tensors
+
+    def make(positions):
+        return step.Step(num_q_heads=4, block_tables=[np.array([1], np.int32)], num_tokens=5, num_queries=4, positions=positions)
+    accepted(make(torch.zeros(4, 3, dtype=torch.int32)))
+    for bad in (torch.zeros(4, 3, dtype=torch.int64), torch.zeros(3, 4, dtype=torch.int32).t(), torch.zeros(3, 3, dtype=torch.int32)):
+        refused(make(bad))
+
+
+def test_tensors_of_the_host_are_refused():
+    torch = pytest.importorskip("torch")
+    for name in good_rows(torch):
+        rows = {k: (v if k == name else FAKE) for k, v in good_rows(torch).items()}
+        with pytest.raises(ValueError):
+            step.append(a_plan(), 0, **rows)
+    with pytest.raises(ValueError):
+        step.attend(a_plan(), 0, torch.zeros(3, 256, dtype=torch.bfloat16), FAKE, 1.0)
