@@ -156,7 +156,8 @@ kamera_status kamera_copy_pages(const kamera_layout* layout, const kamera_pool* 
 /* Moves the live pages - those named by the tables - together at the pool's start: with n
  * distinct live pages, those with ids >= n move, in ascending order, to the ids < n that no
  * table names, in ascending order. The HOST tables are rewritten in place (only on success)
- * and *num_live receives n. A page named several times (shared) moves once. The workspace
+ * and *num_live receives n. A page named several times (shared) moves once, and tables may be
+ * parts of one array, the same parts among them. The workspace
  * needs kamera_copy_pages_workspace_bytes(pages that move) bytes; their number is at most n. */
 kamera_status kamera_compact_pages(const kamera_layout* layout, const kamera_pool* pool, int32_t* const* tables,
                                    const int32_t* lengths, int32_t num_tables, int32_t* num_live, void* workspace,

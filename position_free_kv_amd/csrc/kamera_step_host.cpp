@@ -896,7 +896,9 @@ kamera_status kamera_compact_pages(const kamera_layout* layout, const kamera_poo
       while (to[(size_t)hole] >= 0) ++hole;  // as many holes below `live` as live pages from it on
       src.push_back(p);
       dst.push_back(hole);
-      to[(size_t)p] = hole++;
+      to[(size_t)p] = hole;
+      to[(size_t)hole] = hole;  // entries reached through two of the tables are rewritten twice: the second time is no change
+      ++hole;
     }
     const int32_t n = (int32_t)src.size();
     st = check_workspace(workspace, workspace_bytes, copies_bytes(n));
