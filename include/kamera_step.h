@@ -100,8 +100,8 @@ typedef struct kamera_step_plan {
 size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_step* step);
 
 /* Validate a step and put its description into the workspace (256-byte aligned), on `stream`,
- * through the same staging slots as kamera_plan_upload (which see for blocking and graph
- * capture). Pool slots that the step appends to must be distinct and must not belong to a
+ * through the same staging slots as kamera_plan_upload (which see for blocking); not from a
+ * capturing stream (KAMERA_E_UNSUPPORTED): record the launches of the plan instead. Pool slots that the step appends to must be distinct and must not belong to a
  * prefix of the step (KAMERA_E_OVERLAP). */
 kamera_status kamera_step_upload(const kamera_layout* layout, const kamera_step* step, const kamera_pool* pool,
                                  void* workspace, size_t workspace_bytes, void* stream, kamera_step_plan* plan);
@@ -147,7 +147,9 @@ kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, co
 /* In every layer, K and V: page dst[i] becomes what page src[i] was before the call, for all
  * i at once (a page may be both a source and a destination; a source may feed several).
  * src and dst are HOST arrays; the dst pages must differ (KAMERA_E_OVERLAP). The workspace
- * needs kamera_copy_pages_workspace_bytes(n) bytes, 256-byte aligned. */
+ * needs kamera_copy_pages_workspace_bytes(n) bytes, 256-byte aligned. Up to 400 copies none of
+ * which writes a page that another reads travel as kernel arguments and can be recorded in a
+ * captured graph; other lists are staged and cannot (KAMERA_E_UNSUPPORTED). */
 size_t kamera_copy_pages_workspace_bytes(int32_t num_copies);
 kamera_status kamera_copy_pages(const kamera_layout* layout, const kamera_pool* pool, const int32_t* src,
                                 const int32_t* dst, int32_t num_copies, void* workspace, size_t workspace_bytes,

@@ -692,6 +692,11 @@ kamera_status host_check_layout(const kamera_layout* L) { return check_layout(L)
 kamera_status host_stage(const void* src, size_t bytes, void* dst, hipStream_t stream) {
   // the copy-in kernel moves whole 16-byte words: a shorter tail would stay behind
   if (bytes % 16) return fail(KAMERA_E_SHAPE, "staged blocks are multiples of 16 bytes (got %zu)", bytes);
+  // a replay would read the staging slot, which later calls have filled with other tables
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  const hipError_t e = hipStreamIsCapturing(stream, &capture);
+  if (e != hipSuccess) return fail(KAMERA_E_HIP, "hipStreamIsCapturing failed: %s", hipGetErrorString(e));
+  if (capture != hipStreamCaptureStatusNone) return fail(KAMERA_E_UNSUPPORTED, "a staged call cannot be recorded in a captured graph");
   return upload(src, bytes, dst, stream);
 }
 }  // namespace kamera
