@@ -33,7 +33,8 @@ extern "C" {
 /* step flags: what the step's plan will be launched for */
 enum {
   KAMERA_STEP_APPEND = 1u, /* kamera_step_append */
-  KAMERA_STEP_ATTEND = 2u  /* kamera_step_attend */
+  KAMERA_STEP_ATTEND = 2u, /* kamera_step_attend */
+  KAMERA_STEP_FIT = 4u     /* the plan keeps to the workspace it is given (see kamera_step_workspace_bytes) */
 };
 /* request flags */
 enum {
@@ -79,7 +80,7 @@ typedef struct kamera_step {
   int32_t num_q_heads;            /* GQA: a multiple of num_kv_heads, query head h reading KV head
                                      h / (num_q_heads / num_kv_heads); MLA: any; 0 with
                                      KAMERA_STEP_APPEND alone: no queries                          */
-  uint32_t flags;                 /* KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND (at least one)        */
+  uint32_t flags;                 /* KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND (at least one), FIT   */
   int32_t reserved[2];            /* must be 0                                                   */
 } kamera_step;
 
@@ -96,7 +97,14 @@ typedef struct kamera_step_plan {
 
 /* Bytes of device workspace a step needs, whatever the pool's alignment (packed tables,
  * cos/sin of the appended tokens, partial results of the attention); 0 if the arguments are
- * invalid. */
+ * invalid. They rise and fall as the lengths grow, with the number of ranges that the keys are
+ * cut into. A server that allocates once asks for its largest step, with KAMERA_STEP_FIT: the
+ * buffer then serves every smaller step too, that is, one made of some of the largest one's
+ * requests and prefixes with at most as many tokens, queries and page-table entries each, of the
+ * same layout, flags and num_q_heads. Where the fastest plan does not fit, kamera_step_upload
+ * cuts the keys into fewer ranges, or lets requests read their prefix for themselves. Such a plan
+ * may be slower: the largest size over the lengths that occur keeps every plan the fastest.
+ * Without KAMERA_STEP_FIT a smaller workspace is refused (KAMERA_E_WORKSPACE). */
 size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_step* step);
 
 /* Validate a step and put its description into the workspace (256-byte aligned), on `stream`,
@@ -139,8 +147,9 @@ kamera_status kamera_step_append(const kamera_step_plan* plan, int32_t layer, co
  * lse (fp32 [N][num_q_heads], packed, may be NULL) receives log(sum(exp(scale q.k))).
  * Scores, softmax statistics and sums are fp32; on the matrix cores the probabilities enter
  * the second product in bf16. Values of unseen tokens and unused slots are not read into any
- * result, whatever they hold. Results are the same bits on every run. The plan's workspace
- * holds the partial results, so launches of one plan belong on one stream at a time. */
+ * result, whatever they hold. Results are the same bits on every run of a step (KAMERA_STEP_FIT:
+ * in a workspace of the same size). The plan's workspace holds the partial results, so launches
+ * of one plan belong on one stream at a time. */
 kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
                                  void* out, int64_t out_stride, float* lse, float scale, void* stream);
 

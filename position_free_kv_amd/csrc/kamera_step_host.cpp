@@ -49,7 +49,7 @@ kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n
   kamera_status st = host_check_layout(L);
   if (st != KAMERA_OK) return st;
   if (!s) return host_fail(KAMERA_E_NULL, "step is NULL");
-  if (s->flags == 0 || (s->flags & ~(uint32_t)(KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND)))
+  if (!(s->flags & (KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND)) || (s->flags & ~(uint32_t)(KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND | KAMERA_STEP_FIT)))
     return host_fail(KAMERA_E_UNSUPPORTED, "step.flags 0x%x", s->flags);
   if (s->num_requests < 0 || s->num_prefixes < 0) return host_fail(KAMERA_E_SHAPE, "negative count of requests or prefixes");
   if (s->reserved[0] || s->reserved[1]) return host_fail(KAMERA_E_SHAPE, "step.reserved must be 0");
@@ -152,6 +152,14 @@ struct Work {
   std::vector<MergeToken> merge;
   int64_t part_rows = 0;
   int32_t wide = 0, pairs = 0, max_parts = 0;
+  bool split = false, shared = false;  // keys of a run cut into ranges, a prefix read by a run of its own
+};
+
+// A plan for less workspace than the fastest one takes: ranges of 2^coarser times the length, and
+// prefixes read by each request for itself. Without ranges and sharing no partial row is left.
+struct Fit {
+  int coarser = 0;
+  bool share = true;
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -173,7 +181,7 @@ int pick_kernel(const kamera_layout* L, const kamera_pool* pool) {
   return kernel;
 }
 
-void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Work& w) {
+void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
   const Shape h = shape_of(L, s->num_q_heads);
   const int G = h.group;
   w.runs.clear();
@@ -182,10 +190,11 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   w.merge.clear();
   w.part_rows = 0;
   w.max_parts = 0;
+  w.split = w.shared = false;
   // members of each prefix whose rows are few enough to share its reads
   std::vector<int32_t> members((size_t)s->num_prefixes, 0);
   auto few = [&](const kamera_request& r) {
-    return r.num_queries > 0 && r.prefix >= 0 && s->prefixes[r.prefix].num_tokens > 0 && (int64_t)r.num_queries * G < kShareRows;
+    return fit.share && r.num_queries > 0 && r.prefix >= 0 && s->prefixes[r.prefix].num_tokens > 0 && (int64_t)r.num_queries * G < kShareRows;
   };
   for (int i = 0; i < s->num_requests; ++i)
     if (few(s->requests[i])) ++members[(size_t)s->requests[i].prefix];
@@ -194,6 +203,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   std::vector<int32_t> prefix_run((size_t)s->num_prefixes, -1);
   for (int p = 0; p < s->num_prefixes; ++p) {
     if (members[(size_t)p] < 2) continue;
+    w.shared = true;
     AttendRun r;
     std::memset(&r, 0, sizeof(r));
     r.pg_a = tb.prefix[(size_t)p];
@@ -231,7 +241,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     r.pg_b = tb.request[(size_t)i];
     r.slot_b = q.slot0;
     r.kv = r.len_a + q.num_tokens;
-    if (r.kv == 0) continue;
+    if (r.kv == 0 && shares(q)) continue;  // (no key at all: a run without keys writes the zeros)
     if (q.flags & KAMERA_REQUEST_ALL) {
       r.lim0 = r.kv - 1;
     } else {
@@ -301,6 +311,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       const int64_t n = (int64_t)(round * slots / (c.tiles * h.heads));
       if (n > 0) consider(std::max(lowest, (int64_t)round_up((size_t)ceil_div(c.longest, n), (size_t)gran)));
     }
+    for (int i = 0; i < fit.coarser && chunk_of[k] < c.longest; ++i) chunk_of[k] *= 2;
   }
   int32_t start[4] = {0, 0, 0, 0};  // each class's first item
   for (int c = 0; c < 3; ++c) {
@@ -309,11 +320,14 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       const int64_t rows = (int64_t)r.ntok * G;
       const int tile = tile_rows(kernel, c);
       if (r.tile != c) continue;
-      const int64_t splits = ceil_div(r.kv, chunk_of[c]);
-      const int64_t chunk = (int64_t)round_up((size_t)ceil_div(r.kv, splits), (size_t)gran);
-      const int64_t n = ceil_div(r.kv, chunk);
+      const int64_t splits = std::max<int64_t>(ceil_div(r.kv, chunk_of[c]), 1);
+      const int64_t chunk = (int64_t)round_up((size_t)std::max<int64_t>(ceil_div(r.kv, splits), 1), (size_t)gran);
+      const int64_t n = std::max<int64_t>(ceil_div(r.kv, chunk), 1);
       r.splits = (int32_t)n;
-      if (n > 1) r.direct = 0;
+      if (n > 1) {
+        r.direct = 0;
+        w.split = true;
+      }
       if (!r.direct) {
         r.part0 = w.part_rows;
         w.part_rows += n * h.heads * rows;
@@ -340,7 +354,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   }
   w.wide = start[1];
   w.pairs = start[2] - start[1];
-  // tokens joined from parts (or that see no key at all)
+  // tokens joined from parts
   std::vector<int32_t> listed((size_t)s->num_prefixes, 0);  // tokens of each prefix run so far
   auto part = [&](MergeToken& m, int slot, int run, int64_t j) {
     const AttendRun& r = w.runs[(size_t)run];
@@ -371,7 +385,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 struct Offsets {
   size_t pages, items, tok, merge, slots, pos, theta, upload, phase, ml, o, total;
 };
-Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Work& w) {
+Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, size_t items, size_t tok, size_t merge, int64_t part_rows) {
   Offsets f;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -382,18 +396,32 @@ Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, con
   const bool append = s->flags & KAMERA_STEP_APPEND;
   const Shape h = shape_of(L, s->num_q_heads);
   f.pages = take((size_t)n.entries * 4);
-  f.items = take(w.items.size() * sizeof(AttendItem));
-  f.tok = take(w.tok.size() * 4);
-  f.merge = take(w.merge.size() * sizeof(MergeToken));
+  f.items = take(items * sizeof(AttendItem));
+  f.tok = take(tok * 4);
+  f.merge = take(merge * sizeof(MergeToken));
   f.slots = take(append ? (size_t)n.tokens * 8 : 0);
   f.pos = take(append && !s->positions ? (size_t)n.tokens * 4 : 0);
   f.theta = take(append ? (size_t)h.d_rot / 2 * 8 : 0);
   f.upload = at;
   f.phase = take(append ? (size_t)n.tokens * h.d_rot * 4 : 0);
-  f.ml = take((size_t)w.part_rows * 8);
-  f.o = take((size_t)w.part_rows * h.dv * 4);
+  f.ml = take((size_t)part_rows * 8);
+  f.o = take((size_t)part_rows * h.dv * 4);
   f.total = std::max<size_t>(at, kAlign);
   return f;
+}
+Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Work& w) {
+  return carve(L, s, n, w.items.size(), w.tok.size(), w.merge.size(), w.part_rows);
+}
+
+// Bytes that a plan without ranges and sharing takes on any pool: it has no partial rows, and an item a
+// tile, most of them in the kernel with the smallest tiles. Unlike the fastest plan's, they never grow
+// when a request loses tokens or queries.
+size_t least_bytes(const kamera_layout* L, const kamera_step* s, const Counts& n) {
+  const int64_t group = shape_of(L, s->num_q_heads).group;
+  size_t items = 0;
+  if (s->flags & KAMERA_STEP_ATTEND)
+    for (int i = 0; i < s->num_requests; ++i) items += (size_t)ceil_div(s->requests[i].num_queries * group, tile_rows(ATTEND_PLAIN, TILE_NARROW));
+  return carve(L, s, n, items, 0, 0, 0).total;
 }
 
 void place_tables(const kamera_layout* L, const kamera_step* s, Tables& tb) {
@@ -482,9 +510,16 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   thread_local Work w;
   place_tables(L, s, tb);
   const int kernel = pick_kernel(L, pool);
-  if (attend) plan_attention(L, s, tb, kernel, w);
+  Fit fit;
+  if (attend) plan_attention(L, s, tb, kernel, fit, w);
   else w = Work();
-  const Offsets f = carve(L, s, n, w);
+  Offsets f = carve(L, s, n, w);
+  while ((s->flags & KAMERA_STEP_FIT) && f.total > ws_bytes && (w.split || w.shared)) {  // (each turn halves the partial rows, or ends the sharing)
+    if (w.split) ++fit.coarser;
+    else fit = Fit{0, false};
+    plan_attention(L, s, tb, kernel, fit, w);
+    f = carve(L, s, n, w);
+  }
   st = check_workspace(ws, ws_bytes, f.total);
   if (st != KAMERA_OK) return st;
   if ((int64_t)w.items.size() * h.heads >= (int64_t(1) << 31)) return host_fail(KAMERA_E_SHAPE, "too many work items");
@@ -771,10 +806,11 @@ size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_ste
     place_tables(layout, step, tb);
     const bool attend = step->flags & KAMERA_STEP_ATTEND;
     // the pool's alignment decides between the kernels: enough for either
-    if (attend) plan_attention(layout, step, tb, ATTEND_PLAIN, w);
+    if (attend) plan_attention(layout, step, tb, ATTEND_PLAIN, Fit{}, w);
     size_t need = carve(layout, step, n, w).total;
+    if (step->flags & KAMERA_STEP_FIT) need = std::max(need, least_bytes(layout, step, n));
     if (attend && matrix_kernel(layout) != ATTEND_PLAIN) {
-      plan_attention(layout, step, tb, matrix_kernel(layout), w);
+      plan_attention(layout, step, tb, matrix_kernel(layout), Fit{}, w);
       need = std::max(need, carve(layout, step, n, w).total);
     }
     bytes = need;

@@ -14,7 +14,7 @@ import numpy as np
 from . import abi
 from .abi import Layout, Pool, _check, _ptr, _ws
 
-APPEND, ATTEND = 1, 2
+APPEND, ATTEND, FIT = 1, 2, 4
 REQUEST_ALL = 1
 ATTEND_MAX_DIM = 1024
 
@@ -186,6 +186,8 @@ class Step:
 
 
 def workspace_bytes(layout: Layout, step: Step) -> int:
+    """Bytes that a step needs. They do not only grow with its lengths: a buffer for the largest step serves the
+    smaller ones too if FIT is among their flags."""
     return int(_lib().kamera_step_workspace_bytes(ctypes.byref(layout), ctypes.byref(step.c)))
 
 

@@ -45,3 +45,69 @@ def test_staged_calls_are_refused_while_capturing():
         step.upload(c.lay, s, c.pool, other)  # eager calls take the staging slots in between
         step.copy_pages(lay, pool, [401, 402], [402, 401], copies)
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ one workspace for many steps
+def check(c, out, lse, scale):
+    """Outputs of every layer against the 64-bit expectation, within Case's bounds."""
+    torch.cuda.synchronize()
+    for layer in range(c.layers):
+        o, tol, z, ltol = c.expect_attend(layer, scale)
+        got, gz = out[layer].double().cpu().numpy(), lse[layer].double().cpu().numpy()
+        assert (np.abs(got - o) <= tol).all(), layer
+        empty = np.isneginf(z)
+        assert (np.isneginf(gz) == empty).all()
+        assert (np.abs(np.where(empty, 0, gz) - np.where(empty, 0, z)) <= ltol).all(), layer
+
+
+def attend(c, s, ws, scale):
+    plan = step.upload(c.lay, s, c.pool, ws)
+    out = torch.full((c.layers, c.n, c.heads * c.dv), 7.0, dtype=c.q.dtype, device="cuda")
+    lse = torch.full((c.layers, c.n, c.heads), 7.0, device="cuda")
+    for layer in range(c.layers):
+        step.attend(plan, layer, c.q[layer], out[layer], scale, lse=lse[layer])
+    return out, lse
+
+
+KINDS = [dict(heads=8, kv_heads=2, head_dim=128), dict(heads=3, kv_heads=3, head_dim=64), dict(dtype=F32, heads=4, kv_heads=2, head_dim=64),
+         dict(heads=4, kv_heads=2, head_dim=80), dict(family=MLA, heads=16, latent=512, rope=64), dict(family=MLA, heads=3, latent=20, rope=6)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_step_uploaded_again_with_other_lengths_into_one_workspace(kind):
+    """A loop that changes a Step in place: longer, shorter, empty, and back, in the buffer of the longest."""
+    longest = [700, 33, 260, 64]
+    c = Case(layers=1, prefixes=[1100], requests=[(0, n, 1) for n in longest] + [(-1, 300, 2)], seed=5, **kind)
+    rows = list(c.rows)
+    s = c.step(step.ATTEND | step.FIT)
+    ws = c.workspace(s)
+    for lengths in (longest, [1, 1, 1, 1], [0, 33, 17, 5], [700, 0, 0, 64], [129, 32, 128, 63], [0, 0, 0, 0], longest):
+        c.requests = [(0, n, 1, 0) for n in lengths] + [(-1, 300 if lengths[0] else 1, 2, 0)]
+        c.rows = [r[:r.size if i == 0 else c.requests[i - 1][1]] for i, r in enumerate(rows)]
+        s.requests["num_tokens"] = [r[1] for r in c.requests]
+        check(c, *attend(c, s, ws, 0.2), 0.2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_in_less_workspace(kind):
+    """Fewer ranges, then no sharing of the prefix, down to no partial rows; then a refusal."""
+    c = Case(layers=1, prefixes=[2500], requests=[(0, 400, 1), (0, 1, 1), (0, 0, 2), (0, 90, 3), (-1, 900, 1), (-1, 0, 2), (0, 130, 130)], seed=6, **kind)
+    s = c.step(step.ATTEND | step.FIT)
+    ws = c.workspace(s)
+    sizes, results = ws.numel(), set()
+    while True:
+        try:
+            out, lse = attend(c, s, (ws.data_ptr(), sizes), 0.2)
+        except abi.KameraError as e:
+            assert e.name == "KAMERA_E_WORKSPACE"
+            break
+        check(c, out, lse, 0.2)
+        again, _ = attend(c, s, (ws.data_ptr(), sizes), 0.2)
+        assert torch.equal(out, again)
+        results.add(out.view(torch.int16 if out.dtype == torch.bfloat16 else torch.int32).cpu().numpy().tobytes())
+        sizes = sizes * 2 // 3
+    assert len(results) > 1  # other plans, other roundings
+    exact = c.step(step.ATTEND)
+    with pytest.raises(abi.KameraError) as e:
+        step.upload(c.lay, exact, c.pool, (ws.data_ptr(), sizes * 3 // 2))
+    assert e.value.name == "KAMERA_E_WORKSPACE"
