@@ -144,6 +144,7 @@ struct State {
   typedef float Acc __attribute__((ext_vector_type(kScores)));
   Acc o[kBlocks];
   float m, l;  // l: this lane's keys only (a row's lanes are added at the end)
+  bool low;    // MLA: a row of the wave has met a score of -inf in a step with a mask
 
   static __device__ __forceinline__ int group() { return (threadIdx.x & 63) / ROWS; }
   static __device__ __forceinline__ int row() { return threadIdx.x & (ROWS - 1); }
@@ -161,6 +162,7 @@ struct State {
     for (int b = 0; b < kBlocks; ++b) o[b] = (Acc)(0.0f);
     m = -INFINITY;
     l = 0.0f;
+    low = false;
   }
 
   // First column of operand ks. With 32 rows they follow each other; with 16 two operands share 64
@@ -222,11 +224,37 @@ struct State {
     return *(const KLDS bf16x8*)(rest + ((at ^ (c2 % 128)) + (c2 / 128) * 128 + tile * ROWS * kRestRow));
   }
 
-  // O += P V for a step whose keys some row does not see: a value that is not finite must reach the
-  // rows that see its key (weight > 0) and no other, where a product would make 0 * inf = NaN. Such
-  // values are left out of the product; where there is one, products of the same weights with marks
-  // (1 for inf, -inf; both for NaN) tell which results it reaches.
-  __device__ __forceinline__ void careful(const bf16x8 (&p)[kPSteps], const KLDS char* v) {
+  // Operand u: ones for the keys before `end` whose weight is 0 (t: the first of the 32), zeros elsewhere.
+  static __device__ __forceinline__ bf16x8 seen_without_weight(const bf16x8& p, int u, int t, int end) {
+    const u32x4 w = __builtin_bit_cast(u32x4, p);
+    u32x4 z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * i + e;
+        const int key = t + (ROWS == 32 ? slot_key(0, 8 * u + j) : slot_key(j >> 2, j & 3));
+        if (key < end && ((w[i] >> (16 * e)) & 0x7f80u) == 0) z[i] |= 0x3f80u << (16 * e);
+      }
+    }
+    return __builtin_bit_cast(bf16x8, z);
+  }
+
+  // Adds `what` to the results of block b that a mark reaches with a weight.
+  __device__ __forceinline__ void reach(int b, u32x4 marks, bf16x8 weights, float what) {
+    const Acc x = mfma(__builtin_bit_cast(bf16x8, marks), weights, (Acc)(0.0f));
+#pragma unroll
+    for (int i = 0; i < kScores; ++i) o[b][i] += x[i] > 0.0f ? what : 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // O += P V for a step whose keys some row does not see (end: the keys that the lane's row sees): a value
+  // that is not finite must reach the rows that see its key and no other, where a product would make 0 * inf
+  // = NaN. Such values are left out of the product; where there is one, products of the weights with marks
+  // (1 for inf, -inf; both for NaN) tell which results it reaches, and a product of marks with the seen keys
+  // of weight 0 tells where 0 * inf is due, as in the steps without a mask.
+  __device__ __forceinline__ void careful(const bf16x8 (&p)[kPSteps], const KLDS char* v, int t, int end) {
 #pragma nounroll
     for (int u = 0; u < kPSteps; ++u) {
       const bf16x8 pw = kPSteps == 2 && u ? p[kPSteps - 1] : p[0];
@@ -251,17 +279,18 @@ struct State {
               w[i] &= e ? 0xffffu : 0xffff0000u;
             }
           }
-          const Acc x = mfma(__builtin_bit_cast(bf16x8, up), pw, (Acc)(0.0f)), y = mfma(__builtin_bit_cast(bf16x8, down), pw, (Acc)(0.0f));
-#pragma unroll
-          for (int i = 0; i < kScores; ++i) o[b][i] += (x[i] > 0.0f ? INFINITY : 0.0f) + (y[i] > 0.0f ? -INFINITY : 0.0f);
+          reach(b, up, pw, INFINITY);
+          reach(b, down, pw, -INFINITY);
+          reach(b, up | down, seen_without_weight(pw, u, t, end), NAN);
         }
         o[b] = mfma(__builtin_bit_cast(bf16x8, w), pw, o[b]);
       }
     }
   }
 
-  // The same where values are columns of the keys (MLA): a row that sees such a key has no finite score
-  // for it and is NaN by that, so leaving the value out is enough.
+  // The same where values are columns of the keys (MLA): they are left out of the product. A row that sees a
+  // value that is not finite has no finite score for its key. One of inf or NaN makes the whole row NaN by
+  // itself; one of -inf gives a weight of 0, and the 0 * inf that is due is put into the result afterwards (low).
   static __device__ __forceinline__ bf16x8 finite(bf16x8 x) {
     u32x4 w = __builtin_bit_cast(u32x4, x);
 #pragma unroll
@@ -295,11 +324,11 @@ struct State {
     }
   }
 
-  // O += P V for 32 keys
+  // O += P V for 32 keys from t on
   template <bool EDGE>
-  __device__ __forceinline__ void add(const bf16x8 (&p)[kPSteps], const KLDS char* v) {
+  __device__ __forceinline__ void add(const bf16x8 (&p)[kPSteps], const KLDS char* v, int t, int end) {
     if constexpr (EDGE && kRestRow == 0) {
-      careful(p, v);
+      careful(p, v, t, end);
       return;
     }
     constexpr int kProducts = kPSteps * kBlocks, A = kTight ? 2 : kProducts;
@@ -354,16 +383,18 @@ struct State {
     Acc s[NT][kTiles];
 #pragma unroll
     for (int n = 0; n < NT; ++n) score(s[n], q, k + n * 32 * kRow, rest + n * 32 * kRestRow);
-    float top = -INFINITY;
+    float top = -INFINITY, bottom = INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
         for (int i = 0; i < kScores; ++i) {
+          if (EDGE && kRestRow != 0) bottom = fminf(bottom, s[n][x][i]);
           if (EDGE && t0 + n * 32 + slot_key(x, i) >= end) s[n][x][i] = -INFINITY;
           top = fmaxf(top, s[n][x][i]);
         }
+    if (EDGE && kRestRow != 0) low |= __any(bottom == -INFINITY) != 0;
     top = row_max<ROWS>(top) * scale2;
     if (__any(top > m + kGrow)) {
       const float to = fmaxf(m, top);
@@ -378,7 +409,7 @@ struct State {
 #pragma unroll
     for (int n = 0; n < NT; ++n) weigh(p[n], s[n], scale2, base);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) add<EDGE>(p[n], v + n * 32 * kRow);
+    for (int n = 0; n < NT; ++n) add<EDGE>(p[n], v + n * 32 * kRow, t0 + n * 32, end);
   }
 
   // column of values 4 i on of output tile b

@@ -61,12 +61,44 @@ struct LatentRows {
   }
 };
 
+// Steps with a mask leave values that are not finite out of the product (State::finite). A row that sees one
+// under a weight of 0 gets its NaN here, after the wave has written the 16 rows from row0 on: over the item's
+// keys, a lane for 8 columns. Taken only where a score of -inf was met, so it costs the usual case a test.
+__device__ __forceinline__ void zero_times_inf(const StepArgs& a, const AttendIo& io, const AttendItem& it, int row0) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* k = a.k_pool + io.layer0 + lane * 8;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the rows are written
+#pragma nounroll
+  for (int t = it.kv0; t < it.kv1; ++t) {
+    int place;
+    const int page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, it.run, t, place)];
+    const u32x4 w = *(const KGLOBAL u32x4*)(k + ((int64_t)page * a.page_size + place) * kKey);
+    uint32_t marks = 0;  // columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      marks |= ((w[i] & 0x7f80u) == 0x7f80u ? 1u << (2 * i) : 0u) | ((w[i] & 0x7f800000u) == 0x7f800000u ? 2u << (2 * i) : 0u);
+    if (!__any(marks != 0)) continue;
+#pragma nounroll
+    for (int i = 0; i < 16; ++i) {
+      const Lane r = lane_row(a, it, 0, row0 + i);
+      if (!r.owned || t >= r.end) continue;
+#pragma nounroll
+      for (int e = 0; e < 8; ++e) {
+        if (!(marks >> e & 1)) continue;
+        const int c = lane * 8 + e;
+        if (it.run.direct) ((KGLOBAL uint16_t*)io.out)[(int64_t)r.token * io.out_stride + (int64_t)r.qh * kLatent + c] = 0x7fc0;
+        else ((KGLOBAL float*)a.part_o)[part_row(a, it, 0, r.row) * kLatent + c] = NAN;
+      }
+    }
+  }
+}
+
 // ============================================================================
 // Tiles of 128 rows: 8 waves of 16 rows share stages of 32 keys.
 // ============================================================================
 constexpr int kWideWaves = 8;
 __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, KLDS char* k0, KLDS char* k1,
-                                          KLDS char* r0, KLDS char* r1) {
+                                          KLDS char* r0, KLDS char* r1, volatile KLDS int* low) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   constexpr int PER = kKeys / kWideWaves;  // rows a wave brings in
@@ -101,9 +133,11 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
     }
   }
   const float l = row_sum<16>(st.l);
+  low[wave] = st.low;
   int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
   asm volatile("" : "+v"(tid));
   put_state(a, io, it, 0, lane_row(a, it, 0, it.row0 + (tid >> 6) * 16 + (tid & 15)), st, l);
+  if (low[wave]) zero_times_inf(a, io, it, it.row0 + wave * 16);
 }
 
 // ============================================================================
@@ -111,7 +145,7 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
 // the four out of step with each other, and the results are joined pairwise through LDS.
 // ============================================================================
 __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, KLDS char* mine, KLDS char* band,
-                                            KLDS char* place0, KLDS char* place1, float (&ml)[2][kWaves][64]) {
+                                            KLDS char* place0, KLDS char* place1, float (&ml)[2][kWaves][64], volatile KLDS int* low) {
   const AttendRun& run = it.run;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int last = it.kv1 - 1;
@@ -138,10 +172,13 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   }
   float l = row_sum<16>(st.l);
   static_assert(kLatents >= 64 * LatentState::kBlocks * 16, "a wave's result fits where a stage was");
+  low[wave] = st.low;
   join_waves(st, l, (f32x4*)place0, (f32x4*)place1, ml);
   int tid = threadIdx.x;  // (as in the wide tile)
   asm volatile("" : "+v"(tid));
-  if (wave == 0) put_state(a, io, it, 0, lane_row(a, it, 0, it.row0 + (tid & 15)), st, l);
+  if (wave != 0) return;
+  put_state(a, io, it, 0, lane_row(a, it, 0, it.row0 + (tid & 15)), st, l);
+  if (low[0] | low[1] | low[2] | low[3]) zero_times_inf(a, io, it, it.row0);
 }
 
 // One launch for both kinds of tiles, the wide ones first. Narrow tiles have work for 4 of the 8 waves.
@@ -149,15 +186,16 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attend_latent(StepArgs a, 
   __shared__ __align__(1024) char k0[kLatents], k1[kLatents], k2[kLatents], k3[kLatents];
   __shared__ __align__(1024) char r0[kBands], r1[kBands], r2[kBands], r3[kBands];
   __shared__ float ml[2][kWaves][64];
+  __shared__ int low[kWideWaves];
   const AttendItem it = a.items[blockIdx.x];
   if ((int)blockIdx.x < a.num_wide) {
-    wide_tile(a, io, it, (KLDS char*)k0, (KLDS char*)k1, (KLDS char*)r0, (KLDS char*)r1);
+    wide_tile(a, io, it, (KLDS char*)k0, (KLDS char*)k1, (KLDS char*)r0, (KLDS char*)r1, (KLDS int*)low);
   } else {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= kWaves) return;  // (barriers count the waves that are left)
     KLDS char* mine = wave < 2 ? (wave ? (KLDS char*)k1 : (KLDS char*)k0) : (wave == 2 ? (KLDS char*)k2 : (KLDS char*)k3);
     KLDS char* band = wave < 2 ? (wave ? (KLDS char*)r1 : (KLDS char*)r0) : (wave == 2 ? (KLDS char*)r2 : (KLDS char*)r3);
-    narrow_tile(a, io, it, mine, band, (KLDS char*)k0, (KLDS char*)k1, ml);
+    narrow_tile(a, io, it, mine, band, (KLDS char*)k0, (KLDS char*)k1, ml, (KLDS int*)low);
   }
 }
 

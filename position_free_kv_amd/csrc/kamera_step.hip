@@ -407,9 +407,9 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
     for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d, 16);
     if (!seen) continue;
     const float to = fmaxf(m, s);
-    const float alpha = shrink(m, to), p = shrink(s, to);
     const bool nothing = to == -INFINITY && s == -INFINITY;  // only -inf so far: weight 0, not exp(-inf + inf)
-    l = l * alpha + (nothing ? 0.0f : p);
+    const float alpha = shrink(m, to), p = nothing ? 0.0f : exp2f(s - to);  // (a score of inf: NaN)
+    l = l * alpha + p;
     m = to;
 #pragma unroll
     for (int i = 0; i < NJ; ++i) {
@@ -417,17 +417,17 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
       if (d >= a.dv) continue;
       float v[VEC];
       load_floats<T, VEC>(vp + at + d, v);
-      for (int e = 0; e < VEC; ++e) o[i * VEC + e] = nothing ? 0.0f : o[i * VEC + e] * alpha + p * v[e];
+      for (int e = 0; e < VEC; ++e) o[i * VEC + e] = o[i * VEC + e] * alpha + p * v[e];  // (0 * inf is NaN)
     }
   }
   float top = m;
   for (int d = 16; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-  const float w = l == 0.0f ? 0.0f : shrink(m, top);
+  const float w = shrink(m, top);
   float sum = l * w;
   for (int d = 16; d < 64; d <<= 1) sum += __shfl_xor(sum, d, kWave);
 #pragma unroll
   for (int i = 0; i < NJ * VEC; ++i) {
-    float x = l == 0.0f ? 0.0f : o[i] * w;
+    float x = o[i] * w;
     for (int d = 16; d < 64; d <<= 1) x += __shfl_xor(x, d, kWave);
     o[i] = x;
   }
@@ -534,8 +534,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
     for (int k = first; k < n; k += side) {
       const float w = weight[sub][k];
       const f32x4 x = rows[p.row(k) * quads + c];
-      if (w != 0.0f)  // (an empty part's row may hold anything)
-        for (int e = 0; e < 4; ++e) o[e] += x[e] * w;
+      for (int e = 0; e < 4; ++e) o[e] += x[e] * w;  // (an empty part's row is 0)
     }
   }
   if (side > 1) {
@@ -590,8 +589,8 @@ __global__ __launch_bounds__(kThreads) void attend_join_few(StepArgs a, AttendIo
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    if (k >= n || ml[k].y == 0.0f) continue;  // (an empty part's row may hold anything)
-    const float w = shrink(ml[k].x, top);
+    if (k >= n) continue;
+    const float w = ml[k].y == 0.0f ? 0.0f : shrink(ml[k].x, top);  // (an empty part's row is 0)
     sum += ml[k].y * w;
     for (int e = 0; e < 4; ++e) o[e] += x[k][e] * w;
   }
@@ -623,8 +622,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_any(StepArgs a, AttendIo
     for (int k = 0; k < n; ++k) {
       const int64_t pr = p.row(k);
       const float2 ml = a.part_ml[pr];
-      if (ml.y == 0.0f) continue;
-      const float w = shrink(ml.x, top);
+      const float w = ml.y == 0.0f ? 0.0f : shrink(ml.x, top);  // (an empty part's row is 0)
       sum += ml.y * w;
       if (c < a.dv) o += a.part_o[pr * a.dv + c] * w;
     }

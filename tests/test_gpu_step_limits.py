@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from position_free_kv_amd import abi, step
-from tests.step_util import Case
+from tests.step_util import E32, HALF, Case
 from tests.test_gpu_step import page_pool
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,109 @@ def test_attend_in_less_workspace(kind):
     with pytest.raises(abi.KameraError) as e:
         step.upload(c.lay, exact, c.pool, (ws.data_ptr(), sizes * 3 // 2))
     assert e.value.name == "KAMERA_E_WORKSPACE"
+
+
+# ------------------------------------------------------------------ numbers that are not finite, where they are seen
+def formula(q, k, v, scale, last):
+    """softmax(scale q k^T) v as it stands, 0 * inf = NaN included, for queries [n][G][dk] over keys [T][dk]; keys of score
+    -inf weigh nothing, and where all do the sum of weights is 0: output 0 (NaN where 0 * inf), lse -inf. Also the sums
+    that Case's bounds are made of, over what is finite."""
+    n, g, _ = q.shape
+    out, absv = np.zeros((n, g, v.shape[1])), np.zeros((n, g, v.shape[1]))
+    lse, terms = np.full((n, g), -np.inf), np.zeros((n, g))
+    for i in range(n):
+        t = int(last[i]) + 1
+        for h in range(g if t > 0 else 0):
+            prods = scale * q[i, h] * k[:t]
+            s = prods.sum(1)
+            m = np.nan if np.isnan(s).any() else s.max()
+            p = np.zeros(t) if m == -np.inf else np.exp(s - m)
+            total = p.sum()
+            out[i, h] = (p[:, None] * v[:t]).sum(0) / (total if total != 0 else 1.0)
+            absv[i, h] = (p[:, None] * np.abs(np.where(np.isfinite(v[:t]), v[:t], 0))).sum(0) / (total if total != 0 else 1.0)
+            lse[i, h] = m + np.log(total) if total != 0 else -np.inf
+            live = np.isfinite(s) & (p > 0)
+            if live.any():
+                terms[i, h] = np.abs(prods[live]).sum(1).max()
+    return out, lse, absv, terms
+
+
+def check_formula(c, s, ws, scale):
+    """One layer's outputs against formula(): the same infinities and NaN, the rest within Case's bounds."""
+    got, gz = attend(c, s, ws, scale)
+    torch.cuda.synchronize()
+    got, gz = got[0].double().cpu().numpy().reshape(c.n, c.heads, c.dv), gz[0].double().cpu().numpy()
+    f64 = [p[0].double().cpu().numpy() for p in c.pools]
+    q = c.q[0].double().cpu().numpy().reshape(c.n, c.heads, c.dk)
+    n0, np_ = 0, len(c.prefix_tokens)
+    with np.errstate(all="ignore"):
+        for r, (pre, own, nq, flags) in enumerate(c.requests):
+            head = c.rows[pre] if pre >= 0 else np.zeros(0, np.int64)
+            at = np.concatenate([head, c.rows[np_ + r]])
+            last = np.maximum(head.size + own - nq + np.arange(nq), head.size - 1)
+            for h in range(c.hkv):
+                k, v = f64[0][at, h * c.dk:(h + 1) * c.dk], f64[-1][at, h * c.dk:h * c.dk + c.dv]
+                sl = slice(h * c.g, (h + 1) * c.g)
+                o, z, a, terms = formula(q[n0:n0 + nq, sl], k, v, scale, last)
+                x, y = got[n0:n0 + nq, sl], gz[n0:n0 + nq, sl]
+                where = (r, h)
+                assert (np.isnan(x) == np.isnan(o)).all(), (where, np.argwhere(np.isnan(x) != np.isnan(o))[:4].tolist(), int(np.isnan(o).sum()))
+                assert (np.isinf(x) == np.isinf(o)).all() and (x[np.isinf(o)] == o[np.isinf(o)]).all(), where
+                assert (np.isnan(y) == np.isnan(z)).all() and (np.isneginf(y) == np.isneginf(z)).all(), where
+                # as in Case.expect_attend; a weight too small for fp32 may be 0: 2^-126 of a value
+                ds = (c.dk + 8) * E32 * terms[..., None]
+                rel = 2 * ds + (2 * at.size + 128) * E32 + (HALF[BF16] if c.dtype == BF16 else 0.0)
+                fin = np.isfinite(o)
+                assert (np.abs(x - o) <= rel * (a + np.abs(o)) + HALF[c.dtype] * np.abs(o) + 1e-37)[fin].all(), where
+                fin = np.isfinite(z)
+                assert (np.abs(y - z) <= ds[..., 0] + (at.size + 128) * E32 + 8 * E32 * np.abs(z))[fin].all(), where
+            n0 += nq
+
+
+SPOILS = ["inf under no weight", "inf", "nan", "inf and -inf", "key -inf", "key inf", "key nan", "all keys -inf"]
+
+
+def spoil(c, what, slots, col):
+    """Puts what is not finite into key and value rows; queries are positive, so a key column of -inf is a score of -inf."""
+    k, v = c.pools[0][0], c.pools[-1][0]
+    at = torch.from_numpy(np.asarray(slots)).cuda()
+    inf = float("inf")
+    for h in range(c.hkv):
+        if what == "inf under no weight":
+            k[at, h * c.dk:(h + 1) * c.dk] = -200.0
+            v[at, h * c.dk + col] = -inf if c.family == MLA else inf
+        elif what in ("inf", "nan"):
+            v[at, h * c.dk + col] = float(what)
+        elif what == "inf and -inf":
+            v[at[::2], h * c.dk + col] = inf
+            v[at[1::2], h * c.dk + col] = -inf
+        elif what.startswith("key"):
+            k[at, h * c.dk + (c.dk - 1 if c.family == MLA else col)] = float(what[4:])  # (MLA: in the rope band)
+        else:
+            k[at, h * c.dk + col] = -inf
+
+
+@pytest.mark.parametrize("what", SPOILS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_seen_numbers_that_are_not_finite_act_as_in_the_formula(kind, what):
+    """Whatever the plan: keys in the middle of a range, at its masked end, alone in a part, in shared and own tokens."""
+    for seed, (prefix, own, nq) in enumerate([(300, 70, 2), (2100, 45, 1), (0, 150, 40), (40, 3, 3)]):
+        c = Case(layers=1, prefixes=[prefix], requests=[(0, own, nq), (0, 33, 1), (0, own + 9, 1), (-1, 40, 2)], seed=seed, **kind)
+        c.q.abs_()
+        for r, rows in enumerate(c.rows):
+            if rows.size == 0:
+                continue
+            n = rows.size
+            some = rows if what == "all keys -inf" and r == 3 else rows[sorted({n // 3, max(n - 3, 0), n - 1})] if r % 2 == 0 else rows[:1]
+            spoil(c, what, some, (5 * r + 1) % c.dv)
+        s = c.step(step.ATTEND | step.FIT)
+        ws = c.workspace(s)
+        for part in (1.0, 0.5, 0.05, 0.0):
+            least = (int(ws.numel() * part) + 255) // 256 * 256
+            while True:  # the first size from there on that is taken
+                try:
+                    check_formula(c, s, (ws.data_ptr(), least), 0.25)
+                    break
+                except abi.KameraError as e:
+                    assert e.name == "KAMERA_E_WORKSPACE"
+                    least = least * 5 // 4 + 256
