@@ -21,6 +21,14 @@ constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// Workgroups of a launch, in rows of kGridRow along the grid's second dimension: the runtime takes fewer
+// than 2^32 threads along the first. The last row may have some to spare.
+constexpr int64_t kGridRow = int64_t(1) << 22;
+dim3 grid_of(int64_t blocks, unsigned z = 1) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks, 1, z) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow), z);
+}
+__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
+
 // Element types by their storage: uint16_t holds bf16 bits, float itself.
 template <typename T>
 __device__ __forceinline__ float to_float(T x);
@@ -76,7 +84,7 @@ __device__ __forceinline__ int64_t pool_row(const StepArgs& a, const KGLOBAL int
 __global__ __launch_bounds__(kThreads) void step_phase(StepArgs a) {
   const int half = a.d_rot >> 1;
   const int64_t n = (int64_t)a.num_tokens * half;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = (int64_t)block_number() * kThreads + threadIdx.x;
   if (i >= n) return;
   const int64_t t = i / half;
   const int p = (int)(i - t * half);
@@ -111,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void append_plain(StepArgs a, int64_t lay
   const int lane = threadIdx.x & 63;
   const int nq = r.q ? a.num_q_heads : 0;
   const int units = nq + a.heads + (a.family == KAMERA_GQA ? 1 : 0);
-  const int64_t task = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t task = (int64_t)block_number() * (kThreads / kWave) + (threadIdx.x >> 6);
   const int64_t t = task / units;
   if (t >= a.num_tokens) return;
   const int u = (int)(task - t * units);
@@ -223,7 +231,7 @@ __device__ __forceinline__ void load_phase(const StepArgs& a, int64_t t, int lan
 
 template <bool NEOX>
 __global__ __launch_bounds__(kThreads) void append_heads(StepArgs a, int64_t layer0, kamera_append_rows r, int lanes, int parts) {
-  const int64_t wave = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t wave = (int64_t)block_number() * (kThreads / kWave) + (threadIdx.x >> 6);
   const int64_t t = wave / parts;
   if (t >= a.num_tokens) return;
   const int lane = threadIdx.x & (lanes - 1), seat = (threadIdx.x & 63) / lanes, seats = kWave / lanes;
@@ -284,7 +292,7 @@ constexpr int kCopyTurns = 4;    // pieces a lane copies
 template <bool NEOX>
 __global__ __launch_bounds__(kThreads) void append_latent(StepArgs a, int64_t layer0, kamera_append_rows r, int lanes, int bands, int copies) {
   const int waves = bands + 1 + copies;
-  const int64_t wave = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t wave = (int64_t)block_number() * (kThreads / kWave) + (threadIdx.x >> 6);
   const int64_t t = wave / waves;
   if (t >= a.num_tokens) return;
   const int j = (int)(wave - t * waves), tid = threadIdx.x & 63;
@@ -364,7 +372,8 @@ __device__ __forceinline__ float shrink(float m, float to) { return m == to ? 1.
 
 template <typename T, int VEC, int NJ>
 __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io) {
-  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const int block = (int)block_number(), item = block / a.heads, head = block - item * a.heads;
+  if (item >= a.num_items) return;
   const AttendItem it = a.items[item];
   const AttendRun& run = it.run;
   const int lane = threadIdx.x & 63, dl = lane & 15, tg = lane >> 4;
@@ -462,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
 // taken in a fixed order, so the result does not depend on which workgroup finished first.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
-constexpr int kJoinQuads = kWave;  // quads of columns a workgroup takes (grid.y): a wave's parts side by side
+constexpr int kJoinQuads = kWave;  // quads of columns a workgroup takes (grid.z): a wave's parts side by side
 
 struct Parts {
   MergeToken mt;
@@ -498,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
   __shared__ f32x4 held[ROWS][TPR];
   __shared__ float red[ROWS][4];
   const int sub = threadIdx.x / TPR, tid = threadIdx.x - sub * TPR;
-  const int64_t task = (int64_t)blockIdx.x * ROWS + sub;
+  const int64_t task = (int64_t)block_number() * ROWS + sub;
   const int64_t i = min(task / a.num_q_heads, (int64_t)a.num_merge - 1);
   const int qh = (int)(task % a.num_q_heads);
   const bool live = task < (int64_t)a.num_merge * a.num_q_heads;
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
   }
   sum = over_threads<TPR, false>(sum, red[sub]);
   __syncthreads();
-  const int quads = a.dv / 4, c0 = blockIdx.y * kJoinQuads, wide = min(quads - c0, kJoinQuads);
+  const int quads = a.dv / 4, c0 = blockIdx.z * kJoinQuads, wide = min(quads - c0, kJoinQuads);
   T* out = (T*)io.out + (int64_t)a.merge[i].token * io.out_stride + (int64_t)qh * a.dv;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const KGLOBAL f32x4* rows = (const KGLOBAL f32x4*)a.part_o;
@@ -553,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(StepArgs a, AttendIo io)
   }
   if (live && first == 0)
     for (int e = 0; e < 4; ++e) out[4 * c + e] = from_float<T>(o[e] * inv);
-  if (live && io.lse && tid == 0 && blockIdx.y == 0)
+  if (live && io.lse && tid == 0 && blockIdx.z == 0)
     io.lse[(int64_t)a.merge[i].token * a.num_q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
@@ -564,7 +573,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void attend_join_few(StepArgs a, AttendIo io) {
   constexpr int P = kFewParts;
   const int quads = a.dv / 4;
-  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, task = at / quads;
+  const int64_t at = (int64_t)block_number() * kThreads + threadIdx.x, task = at / quads;
   const int c = (int)(at - task * quads);
   const int64_t i = task / a.num_q_heads;
   if (i >= a.num_merge) return;
@@ -603,7 +612,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_few(StepArgs a, AttendIo
 // Rows that are not whole 16-byte pieces: a wave a row, one part after the other.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void attend_join_any(StepArgs a, AttendIo io) {
-  const int64_t task = (int64_t)blockIdx.x * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t task = (int64_t)block_number() * (kThreads / kWave) + (threadIdx.x >> 6);
   const int64_t i = task / a.num_q_heads;
   if (i >= a.num_merge) return;
   const int qh = (int)(task - i * a.num_q_heads);
@@ -647,13 +656,13 @@ template <typename U, bool CHAINS>
 __global__ __launch_bounds__(kThreads) void copy_pages(CopyArgs a, InlineCopies in) {
   const int64_t cols = a.page_bytes / (int64_t)sizeof(U);
   const int64_t blocks = (cols + kThreads - 1) / kThreads;
-  int64_t b = blockIdx.x;
+  int64_t b = block_number();
   const int64_t col = (b % blocks) * kThreads + threadIdx.x;
   b /= blocks;
   const int chain = (int)(b % a.chains);
   b /= a.chains;
   const int layer = (int)(b % a.layers), tensor = (int)(b / a.layers);
-  if (col >= cols) return;
+  if (col >= cols || tensor >= a.tensors) return;
   U* base = (U*)(a.pool[tensor] + layer * a.layer_bytes) + col;
   if constexpr (!CHAINS) {  // each copy alone
     const PageCopy p = a.copies ? a.copies[chain] : in.c[chain];
@@ -686,12 +695,13 @@ template <typename U>
 __global__ __launch_bounds__(kThreads) void copy_rings(CopyArgs a) {
   const int64_t cols = a.page_bytes / (int64_t)sizeof(U);
   const int64_t blocks = (cols + kColumns - 1) / kColumns;
-  int64_t b = blockIdx.x;
+  int64_t b = block_number();
   const int64_t col = (b % blocks) * kColumns + threadIdx.x % kColumns;
   b /= blocks;
   const int ring = a.chains + (int)(b % a.rings);
   b /= a.rings;
   const int layer = (int)(b % a.layers), tensor = (int)(b / a.layers);
+  if (tensor >= a.tensors) return;  // (a whole workgroup)
   const KGLOBAL int32_t* copies = (const KGLOBAL int32_t*)a.copies;  // source, destination, source, ...
   const int r0 = a.chain[ring], n = a.chain[ring + 1] - r0, each = (n + kSegments - 1) / kSegments;
   const int c0 = r0 + min((int)(threadIdx.x / kColumns) * each, n), c1 = min(c0 + each, r0 + n);
@@ -724,7 +734,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <typename T, int VEC>
 hipError_t plain_attend(const StepArgs& a, const AttendIo& io, int64_t grid, hipStream_t stream) {
   const int nj = (a.dk + 16 * VEC - 1) / (16 * VEC);
-  const dim3 g((unsigned)grid), b(kThreads);
+  const dim3 g = grid_of(grid), b(kThreads);
   if (nj * VEC <= 8) hipLaunchKernelGGL((attend_plain<T, VEC, 8 / VEC>), g, b, 0, stream, a, io);
   else if (nj * VEC <= 16) hipLaunchKernelGGL((attend_plain<T, VEC, 16 / VEC>), g, b, 0, stream, a, io);
   else if (nj * VEC <= 40) hipLaunchKernelGGL((attend_plain<T, VEC, 40 / VEC>), g, b, 0, stream, a, io);
@@ -749,12 +759,12 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
   const int64_t rows = (int64_t)a.num_merge * a.num_q_heads;
   if (rows == 0) return hipSuccess;
   const dim3 b(kThreads);
-  const unsigned by_wave = (unsigned)ceil_div(rows, kThreads / kWave);
+  const int64_t by_wave = ceil_div(rows, kThreads / kWave);
   const unsigned blocks = (unsigned)ceil_div(a.dv / 4, kJoinQuads);
-  if (a.dv % 4) hipLaunchKernelGGL((attend_join_any<T>), dim3(by_wave), b, 0, stream, a, io);
-  else if (a.max_parts <= kFewParts) hipLaunchKernelGGL((attend_join_few<T>), dim3((unsigned)ceil_div(rows * (a.dv / 4), kThreads)), b, 0, stream, a, io);
-  else if (join_by_wave(rows, a.max_parts)) hipLaunchKernelGGL((attend_join<T, kWave>), dim3(by_wave, blocks), b, 0, stream, a, io);
-  else hipLaunchKernelGGL((attend_join<T, kThreads>), dim3((unsigned)rows, blocks), b, 0, stream, a, io);
+  if (a.dv % 4) hipLaunchKernelGGL((attend_join_any<T>), grid_of(by_wave), b, 0, stream, a, io);
+  else if (a.max_parts <= kFewParts) hipLaunchKernelGGL((attend_join_few<T>), grid_of(ceil_div(rows * (a.dv / 4), kThreads)), b, 0, stream, a, io);
+  else if (join_by_wave(rows, a.max_parts)) hipLaunchKernelGGL((attend_join<T, kWave>), grid_of(by_wave, blocks), b, 0, stream, a, io);
+  else hipLaunchKernelGGL((attend_join<T, kThreads>), grid_of(rows, blocks), b, 0, stream, a, io);
   return hipGetLastError();
 }
 
@@ -763,7 +773,7 @@ hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t strea
 hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream) {
   const int64_t blocks = ceil_div((int64_t)a.num_tokens * (a.d_rot / 2), kThreads);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(step_phase, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(step_phase, grid_of(blocks), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -789,7 +799,7 @@ hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_
     while (parts > 1 && (int64_t)a.num_tokens * (parts / 2) >= 4096) parts /= 2;
     blocks = grid((int64_t)a.num_tokens * parts);
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    const dim3 g((unsigned)blocks);
+    const dim3 g = grid_of(blocks);
     if (a.pairing == KAMERA_NEOX) hipLaunchKernelGGL((append_heads<true>), g, b, 0, stream, a, layer0, rows, lanes, parts);
     else hipLaunchKernelGGL((append_heads<false>), g, b, 0, stream, a, layer0, rows, lanes, parts);
   } else if (vec) {
@@ -797,13 +807,13 @@ hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_
     const int copies = nq == 0 || rows.q == rows.q_out ? 0 : (int)ceil_div((int64_t)nq * (a.latent / 8), kCopyTurns * kWave);
     blocks = grid((int64_t)a.num_tokens * (bands + 1 + copies));
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    const dim3 g((unsigned)blocks);
+    const dim3 g = grid_of(blocks);
     if (a.pairing == KAMERA_NEOX) hipLaunchKernelGGL((append_latent<true>), g, b, 0, stream, a, layer0, rows, lanes, bands, copies);
     else hipLaunchKernelGGL((append_latent<false>), g, b, 0, stream, a, layer0, rows, lanes, bands, copies);
   } else {
     blocks = grid((int64_t)a.num_tokens * (nq + a.heads + (gqa ? 1 : 0)));
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    const dim3 g((unsigned)blocks);
+    const dim3 g = grid_of(blocks);
     if (a.dtype == KAMERA_BF16) hipLaunchKernelGGL((append_plain<uint16_t>), g, b, 0, stream, a, layer0, rows);
     else hipLaunchKernelGGL((append_plain<float>), g, b, 0, stream, a, layer0, rows);
   }
@@ -827,7 +837,7 @@ hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStre
   if (blocks > 0x7fffffffLL || ring_blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   static const InlineCopies kNone = {};
   const InlineCopies& in = inl ? *inl : kNone;
-  const dim3 g((unsigned)blocks), b(kThreads), gr((unsigned)ring_blocks);
+  const dim3 g = grid_of(blocks), b(kThreads), gr = grid_of(ring_blocks);
   if (blocks > 0 && a.chain) {
     if (a.unit == 16) hipLaunchKernelGGL((copy_pages<u32x4, true>), g, b, 0, stream, a, in);
     else if (a.unit == 4) hipLaunchKernelGGL((copy_pages<uint32_t, true>), g, b, 0, stream, a, in);

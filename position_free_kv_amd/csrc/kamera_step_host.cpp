@@ -522,7 +522,9 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   }
   st = check_workspace(ws, ws_bytes, f.total);
   if (st != KAMERA_OK) return st;
-  if ((int64_t)w.items.size() * h.heads >= (int64_t(1) << 31)) return host_fail(KAMERA_E_SHAPE, "too many work items");
+  // (the matrix-core kernels' workgroups lie along one dimension of the grid, which takes fewer than 2^32 threads)
+  const int most = kernel == ATTEND_PLAIN ? 31 : kernel == ATTEND_HEADS ? 24 : 23;
+  if ((int64_t)w.items.size() * h.heads >= (int64_t(1) << most)) return host_fail(KAMERA_E_SHAPE, "too many work items");
 
   thread_local std::vector<unsigned char> blob;
   blob.assign(f.upload, 0);

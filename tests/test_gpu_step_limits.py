@@ -217,3 +217,61 @@ def test_seen_numbers_that_are_not_finite_act_as_in_the_formula(kind, what):
                 except abi.KameraError as e:
                     assert e.name == "KAMERA_E_WORKSPACE"
                     least = least * 5 // 4 + 256
+
+
+# ------------------------------------------------------------------ launches of more than 2^32 threads
+def small_pages(layers, pages, tensors):
+    """Pools of 4-byte pages, every page of every layer with bits of its own."""
+    family = GQA if tensors == 2 else MLA
+    lay = abi.make_layout(family, BF16, layers, num_kv_heads=1, head_dim=2, latent_dim=0, rope_dim=2, page_size=1)
+    pools = [torch.arange(layers * pages, dtype=torch.int32, device="cuda").mul_(2654435761 % 2 ** 31).add_(t).view(layers, pages) for t in range(tensors)]
+    return lay, abi.make_pool(pools[0], pools[1] if tensors == 2 else None, pages), pools
+
+
+@pytest.mark.parametrize("layers,pages,n,chained,tensors", [
+    (520, 33000, 16384, False, 2),       # 17.0M workgroups, one a page and layer
+    (700, 33000, 16384, True, 2),        # pairs of pages change places: 11.5M, two copies and a kept page each
+    (1100, 33000, 16384, True, 2),       # 18.0M
+    ((1 << 24) + 70000, 66, 65, True, 1),  # a ring in each of 16.8M layers
+])
+def test_page_copies_of_more_than_2_24_workgroups(layers, pages, n, chained, tensors):
+    rng = np.random.default_rng(n)
+    order = rng.permutation(pages).astype(np.int32)
+    if n < 1000:
+        src, dst = np.roll(order[:n], -1), order[:n]
+    elif chained:
+        src, dst = order[:n], order[:n].reshape(-1, 2)[:, ::-1].reshape(-1)
+    else:
+        src, dst = order[:n], order[n:2 * n]
+    lay, pool, pools = small_pages(layers, pages, tensors)
+    want = [p.clone() for p in pools]
+    s, d = (torch.from_numpy(x.astype(np.int64)).cuda() for x in (src, dst))
+    for w, p in zip(want, pools):
+        w[:, d] = p[:, s]
+    ws = torch.empty(step.copy_pages_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    step.copy_pages(lay, pool, src, dst, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
+def test_append_and_attend_of_more_than_2_24_workgroups():
+    """65536 heads of two columns: 17.0M and 34.1M workgroups; position 0 turns nothing, and one key is its value."""
+    heads, n = 65536, 520
+    f = 2 * heads
+    lay = abi.make_layout(GQA, BF16, 1, num_kv_heads=heads, head_dim=2, page_size=1)
+    pools = [torch.zeros(1, n, f, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pool = abi.make_pool(*pools, n)
+    table = np.random.default_rng(0).permutation(n).astype(np.int32)
+    rows = [torch.randint(-100, 100, (n, f), dtype=torch.int16, device="cuda").bfloat16() for _ in range(3)]
+    positions = torch.zeros(n, 3, dtype=torch.int32, device="cuda")
+    s = step.Step(num_q_heads=heads, block_tables=table.reshape(n, 1), num_tokens=1, num_queries=1, positions=positions)
+    ws = torch.empty(step.workspace_bytes(lay, s), dtype=torch.uint8, device="cuda")
+    plan = step.upload(lay, s, pool, ws)
+    q, out = torch.empty_like(rows[0]), torch.empty_like(rows[0])
+    step.append(plan, 0, q=rows[0], k=rows[1], v=rows[2], q_out=q)
+    step.attend(plan, 0, q, out, 1.0)
+    torch.cuda.synchronize()
+    at = torch.from_numpy(table.astype(np.int64)).cuda()
+    assert torch.equal(q, rows[0])
+    assert torch.equal(pools[0][0, at], rows[1]) and torch.equal(pools[1][0, at], rows[2])
+    assert torch.equal(out, rows[2])
