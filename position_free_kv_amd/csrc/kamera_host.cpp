@@ -159,6 +159,9 @@ int row_width(const kamera_layout* L) {
   return L->family == KAMERA_GQA ? L->num_kv_heads * L->head_dim : L->latent_dim + L->rope_dim;
 }
 
+// A launch has fewer threads along a dimension of its grid; the runtime would run a larger one in part.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
 struct Packed {
   std::vector<unsigned char>& blob;  // header | chunks | pages (thread-local, reused across calls)
   std::vector<int64_t>& page_off;    // per chunk: offset (entries) of its page table, -1 if dense
@@ -521,6 +524,8 @@ kamera_status pack_batch(const kamera_layout* L, const kamera_chunk* chunks, int
   hd->total_tasks = task;
   out.phase_blocks = (out.phase_max + kBlockThreads - 1) / kBlockThreads;
   hd->phase_blocks = (int32_t)std::min<int64_t>(out.phase_blocks, 0x7fffffff);  // the launcher rejects larger
+  if (task * (mfma ? kWaveSize : kBlockThreads) >= kMaxThreads - 1024 || out.phase_blocks * kBlockThreads >= kMaxThreads)
+    return fail(KAMERA_E_SHAPE, "too much work for one launch (%lld tasks): split the batch", (long long)task);
   out.tasks = task;
   out.kernel = task == 0 ? 0 : (mfma ? 1 : 2);
   out.variant = 0;
@@ -557,9 +562,12 @@ const DevChunk* ws_chunks(const void* ws) {
 // batch has re-anchored chunks) are computed there, on the same stream.
 kamera_status launch_phase_tables(const Packed& pk, int n, void* ws, void* stream) {
   if (pk.phase_entries <= 0) return KAMERA_OK;
-  const hipError_t e = launch_phase_table(ws_header(ws), ws_chunks(ws), n, pk.phase_blocks, (hipStream_t)stream,
-                                          nullptr);
-  if (e != hipSuccess) return fail(KAMERA_E_HIP, "phase table launch failed: %s", hipGetErrorString(e));
+  const int64_t some = std::max<int64_t>((kMaxThreads - 1) / (kBlockThreads * pk.phase_blocks), 1);  // chunks a launch takes
+  for (int64_t i = 0; i < n; i += some) {
+    const hipError_t e = launch_phase_table(ws_header(ws), ws_chunks(ws) + i, (int)std::min<int64_t>(some, n - i), pk.phase_blocks,
+                                            (hipStream_t)stream, nullptr);
+    if (e != hipSuccess) return fail(KAMERA_E_HIP, "phase table launch failed: %s", hipGetErrorString(e));
+  }
   return KAMERA_OK;
 }
 
