@@ -138,8 +138,9 @@ def formula(q, k, v, scale, last):
     return out, lse, absv, terms
 
 
-def check_formula(c, s, ws, scale):
-    """One layer's outputs against formula(): the same infinities and NaN, the rest within Case's bounds."""
+def check_formula(c, s, ws, scale, rounded=True):
+    """One layer's outputs against formula(): the same infinities and NaN, the rest within Case's bounds (rounded: with the
+    probabilities' rounding to bf16)."""
     got, gz = attend(c, s, ws, scale)
     torch.cuda.synchronize()
     got, gz = got[0].double().cpu().numpy().reshape(c.n, c.heads, c.dv), gz[0].double().cpu().numpy()
@@ -162,7 +163,7 @@ def check_formula(c, s, ws, scale):
                 assert (np.isnan(y) == np.isnan(z)).all() and (np.isneginf(y) == np.isneginf(z)).all(), where
                 # as in Case.expect_attend; a weight too small for fp32 may be 0: 2^-126 of a value
                 ds = (c.dk + 8) * E32 * terms[..., None]
-                rel = 2 * ds + (2 * at.size + 128) * E32 + (HALF[BF16] if c.dtype == BF16 else 0.0)
+                rel = 2 * ds + (2 * at.size + 128) * E32 + (HALF[BF16] if c.dtype == BF16 and rounded else 0.0)
                 fin = np.isfinite(o)
                 assert (np.abs(x - o) <= rel * (a + np.abs(o)) + HALF[c.dtype] * np.abs(o) + 1e-37)[fin].all(), where
                 fin = np.isfinite(z)
@@ -275,3 +276,13 @@ def test_append_and_attend_of_more_than_2_24_workgroups():
     assert torch.equal(q, rows[0])
     assert torch.equal(pools[0][0, at], rows[1]) and torch.equal(pools[1][0, at], rows[2])
     assert torch.equal(out, rows[2])
+
+
+# ------------------------------------------------------------------ the plain kernel's roundings
+@pytest.mark.parametrize("kind", [dict(heads=4, kv_heads=2, head_dim=80), dict(heads=3, kv_heads=1, head_dim=10), dict(family=MLA, heads=3, latent=20, rope=6),
+                                  dict(heads=4, kv_heads=2, head_dim=128, offset=1)])
+def test_plain_attention_rounds_bf16_once(kind):
+    """Outside the matrix cores no probability is rounded: all that is left is fp32 arithmetic and the output's own rounding."""
+    c = Case(layers=1, prefixes=[300], requests=[(0, 40, 1), (0, 9, 3), (-1, 70, 2), (-1, 2, 1), (-1, 3, 2)], seed=8, **kind)
+    s = c.step(step.ATTEND)
+    check_formula(c, s, c.workspace(s), 0.2, rounded=False)
