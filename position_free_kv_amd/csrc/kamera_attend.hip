@@ -50,8 +50,9 @@ constexpr int kPlace = kStageKeys * 2 * D;
 // take the second half (PAIRS); the pairs' results are joined at the end.
 //
 // Bound by the loads into LDS and the clock together: 2481 query tokens of 28 + 4 heads over 8192 shared
-// and their own keys (308 GFLOP) take 395 us, 0.78 PFLOP/s (a large library product: 1.22); without loads
-// 335 us, loads alone 155, without the exponentials 400 of 427. Two workgroups of 64 KB share a CU: a
+// and their own keys (308 GFLOP) take 361 us, 0.85 PFLOP/s (a large library product: 1.22), while the clock
+// holds (steps one after the other; the first twenty from rest 376 to 447). Of 427 us on another occasion:
+// 335 without loads, 155 loads alone, 400 without the exponentials. Two workgroups of 64 KB share a CU: a
 // tile of 256 rows with 8 waves (half the loads) took as long, four stages of 32 keys 443 us, and raised
 // wave priority around the products 438.
 // ============================================================================
@@ -114,7 +115,7 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
 // 4 waves walks stages of 32 keys of its own, at its own pace, and the four results are joined in LDS.
 // One buffer a wave: two workgroups share a CU, so that the other waves' reads are in flight while one
 // computes. Up to 16 rows take the products of 16 rows. Bound by reading pages: 32 + 8 heads, 16 requests
-// over 131072 shared keys and 28296 own ones, 652 MB a layer in 132 us (4.9 TB/s; loads without products
+// over 131072 shared keys and 28296 own ones, 652 MB a layer in 130 us (5.0 TB/s; loads without products
 // 135 us, products without loads 62). All heads of an item on one XCD: 139 us.
 // ============================================================================
 template <int D, int ROWS>

@@ -6,12 +6,12 @@
 // registers of queries and 128 of output, so that two waves share a SIMD and one's softmax runs under
 // the other's products. LDS bounds the wide kernel: per 32 keys each of its 8 waves issues 68 products
 // (1088 cycles; two waves a SIMD) and reads 68 KB, 544 KB together at 128 bytes a cycle: 4250 cycles,
-// 1.29 PFLOP/s. 32 rows a wave would halve that traffic, but its 400 registers did not compile
-// without spills.
+// 1.29 PFLOP/s. 32 rows a wave would halve that traffic, but its 400 registers did not compile without
+// many spills; this form has 9 (24 bytes of scratch a lane), a few of them reloaded in every step.
 //
 // 32 requests of 16 heads over 4096 shared and 15888 own keys take 28 us a layer: launch and the first
-// dependent reads 7, queries 4, the partial rows (36 MB) 6, the keys 11. Tiles of 256 keys instead of 128
-// halve the partial rows but take 34 us, the join 8.8 instead of 9.7.
+// dependent reads 7, queries 4, the partial rows (36 MB) 6, the keys 11; then the join, 9. Items of 256 keys
+// instead of 128 halve the partial rows but took 34 us, the join 8.8 instead of 9.7.
 #include "kamera_attend.h"
 
 namespace kamera {

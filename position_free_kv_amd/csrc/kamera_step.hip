@@ -363,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void append_latent(StepArgs a, int64_t la
 // wave per row of the tile. A wave reads 4 tokens at a time, 16 lanes to a token, each lane
 // holding VEC * NJ of the key's columns; every 16-lane group runs its own online softmax
 // (running maximum m and sum l in base-2 logarithms, o scaled by exp2(m_old - m)) and the four
-// are joined at the end. Bound by latency: 5 requests of 8 f32 heads over 300 shared keys take 11.0 us, of
+// are joined at the end. Bound by latency: 5 requests of 8 f32 heads over 300 shared keys take 10.4 us, of
 // which the chain item, page id, row is most. On large work it is far behind the matrix cores (decode of
 // 64 requests over 8192 shared keys, 4 layers: 5873 us, 255 with them), which take every bf16 layout they can.
 // ============================================================================
@@ -467,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
 // (token, query head). First every part's maximum and sum become its weight, all parts at once; then
 // the weighted rows are added, 16 bytes a thread, several parts side by side where a row is shorter
 // than the threads; rows of more than 256 columns are shared by workgroups, which fills the chip where
-// rows are few (512 MLA rows of 36 parts: 12.9 us with one workgroup a row, 9.7 with two). Parts are
+// rows are few (512 MLA rows of 36 parts: 9.4 us with one workgroup a row, 9.2 with two). Parts are
 // taken in a fixed order, so the result does not depend on which workgroup finished first.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;

@@ -94,8 +94,8 @@ constexpr int tile_rows(int kernel, int tile) {
 }
 
 constexpr int kMaxSplits = 512;  // ranges a run's keys are cut into, at most
-// A wave joins a row where rows abound (2048 rows of 10 parts: 7.6 us, 9.3 us by workgroups; 1024 rows of
-// 11: 6.7 us and 6.0) or parts are few, a workgroup otherwise.
+// A wave joins a row where rows abound (2048 rows of 10 parts: 7.0 us, 8.9 us by workgroups; 1024 rows of
+// 11: 6.4 us and 5.8) or parts are few, a workgroup otherwise.
 constexpr bool join_by_wave(int64_t rows, int parts) { return parts <= 8 || (parts <= 64 && rows >= 2048); }
 
 // One attention launch: what kamera_step_attend was given.
