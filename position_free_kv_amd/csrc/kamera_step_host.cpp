@@ -270,6 +270,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     double tiles = 0, keys = 0;
   } cls[3];
   for (const AttendRun& r : w.runs) {
+    if (r.kv == 0) continue;
     const int64_t rows = (int64_t)r.ntok * G;
     Class& c = cls[r.tile];
     const double tiles = (double)ceil_div(rows, tile_rows(kernel, r.tile));

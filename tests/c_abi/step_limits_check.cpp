@@ -150,6 +150,17 @@ struct Steps {
   }
 };
 
+// Requests that see no key leave the others' ranges as they are.
+void empty_requests() {
+  std::vector<std::pair<int64_t, int64_t>> requests(40, {300, 1});
+  Steps some(KAMERA_GQA, KAMERA_BF16, 32, 8, 128, {}, requests);
+  requests.resize(200, {0, 1});
+  Steps more(KAMERA_GQA, KAMERA_BF16, 32, 8, 128, {}, requests);
+  const size_t bytes = std::max(some.bytes(), more.bytes());
+  Buffer ws(bytes);
+  CHECK(some.run(ws.p, bytes) == more.run(ws.p, bytes));
+}
+
 // One buffer, sized for the longest step, serves every shorter one.
 void one_workspace(Rng& r) {
   struct Kind {
@@ -228,6 +239,7 @@ int main() {
   Rng r(4711);
   compaction(r);
   one_workspace(r);
+  empty_requests();
   std::printf("ok\n");
   return 0;
 }
