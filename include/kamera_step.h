@@ -147,11 +147,11 @@ kamera_status kamera_step_append(const kamera_step_plan* plan, int32_t layer, co
  * lse (fp32 [N][num_q_heads], packed, may be NULL) receives log(sum(exp(scale q.k))).
  * Scores, softmax statistics and sums are fp32; on the matrix cores the probabilities enter
  * the second product in bf16. Values of unseen tokens and unused slots are not read into any
- * result, whatever they hold; infinities and NaN that a query sees act as in the formula (0 * inf
- * is NaN), but a query all of whose scores are -inf has sum 0, output 0 and lse -inf. Results
- * are the same bits on every run of a step (KAMERA_STEP_FIT: in a workspace of the same size).
- * The plan's workspace holds the partial results, so launches of one plan belong on one stream
- * at a time. */
+ * result, whatever they hold. Infinities and NaN that a query sees act as in the formula (0 * inf
+ * is NaN; with a scale of 0, keys that are not finite give unspecified results), but a query all
+ * of whose scores are -inf has sum 0, output 0 and lse -inf. Results are the same bits on every
+ * run of a step (KAMERA_STEP_FIT: in a workspace of the same size). The plan's workspace holds
+ * the partial results, so launches of one plan belong on one stream at a time. */
 kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
                                  void* out, int64_t out_stride, float* lse, float scale, void* stream);
 
