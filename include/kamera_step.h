@@ -12,6 +12,13 @@
  *                        write the new K and V rows into the pool's pages
  *   kamera_step_attend   per layer: attention of every query token over its request's
  *                        prefix and own tokens, a shared prefix read once for all of them
+ *   kamera_step_attend_diff
+ *                        per layer, instead: differential attention, the difference of two
+ *                        softmax maps with learned weights
+ *   kamera_step_weigh    per layer: add what each cached token received of the step's attention
+ *                        weights to scores kept beside the pool
+ *   kamera_evict         the tokens of least score leave their sequences, in every layer: the
+ *                        others move together, in their order
  *   kamera_copy_pages, kamera_compact_pages
  *                        copy pages inside the pool, in every layer: fork a tail page,
  *                        reorder pages, move the live pages together
@@ -34,7 +41,10 @@ extern "C" {
 enum {
   KAMERA_STEP_APPEND = 1u, /* kamera_step_append */
   KAMERA_STEP_ATTEND = 2u, /* kamera_step_attend */
-  KAMERA_STEP_FIT = 4u     /* the plan keeps to the workspace it is given (see kamera_step_workspace_bytes) */
+  KAMERA_STEP_FIT = 4u,    /* the plan keeps to the workspace it is given (see kamera_step_workspace_bytes) */
+  KAMERA_STEP_WEIGH = 16u, /* kamera_step_weigh */
+  KAMERA_STEP_DIFFERENTIAL = 32u /* with ATTEND: kamera_step_attend_diff instead of kamera_step_attend;
+                                    with WEIGH: query heads belong to key heads as there */
 };
 /* request flags */
 enum {
@@ -80,7 +90,8 @@ typedef struct kamera_step {
   int32_t num_q_heads;            /* GQA: a multiple of num_kv_heads, query head h reading KV head
                                      h / (num_q_heads / num_kv_heads); MLA: any; 0 with
                                      KAMERA_STEP_APPEND alone: no queries                          */
-  uint32_t flags;                 /* KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND (at least one), FIT   */
+  uint32_t flags;                 /* KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND | KAMERA_STEP_WEIGH (at
+                                     least one), FIT, DIFFERENTIAL                                 */
   int32_t reserved[2];            /* must be 0                                                   */
 } kamera_step;
 
@@ -110,7 +121,8 @@ size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_ste
 /* Validate a step and put its description into the workspace (256-byte aligned), on `stream`,
  * through the same staging slots as kamera_plan_upload (which see for blocking); not from a
  * capturing stream (KAMERA_E_UNSUPPORTED): record the launches of the plan instead. Pool slots that the step appends to must be distinct and must not belong to a
- * prefix of the step (KAMERA_E_OVERLAP). */
+ * prefix of the step (KAMERA_E_OVERLAP). With KAMERA_STEP_WEIGH, the slots of the requests that have
+ * queries and of their prefixes must be distinct: each score is added to once (KAMERA_E_OVERLAP). */
 kamera_status kamera_step_upload(const kamera_layout* layout, const kamera_step* step, const kamera_pool* pool,
                                  void* workspace, size_t workspace_bytes, void* stream, kamera_step_plan* plan);
 
@@ -154,6 +166,92 @@ kamera_status kamera_step_append(const kamera_step_plan* plan, int32_t layer, co
  * the partial results, so launches of one plan belong on one stream at a time. */
 kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
                                  void* out, int64_t out_stride, float* lse, float scale, void* stream);
+
+/* Differential attention of the step's N query tokens in layer `layer` (KAMERA_GQA, num_kv_heads even,
+ * a step of KAMERA_STEP_ATTEND | KAMERA_STEP_DIFFERENTIAL). KV heads 2p and 2p + 1 are a pair: each has
+ * its keys, and the pair's values are the 2 head_dim columns of both. Query heads 2i and 2i + 1 are the
+ * two maps of output head i; its pair is p = i / (num_q_heads / num_kv_heads), the first map reads the keys
+ * of KV head 2p, the second those of 2p + 1. With A the softmax of scale * q . K^T over the tokens that
+ * the query sees:
+ *     x = A_first V - lambda A_second V
+ *     lambda = exp(lambdas[0] . lambdas[1]) - exp(lambdas[2] . lambdas[3]) + lambda_init
+ *     out = x / sqrt(mean(x^2) + eps) * norm_weight * out_scale   (KAMERA_DIFF_NORM; else x * out_scale)
+ * q [N][num_q_heads][head_dim], out [N][num_q_heads / 2][2 head_dim], element type the layout's,
+ * strides in elements between tokens, 0: packed. lse (fp32 [N][num_q_heads], packed, may be NULL) as
+ * kamera_step_attend's, of each map. A map all of whose scores are -inf, or that sees nothing, is 0, and
+ * a row of zeros stays zero under the norm, whatever eps. Everything else as kamera_step_attend:
+ * fp32 but for the probabilities, one rounding at the end, unseen tokens not read into any result. */
+enum { KAMERA_DIFF_NORM = 1u };
+typedef struct kamera_differential {
+  const float* lambdas;    /* device [4][head_dim] fp32; NULL: lambda = lambda_init         */
+  const void* norm_weight; /* device [2 head_dim], the layout's type, or NULL (ones)        */
+  float lambda_init;       /* finite                                                        */
+  float out_scale;         /* finite                                                        */
+  float eps;               /* >= 0, finite                                                  */
+  uint32_t flags;          /* KAMERA_DIFF_NORM                                              */
+} kamera_differential;
+kamera_status kamera_step_attend_diff(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
+                                      void* out, int64_t out_stride, float* lse, float scale,
+                                      const kamera_differential* diff, void* stream);
+
+/* Adds the attention weights of the step's N query tokens in layer `layer` to the scores of the tokens
+ * that receive them (a step of KAMERA_STEP_WEIGH):
+ *     scores[t][h] = decay * scores[t][h] + sum of exp(scale * q . K[t][h] - lse)
+ * over the query rows of KV head h that see token t; q and lse are what the layer's attention read and
+ * wrote, scale its scale. scores: fp32, of this layer, in pages like the pool's: score of KV head h (MLA:
+ * 0) at slot o of page p at [(p * heads + h) * page_size + o]. Every token of a request with queries and of
+ * its prefix is met once, a shared prefix by the sum over all its requests' queries; the scores of other
+ * slots are not touched. decay 0: scores are not read. Sums are fp32, in an order that the plan fixes. A row
+ * whose lse is -inf adds nothing; otherwise infinities and NaN that a row sees act as in the formula,
+ * what it does not see has no effect. The plan's workspace holds partial sums, so launches of one plan
+ * belong on one stream at a time. */
+kamera_status kamera_step_weigh(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
+                                const float* lse, float* scores, float scale, float decay, void* stream);
+
+/* A sequence of cached tokens that loses some. */
+typedef struct kamera_evict_seq {
+  const int32_t* block_table; /* HOST page ids: token t lies at slot slot0 + t of the table (may be NULL if num_tokens == 0) */
+  int32_t slot0;              /* 0 <= slot0 < page_size                                          */
+  int32_t num_tokens;         /* >= 0                                                            */
+  int32_t keep;               /* >= 0: tokens that stay; num_tokens and more: all of them        */
+  int32_t first, last;        /* >= 0: of them the first and the last of the sequence, whatever their scores;
+                                 first + last <= keep, unless all tokens stay                    */
+  int32_t reserved;           /* must be 0                                                       */
+} kamera_evict_seq;
+
+enum {
+  KAMERA_EVICT_REANCHOR = 1u /* a key that moves from token i to token j of its sequence is turned by j - i positions
+                                (R(j - i) of kamera.h over the whole band): survivors stand at consecutive positions */
+};
+
+/* In every layer, and for each group of heads_together KV heads (MLA: 1), the `keep` tokens of each
+ * sequence that stay: its first and last ones, and of those between the ones with the highest scores, equal
+ * scores from the lowest token on (0 and -0 are equal, NaN is lowest, below -inf). A group's score is the fp32 sum of
+ * its heads' scores, added in their order. Layers and groups keep tokens of their own. The kept tokens' K and V
+ * columns and scores move to the sequence's first `keep` slots, in their order; what lies behind them is left as it
+ * was. (The caller then lowers the request's num_tokens; with REANCHOR position0 + token stays the
+ * position of every token.) Pool slots of different sequences must be distinct (KAMERA_E_OVERLAP). Moved bits are unchanged
+ * but for turned keys, computed in fp32 (cos/sin rounded once from fp64) and rounded once. */
+typedef struct kamera_eviction {
+  const kamera_evict_seq* seqs; /* HOST [num_seqs]                                                 */
+  float* scores;                /* device fp32: layer l's (as kamera_step_weigh's) at scores + l * scores_stride */
+  int64_t scores_stride;        /* elements; 0: packed, num_pages * heads * page_size              */
+  int32_t* kept;                /* device [num_layers][groups][sum of min(keep, num_tokens)], or NULL: receives the
+                                   token numbers that stayed, ascending, sequence after sequence    */
+  int32_t num_seqs;
+  int32_t heads_together;       /* divides num_kv_heads; 2 for kamera_step_attend_diff's pairs     */
+  uint32_t flags;               /* KAMERA_EVICT_REANCHOR                                           */
+  int32_t reserved;             /* must be 0                                                       */
+} kamera_eviction;
+/* Bytes of device workspace of an eviction (256-byte aligned; 0 if the arguments are invalid). The tables are
+ * staged, so the call cannot be recorded in a captured graph (KAMERA_E_UNSUPPORTED). */
+size_t kamera_evict_workspace_bytes(const kamera_layout* layout, const kamera_eviction* eviction);
+kamera_status kamera_evict(const kamera_layout* layout, const kamera_pool* pool, const kamera_eviction* eviction,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* The layout under which kamera_copy_pages and kamera_compact_pages move the scores of a pool of layout
+ * `layout` like its pages: a pool of one tensor (k_pool = scores, v_pool = NULL), as many pages. */
+kamera_status kamera_scores_layout(const kamera_layout* layout, kamera_layout* scores);
 
 /* In every layer, K and V: page dst[i] becomes what page src[i] was before the call, for all
  * i at once (a page may be both a source and a destination; a source may feed several).

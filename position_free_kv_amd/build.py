@@ -6,8 +6,9 @@ The library is the C ABI of include/kamera.h: host validation and packing
 (csrc/kamera_host.cpp) plus the gfx950 kernels: the operator
 (csrc/kamera_kernels.hip), the patch builder (csrc/kamera_builder.hip) and the
 streaming probes used for measurement (csrc/kamera_probe.hip); and the serving step of
-include/kamera_step.h: its host part (csrc/kamera_step_host.cpp) and kernels
-(csrc/kamera_step.hip, csrc/kamera_attend*.hip).
+include/kamera_step.h: its host parts (csrc/kamera_step_host.cpp,
+csrc/kamera_evict_host.cpp) and kernels (csrc/kamera_step.hip, csrc/kamera_attend*.hip,
+csrc/kamera_weigh.hip, csrc/kamera_evict.hip).
 """
 from __future__ import annotations
 
@@ -30,7 +31,9 @@ ARCH = os.environ.get("KAMERA_OFFLOAD_ARCH", "gfx950")
 HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
 
-STEP_KERNELS = ["kamera_step", "kamera_attend", "kamera_attend_latent"]
+# The serving step beside its planner (kamera_step_host): kernels (.hip), and entry points of their own (.cpp).
+STEP_KERNELS = ["kamera_step", "kamera_attend", "kamera_attend_latent", "kamera_attend_diff", "kamera_weigh", "kamera_evict",
+                "kamera_evict_host"]
 
 
 def hipcc() -> str:
@@ -62,13 +65,14 @@ def build(verbose_asm: bool = False) -> str:
     _run([cc, "-x", "c++", *COMMON, "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", "-c",
           os.path.join(CSRC, "kamera_host.cpp"), "-o", hobj])
     step_objs = []
-    for name in STEP_KERNELS:
+    for name in [*STEP_KERNELS, "kamera_step_host"]:
         step_objs.append(os.path.join(objdir, name + ".o"))
-        _run([cc, f"--offload-arch={ARCH}", *COMMON, *HIP_FLAGS, "-c", os.path.join(CSRC, name + ".hip"),
-              "-o", step_objs[-1]])
-    step_objs.append(os.path.join(objdir, "kamera_step_host.o"))
-    _run([cc, "-x", "c++", *COMMON, "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", "-c",
-          os.path.join(CSRC, "kamera_step_host.cpp"), "-o", step_objs[-1]])
+        source = os.path.join(CSRC, name + ".hip")
+        if os.path.exists(source):
+            _run([cc, f"--offload-arch={ARCH}", *COMMON, *HIP_FLAGS, "-c", source, "-o", step_objs[-1]])
+        else:
+            _run([cc, "-x", "c++", *COMMON, "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", "-c",
+                  os.path.join(CSRC, name + ".cpp"), "-o", step_objs[-1]])
     tmp = LIB + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", kobj, bobj, pobj, hobj, *step_objs, "-o", tmp])
     os.replace(tmp, LIB)

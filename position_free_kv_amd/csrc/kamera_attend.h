@@ -125,14 +125,15 @@ __device__ __forceinline__ int key_entry(const StepArgs& a, const AttendRun& run
 }
 
 // Running state of a wave's ROWS (32 or 16) query rows: keys of DK columns, values of DV. In LDS the
-// first DV columns of a key are a row of 2 DV bytes, the others (MLA's rope band) a row of another
+// first DV columns of a key (DK if there are fewer) are a row, the others (MLA's rope band) a row of another
 // place. 32 rows: v_mfma_f32_32x32x16_bf16, lane = 32 g + n; 16 rows:
 // v_mfma_f32_16x16x32_bf16, lane = 16 g + n (n: the row; g: the k slots of an operand, 8 each). A step
 // takes 32 keys. Score i of lane (g, n) is that of key slot_key(i).
 template <int DK, int DV, int ROWS>
 struct State {
   static constexpr int kRow = 2 * DV;
-  static constexpr int kRestRow = 2 * (DK - DV);       // 0: no other columns
+  static constexpr int kKeyRow = 2 * (DK < DV ? DK : DV);
+  static constexpr int kRestRow = 2 * DK - kKeyRow;    // 0: no other columns
   static constexpr int kGroups = 64 / ROWS;            // 2 or 4
   static constexpr int kDepth = 8 * kGroups;           // k slots of a product: 16 or 32
   static constexpr int kKSteps = DK / kDepth;          // products of a score tile
@@ -215,12 +216,12 @@ struct State {
   static __device__ __forceinline__ bf16x8 k_operand(const KLDS char* k, const KLDS char* rest, int tile, int ks) {
     constexpr int kLaneBytes = ROWS == 32 ? 16 : 32;           // between groups
     const int c = ROWS == 32 ? 32 * ks : 128 * (ks >> 1) + 16 * (ks & 1);  // bytes of operand ks in the row
-    if (c < kRow) {
-      constexpr int kSpan = kRow % 256 == 0 ? 256 : 128;
-      const int at = row() * kRow + ((group() * kLaneBytes) ^ (swz<ROWS, kRow>(row()) << 4));
-      return *(const KLDS bf16x8*)(k + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + tile * ROWS * kRow));
+    if (c < kKeyRow) {
+      constexpr int kSpan = kKeyRow % 256 == 0 ? 256 : 128;
+      const int at = row() * kKeyRow + ((group() * kLaneBytes) ^ (swz<ROWS, kKeyRow>(row()) << 4));
+      return *(const KLDS bf16x8*)(k + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + tile * ROWS * kKeyRow));
     }
-    const int at = row() * kRestRow + ((group() * kLaneBytes) ^ (swz<ROWS, 128>(row()) << 4)), c2 = c - kRow;
+    const int at = row() * kRestRow + ((group() * kLaneBytes) ^ (swz<ROWS, 128>(row()) << 4)), c2 = c - kKeyRow;
     return *(const KLDS bf16x8*)(rest + ((at ^ (c2 % 128)) + (c2 / 128) * 128 + tile * ROWS * kRestRow));
   }
 
@@ -382,7 +383,7 @@ struct State {
                                        int end, float scale2) {
     Acc s[NT][kTiles];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) score(s[n], q, k + n * 32 * kRow, rest + n * 32 * kRestRow);
+    for (int n = 0; n < NT; ++n) score(s[n], q, k + n * 32 * kKeyRow, rest + n * 32 * kRestRow);
     float top = -INFINITY, bottom = INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -427,12 +428,13 @@ __device__ __forceinline__ void stage_barrier() {
 template <int TS, int NT, int DK, int DV, int ROWS>
 __device__ __forceinline__ void walk(State<DK, DV, ROWS>& st, const bf16x8 (&q)[State<DK, DV, ROWS>::kKSteps], const KLDS char* k,
                                      const KLDS char* rest, const KLDS char* v, int t, int end, int end_min, int end_max, float scale2) {
+  typedef State<DK, DV, ROWS> S;
   int s = 0;
 #pragma nounroll
   for (; s < TS && t + s + 32 * NT <= end_min; s += 32 * NT)
-    st.template step<NT, false>(q, k + s * 2 * DV, rest + s * 2 * (DK - DV), v + s * 2 * DV, t + s, end, scale2);
+    st.template step<NT, false>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * 2 * DV, t + s, end, scale2);
 #pragma nounroll
-  for (; s < TS && t + s < end_max; s += 32) st.template step<1, true>(q, k + s * 2 * DV, rest + s * 2 * (DK - DV), v + s * 2 * DV, t + s, end, scale2);
+  for (; s < TS && t + s < end_max; s += 32) st.template step<1, true>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * 2 * DV, t + s, end, scale2);
 }
 
 // N consecutive columns of a row's result: normalised into the output, or as a partial row.

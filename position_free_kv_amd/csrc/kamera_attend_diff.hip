@@ -1,0 +1,348 @@
+// Differential attention over the paged pool (include/kamera_step.h): bf16 heads of 64 or 128 columns on the
+// matrix cores (method and register layouts: kamera_attend.h; work list: kamera_step_desc.h), and the join of
+// partial rows that makes an output row of its two maps, for any layout.
+//
+// The "head" of an item is a pair of KV heads: two keys of D columns a token, one value of 2 D columns. Rows
+// of a run alternate between the maps (row = token's number * group + query head of the pair), and a wave takes
+// 32 (or 16) rows of one map, so that a stage's values are brought into LDS once for both maps.
+#include "kamera_attend.h"
+
+namespace kamera {
+
+namespace {
+
+constexpr int kWaveSize = 64;
+constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
+dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+
+// Stages lie in one array: keys of the first map, of the second, values.
+template <int D>
+constexpr int kKeyBytes = 2 * D;
+template <int D>
+constexpr int kValueBytes = 4 * D;
+constexpr int kLds = 65536;
+
+// N keys of a stage of TS from `first` on, by one wave. Lane i looks up the pool row of key first + i % N one
+// stage ahead, and the loads take it from there.
+template <int D, int TS, int N, int ROWS>
+struct PairRows {
+  int row;
+  __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int last) {
+    int place;
+    const int t = min(t0 + first + ((int)threadIdx.x & (N - 1)), last);
+    const int page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, t, place)];
+    row = page * a.page_size + place;
+  }
+  // k and v: the layer's rows from the pair's first column on
+  __device__ __forceinline__ void load(const StepArgs& a, const uint16_t* k, const uint16_t* v, KLDS char* stage, int first) const {
+    constexpr int RK = 1024 / kKeyBytes<D>, LK = 64 / RK, RV = 1024 / kValueBytes<D>, LV = 64 / RV;  // rows of an instruction, lanes of a row
+    static_assert(N % RK == 0, "whole instructions");
+    const int lane = threadIdx.x & 63;
+    KLDS char* values = stage + 2 * TS * kKeyBytes<D>;
+#pragma unroll
+    for (int i = 0; i < N; i += RK) {
+      const int64_t at = (int64_t)__shfl(row, i + lane / LK, kWaveSize) * a.row + ((lane & (LK - 1)) ^ swz<ROWS, kKeyBytes<D>>(first + i + lane / LK)) * 8;
+#pragma unroll
+      for (int map = 0; map < 2; ++map)
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(k + at + map * D), (KLDS void*)(stage + (map * TS + first + i) * kKeyBytes<D>), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += RV) {
+      const int64_t at = (int64_t)__shfl(row, i + lane / LV, kWaveSize) * a.row + ((lane & (LV - 1)) ^ swz<ROWS, kValueBytes<D>>(first + i + lane / LV)) * 8;
+      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(v + at), (KLDS void*)(values + (first + i) * kValueBytes<D>), 16, 0, 0);
+    }
+  }
+};
+
+// ============================================================================
+// Tiles of 128 rows: two waves a map, 32 rows each, share stages of 32 (D = 128) or 64 keys, two in LDS.
+// ============================================================================
+template <int D>
+__device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds) {
+  constexpr int TS = 4096 / D, N = TS / kWaves, NT = TS / 32;
+  typedef State<D, 2 * D, 32> S;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, map = wave & 1;
+  const uint16_t* kp = a.k_pool + io.layer0 + head * 2 * D;
+  const uint16_t* vp = a.v_pool + io.layer0 + head * 2 * D;
+  const int first = wave * N, last = it.kv1 - 1;
+  const bool any = it.kv1 > it.kv0;
+  KLDS char* const stage[2] = {lds, lds + kLds / 2};
+  PairRows<D, TS, N, 32> rows;
+  if (any) {
+    rows.find(a, it.run, it.kv0, first, last);
+    rows.load(a, kp, vp, stage[0], first);
+    rows.find(a, it.run, it.kv0 + TS, first, last);
+  }
+  const Lane r = lane_row(a, it, head, it.row0 + (wave >> 1) * 64 + 2 * (lane & 31) + map);
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, 31);
+  bf16x8 q[S::kKSteps];
+  S::load_q(io, r, q);
+  S st;
+  st.clear();
+  auto work = [&](const KLDS char* s, int t) {
+    const KLDS char* k = s + map * TS * kKeyBytes<D>;
+    walk<TS, NT>(st, q, k, k, s + 2 * TS * kKeyBytes<D>, t, r.end, end_min, end_max, io.scale2);
+  };
+  if (any) {
+    for (int t = it.kv0;;) {
+      stage_barrier();
+      if (t + TS < it.kv1) {
+        rows.load(a, kp, vp, stage[1], first);
+        rows.find(a, it.run, t + 2 * TS, first, last);
+      }
+      work(stage[0], t);
+      if ((t += TS) >= it.kv1) break;
+      stage_barrier();
+      if (t + TS < it.kv1) {
+        rows.load(a, kp, vp, stage[0], first);
+        rows.find(a, it.run, t + 2 * TS, first, last);
+      }
+      work(stage[1], t);
+      if ((t += TS) >= it.kv1) break;
+    }
+  }
+  const float l = row_sum<32>(st.l);
+  put_state(a, io, it, head, r, st, l);
+}
+
+// ============================================================================
+// Tiles of up to 64 rows (32: ROWS 16): a wave for each map and half of a stage of 64 (D = 128) or 128 keys. One
+// buffer: the other workgroup of the CU computes while this one loads. The halves are joined at the end.
+// ============================================================================
+template <int D, int ROWS>
+__device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds,
+                                            float (&ml)[2][kWaves][64]) {
+  constexpr int TS = 8192 / D, N = TS / kWaves, HALF = TS / 2;
+  typedef State<D, 2 * D, ROWS> S;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), map = wave & 1, part = wave >> 1;
+  const uint16_t* kp = a.k_pool + io.layer0 + head * 2 * D;
+  const uint16_t* vp = a.v_pool + io.layer0 + head * 2 * D;
+  const int first = wave * N, last = it.kv1 - 1;
+  PairRows<D, TS, N, ROWS> rows;
+  if (it.kv1 > it.kv0) {
+    rows.find(a, it.run, it.kv0, first, last);
+    rows.load(a, kp, vp, lds, first);
+  }
+  const Lane r = lane_row(a, it, head, it.row0 + 2 * S::row() + map);
+  const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, ROWS - 1);
+  bf16x8 q[S::kKSteps];
+  S::load_q(io, r, q);
+  S st;
+  st.clear();
+  for (int t = it.kv0; t < it.kv1; t += TS) {
+    if (t + TS < it.kv1) rows.find(a, it.run, t + TS, first, last);
+    stage_barrier();
+    const KLDS char* k = (const KLDS char*)lds + (map * TS + part * HALF) * kKeyBytes<D>;
+    const KLDS char* v = (const KLDS char*)lds + 2 * TS * kKeyBytes<D> + part * HALF * kValueBytes<D>;
+    walk<HALF, 1>(st, q, k, k, v, t + part * HALF, r.end, end_min, end_max, io.scale2);
+    if (t + TS >= it.kv1) break;
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
+    __syncthreads();
+    rows.load(a, kp, vp, lds, first);
+  }
+  float l = row_sum<ROWS>(st.l);
+  static_assert(2 * 64 * S::kBlocks * S::kScores * 4 <= kLds, "two waves' results fit in LDS");
+  join_two(st, l, part == 1, map, (f32x4*)(KLDS f32x4*)(lds + map * (kLds / 2)), ml);
+  if (part == 0) put_state(a, io, it, head, r, st, l);
+}
+
+// One launch for all tiles, the wide ones first.
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo io) {
+  __shared__ __align__(1024) char lds[kLds];
+  __shared__ float ml[2][kWaves][64];
+  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const AttendItem it = a.items[item];
+  if (item < a.num_wide) wide_tile<D>(a, io, it, head, (KLDS char*)lds);
+  else if (item < a.num_wide + a.num_pairs) narrow_tile<D, 32>(a, io, it, head, (KLDS char*)lds, ml);
+  else narrow_tile<D, 16>(a, io, it, head, (KLDS char*)lds, ml);
+}
+
+// ============================================================================
+// Join of partial rows: an output row's two maps lie in neighbouring partial rows, 2 dv numbers side by side, which
+// the threads share in 16-byte pieces. WPR waves a row; parts are taken in a fixed order. The maps' normalised
+// rows meet in LDS, and the norm follows.
+// ============================================================================
+constexpr int kJoinParts = 2 * kMaxSplits;
+
+__device__ __forceinline__ float wave_sum(float x) {
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, kWaveSize);
+  return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+  for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, kWaveSize));
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ T narrowed(float x) {
+  if constexpr (sizeof(T) == 2) return (T)pack2(x, 0.0f);
+  else return x;
+}
+template <typename T>
+__device__ __forceinline__ float widened(T x) {
+  if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)x << 16);
+  else return x;
+}
+
+// PIECES: 16-byte pieces of the two rows that a lane takes
+template <typename T, int WPR, int PIECES>
+__global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
+  constexpr int ROWS = kWaves / WPR;
+  __shared__ float2 weight[ROWS][WPR == 1 ? kWaveSize : kJoinParts];
+  __shared__ f32x4 held[kWaves][PIECES * kWaveSize];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = wave / WPR, seat = wave % WPR;
+  const int outs = a.num_q_heads / 2;
+  const int64_t task = (int64_t)(blockIdx.y * (uint32_t)kGridRow + blockIdx.x) * ROWS + sub;
+  const bool live = task < (int64_t)a.num_merge * outs;
+  const int64_t i = live ? task / outs : 0;
+  const int oh = (int)(task % outs), head = 2 * oh / a.group, g = 2 * oh % a.group;
+  const MergeToken mt = a.merge[i];
+  const int n = mt.splits[0] + mt.splits[1];
+  auto row = [&](int k) {  // of the first map; the second's is the next
+    const int s = k >= mt.splits[0];
+    return mt.part[s] + ((int64_t)(s ? k - mt.splits[0] : k) * a.heads + head) * mt.rows[s] + mt.row0[s] + g;
+  };
+  // lambda, while the parts' statistics are on their way
+  float lambda = diff.lambda_init;
+  float d0 = 0.0f, d1 = 0.0f;
+  if (diff.lambdas) {
+    const KGLOBAL float* p = (const KGLOBAL float*)diff.lambdas;
+    for (int c = lane; c < a.dk; c += kWaveSize) {
+      d0 += p[c] * p[a.dk + c];
+      d1 += p[2 * a.dk + c] * p[3 * a.dk + c];
+    }
+  }
+  float top0 = -INFINITY, top1 = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
+  const KGLOBAL f32x4* stats = (const KGLOBAL f32x4*)a.part_ml;  // (rows of the first map are even)
+  for (int k = lane; k < n; k += kWaveSize) {
+    const f32x4 s = stats[row(k) >> 1];
+    if (s[1] != 0.0f) top0 = fmaxf(top0, s[0]);
+    if (s[3] != 0.0f) top1 = fmaxf(top1, s[2]);
+  }
+  top0 = wave_max(top0);
+  top1 = wave_max(top1);
+  for (int k = lane; k < n; k += kWaveSize) {
+    const f32x4 s = stats[row(k) >> 1];
+    const float w0 = s[1] == 0.0f ? 0.0f : s[0] == top0 ? 1.0f : __builtin_amdgcn_exp2f(s[0] - top0);
+    const float w1 = s[3] == 0.0f ? 0.0f : s[2] == top1 ? 1.0f : __builtin_amdgcn_exp2f(s[2] - top1);
+    sum0 += s[1] * w0;
+    sum1 += s[3] * w1;
+    if (k % WPR == seat || WPR == 1) weight[sub][k] = make_float2(w0, w1);
+  }
+  sum0 = wave_sum(sum0);
+  sum1 = wave_sum(sum1);
+  if (diff.lambdas) lambda += expf(wave_sum(d0)) - expf(wave_sum(d1));
+  __syncthreads();
+  const int quads = a.dv / 4;  // of a map's row
+  const KGLOBAL f32x4* parts = (const KGLOBAL f32x4*)a.part_o;
+  f32x4 o[PIECES];
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) o[j] = (f32x4)(0.0f);
+#pragma unroll 4
+  for (int k = seat; k < n; k += WPR) {
+    const float2 w = weight[sub][k];
+    const KGLOBAL f32x4* p = parts + row(k) * quads;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const int f = j * kWaveSize + lane;
+      if (f >= 2 * quads) continue;
+      const f32x4 x = p[f];
+      const float wf = f < quads ? w.x : w.y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] += x[e] * wf;  // (an empty part's row is 0)
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) held[wave][j * kWaveSize + lane] = o[j];
+  __syncthreads();
+  if (seat != 0 || !live) return;
+  const float inv0 = sum0 == 0.0f ? 0.0f : 1.0f / sum0, inv1 = sum1 == 0.0f ? 0.0f : 1.0f / sum1;
+  f32x4 x[(PIECES + 1) / 2];
+  float square = 0.0f;
+#pragma unroll
+  for (int j = 0; j < (PIECES + 1) / 2; ++j) {
+    const int c = j * kWaveSize + lane;
+    x[j] = (f32x4)(0.0f);
+    if (c >= quads) continue;
+    f32x4 y = held[wave][c], z = held[wave][quads + c];
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const f32x4 y2 = held[wave + w][c], z2 = held[wave + w][quads + c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] += y2[e];
+        z[e] += z2[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[j][e] = y[e] * inv0 - lambda * (z[e] * inv1);
+      square += x[j][e] * x[j][e];
+    }
+  }
+  float scale = diff.out_scale;
+  if (diff.flags & KAMERA_DIFF_NORM) {
+    const float ms = wave_sum(square) / (float)a.dv + diff.eps;
+    scale = ms == 0.0f ? 0.0f : scale / sqrtf(ms);
+  }
+  T* out = (T*)io.out + (int64_t)mt.token * io.out_stride + (int64_t)oh * a.dv;
+  const T* weights = (diff.flags & KAMERA_DIFF_NORM) ? (const T*)diff.norm_weight : nullptr;
+#pragma unroll
+  for (int j = 0; j < (PIECES + 1) / 2; ++j) {
+    const int c = j * kWaveSize + lane;
+    if (c >= quads) continue;
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = x[j][e] * scale * (weights ? widened<T>(weights[4 * c + e]) : 1.0f);
+    if (sizeof(T) == 2 && io.out_vec) {
+      *(KGLOBAL u32x2*)(KGLOBAL void*)(out + 4 * c) = (u32x2){pack2(y[0], y[1]), pack2(y[2], y[3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[4 * c + e] = narrowed<T>(y[e]);
+    }
+  }
+  if (io.lse && lane < 2) {
+    const float sum = lane ? sum1 : sum0, top = lane ? top1 : top0;
+    io.lse[(int64_t)mt.token * a.num_q_heads + 2 * oh + lane] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+template <typename T, int WPR>
+hipError_t join(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, hipStream_t stream) {
+  const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
+  const dim3 g = grid_of((rows + kWaves / WPR - 1) / (kWaves / WPR)), b(kThreads);
+  const int pieces = (a.dv / 2 + kWaveSize - 1) / kWaveSize;
+  if (pieces <= 1) hipLaunchKernelGGL((diff_join<T, WPR, 1>), g, b, 0, stream, a, io, diff);
+  else if (pieces <= 2) hipLaunchKernelGGL((diff_join<T, WPR, 2>), g, b, 0, stream, a, io, diff);
+  else if (pieces <= 4) hipLaunchKernelGGL((diff_join<T, WPR, 4>), g, b, 0, stream, a, io, diff);
+  else hipLaunchKernelGGL((diff_join<T, WPR, 8>), g, b, 0, stream, a, io, diff);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                                   float* lse, float scale, const kamera_differential& diff, hipStream_t stream) {
+  AttendIo io{q, out, lse, q_stride, out_stride, layer * a.layer_stride, fabsf(scale) * 1.44269504088896340736f, scale < 0.0f, 0, 0};
+  // -inf marks a masked score: a scale of zero would make it NaN, the smallest one keeps it
+  if (a.kernel != ATTEND_PLAIN) io.scale2 = fmaxf(io.scale2, 1.17549435e-38f);
+  io.q_vec = q_stride % 8 == 0 && (uintptr_t)q % 16 == 0;
+  io.out_vec = out_stride % 4 == 0 && (uintptr_t)out % 8 == 0;
+  hipError_t e = hipSuccess;
+  if (a.kernel == ATTEND_PLAIN) {
+    e = launch_attend_plain(a, io, stream);
+  } else if (a.num_items > 0) {
+    const dim3 g((unsigned)((int64_t)a.num_items * a.heads)), b(kThreads);
+    if (a.dk == 128) hipLaunchKernelGGL((attend_diff<128>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((attend_diff<64>), g, b, 0, stream, a, io);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || a.num_merge == 0) return e;
+  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && (int64_t)a.num_merge * a.num_q_heads < 4096);
+  if (a.dtype == KAMERA_BF16) return wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
+  return wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);
+}
+
+}  // namespace kamera

@@ -1,0 +1,390 @@
+// Eviction (include/kamera_step.h) for gfx950: which tokens stay, and their rows moved together.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kamera_step_desc.h"
+
+namespace kamera {
+
+#define KGLOBAL __attribute__((address_space(1)))
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWave = 64;
+constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
+dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Page and place in it of token t of a sequence.
+__device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s, int t, int& place) {
+  const int slot = s.slot0 + t;
+  const int pg = (int)(((uint64_t)(uint32_t)slot * a.page_magic) >> a.page_bits);
+  place = slot - pg * a.page_size;
+  return ((const KGLOBAL int32_t*)a.pages)[s.pg + pg];
+}
+
+// ============================================================================
+// Which tokens stay: a workgroup for each list (layer, group of heads, sequence). Scores become 32-bit
+// numbers of the same order; the `want`-th highest of the tokens between the first and the last ones is
+// found digit by digit (11, 11 and 10 bits, a count of each digit in LDS), then one pass in the tokens' order
+// writes the numbers of those above it and of the first few equal to it. No order of atomics matters:
+// counts are whole numbers.
+// ============================================================================
+constexpr int kSelect = 512;   // threads
+constexpr int kDigits = 2048;
+constexpr int kEach = 4;       // tokens of a thread in one turn of the last pass
+
+__device__ __forceinline__ uint32_t rank_of(float x) {
+  if (x != x) return 0;
+  const uint32_t u = __float_as_uint(x + 0.0f);  // (-0 becomes 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct List {
+  EvictSeq seq;
+  const KGLOBAL float* scores;  // of the layer, from the group's first head on
+  int group;
+  __device__ __forceinline__ int64_t score_at(const EvictArgs& a, int t) const {
+    int place;
+    const int64_t page = page_of(a, seq, t, place);
+    return page * a.heads * a.page_size + place;
+  }
+  __device__ __forceinline__ uint32_t rank(const EvictArgs& a, int t) const {
+    const KGLOBAL float* p = scores + score_at(a, t);
+    float x = p[0];
+    for (int h = 1; h < a.together; ++h) x += p[(int64_t)h * a.page_size];
+    return rank_of(x);
+  }
+};
+
+__device__ __forceinline__ int wave_prefix(uint64_t mask) { return __popcll(mask & ((uint64_t(1) << (threadIdx.x & 63)) - 1)); }
+
+__global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
+  __shared__ uint32_t count[kDigits];
+  __shared__ int sums[kSelect / kWave][2];
+  __shared__ int found[2];
+  __shared__ int gone;
+  const int groups = a.heads / a.together, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t b = block_number();
+  const int si = (int)(b % a.num_seqs);
+  b /= a.num_seqs;
+  const int group = (int)(b % groups), layer = (int)(b / groups);
+  if (layer >= a.layers) return;
+  List l;
+  l.seq = a.seqs[si];
+  l.group = group;
+  l.scores = (const KGLOBAL float*)a.scores + layer * a.scores_stride + (int64_t)group * a.together * a.page_size;
+  const int n = l.seq.num_tokens, keep = min(l.seq.keep, n);
+  KGLOBAL int32_t* kept = (KGLOBAL int32_t*)a.kept + ((int64_t)layer * groups + group) * a.total + l.seq.kept0;
+  KGLOBAL int32_t* start = (KGLOBAL int32_t*)a.starts + ((int64_t)layer * groups + group) * a.num_seqs + si;
+  if (keep == n || keep == 0) {
+    for (int j = tid; j < keep; j += kSelect) kept[j] = j;
+    if (tid == 0) *start = keep;
+    return;
+  }
+  const int lo = l.seq.first, hi = n - l.seq.last;  // those that are ranked
+  int want = keep - l.seq.first - l.seq.last;
+  uint32_t border = 0, known = 0;  // bits of the border's rank found so far
+  for (int pass = 0; pass < 3 && want > 0; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < kDigits; i += kSelect) count[i] = 0;
+    __syncthreads();
+    for (int t = lo + tid; t < hi; t += kSelect) {
+      const uint32_t r = l.rank(a, t);
+      if ((r & known) == border) atomicAdd(&count[(r >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    __syncthreads();
+    // the digit at which the counts from the highest on reach `want`
+    constexpr int PER = kDigits / kSelect;
+    int mine = 0;
+    for (int i = 0; i < PER; ++i) mine += (int)count[kDigits - 1 - (tid * PER + i)];
+    int up = mine;  // inclusive sum over the wave
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int y = __shfl_up(up, d, kWave);
+      if (lane >= d) up += y;
+    }
+    if (lane == 63) sums[wave][0] = up;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) up += sums[w][0];
+    int before = up - mine;
+    if (before < want && up >= want)
+      for (int i = 0; i < PER; ++i) {
+        const int digit = kDigits - 1 - (tid * PER + i), c = (int)count[digit];
+        if (before < want && before + c >= want) {
+          found[0] = digit;
+          found[1] = want - before;
+        }
+        before += c;
+      }
+    __syncthreads();
+    border |= (uint32_t)found[0] << shift;
+    want = found[1];  // of those with the digit
+    known |= ((1u << bits) - 1) << shift;
+    __syncthreads();
+  }
+  const bool ranked = known != 0;
+  // tokens that stay, in their order
+  if (tid == 0) gone = n;
+  int above = 0, equal = 0;  // of the turns before
+  for (int t0 = 0; t0 < n; t0 += kSelect * kEach) {
+    bool hit[kEach], tie[kEach];
+    int at[kEach], tied[kEach], a0 = 0, e0 = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = t0 + (wave * kEach + i) * kWave + lane;
+      hit[i] = t < n && (t < lo || t >= hi);
+      tie[i] = false;
+      if (ranked && t >= lo && t < hi) {
+        const uint32_t r = l.rank(a, t);
+        hit[i] = r > border;
+        tie[i] = r == border;
+      }
+      const uint64_t h = __ballot(hit[i]), e = __ballot(tie[i]);
+      at[i] = a0 + wave_prefix(h);
+      tied[i] = e0 + wave_prefix(e);
+      a0 += __popcll(h);
+      e0 += __popcll(e);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sums[wave][0] = a0;
+      sums[wave][1] = e0;
+    }
+    __syncthreads();
+    int abase = above, ebase = equal;
+    for (int w = 0; w < kSelect / kWave; ++w) {
+      if (w < wave) {
+        abase += sums[w][0];
+        ebase += sums[w][1];
+      }
+      above += sums[w][0];
+      equal += sums[w][1];
+    }
+    int leaves = n;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = t0 + (wave * kEach + i) * kWave + lane;
+      const int ties = ebase + tied[i];
+      if (hit[i] || (tie[i] && ties < want)) kept[abase + at[i] + min(ties, want)] = t;
+      else if (t < n) leaves = min(leaves, t);
+    }
+    if (leaves < n) atomicMin(&gone, leaves);
+  }
+  __syncthreads();  // (the list is written, and visible to the workgroup)
+  const int s0 = min(gone, keep);
+  if (tid == 0) *start = s0;
+  // The scores move with their tokens: a turn's reads are over before its writes begin, and later turns read
+  // from places that earlier ones do not write, as token kept[j] >= j.
+  KGLOBAL float* scores = (KGLOBAL float*)(float*)l.scores;
+  for (int h = 0; h < a.together; ++h)
+    for (int j0 = s0; j0 < keep; j0 += kSelect * kEach) {
+      float x[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = j0 + i * kSelect + tid;
+        if (j < keep) x[i] = scores[l.score_at(a, kept[j]) + (int64_t)h * a.page_size];
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = j0 + i * kSelect + tid;
+        if (j < keep) scores[l.score_at(a, j) + (int64_t)h * a.page_size] = x[i];
+      }
+    }
+}
+
+// cos/sin of turning back by t positions, formed in fp64 and rounded once
+__global__ __launch_bounds__(256) void evict_phase(EvictArgs a) {
+  const int half = a.d_rot >> 1;
+  const int64_t i = (int64_t)block_number() * 256 + threadIdx.x, t = i / half;
+  if (t >= a.shifts) return;
+  const int p = (int)(i - t * half);
+  double s, c;
+  sincos(-(double)t * ((const KGLOBAL double*)a.theta)[p], &s, &c);
+  a.phase[t * a.d_rot + p] = (float)c;
+  a.phase[t * a.d_rot + half + p] = (float)s;
+}
+
+// ============================================================================
+// Moves the kept rows together: a workgroup for each list, tensor and slice of the group's columns walks the
+// list in turns of ROWS rows. All reads of a turn are over before its writes begin; a later turn's rows lie
+// behind every row written so far (kept[j] >= j, ascending), so no other order is needed.
+// ============================================================================
+constexpr int kMove = 256;  // threads
+constexpr int kTurn = 8;    // rows of a thread in one turn
+
+// Columns as they are, in pieces of a U.
+template <typename U>
+struct Plain {
+  typedef U Held;
+  static __device__ __forceinline__ void read(const EvictArgs&, const KGLOBAL char* row, int unit, Held& x) { x = ((const KGLOBAL U*)row)[unit]; }
+  static __device__ __forceinline__ void write(const EvictArgs&, KGLOBAL char* row, int unit, const Held& x, int) { ((KGLOBAL U*)row)[unit] = x; }
+};
+
+template <typename T>
+__device__ __forceinline__ float wide(T x);
+template <>
+__device__ __forceinline__ float wide<uint16_t>(uint16_t x) {
+  return __uint_as_float((uint32_t)x << 16);
+}
+template <>
+__device__ __forceinline__ float wide<float>(float x) {
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ T rounded(float x);
+template <>
+__device__ __forceinline__ uint16_t rounded<uint16_t>(float x) {
+  return __builtin_bit_cast(uint16_t, (__bf16)x);  // to nearest even
+}
+template <>
+__device__ __forceinline__ float rounded<float>(float x) {
+  return x;
+}
+
+// Pairs of rotated columns, one a unit; `units` of them make a head, whose columns lie side by side.
+template <typename T>
+struct Turned {
+  struct Held {
+    T a, b;
+  };
+  static __device__ __forceinline__ void places(const EvictArgs& a, int unit, int& p, int& i, int& j) {
+    const int half = a.d_rot >> 1, head = unit / half;
+    p = unit - head * half;
+    const int c0 = head * (a.head_bytes / (int)sizeof(T));
+    i = c0 + (a.pairing == KAMERA_NEOX ? p : 2 * p);
+    j = a.pairing == KAMERA_NEOX ? i + half : i + 1;
+  }
+  static __device__ __forceinline__ void read(const EvictArgs& a, const KGLOBAL char* row, int unit, Held& x) {
+    int p, i, j;
+    places(a, unit, p, i, j);
+    x.a = ((const KGLOBAL T*)row)[i];
+    x.b = ((const KGLOBAL T*)row)[j];
+  }
+  static __device__ __forceinline__ void write(const EvictArgs& a, KGLOBAL char* row, int unit, const Held& x, int back) {
+    int p, i, j;
+    places(a, unit, p, i, j);
+    const KGLOBAL float* cs = (const KGLOBAL float*)a.phase + (int64_t)back * a.d_rot;
+    const float c = cs[p], s = cs[(a.d_rot >> 1) + p], xa = wide<T>(x.a), xb = wide<T>(x.b);
+    ((KGLOBAL T*)row)[i] = rounded<T>(xa * c - xb * s);
+    ((KGLOBAL T*)row)[j] = rounded<T>(xa * s + xb * c);
+  }
+};
+
+// What a launch moves: `tensors` of the pool from tensor0 on, columns from byte `at` of a group on, `units` units
+// of them in slices of `slice`.
+struct Move {
+  int tensor0, tensors, at, units, slice, slices;
+};
+
+template <typename C>
+__global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, Move m) {
+  const int groups = a.heads / a.together, tid = threadIdx.x;
+  int64_t b = block_number();
+  const int slice = (int)(b % m.slices);
+  b /= m.slices;
+  const int si = (int)(b % a.num_seqs);
+  b /= a.num_seqs;
+  const int group = (int)(b % groups);
+  b /= groups;
+  const int tensor = m.tensor0 + (int)(b % m.tensors), layer = (int)(b / m.tensors);
+  if (layer >= a.layers) return;
+  const EvictSeq seq = a.seqs[si];
+  const int keep = min(seq.keep, seq.num_tokens);
+  if (keep == seq.num_tokens) return;
+  const int64_t list = (int64_t)layer * groups + group;
+  const int start = ((const KGLOBAL int32_t*)a.starts)[list * a.num_seqs + si];
+  const KGLOBAL int32_t* kept = (const KGLOBAL int32_t*)a.kept + list * a.total + seq.kept0;
+  KGLOBAL char* pool = (KGLOBAL char*)(a.pool[tensor] + layer * a.layer_bytes + (int64_t)group * a.together * a.head_bytes + m.at);
+  const int width = min(m.slice, m.units - slice * m.slice);  // units of this slice
+  const int side = kMove / m.slice;                            // rows side by side
+  const int row = tid / m.slice, in = tid - row * m.slice, unit = slice * m.slice + in;
+  const bool mine = row < side && in < width;
+  for (int j0 = start; j0 < keep; j0 += side * kTurn) {
+    typename C::Held x[kTurn];
+    int from[kTurn];
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      const int j = j0 + i * side + row;
+      from[i] = mine && j < keep ? kept[j] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      if (from[i] < 0) continue;
+      int place;
+      const int64_t page = page_of(a, seq, from[i], place);
+      C::read(a, pool + (page * a.page_size + place) * a.row_bytes, unit, x[i]);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      if (from[i] < 0) continue;
+      const int j = j0 + i * side + row;
+      int place;
+      const int64_t page = page_of(a, seq, j, place);
+      C::write(a, pool + (page * a.page_size + place) * a.row_bytes, unit, x[i], from[i] - j);
+    }
+  }
+}
+
+template <typename C>
+hipError_t move(const EvictArgs& a, Move m, hipStream_t stream) {
+  m.slice = m.units < 16 ? m.units : 16;
+  m.slices = (m.units + m.slice - 1) / m.slice;
+  const int64_t blocks = (int64_t)a.layers * m.tensors * (a.heads / a.together) * a.num_seqs * m.slices;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  if (blocks > 0) hipLaunchKernelGGL((evict_move<C>), grid_of(blocks), dim3(kMove), 0, stream, a, m);
+  return hipGetLastError();
+}
+
+// columns [at, at + bytes) of every group as they are
+hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, hipStream_t stream) {
+  if (bytes == 0 || tensors == 0) return hipSuccess;
+  auto fits = [&](int unit) {
+    bool ok = at % unit == 0 && bytes % unit == 0 && a.row_bytes % unit == 0 && a.layer_bytes % unit == 0 && (a.together * a.head_bytes) % unit == 0;
+    for (int t = tensor0; t < tensor0 + tensors; ++t) ok = ok && (uintptr_t)a.pool[t] % unit == 0;
+    return ok;
+  };
+  Move m{tensor0, tensors, at, bytes, 0, 0};
+  if (fits(16)) {
+    m.units = bytes / 16;
+    return move<Plain<u32x4>>(a, m, stream);
+  }
+  if (fits(4)) {
+    m.units = bytes / 4;
+    return move<Plain<uint32_t>>(a, m, stream);
+  }
+  m.units = bytes / 2;
+  return move<Plain<uint16_t>>(a, m, stream);
+}
+
+}  // namespace
+
+hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
+  const int64_t lists = (int64_t)a.layers * (a.heads / a.together) * a.num_seqs;
+  if (lists > 0x7fffffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(evict_select, grid_of(lists), dim3(kSelect), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.most_kept == 0) return e;
+  const int all = a.together * a.head_bytes;
+  if (!a.phase) return move_plain(a, 0, a.tensors, 0, all, stream);
+  const int64_t phases = ceil_div((int64_t)a.shifts * (a.d_rot / 2), 256);
+  if (phases > 0x7fffffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(evict_phase, grid_of(phases), dim3(256), 0, stream, a);
+  e = hipGetLastError();
+  const int es = a.dtype == KAMERA_BF16 ? 2 : 4;
+  if (e == hipSuccess) e = move_plain(a, 0, 1, 0, a.band0 * es, stream);
+  Move m{0, 1, a.band0 * es, a.together * (a.d_rot / 2), 0, 0};
+  if (e == hipSuccess) e = a.dtype == KAMERA_BF16 ? move<Turned<uint16_t>>(a, m, stream) : move<Turned<float>>(a, m, stream);
+  if (e == hipSuccess && a.tensors == 2) e = move_plain(a, 1, 1, 0, all, stream);
+  return e;
+}
+
+}  // namespace kamera

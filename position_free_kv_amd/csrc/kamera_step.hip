@@ -383,8 +383,9 @@ __global__ __launch_bounds__(kThreads) void attend_plain(StepArgs a, AttendIo io
   const int token = run.listed ? a.tok[run.tok0 + j] : run.tok0 + j;
   const int qh = head * a.group + g;
   const int end = min(it.kv1, max(run.len_a - 1, run.lim0 + j * run.lstep) + 1);
-  const KGLOBAL T* kp = (const KGLOBAL T*)a.k_pool + io.layer0 + (int64_t)head * a.dk;
-  const KGLOBAL T* vp = (const KGLOBAL T*)a.v_pool + io.layer0 + (int64_t)head * a.dk;
+  // (differential attention: a head is a pair of KV heads, whose keys belong to one map each)
+  const KGLOBAL T* kp = (const KGLOBAL T*)a.k_pool + io.layer0 + (int64_t)(a.differential ? 2 * head + (g & 1) : head) * a.dk;
+  const KGLOBAL T* vp = (const KGLOBAL T*)a.v_pool + io.layer0 + (int64_t)head * a.dv;
   const KGLOBAL int32_t* pages = (const KGLOBAL int32_t*)a.pages;
   const KGLOBAL T* qp = (const KGLOBAL T*)io.q + (int64_t)token * io.q_stride + (int64_t)qh * a.dk;
   float q[NJ * VEC], o[NJ * VEC];
@@ -733,7 +734,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <typename T, int VEC>
 hipError_t plain_attend(const StepArgs& a, const AttendIo& io, int64_t grid, hipStream_t stream) {
-  const int nj = (a.dk + 16 * VEC - 1) / (16 * VEC);
+  const int nj = ((a.dk > a.dv ? a.dk : a.dv) + 16 * VEC - 1) / (16 * VEC);
   const dim3 g = grid_of(grid), b(kThreads);
   if (nj * VEC <= 8) hipLaunchKernelGGL((attend_plain<T, VEC, 8 / VEC>), g, b, 0, stream, a, io);
   else if (nj * VEC <= 16) hipLaunchKernelGGL((attend_plain<T, VEC, 16 / VEC>), g, b, 0, stream, a, io);
@@ -743,17 +744,21 @@ hipError_t plain_attend(const StepArgs& a, const AttendIo& io, int64_t grid, hip
 }
 
 template <typename T>
-hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
+hipError_t plain_typed(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
   const int64_t grid = (int64_t)a.num_items * a.heads;
-  if (grid > 0) {
-    // four columns at a time where every row and head starts on a four-column boundary
-    const size_t al = 4 * sizeof(T);
-    const bool vec = a.dk % 4 == 0 && a.dv % 4 == 0 && a.row % 4 == 0 && io.q_stride % 4 == 0 && io.layer0 % 4 == 0 &&
-                     (uintptr_t)io.q % al == 0 && (uintptr_t)a.k_pool % al == 0 && (uintptr_t)a.v_pool % al == 0;
+  // four columns at a time where every row and head starts on a four-column boundary
+  const size_t al = 4 * sizeof(T);
+  const bool vec = a.dk % 4 == 0 && a.dv % 4 == 0 && a.row % 4 == 0 && io.q_stride % 4 == 0 && io.layer0 % 4 == 0 &&
+                   (uintptr_t)io.q % al == 0 && (uintptr_t)a.k_pool % al == 0 && (uintptr_t)a.v_pool % al == 0;
+  return vec ? plain_attend<T, 4>(a, io, grid, stream) : plain_attend<T, 1>(a, io, grid, stream);
+}
+
+template <typename T>
+hipError_t attend_typed(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
+  if (a.num_items > 0) {
     const hipError_t e = a.kernel == ATTEND_HEADS    ? launch_attend_heads(a, io, stream)
                          : a.kernel == ATTEND_LATENT ? launch_attend_latent(a, io, stream)
-                         : vec                       ? plain_attend<T, 4>(a, io, grid, stream)
-                                                     : plain_attend<T, 1>(a, io, grid, stream);
+                                                     : plain_typed<T>(a, io, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t rows = (int64_t)a.num_merge * a.num_q_heads;
@@ -829,6 +834,11 @@ hipError_t launch_step_attend(const StepArgs& a, int layer, const void* q, int64
   io.out_vec = out_stride % 4 == 0 && (uintptr_t)out % 8 == 0;
   if (a.dtype == KAMERA_BF16) return attend_typed<uint16_t>(a, io, stream);
   return attend_typed<float>(a, io, stream);
+}
+
+hipError_t launch_attend_plain(const StepArgs& a, const AttendIo& io, hipStream_t stream) {
+  if (a.num_items == 0) return hipSuccess;
+  return a.dtype == KAMERA_BF16 ? plain_typed<uint16_t>(a, io, stream) : plain_typed<float>(a, io, stream);
 }
 
 hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStream_t stream) {

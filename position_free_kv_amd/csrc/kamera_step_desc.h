@@ -55,6 +55,26 @@ struct alignas(16) MergeToken {
 };
 static_assert(sizeof(MergeToken) == 48, "merge record");
 
+// ---------------------------------------------------------------- weighing work list
+// A workgroup's work for each KV head: the weights that rows [row0, row1) of a run give to keys [kv0, kv1)
+// of one segment (a prefix, or a request's own tokens). Rows as in AttendRun; token j sees keys
+// t <= lim0 + j * lstep.
+struct alignas(16) WeighItem {
+  int32_t pg, slot, kv0, kv1;
+  int32_t tok0, ntok, listed, lim0;
+  int32_t lstep, row0, row1, split;
+  int64_t part;  // partial sums of the run: part + (split * heads + head) * kv + key; -1: straight to the scores
+  int32_t kv, pad;
+};
+static_assert(sizeof(WeighItem) == 64, "weigh record");
+// A run whose rows are cut into `splits` ranges of `rows` rows: its keys' sums are joined from those.
+struct alignas(16) WeighJoin {
+  int64_t part;
+  int32_t pg, slot, kv, splits;
+  int32_t rows, lim0, lstep, tile;  // tile: keys of an item (the ranges before the first row that sees any of them hold nothing)
+};
+static_assert(sizeof(WeighJoin) == 48, "weigh join record");
+
 // Kernel arguments of a step (held in the plan).
 struct StepArgs {
   uint16_t* k_pool;
@@ -81,13 +101,20 @@ struct StepArgs {
   int32_t page_bits;
   int32_t max_parts;    // most parts of a joined row
   int32_t num_wide, num_pairs;  // the items' order: wide, pairs, narrow
+  const WeighItem* weigh;
+  const WeighJoin* weigh_join;
+  float* weigh_part;
+  int32_t num_weigh, num_weigh_join, weigh_kernel, weigh_longest;  // longest: most keys of a joined run
+  uint32_t group_magic;         // row / rows_of_a_token = row * group_magic >> group_bits, for weighing
+  int32_t group_bits;
+  int32_t differential;
 };
 static_assert(sizeof(StepArgs) <= sizeof(kamera_step_plan::detail), "step arguments held in the plan");
 
 // PLAIN: any layout. HEADS: bf16 GQA/MHA heads of 64 or 128 columns; LATENT: bf16 MLA rows of 512 + 64
-// columns, both on the matrix cores.
-enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2 };
-// Tiles of rows. HEADS: narrow 32, pairs 64, wide 128 rows; LATENT: narrow 16, wide 128; PLAIN: narrow 4.
+// columns; DIFF: differential attention of bf16 heads of 64 or 128 columns; all on the matrix cores.
+enum AttendKernel { ATTEND_PLAIN = 0, ATTEND_HEADS = 1, ATTEND_LATENT = 2, ATTEND_DIFF = 3 };
+// Tiles of rows. HEADS, DIFF: narrow 32, pairs 64, wide 128 rows; LATENT: narrow 16, wide 128; PLAIN: narrow 4.
 enum TileClass { TILE_WIDE = 0, TILE_PAIRS = 1, TILE_NARROW = 2 };
 constexpr int tile_rows(int kernel, int tile) {
   return tile == TILE_WIDE ? 128 : tile == TILE_PAIRS ? 64 : kernel == ATTEND_PLAIN ? 4 : kernel == ATTEND_LATENT ? 16 : 32;
@@ -110,6 +137,16 @@ struct AttendIo {
 };
 hipError_t launch_attend_heads(const StepArgs& a, const AttendIo& io, hipStream_t stream);
 hipError_t launch_attend_latent(const StepArgs& a, const AttendIo& io, hipStream_t stream);
+// partial rows by the plain kernel (kamera_step.hip), which differential attention joins by itself
+hipError_t launch_attend_plain(const StepArgs& a, const AttendIo& io, hipStream_t stream);
+// Differential attention; a: the step's arguments for pairs of KV heads (differential_args)
+hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                                   float* lse, float scale, const kamera_differential& diff, hipStream_t stream);
+
+// Keys of a weighing workgroup: PLAIN 16; on the matrix cores HEADS 256, LATENT 128.
+constexpr int weigh_keys(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 128 : 256; }
+hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_t q_stride, const float* lse, float* scores, float scale,
+                             float decay, hipStream_t stream);
 
 hipError_t launch_step_phase(const StepArgs& a, hipStream_t stream);
 hipError_t launch_step_append(const StepArgs& a, int layer, const kamera_append_rows& rows, hipStream_t stream);
@@ -139,5 +176,32 @@ struct InlineCopies {
   PageCopy c[kInlineCopies];
 };
 hipError_t launch_copy_pages(const CopyArgs& a, const InlineCopies* inl, hipStream_t stream);
+
+// ---------------------------------------------------------------- eviction
+struct alignas(16) EvictSeq {
+  int32_t pg, slot0, num_tokens, keep;  // pg: tables entry
+  int32_t first, last, kept0, pad;      // kept0: sum of min(keep, num_tokens) of the sequences before it
+};
+static_assert(sizeof(EvictSeq) == 32, "eviction record");
+
+struct EvictArgs {
+  char* pool[2];
+  int64_t layer_bytes;   // between layers of the pool
+  float* scores;
+  int64_t scores_stride;
+  const EvictSeq* seqs;
+  const int32_t* pages;
+  int32_t* kept;         // [layers][groups][total]
+  int32_t* starts;       // [layers][groups][num_seqs]: kept tokens before the first one that moves
+  float* phase;          // [shifts][d_rot]: cosines, then sines, of turning back by 0, 1, ... positions; NULL: keys are not turned
+  const double* theta;
+  int32_t num_seqs, layers, heads, together;
+  int32_t total, page_size, page_bits;
+  uint32_t page_magic;
+  int32_t row_bytes, head_bytes, tensors, dtype;  // bytes of a pool row, and of a head's columns in it
+  int32_t d_rot, band0, pairing, shifts;          // band0: first rotated column of a head
+  int32_t longest, most_kept;                     // most tokens, and most kept tokens, of a sequence that loses some
+};
+hipError_t launch_evict(const EvictArgs& a, hipStream_t stream);
 
 }  // namespace kamera

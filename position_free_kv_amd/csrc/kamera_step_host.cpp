@@ -8,21 +8,11 @@
 #include <new>
 #include <vector>
 
-#include "kamera_step_desc.h"
+#include "kamera_step_host.h"
 
 using namespace kamera;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-size_t elem_bytes(const kamera_layout* L) { return L->dtype == KAMERA_BF16 ? 2 : 4; }
-
-int row_width(const kamera_layout* L) {
-  return L->family == KAMERA_GQA ? L->num_kv_heads * L->head_dim : L->latent_dim + L->rope_dim;
-}
 
 // Shapes of a step that follow from the layout.
 struct Shape {
@@ -33,6 +23,12 @@ Shape shape_of(const kamera_layout* L, int num_q_heads) {
     return Shape{L->num_kv_heads, num_q_heads / L->num_kv_heads, L->head_dim, L->head_dim, L->head_dim};
   return Shape{1, num_q_heads, L->latent_dim + L->rope_dim, L->latent_dim, L->rope_dim};
 }
+// Of its attention: a differential one has a pair of KV heads in the place of one, with the values of both.
+Shape attend_shape(const kamera_layout* L, const kamera_step* s) {
+  Shape h = shape_of(L, s->num_q_heads);
+  if (s->flags & KAMERA_STEP_DIFFERENTIAL) h = Shape{h.heads / 2, h.group * 2, h.dk, h.dv * 2, h.d_rot};
+  return h;
+}
 
 // ------------------------------------------------------------------ validation
 // Counts of a valid step: query tokens, page-table entries used.
@@ -40,28 +36,28 @@ struct Counts {
   int64_t tokens = 0, entries = 0;
 };
 
-// slots and key numbers are 32-bit in the kernels, with room for a tile beyond the last
-constexpr int64_t kMaxSlot = (int64_t(1) << 31) - 4096;
-
-int64_t table_entries(int32_t slot0, int64_t tokens, int P) { return tokens > 0 ? ceil_div(slot0 + tokens, P) : 0; }
-
 kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n) {
   kamera_status st = host_check_layout(L);
   if (st != KAMERA_OK) return st;
   if (!s) return host_fail(KAMERA_E_NULL, "step is NULL");
-  if (!(s->flags & (KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND)) || (s->flags & ~(uint32_t)(KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND | KAMERA_STEP_FIT)))
+  constexpr uint32_t launches = KAMERA_STEP_APPEND | KAMERA_STEP_ATTEND | KAMERA_STEP_WEIGH;
+  if (!(s->flags & launches) || (s->flags & ~(uint32_t)(launches | KAMERA_STEP_FIT | KAMERA_STEP_DIFFERENTIAL)))
     return host_fail(KAMERA_E_UNSUPPORTED, "step.flags 0x%x", s->flags);
   if (s->num_requests < 0 || s->num_prefixes < 0) return host_fail(KAMERA_E_SHAPE, "negative count of requests or prefixes");
   if (s->reserved[0] || s->reserved[1]) return host_fail(KAMERA_E_SHAPE, "step.reserved must be 0");
   if ((s->num_requests && !s->requests) || (s->num_prefixes && !s->prefixes))
     return host_fail(KAMERA_E_NULL, "requests or prefixes is NULL");
-  const bool attend = s->flags & KAMERA_STEP_ATTEND, append = s->flags & KAMERA_STEP_APPEND;
+  const bool append = s->flags & KAMERA_STEP_APPEND, diff = s->flags & KAMERA_STEP_DIFFERENTIAL;
+  const bool attend = s->flags & (KAMERA_STEP_ATTEND | KAMERA_STEP_WEIGH);
+  if (diff && !attend) return host_fail(KAMERA_E_UNSUPPORTED, "a differential step attends or weighs (flags 0x%x)", s->flags);
+  if (diff && (L->family != KAMERA_GQA || L->num_kv_heads % 2))
+    return host_fail(KAMERA_E_UNSUPPORTED, "differential heads are pairs of GQA KV heads");
   if (s->num_q_heads < (attend ? 1 : 0) || s->num_q_heads > (1 << 16))
     return host_fail(KAMERA_E_SHAPE, "num_q_heads %d", s->num_q_heads);
   if (L->family == KAMERA_GQA && s->num_q_heads % L->num_kv_heads)
     return host_fail(KAMERA_E_SHAPE, "num_q_heads %d is not a multiple of num_kv_heads %d", s->num_q_heads, L->num_kv_heads);
   const Shape h = shape_of(L, s->num_q_heads);
-  if (attend && h.dv < 1) return host_fail(KAMERA_E_SHAPE, "attention over rows without a latent");
+  if ((s->flags & KAMERA_STEP_ATTEND) && h.dv < 1) return host_fail(KAMERA_E_SHAPE, "attention over rows without a latent");
   if (attend && h.dk > KAMERA_ATTEND_MAX_DIM)
     return host_fail(KAMERA_E_UNSUPPORTED, "key heads of %d columns (at most %d)", h.dk, (int)KAMERA_ATTEND_MAX_DIM);
   if (append && s->positions && !aligned(s->positions, sizeof(int32_t)))
@@ -105,28 +101,6 @@ kamera_status check_step(const kamera_layout* L, const kamera_step* s, Counts& n
   return KAMERA_OK;
 }
 
-kamera_status check_pool(const kamera_layout* L, const kamera_pool* pool) {
-  if (!pool) return host_fail(KAMERA_E_NULL, "pool is NULL");
-  const size_t es = elem_bytes(L);
-  if (pool->num_pages < 1) return host_fail(KAMERA_E_SHAPE, "pool.num_pages must be >= 1");
-  if (pool->reserved != 0) return host_fail(KAMERA_E_SHAPE, "pool.reserved must be 0");
-  if (!pool->k_pool || (L->family == KAMERA_GQA && !pool->v_pool)) return host_fail(KAMERA_E_NULL, "a pool pointer is NULL");
-  if (!aligned(pool->k_pool, es) || (pool->v_pool && !aligned(pool->v_pool, es)))
-    return host_fail(KAMERA_E_ALIGN, "pool pointers must be aligned to %zu bytes", es);
-  const int64_t min_ls = (int64_t)pool->num_pages * L->page_size * row_width(L);
-  if (pool->layer_stride < 0 || (pool->layer_stride != 0 && pool->layer_stride < min_ls))
-    return host_fail(KAMERA_E_SHAPE, "pool.layer_stride %lld smaller than one layer (%lld)",
-                     (long long)pool->layer_stride, (long long)min_ls);
-  return KAMERA_OK;
-}
-
-kamera_status check_workspace(const void* ws, size_t have, size_t need) {
-  if (!ws) return host_fail(KAMERA_E_WORKSPACE, "workspace is NULL");
-  if (!aligned(ws, kAlign)) return host_fail(KAMERA_E_ALIGN, "workspace must be %zu-byte aligned", kAlign);
-  if (have < need) return host_fail(KAMERA_E_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
-  return KAMERA_OK;
-}
-
 // ------------------------------------------------------------------ attention work list
 // A request whose rows alone fill a tile gains little from sharing its prefix's reads: it reads the
 // prefix and its own tokens as one sequence, and its result needs no joining. (32 requests over an
@@ -142,6 +116,7 @@ constexpr double kStartNs = 6000, kPartNs = 0.001;
 double key_ns(int kernel, int tile) {
   if (kernel == ATTEND_LATENT) return tile == TILE_WIDE ? 60 : 20;
   if (kernel == ATTEND_HEADS) return tile == TILE_WIDE ? 30 : tile == TILE_PAIRS ? 38 : 25;
+  if (kernel == ATTEND_DIFF) return tile == TILE_WIDE ? 55 : 50;
   return 40;
 }
 
@@ -153,6 +128,10 @@ struct Work {
   int64_t part_rows = 0;
   int32_t wide = 0, pairs = 0, max_parts = 0;
   bool split = false, shared = false;  // keys of a run cut into ranges, a prefix read by a run of its own
+  std::vector<WeighItem> weigh;
+  std::vector<WeighJoin> weigh_join;
+  int64_t weigh_part = 0;  // partial sums
+  int32_t weigh_longest = 0;
 };
 
 // A plan for less workspace than the fastest one takes: ranges of 2^coarser times the length, and
@@ -160,6 +139,7 @@ struct Work {
 struct Fit {
   int coarser = 0;
   bool share = true;
+  bool split_rows = true;  // weighing: rows of a run cut into ranges
 };
 
 // Where each prefix's and request's table starts among the packed entries.
@@ -169,21 +149,22 @@ struct Tables {
 
 // Layouts of the matrix-core kernels; they also need the pool in 16-byte pieces, and row numbers of
 // 32 bits.
-int matrix_kernel(const kamera_layout* L) {
+int matrix_kernel(const kamera_layout* L, bool diff = false) {
   if (L->dtype != KAMERA_BF16) return ATTEND_PLAIN;
-  if (L->family == KAMERA_GQA) return L->head_dim == 64 || L->head_dim == 128 ? ATTEND_HEADS : ATTEND_PLAIN;
+  if (L->family == KAMERA_GQA) return L->head_dim == 64 || L->head_dim == 128 ? (diff ? ATTEND_DIFF : ATTEND_HEADS) : ATTEND_PLAIN;
   return L->latent_dim == 512 && L->rope_dim == 64 ? ATTEND_LATENT : ATTEND_PLAIN;
 }
-int pick_kernel(const kamera_layout* L, const kamera_pool* pool) {
-  const int kernel = matrix_kernel(L);
+int pick_kernel(const kamera_layout* L, const kamera_pool* pool, bool diff = false) {
+  const int kernel = matrix_kernel(L, diff);
   if (!aligned(pool->k_pool, 16) || (L->family == KAMERA_GQA && !aligned(pool->v_pool, 16)) || pool->layer_stride % 8) return ATTEND_PLAIN;
   if ((int64_t)pool->num_pages * L->page_size >= (int64_t(1) << 31)) return ATTEND_PLAIN;
   return kernel;
 }
 
 void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
-  const Shape h = shape_of(L, s->num_q_heads);
+  const Shape h = attend_shape(L, s);
   const int G = h.group;
+  const bool diff = s->flags & KAMERA_STEP_DIFFERENTIAL;  // (its results are always joined: two rows make one)
   w.runs.clear();
   w.items.clear();
   w.tok.clear();
@@ -250,7 +231,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     }
     r.tok0 = (int32_t)tok;
     r.ntok = q.num_queries;
-    r.direct = !shares(q);
+    r.direct = !shares(q) && !diff;
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
@@ -260,7 +241,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   for (AttendRun& r : w.runs) {
     const int64_t rows = (int64_t)r.ntok * G;
     if (plain || rows <= tile_rows(kernel, TILE_NARROW)) r.tile = TILE_NARROW;
-    else r.tile = kernel == ATTEND_HEADS && rows <= tile_rows(kernel, TILE_PAIRS) ? TILE_PAIRS : TILE_WIDE;
+    else r.tile = kernel != ATTEND_LATENT && rows <= tile_rows(kernel, TILE_PAIRS) ? TILE_PAIRS : TILE_WIDE;
   }
   // Keys per item (a multiple of gran), for each class of tiles: the least estimate of the launch's
   // time. All classes share `slots` places; a class whose items are alike takes whole rounds of them
@@ -382,11 +363,122 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   }
 }
 
+// ------------------------------------------------------------------ weighing work list
+// A run is a segment (a prefix with all its requests' query tokens, or a request's own tokens); an item a
+// tile of its keys and the rows that see any of them. Where that leaves the chip without work for all its
+// workgroups, rows are cut into ranges whose sums are joined (in the order of the ranges).
+constexpr int64_t kWeighSlots = 1024, kWeighRows = 512;
+void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
+  const Shape h = shape_of(L, s->num_q_heads);
+  const int G = h.group;
+  thread_local std::vector<WeighItem> runs;
+  runs.clear();
+  auto run = [&](int32_t pg, int32_t slot, int32_t kv) {
+    WeighItem r;
+    std::memset(&r, 0, sizeof(r));
+    r.pg = pg;
+    r.slot = slot;
+    r.kv = kv;
+    r.lim0 = kv - 1;
+    return r;
+  };
+  // prefixes: the tokens of each, in the batch's order
+  thread_local std::vector<int32_t> first, at;
+  first.assign((size_t)s->num_prefixes + 1, 0);
+  for (int i = 0; i < s->num_requests; ++i)
+    if (s->requests[i].prefix >= 0) first[(size_t)s->requests[i].prefix + 1] += s->requests[i].num_queries;
+  for (int p = 0; p < s->num_prefixes; ++p) first[(size_t)p + 1] += first[(size_t)p];
+  at.assign(first.begin(), first.end());
+  const size_t tok0 = w.tok.size();
+  w.tok.resize(tok0 + (size_t)first.back());
+  int64_t tok = 0;
+  for (int i = 0; i < s->num_requests; tok += s->requests[i++].num_queries)
+    for (int j = 0; j < s->requests[i].num_queries && s->requests[i].prefix >= 0; ++j)
+      w.tok[tok0 + (size_t)at[(size_t)s->requests[i].prefix]++] = (int32_t)(tok + j);
+  bool listed = false;
+  for (int p = 0; p < s->num_prefixes; ++p) {
+    if (first[(size_t)p + 1] == first[(size_t)p] || s->prefixes[p].num_tokens == 0) continue;
+    WeighItem r = run(tb.prefix[(size_t)p], s->prefixes[p].slot0, s->prefixes[p].num_tokens);
+    r.tok0 = (int32_t)tok0 + first[(size_t)p];
+    r.ntok = first[(size_t)p + 1] - first[(size_t)p];
+    r.listed = 1;
+    const int32_t t0 = w.tok[(size_t)r.tok0];
+    if (w.tok[(size_t)(r.tok0 + r.ntok - 1)] - t0 == r.ntok - 1) {  // ascending and without gaps: no list needed
+      r.listed = 0;
+      r.tok0 = t0;
+    } else {
+      listed = true;
+    }
+    runs.push_back(r);
+  }
+  if (!listed) w.tok.resize(tok0);
+  tok = 0;
+  for (int i = 0; i < s->num_requests; tok += s->requests[i++].num_queries) {
+    const kamera_request& q = s->requests[i];
+    if (q.num_queries == 0 || q.num_tokens == 0) continue;
+    WeighItem r = run(tb.request[(size_t)i], q.slot0, q.num_tokens);
+    r.tok0 = (int32_t)tok;
+    r.ntok = q.num_queries;
+    if (!(q.flags & KAMERA_REQUEST_ALL)) {
+      r.lim0 = q.num_tokens - q.num_queries;
+      r.lstep = 1;
+    }
+    runs.push_back(r);
+  }
+  const int64_t keys = weigh_keys(kernel);
+  auto first_row = [&](const WeighItem& r, int64_t kv0) { return r.lstep ? std::max<int64_t>(kv0 - r.lim0, 0) * G : 0; };
+  double work = 0;
+  for (const WeighItem& r : runs) work += (double)ceil_div(r.kv, keys) * r.ntok * G * h.heads;
+  const int64_t range = fit.split_rows ? std::max<int64_t>(kWeighRows, (int64_t)round_up((size_t)(work / kWeighSlots) + 1, 64)) : int64_t(1) << 40;
+  for (WeighItem& r : runs) {
+    const int64_t rows = (int64_t)r.ntok * G, n = ceil_div(rows, range);
+    const int64_t each = n > 1 ? (int64_t)round_up((size_t)ceil_div(rows, n), 64) : rows, splits = ceil_div(rows, each);
+    r.part = -1;
+    if (splits > 1) {
+      r.part = w.weigh_part;
+      w.weigh_part += splits * h.heads * r.kv;
+      w.weigh_join.push_back(WeighJoin{r.part, r.pg, r.slot, r.kv, (int32_t)splits, (int32_t)each, r.lim0, r.lstep, (int32_t)keys});
+      w.weigh_longest = std::max(w.weigh_longest, r.kv);
+    }
+    for (int64_t kv0 = 0; kv0 < r.kv; kv0 += keys)
+      for (int64_t sp = first_row(r, kv0) / each; sp < splits; ++sp) {
+        r.kv0 = (int32_t)kv0;
+        r.kv1 = (int32_t)std::min<int64_t>(kv0 + keys, r.kv);
+        r.row0 = (int32_t)std::max(first_row(r, kv0), sp * each);
+        r.row1 = (int32_t)std::min(rows, (sp + 1) * each);
+        r.split = (int32_t)sp;
+        w.weigh.push_back(r);
+      }
+  }
+  // the longest first: the short ones fill the gaps at the end
+  std::stable_sort(w.weigh.begin(), w.weigh.end(), [](const WeighItem& x, const WeighItem& y) { return x.row1 - x.row0 > y.row1 - y.row0; });
+}
+
+// What a step's flags ask for, for a pool that the matrix-core kernels take (`matrix`) or any.
+void plan_work(const kamera_layout* L, const kamera_step* s, const Tables& tb, bool matrix, Fit fit, Work& w) {
+  w.weigh.clear();
+  w.weigh_join.clear();
+  w.weigh_part = 0;
+  w.weigh_longest = 0;
+  if (s->flags & KAMERA_STEP_ATTEND)
+    plan_attention(L, s, tb, matrix ? matrix_kernel(L, s->flags & KAMERA_STEP_DIFFERENTIAL) : ATTEND_PLAIN, fit, w);
+  else w = Work();
+  if (s->flags & KAMERA_STEP_WEIGH) plan_weights(L, s, tb, matrix ? matrix_kernel(L) : ATTEND_PLAIN, fit, w);
+}
+
 // ------------------------------------------------------------------ workspace
 struct Offsets {
-  size_t pages, items, tok, merge, slots, pos, theta, upload, phase, ml, o, total;
+  size_t pages, items, tok, merge, slots, pos, theta, weigh, weigh_join, upload, phase, ml, o, weigh_part, total;
 };
-Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, size_t items, size_t tok, size_t merge, int64_t part_rows) {
+struct Sizes {
+  size_t items, tok, merge;
+  int64_t part_rows;
+  size_t weigh, weigh_join;
+  int64_t weigh_part;
+};
+Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Sizes& z) {
+  const size_t items = z.items, tok = z.tok, merge = z.merge;
+  const int64_t part_rows = z.part_rows;
   Offsets f;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -395,7 +487,7 @@ Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, siz
     return here;
   };
   const bool append = s->flags & KAMERA_STEP_APPEND;
-  const Shape h = shape_of(L, s->num_q_heads);
+  const Shape h = attend_shape(L, s);
   f.pages = take((size_t)n.entries * 4);
   f.items = take(items * sizeof(AttendItem));
   f.tok = take(tok * 4);
@@ -403,26 +495,47 @@ Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, siz
   f.slots = take(append ? (size_t)n.tokens * 8 : 0);
   f.pos = take(append && !s->positions ? (size_t)n.tokens * 4 : 0);
   f.theta = take(append ? (size_t)h.d_rot / 2 * 8 : 0);
+  f.weigh = take(z.weigh * sizeof(WeighItem));
+  f.weigh_join = take(z.weigh_join * sizeof(WeighJoin));
   f.upload = at;
   f.phase = take(append ? (size_t)n.tokens * h.d_rot * 4 : 0);
   f.ml = take((size_t)part_rows * 8);
   f.o = take((size_t)part_rows * h.dv * 4);
+  f.weigh_part = take((size_t)z.weigh_part * 4);
   f.total = std::max<size_t>(at, kAlign);
   return f;
 }
 Offsets carve(const kamera_layout* L, const kamera_step* s, const Counts& n, const Work& w) {
-  return carve(L, s, n, w.items.size(), w.tok.size(), w.merge.size(), w.part_rows);
+  return carve(L, s, n, Sizes{w.items.size(), w.tok.size(), w.merge.size(), w.part_rows, w.weigh.size(), w.weigh_join.size(), w.weigh_part});
 }
 
-// Bytes that a plan without ranges and sharing takes on any pool: it has no partial rows, and an item a
-// tile, most of them in the kernel with the smallest tiles. Unlike the fastest plan's, they never grow
-// when a request loses tokens or queries.
+// Bytes that a plan without ranges and sharing takes on any pool: it has no partial rows (a differential
+// attention: one a query row), and an item a tile, most of them in the kernel with the smallest tiles. Unlike
+// the fastest plan's, they never grow when a request loses tokens or queries.
 size_t least_bytes(const kamera_layout* L, const kamera_step* s, const Counts& n) {
-  const int64_t group = shape_of(L, s->num_q_heads).group;
-  size_t items = 0;
+  const int64_t group = attend_shape(L, s).group;
+  Sizes z;
+  std::memset(&z, 0, sizeof(z));
   if (s->flags & KAMERA_STEP_ATTEND)
-    for (int i = 0; i < s->num_requests; ++i) items += (size_t)ceil_div(s->requests[i].num_queries * group, tile_rows(ATTEND_PLAIN, TILE_NARROW));
-  return carve(L, s, n, items, 0, 0, 0).total;
+    for (int i = 0; i < s->num_requests; ++i) z.items += (size_t)ceil_div(s->requests[i].num_queries * group, tile_rows(ATTEND_PLAIN, TILE_NARROW));
+  if ((s->flags & KAMERA_STEP_ATTEND) && (s->flags & KAMERA_STEP_DIFFERENTIAL)) {
+    z.merge = (size_t)n.tokens;
+    z.part_rows = n.tokens * s->num_q_heads;
+  }
+  if (s->flags & KAMERA_STEP_WEIGH) {
+    thread_local std::vector<uint8_t> seen;  // prefixes
+    seen.assign((size_t)s->num_prefixes, 0);
+    for (int i = 0; i < s->num_requests; ++i) {
+      const kamera_request& r = s->requests[i];
+      if (r.num_queries == 0) continue;
+      z.weigh += (size_t)ceil_div(r.num_tokens, weigh_keys(ATTEND_PLAIN));
+      if (r.prefix < 0) continue;
+      z.tok += (size_t)r.num_queries;
+      if (!seen[(size_t)r.prefix]) z.weigh += (size_t)ceil_div(s->prefixes[r.prefix].num_tokens, weigh_keys(ATTEND_PLAIN));
+      seen[(size_t)r.prefix] = 1;
+    }
+  }
+  return carve(L, s, n, z).total;
 }
 
 void place_tables(const kamera_layout* L, const kamera_step* s, Tables& tb) {
@@ -440,6 +553,25 @@ void place_tables(const kamera_layout* L, const kamera_step* s, Tables& tb) {
   }
 }
 
+// Weighed slots: each belongs to one segment, so that one workgroup adds to its score.
+kamera_status check_weighed(const kamera_layout* L, const kamera_step* s, const kamera_pool* pool) {
+  SlotCheck check(pool->num_pages, L->page_size);
+  thread_local std::vector<uint8_t> seen;  // prefixes
+  seen.assign((size_t)s->num_prefixes, 0);
+  for (int i = 0; i < s->num_requests; ++i) {
+    const kamera_request& r = s->requests[i];
+    if (r.num_queries == 0) continue;
+    if (!check.add(r.block_table, r.slot0, r.num_tokens))
+      return host_fail(KAMERA_E_OVERLAP, "request %d weighs slots of page %d that another sequence of the step, or itself, weighs too", i, check.clash);
+    if (r.prefix < 0 || seen[(size_t)r.prefix]) continue;
+    seen[(size_t)r.prefix] = 1;
+    const kamera_prefix& p = s->prefixes[r.prefix];
+    if (!check.add(p.block_table, p.slot0, p.num_tokens))
+      return host_fail(KAMERA_E_OVERLAP, "prefix %d: slots of page %d are weighed twice", r.prefix, check.clash);
+  }
+  return KAMERA_OK;
+}
+
 // Page ids inside the pool; appended slots distinct and outside every prefix.
 kamera_status check_tables(const kamera_layout* L, const kamera_step* s, const kamera_pool* pool) {
   const int P = L->page_size;
@@ -455,6 +587,7 @@ kamera_status check_tables(const kamera_layout* L, const kamera_step* s, const k
     st = in_pool("prefix", i, s->prefixes[i].block_table, table_entries(s->prefixes[i].slot0, s->prefixes[i].num_tokens, P));
   for (int i = 0; i < s->num_requests && st == KAMERA_OK; ++i)
     st = in_pool("request", i, s->requests[i].block_table, table_entries(s->requests[i].slot0, s->requests[i].num_tokens, P));
+  if (st == KAMERA_OK && (s->flags & KAMERA_STEP_WEIGH)) st = check_weighed(L, s, pool);
   if (st != KAMERA_OK || !(s->flags & KAMERA_STEP_APPEND)) return st;
   struct Range {
     int32_t page, lo, hi, request;
@@ -504,28 +637,32 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   if (st == KAMERA_OK) st = check_pool(L, pool);
   if (st == KAMERA_OK) st = check_tables(L, s, pool);
   if (st != KAMERA_OK) return st;
-  const bool append = s->flags & KAMERA_STEP_APPEND, attend = s->flags & KAMERA_STEP_ATTEND;
+  const bool append = s->flags & KAMERA_STEP_APPEND, diff = s->flags & KAMERA_STEP_DIFFERENTIAL;
   const int P = L->page_size;
   const Shape h = shape_of(L, s->num_q_heads);
   thread_local Tables tb;
   thread_local Work w;
   place_tables(L, s, tb);
-  const int kernel = pick_kernel(L, pool);
+  const int kernel = pick_kernel(L, pool, diff), weigh_kernel = pick_kernel(L, pool);
+  const bool matrix = kernel != ATTEND_PLAIN;
   Fit fit;
-  if (attend) plan_attention(L, s, tb, kernel, fit, w);
-  else w = Work();
+  plan_work(L, s, tb, matrix, fit, w);
   Offsets f = carve(L, s, n, w);
-  while ((s->flags & KAMERA_STEP_FIT) && f.total > ws_bytes && (w.split || w.shared)) {  // (each turn halves the partial rows, or ends the sharing)
-    if (w.split) ++fit.coarser;
-    else fit = Fit{0, false};
-    plan_attention(L, s, tb, kernel, fit, w);
+  // (each turn ends the ranges of weighed rows, halves the partial rows, or ends the sharing)
+  while ((s->flags & KAMERA_STEP_FIT) && f.total > ws_bytes && (w.split || w.shared || w.weigh_part)) {
+    if (w.weigh_part) fit.split_rows = false;
+    else if (w.split) ++fit.coarser;
+    else fit = Fit{0, false, fit.split_rows};
+    plan_work(L, s, tb, matrix, fit, w);
     f = carve(L, s, n, w);
   }
   st = check_workspace(ws, ws_bytes, f.total);
   if (st != KAMERA_OK) return st;
   // (the matrix-core kernels' workgroups lie along one dimension of the grid, which takes fewer than 2^32 threads)
-  const int most = kernel == ATTEND_PLAIN ? 31 : kernel == ATTEND_HEADS ? 24 : 23;
-  if ((int64_t)w.items.size() * h.heads >= (int64_t(1) << most)) return host_fail(KAMERA_E_SHAPE, "too many work items");
+  const int most = kernel == ATTEND_PLAIN ? 31 : kernel == ATTEND_LATENT ? 23 : 24;
+  if ((int64_t)w.items.size() * h.heads >= (int64_t(1) << most) ||
+      (int64_t)w.weigh.size() * h.heads >= (int64_t(1) << (weigh_kernel == ATTEND_PLAIN ? 31 : 24)))
+    return host_fail(KAMERA_E_SHAPE, "too many work items");
 
   thread_local std::vector<unsigned char> blob;
   blob.assign(f.upload, 0);
@@ -539,6 +676,8 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
     put(tb.request[(size_t)i], s->requests[i].block_table, table_entries(s->requests[i].slot0, s->requests[i].num_tokens, P));
   if (!w.items.empty()) std::memcpy(blob.data() + f.items, w.items.data(), w.items.size() * sizeof(AttendItem));
   if (!w.tok.empty()) std::memcpy(blob.data() + f.tok, w.tok.data(), w.tok.size() * 4);
+  if (!w.weigh.empty()) std::memcpy(blob.data() + f.weigh, w.weigh.data(), w.weigh.size() * sizeof(WeighItem));
+  if (!w.weigh_join.empty()) std::memcpy(blob.data() + f.weigh_join, w.weigh_join.data(), w.weigh_join.size() * sizeof(WeighJoin));
   if (!w.merge.empty()) std::memcpy(blob.data() + f.merge, w.merge.data(), w.merge.size() * sizeof(MergeToken));
   if (append) {
     int64_t* slots = reinterpret_cast<int64_t*>(blob.data() + f.slots);
@@ -586,15 +725,20 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   a.latent = L->family == KAMERA_MLA ? L->latent_dim : 0;
   a.page_size = P;
   a.page_shift = (P & (P - 1)) == 0 ? __builtin_ctz((unsigned)P) : -1;
-  // with b = ceil(log2 P): floor(2^(31 + b) / P) + 1 exceeds 2^(31 + b) / P by at most 2^b / (P 2^b),
-  // which the 31 bits of a slot cannot raise to a whole
-  a.page_bits = 31;
-  while ((int64_t(1) << (a.page_bits - 31)) < P) ++a.page_bits;
-  a.page_magic = (uint32_t)((uint64_t(1) << a.page_bits) / (uint64_t)P + 1);
+  reciprocal(P, a.page_magic, a.page_bits);
+  reciprocal(std::max(h.group, 1), a.group_magic, a.group_bits);
   a.num_items = (int32_t)w.items.size();
   a.num_merge = (int32_t)w.merge.size();
   a.num_tokens = (int32_t)n.tokens;
   for (int k = 0; k < 3; ++k) a.mrope[k] = L->mrope_section[k];
+  a.weigh = reinterpret_cast<const WeighItem*>(base + f.weigh);
+  a.weigh_join = reinterpret_cast<const WeighJoin*>(base + f.weigh_join);
+  a.weigh_part = reinterpret_cast<float*>(base + f.weigh_part);
+  a.num_weigh = (int32_t)w.weigh.size();
+  a.num_weigh_join = (int32_t)w.weigh_join.size();
+  a.weigh_kernel = weigh_kernel;
+  a.weigh_longest = w.weigh_longest;
+  a.differential = diff;
   a.kernel = kernel;
   a.num_wide = w.wide;
   a.num_pairs = w.pairs;
@@ -614,24 +758,6 @@ kamera_status upload_step(const kamera_layout* L, const kamera_step* s, const ka
   plan->num_layers = L->num_layers;
   plan->flags = s->flags;
   std::memcpy(plan->detail, &a, sizeof(a));
-  return KAMERA_OK;
-}
-
-kamera_status check_launch(const kamera_step_plan* plan, int32_t layer, uint32_t flag, StepArgs& a) {
-  if (!plan) return host_fail(KAMERA_E_NULL, "plan is NULL");
-  if (!plan->workspace) return host_fail(KAMERA_E_WORKSPACE, "plan has no workspace");
-  if (!(plan->flags & flag)) return host_fail(KAMERA_E_UNSUPPORTED, "the step was not uploaded for this call (flags 0x%x)", plan->flags);
-  if (layer < 0 || layer >= plan->num_layers)
-    return host_fail(KAMERA_E_SHAPE, "layer %d outside [0, %d)", layer, plan->num_layers);
-  std::memcpy(&a, plan->detail, sizeof(a));
-  return KAMERA_OK;
-}
-
-kamera_status check_rows(const char* what, const void* p, int64_t& stride, int64_t width, size_t es) {
-  if (!p) return host_fail(KAMERA_E_NULL, "%s is NULL", what);
-  if (!aligned(p, es)) return host_fail(KAMERA_E_ALIGN, "%s must be aligned to %zu bytes", what, es);
-  if (stride == 0) stride = width;
-  if (stride < width) return host_fail(KAMERA_E_SHAPE, "%s: stride %lld below the row's %lld", what, (long long)stride, (long long)width);
   return KAMERA_OK;
 }
 
@@ -781,19 +907,6 @@ kamera_status enqueue_copies(const kamera_layout* L, const kamera_pool* pool, co
   return KAMERA_OK;
 }
 
-// No C++ exception (host memory running out) leaves a C entry.
-template <typename F>
-kamera_status guarded(F f) {
-  host_clear_error();
-  try {
-    return f();
-  } catch (const std::bad_alloc&) {
-    return host_fail(KAMERA_E_SHAPE, "out of host memory");
-  } catch (...) {
-    return host_fail(KAMERA_E_SHAPE, "unexpected host error");
-  }
-}
-
 }  // namespace
 
 extern "C" {
@@ -807,13 +920,12 @@ size_t kamera_step_workspace_bytes(const kamera_layout* layout, const kamera_ste
     Tables tb;
     Work w;
     place_tables(layout, step, tb);
-    const bool attend = step->flags & KAMERA_STEP_ATTEND;
     // the pool's alignment decides between the kernels: enough for either
-    if (attend) plan_attention(layout, step, tb, ATTEND_PLAIN, Fit{}, w);
+    plan_work(layout, step, tb, false, Fit{}, w);
     size_t need = carve(layout, step, n, w).total;
     if (step->flags & KAMERA_STEP_FIT) need = std::max(need, least_bytes(layout, step, n));
-    if (attend && matrix_kernel(layout) != ATTEND_PLAIN) {
-      plan_attention(layout, step, tb, matrix_kernel(layout), Fit{}, w);
+    if ((step->flags & (KAMERA_STEP_ATTEND | KAMERA_STEP_WEIGH)) && matrix_kernel(layout) != ATTEND_PLAIN) {
+      plan_work(layout, step, tb, true, Fit{}, w);
       need = std::max(need, carve(layout, step, n, w).total);
     }
     bytes = need;
@@ -869,6 +981,7 @@ kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, co
     StepArgs a;
     kamera_status st = check_launch(plan, layer, KAMERA_STEP_ATTEND, a);
     if (st != KAMERA_OK) return st;
+    if (plan->flags & KAMERA_STEP_DIFFERENTIAL) return host_fail(KAMERA_E_UNSUPPORTED, "a differential step attends with kamera_step_attend_diff");
     const size_t es = a.dtype == KAMERA_BF16 ? 2 : 4;
     if (!std::isfinite(scale)) return host_fail(KAMERA_E_SHAPE, "scale must be finite");
     if (plan->num_tokens == 0) return KAMERA_OK;

@@ -1,0 +1,257 @@
+// Weighing (include/kamera_step.h): what each cached token receives of the attention weights of a step's queries.
+// Work list: kamera_step_desc.h.
+//
+// Here the keys stay and the query rows pass by, the other way round than in the attention: a lane's sums
+// belong to its keys, so that nothing is exchanged until the end, and every key's sum is one workgroup's (or a few
+// ranges of rows are joined in their order).
+#include "kamera_attend.h"
+
+namespace kamera {
+
+namespace {
+
+constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
+dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
+
+struct WeighIo {
+  const void* q;
+  const float* lse;
+  float* scores;
+  int64_t q_stride, layer0;
+  float scale2;   // scale * log2(e)
+  float decay;
+  int32_t q_vec;  // rows of q in 16-byte pieces
+  int32_t rows_of_token;  // query heads of a key head
+};
+
+constexpr float kLog2 = 1.44269504088896340736f;
+
+// Query row `row` of key head `head`: its token in the run and its query head. (Differential: the heads of a
+// pair of key heads take turns.)
+struct QueryRow {
+  int j, token, qh;
+};
+__device__ __forceinline__ QueryRow query_row(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, int row) {
+  QueryRow r;
+  r.j = (int)(((uint64_t)(uint32_t)row * a.group_magic) >> a.group_bits);
+  const int g = row - r.j * io.rows_of_token;
+  r.token = it.listed ? a.tok[it.tok0 + r.j] : it.tok0 + r.j;
+  r.qh = a.differential ? (head >> 1) * 2 * io.rows_of_token + 2 * g + (head & 1) : head * io.rows_of_token + g;
+  return r;
+}
+
+__device__ __forceinline__ int64_t slot_of(const StepArgs& a, int pg, int slot0, int t, int& place) {
+  const int slot = slot0 + t, e = (int)(((uint64_t)(uint32_t)slot * a.page_magic) >> a.page_bits);
+  place = slot - e * a.page_size;
+  return ((const KGLOBAL int32_t*)a.pages)[pg + e];
+}
+
+__device__ __forceinline__ void add_score(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head, float sum) {
+  KGLOBAL float* p = (KGLOBAL float*)io.scores + (page * a.heads + head) * a.page_size + place;
+  *p = io.decay == 0.0f ? sum : io.decay * *p + sum;
+}
+
+// ============================================================================
+// Any layout: 16 lanes a key, 16 keys a workgroup, every lane VEC * NJ of its columns; the rows one after the other.
+// ============================================================================
+template <typename T>
+__device__ __forceinline__ float widened(T x) {
+  if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)x << 16);
+  else return x;
+}
+
+template <typename T, int NJ>
+__global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) {
+  const uint32_t block = block_number();
+  const int item = (int)(block / (uint32_t)a.heads), head = (int)(block - (uint32_t)item * (uint32_t)a.heads);
+  if (item >= a.num_weigh) return;
+  const WeighItem it = a.weigh[item];
+  const int lane = threadIdx.x & 15, t = it.kv0 + (threadIdx.x >> 4);
+  int place;
+  const int64_t page = slot_of(a, it.pg, it.slot, min(t, it.kv1 - 1), place);
+  const KGLOBAL T* kp = (const KGLOBAL T*)a.k_pool + io.layer0 + (page * a.page_size + place) * a.row + (int64_t)head * a.dk;
+  float k[NJ];
+#pragma unroll
+  for (int i = 0; i < NJ; ++i) {
+    const int d = i * 16 + lane;
+    k[i] = d < a.dk ? widened<T>(kp[d]) : 0.0f;
+  }
+  float sum = 0.0f;
+  for (int row = it.row0; row < it.row1; ++row) {
+    const QueryRow r = query_row(a, io, it, head, row);
+    const KGLOBAL T* qp = (const KGLOBAL T*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * a.dk;
+    const float lse = io.lse[(int64_t)r.token * a.num_q_heads + r.qh];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) {
+      const int d = i * 16 + lane;
+      if (d < a.dk) s += widened<T>(qp[d]) * k[i];
+    }
+    for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d, 16);
+    if (t <= it.lim0 + r.j * it.lstep && lse != -INFINITY) sum += exp2f(s * io.scale2 - lse * kLog2);
+  }
+  if (lane != 0 || t >= it.kv1) return;
+  if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = sum;
+  else add_score(a, io, page, place, head, sum);
+}
+
+// ============================================================================
+// On the matrix cores: S = Q K^T in tiles of 16 rows x 16 keys (v_mfma_f32_16x16x32_bf16). A wave holds
+// 16 KT keys in registers for good; stages of SR query rows go through LDS, laid out as the attention
+// lays out keys, two stages in turn. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
+// row's lse off and adds up the exponentials.
+// ============================================================================
+template <int DK, int DV, int KT, int SR>
+__global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
+  typedef State<DK, DV, 16> S;
+  constexpr int kRows = SR * 2 * DK, kRest = S::kRestRow;
+  __shared__ __align__(1024) char stage[2][kRows];
+  __shared__ __align__(16) float base[2][SR];  // lse * log2(e); inf: the row adds nothing
+  __shared__ __align__(16) int limit[2][SR];   // last key that the row sees
+  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const WeighItem it = a.weigh[item];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
+  const int key0 = it.kv0 + wave * 16 * KT;  // the wave's first key
+  const bool any = key0 < it.kv1;
+  // keys
+  bf16x8 k[KT][S::kKSteps];
+  int page[KT], place[KT];
+#pragma unroll
+  for (int x = 0; x < KT; ++x) page[x] = (int)slot_of(a, it.pg, it.slot, min(key0 + 16 * x + n, it.kv1 - 1), place[x]);
+#pragma unroll
+  for (int x = 0; x < KT; ++x) {
+    const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + ((int64_t)page[x] * a.page_size + place[x]) * a.row + (int64_t)head * DK;
+#pragma unroll
+    for (int ks = 0; ks < S::kKSteps; ++ks) k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
+  }
+  // a stage's rows in pieces of 16 bytes: piece p of row r
+  constexpr int kPieces = DK / 8, kFirst = DV / 8;  // of a row; of them in its first part
+  auto put = [&](int buffer, int row0) {
+    for (int i = threadIdx.x; i < SR * kPieces; i += kThreads) {
+      const int r = i / kPieces, p = i - r * kPieces;
+      const QueryRow q = query_row(a, io, it, head, min(row0 + r, it.row1 - 1));
+      const KGLOBAL uint16_t* x = (const KGLOBAL uint16_t*)io.q + (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK + p * 8;
+      u32x4 w;
+      if (io.q_vec) {
+        w = *(const KGLOBAL u32x4*)x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
+      }
+      char* to = stage[buffer];
+      if (p < kFirst) to += r * S::kKeyRow + ((p ^ swz<16, S::kKeyRow>(r)) << 4);
+      else to += SR * S::kKeyRow + r * kRest + (((p - kFirst) ^ swz<16, 128>(r)) << 4);
+      *(u32x4*)to = w;
+    }
+    if (threadIdx.x < SR) {
+      const int row = row0 + threadIdx.x;
+      const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
+      const float lse = io.lse[(int64_t)q.token * a.num_q_heads + q.qh];
+      const bool adds = row < it.row1 && lse != -INFINITY;
+      base[buffer][threadIdx.x] = lse * kLog2;
+      limit[buffer][threadIdx.x] = adds ? it.lim0 + q.j * it.lstep : -1;
+    }
+  };
+  float sum[KT];
+#pragma unroll
+  for (int x = 0; x < KT; ++x) sum[x] = 0.0f;
+  put(0, it.row0);
+  int buffer = 0;
+  for (int row0 = it.row0; row0 < it.row1; row0 += SR, buffer ^= 1) {
+    __syncthreads();
+    if (row0 + SR < it.row1) put(buffer ^ 1, row0 + SR);
+    if (!any) continue;
+    const KLDS char* rows = (const KLDS char*)stage[buffer];
+#pragma unroll
+    for (int r = 0; r < SR; r += 16) {
+      typename S::Acc s[KT];
+#pragma unroll
+      for (int x = 0; x < KT; ++x) s[x] = (typename S::Acc)(0.0f);
+#pragma unroll
+      for (int ks = 0; ks < S::kKSteps; ++ks) {
+        const bf16x8 q = S::k_operand(rows + r * S::kKeyRow, rows + SR * S::kKeyRow + r * kRest, 0, ks);
+#pragma unroll
+        for (int x = 0; x < KT; ++x) s[x] = S::mfma(q, k[x][ks], s[x]);
+      }
+      const f32x4 b = *(const KLDS f32x4*)&base[buffer][r + 4 * S::group()];
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 lim = *(const KLDS i32x4*)&limit[buffer][r + 4 * S::group()];
+#pragma unroll
+      for (int x = 0; x < KT; ++x) {
+        const int t = key0 + 16 * x + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
+          sum[x] += t <= lim[i] ? w : 0.0f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < KT; ++x) {
+    const float total = row_sum<16>(sum[x]);
+    const int t = key0 + 16 * x + n;
+    if (lane >= 16 || t >= it.kv1) continue;
+    if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = total;
+    else add_score(a, io, page[x], place[x], head, total);
+  }
+}
+
+// Sums of ranges of rows, joined in their order: a thread a key and head. A range that ends before the first row
+// that sees a tile's keys has none of them.
+__global__ __launch_bounds__(kThreads) void weigh_join(StepArgs a, WeighIo io) {
+  const int64_t blocks = (a.weigh_longest + kThreads - 1) / kThreads;
+  int64_t b = block_number();
+  const int t = (int)(b % blocks) * kThreads + (int)threadIdx.x;
+  b /= blocks;
+  const int head = (int)(b % a.heads), run = (int)(b / a.heads);
+  if (run >= a.num_weigh_join) return;
+  const WeighJoin j = a.weigh_join[run];
+  if (t >= j.kv) return;
+  const int kv0 = t / j.tile * j.tile;
+  const int64_t row0 = j.lstep && kv0 > j.lim0 ? (int64_t)(kv0 - j.lim0) * io.rows_of_token : 0;
+  const KGLOBAL float* p = (const KGLOBAL float*)a.weigh_part + j.part + (int64_t)head * j.kv + t;
+  float sum = 0.0f;
+  for (int s = (int)(row0 / j.rows); s < j.splits; ++s) sum += p[(int64_t)s * a.heads * j.kv];
+  int place;
+  const int64_t page = slot_of(a, j.pg, j.slot, t, place);
+  add_score(a, io, page, place, head, sum);
+}
+
+template <typename T>
+hipError_t plain(const StepArgs& a, const WeighIo& io, hipStream_t stream) {
+  const dim3 g = grid_of((int64_t)a.num_weigh * a.heads), b(kThreads);
+  if (a.dk <= 128) hipLaunchKernelGGL((weigh_plain<T, 8>), g, b, 0, stream, a, io);
+  else if (a.dk <= 640) hipLaunchKernelGGL((weigh_plain<T, 40>), g, b, 0, stream, a, io);
+  else hipLaunchKernelGGL((weigh_plain<T, 64>), g, b, 0, stream, a, io);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_t q_stride, const float* lse, float* scores, float scale,
+                             float decay, hipStream_t stream) {
+  WeighIo io{q, lse, scores, q_stride, layer * a.layer_stride, scale * kLog2, decay, 0, a.num_q_heads / a.heads};
+  io.q_vec = q_stride % 8 == 0 && (uintptr_t)q % 16 == 0;
+  if (a.num_weigh == 0) return hipSuccess;
+  hipError_t e;
+  if (a.weigh_kernel == ATTEND_PLAIN) {
+    e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
+  } else {
+    const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 2, 16>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 32>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 32>), g, b, 0, stream, a, io);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || a.num_weigh_join == 0) return e;
+  const int64_t blocks = (int64_t)((a.weigh_longest + kThreads - 1) / kThreads) * a.heads * a.num_weigh_join;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(weigh_join, grid_of(blocks), dim3(kThreads), 0, stream, a, io);
+  return hipGetLastError();
+}
+
+}  // namespace kamera

@@ -14,11 +14,14 @@ import numpy as np
 from . import abi
 from .abi import Layout, Pool, _check, _ptr, _ws
 
-APPEND, ATTEND, FIT = 1, 2, 4
+APPEND, ATTEND, FIT, WEIGH, DIFFERENTIAL = 1, 2, 4, 16, 32
 REQUEST_ALL = 1
+DIFF_NORM = 1
+REANCHOR = 1
 ATTEND_MAX_DIM = 1024
 
 EXPORTED = ["kamera_step_workspace_bytes", "kamera_step_upload", "kamera_step_append", "kamera_step_attend",
+            "kamera_step_attend_diff", "kamera_step_weigh", "kamera_evict_workspace_bytes", "kamera_evict", "kamera_scores_layout",
             "kamera_copy_pages_workspace_bytes", "kamera_copy_pages", "kamera_compact_pages"]
 
 
@@ -51,6 +54,21 @@ class AppendRows(ctypes.Structure):
                 ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class Differential(ctypes.Structure):
+    _fields_ = [("lambdas", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("lambda_init", ctypes.c_float),
+                ("out_scale", ctypes.c_float), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class EvictSeq(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("slot0", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("keep", ctypes.c_int32),
+                ("first", ctypes.c_int32), ("last", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class EvictDesc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_void_p), ("scores", ctypes.c_void_p), ("scores_stride", ctypes.c_int64), ("kept", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_int32), ("heads_together", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
+
+
 _REQUEST = np.dtype({"names": [n for n, _ in Request._fields_],
                      "formats": [np.uint64, np.int32, np.int32, np.int32, np.int32, np.int64, np.uint32, np.int32],
                      "offsets": [getattr(Request, n).offset for n, _ in Request._fields_],
@@ -58,6 +76,9 @@ _REQUEST = np.dtype({"names": [n for n, _ in Request._fields_],
 _PREFIX = np.dtype({"names": [n for n, _ in Prefix._fields_], "formats": [np.uint64, np.int32, np.int32],
                     "offsets": [getattr(Prefix, n).offset for n, _ in Prefix._fields_],
                     "itemsize": ctypes.sizeof(Prefix)})
+
+_EVICT = np.dtype({"names": [n for n, _ in EvictSeq._fields_], "formats": [np.uint64] + [np.int32] * 6,
+                   "offsets": [getattr(EvictSeq, n).offset for n, _ in EvictSeq._fields_], "itemsize": ctypes.sizeof(EvictSeq)})
 
 _bound = None
 
@@ -72,6 +93,11 @@ def _lib() -> ctypes.CDLL:
         L.kamera_step_upload.argtypes = [lay, ctypes.POINTER(StepDesc), pool, vp, sz, vp, plan]
         L.kamera_step_append.argtypes = [plan, i32, ctypes.POINTER(AppendRows), vp]
         L.kamera_step_attend.argtypes = [plan, i32, vp, i64, vp, i64, vp, ctypes.c_float, vp]
+        L.kamera_step_attend_diff.argtypes = [plan, i32, vp, i64, vp, i64, vp, ctypes.c_float, ctypes.POINTER(Differential), vp]
+        L.kamera_step_weigh.argtypes = [plan, i32, vp, i64, vp, vp, ctypes.c_float, ctypes.c_float, vp]
+        L.kamera_evict_workspace_bytes.argtypes = [lay, ctypes.POINTER(EvictDesc)]
+        L.kamera_evict.argtypes = [lay, pool, ctypes.POINTER(EvictDesc), vp, sz, vp]
+        L.kamera_scores_layout.argtypes = [lay, lay]
         L.kamera_copy_pages_workspace_bytes.argtypes = [i32]
         L.kamera_copy_pages.argtypes = [lay, pool, vp, vp, i32, vp, sz, vp]
         L.kamera_compact_pages.argtypes = [lay, pool, ctypes.POINTER(vp), vp, i32, ctypes.POINTER(i32), vp, sz, vp]
@@ -204,6 +230,7 @@ class _Like:
         self.heads = num_q_heads
         self.q, self.out = num_q_heads * self.dk, num_q_heads * (self.dk if gqa else layout.latent_dim)
         self.stats, self.positions = torch.float32, torch.int32
+        self.scores = 0  # elements of a layer's scores (set by upload)
 
 
 def _on_gpu(what: str, x) -> None:
@@ -241,6 +268,8 @@ def upload(layout: Layout, step: Step, pool: Pool, workspace, stream=None) -> Pl
                                      _stream(stream), ctypes.byref(plan)))
     plan._workspace = workspace
     plan._like = like
+    if like is not None:
+        like.scores = pool.num_pages * layout.page_size * (layout.num_kv_heads if like.gqa else 1)
     return plan
 
 
@@ -309,6 +338,96 @@ def attend(plan: Plan, layer: int, q, out, scale: float, lse=None, *, q_stride: 
     status = (_bound or _lib()).kamera_step_attend(ctypes.byref(plan), layer, qp, qs, op, os_, _ptr(lse), scale, _stream(stream))
     if status:
         _check(status)
+
+
+def attend_diff(plan: Plan, layer: int, q, out, scale: float, *, lambda_init: float, lambdas=None, norm_weight=None, norm: bool = True,
+                eps: float = 1e-5, out_scale: Optional[float] = None, lse=None, q_stride: Optional[int] = None,
+                out_stride: Optional[int] = None, stream=None) -> None:
+    """Differential attention of the step's query tokens over layer `layer` of the pool. lambdas: float32 [4][head_dim];
+    out_scale: 1 - lambda_init by default."""
+    n, like = plan.num_tokens, plan._like
+    wq = 0
+    if like is not None:
+        wq = like.q
+        lse = _flat("lse", lse, like.stats, n * like.heads)
+        lambdas = _flat("lambdas", lambdas, like.stats, 4 * like.dk, True)
+        norm_weight = _flat("norm_weight", norm_weight, like.dtype, 2 * like.dk, True)
+    qp, qs = _rows("q", q, q_stride, n, wq, like)
+    op, os_ = _rows("out", out, out_stride, n, wq, like)  # (num_q_heads / 2 heads, twice as wide)
+    d = Differential(_ptr(lambdas), _ptr(norm_weight), lambda_init, 1.0 - lambda_init if out_scale is None else out_scale, eps,
+                     DIFF_NORM if norm else 0)
+    status = (_bound or _lib()).kamera_step_attend_diff(ctypes.byref(plan), layer, qp, qs, op, os_, _ptr(lse), scale, ctypes.byref(d),
+                                                        _stream(stream))
+    if status:
+        _check(status)
+
+
+def weigh(plan: Plan, layer: int, q, lse, scores, scale: float, decay: float = 1.0, *, q_stride: Optional[int] = None, stream=None) -> None:
+    """Add the attention weights of the step's query tokens in layer `layer` to the layer's scores, float32
+    [pages][KV heads][page_size]; q, lse and scale are the attention's."""
+    n, like = plan.num_tokens, plan._like
+    wq = 0
+    if like is not None:
+        wq = like.q
+        lse = _flat("lse", lse, like.stats, n * like.heads)
+        scores = _flat("scores", scores, like.stats, like.scores)
+    qp, qs = _rows("q", q, q_stride, n, wq, like)
+    status = (_bound or _lib()).kamera_step_weigh(ctypes.byref(plan), layer, qp, qs, _ptr(lse), _ptr(scores), scale, decay, _stream(stream))
+    if status:
+        _check(status)
+
+
+class Eviction:
+    """A kamera_eviction without its device arrays, and the host arrays it points into.
+
+    block_tables as for `Step`, a row a sequence, read in place by every call; the other fields are scalars or one
+    value a sequence. `seqs` is the structured array the library reads.
+    """
+
+    def __init__(self, *, block_tables, num_tokens, keep, slot0=0, first=0, last=0, heads_together: int = 1, flags: int = 0):
+        n = len(block_tables)
+        addresses, entries, self._keep = _tables(block_tables, n)
+        self.seqs = np.zeros(n, _EVICT)
+        self.seqs["block_table"] = addresses
+        for name, value in (("slot0", slot0), ("num_tokens", num_tokens), ("keep", keep), ("first", first), ("last", last)):
+            self.seqs[name] = value
+            if (self.seqs[name] != value).any():
+                raise ValueError(f"{name}: a value does not fit its field")
+        self._entries = _Entries("sequence", self.seqs, entries) if n else None
+        self.c = EvictDesc(self.seqs.ctypes.data if n else None, None, 0, None, n, int(heads_together), int(flags), 0)
+
+
+def evict_workspace_bytes(layout: Layout, eviction: Eviction) -> int:
+    """Bytes that an eviction needs (those for longer sequences that keep at least as much serve shorter ones too)."""
+    return int(_lib().kamera_evict_workspace_bytes(ctypes.byref(layout), ctypes.byref(eviction.c)))
+
+
+def evict(layout: Layout, pool: Pool, eviction: Eviction, scores, workspace, *, kept=None, scores_stride: int = 0, stream=None) -> None:
+    """The tokens of least score leave their sequences, in every layer; `kept` (int32 [layers][groups][kept tokens of all
+    sequences]) receives those that stay. scores: float32 [layers][pages][KV heads][page_size]."""
+    if eviction._entries is not None:
+        eviction._entries.check(layout.page_size)
+    heads = layout.num_kv_heads if layout.family == abi.GQA else 1
+    try:
+        import torch
+        size = pool.num_pages * layout.page_size * heads
+        scores = _flat("scores", scores, torch.float32, max(scores_stride, size) * (layout.num_layers - 1) + size)
+        total = int(np.minimum(eviction.seqs["keep"], eviction.seqs["num_tokens"]).sum(dtype=np.int64)) if len(eviction.seqs) else 0
+        kept = _flat("kept", kept, torch.int32, layout.num_layers * (heads // max(eviction.c.heads_together, 1)) * total)
+    except ImportError:  # addresses alone
+        pass
+    c = EvictDesc.from_buffer_copy(eviction.c)  # (a description may be used by several threads)
+    c.scores, c.scores_stride, c.kept = _ptr(scores), scores_stride, _ptr(kept)
+    wp, wb = _ws(workspace)
+    _check(_lib().kamera_evict(ctypes.byref(layout), ctypes.byref(pool), ctypes.byref(c), wp, wb, _stream(stream)))
+
+
+def scores_layout(layout: Layout) -> Layout:
+    """The layout under which copy_pages and compact_pages move the scores of a pool of layout `layout`: a pool
+    made of the scores alone, `abi.make_pool(scores, None, pages)`."""
+    out = Layout()
+    _check(_lib().kamera_scores_layout(ctypes.byref(layout), ctypes.byref(out)))
+    return out
 
 
 def copy_pages_workspace_bytes(num_copies: int) -> int:
