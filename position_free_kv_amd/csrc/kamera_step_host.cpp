@@ -367,7 +367,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 // A run is a segment (a prefix with all its requests' query tokens, or a request's own tokens); an item a
 // tile of its keys and the rows that see any of them. Where that leaves the chip without work for all its
 // workgroups, rows are cut into ranges whose sums are joined (in the order of the ranges).
-constexpr int64_t kWeighSlots = 1024, kWeighRows = 512;
+constexpr int64_t kWeighSlots = 1024;
+constexpr int64_t weigh_rows(int kernel) { return kernel == ATTEND_LATENT ? 128 : 512; }  // fewest of a range
 void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
   const Shape h = shape_of(L, s->num_q_heads);
   const int G = h.group;
@@ -429,7 +430,7 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
   auto first_row = [&](const WeighItem& r, int64_t kv0) { return r.lstep ? std::max<int64_t>(kv0 - r.lim0, 0) * G : 0; };
   double work = 0;
   for (const WeighItem& r : runs) work += (double)ceil_div(r.kv, keys) * r.ntok * G * h.heads;
-  const int64_t range = fit.split_rows ? std::max<int64_t>(kWeighRows, (int64_t)round_up((size_t)(work / kWeighSlots) + 1, 64)) : int64_t(1) << 40;
+  const int64_t range = fit.split_rows ? std::max<int64_t>(weigh_rows(kernel), (int64_t)round_up((size_t)(work / kWeighSlots) + 1, 64)) : int64_t(1) << 40;
   for (WeighItem& r : runs) {
     const int64_t rows = (int64_t)r.ntok * G, n = ceil_div(rows, range);
     const int64_t each = n > 1 ? (int64_t)round_up((size_t)ceil_div(rows, n), 64) : rows, splits = ceil_div(rows, each);

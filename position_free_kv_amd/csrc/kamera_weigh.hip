@@ -104,88 +104,141 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
 // lays out keys, two stages in turn. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
 // row's lse off and adds up the exponentials.
 // ============================================================================
+
+// A wave's share of a stage: PER rows. Lane i looks after row i % PER one stage ahead of its load.
+template <int DK, int DV, int SR>
+struct QueryRows {
+  static constexpr int PER = SR / kWaves;
+  int64_t at;   // element of q where the row begins
+  float base;   // lse * log2(e)
+  int limit;    // last key that the row sees; -1: it adds nothing
+  __device__ __forceinline__ void find(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, int row0) {
+    const int wave = threadIdx.x >> 6, row = row0 + wave * PER + ((int)threadIdx.x & (PER - 1));
+    const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
+    at = (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK;
+    const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)q.token * a.num_q_heads + q.qh];
+    base = lse * kLog2;
+    limit = row < it.row1 && lse != -INFINITY ? it.lim0 + q.j * it.lstep : -1;
+  }
+  // the rows' places among the statistics; whole[wave]: every row sees keys up to `last`
+  __device__ __forceinline__ void note(float* bases, int* limits, int* whole, int last) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const bool all = __all(limit >= last);
+    if (lane < PER) {
+      bases[wave * PER + lane] = base;
+      limits[wave * PER + lane] = limit;
+    }
+    if (lane == 0) whole[wave] = all;
+  }
+  __device__ __forceinline__ const KGLOBAL uint16_t* row(const WeighIo& io, int i) const {
+    const int lo = __shfl((int)(uint32_t)at, i, 64), hi = __shfl((int)(at >> 32), i, 64);
+    return (const KGLOBAL uint16_t*)io.q + (((int64_t)hi << 32) | (uint32_t)lo);
+  }
+  // the rows into LDS, swizzled like keys: the first DV columns (DK if there are fewer), then the others' rows
+  __device__ __forceinline__ void load(const WeighIo& io, KLDS char* stage) const {
+    typedef State<DK, DV, 16> S;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, first = wave * PER;
+    constexpr int LPR = S::kKeyRow / 16 < 64 ? S::kKeyRow / 16 : 64, RPI = 64 / LPR;  // lanes of a row, rows of an instruction
+    static_assert(S::kKeyRow <= 1024 && PER % RPI == 0, "whole instructions");
+    auto bring = [&](const KGLOBAL uint16_t* x, KLDS char* to) {
+      if (io.q_vec) {
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)x, (KLDS void*)to, 16, 0, 0);
+      } else {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
+        *(KLDS u32x4*)(to + lane * 16) = w;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < PER; i += RPI) {
+      const int r = i + lane / LPR;
+      bring(row(io, r) + ((lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(first + r)) * 8, stage + (first + i) * S::kKeyRow);
+    }
+    if constexpr (S::kRestRow != 0) {
+      static_assert(S::kRestRow == 128 && PER % 8 == 0, "bands of 8 rows to an instruction");
+#pragma unroll
+      for (int i = 0; i < PER; i += 8) {
+        const int r = i + lane / 8;
+        bring(row(io, r) + DV + ((lane & 7) ^ swz<16, 128>(first + r)) * 8, stage + SR * S::kKeyRow + (first + i) * 128);
+      }
+    }
+  }
+};
+
 template <int DK, int DV, int KT, int SR>
 __global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
   typedef State<DK, DV, 16> S;
-  constexpr int kRows = SR * 2 * DK, kRest = S::kRestRow;
-  __shared__ __align__(1024) char stage[2][kRows];
-  __shared__ __align__(16) float base[2][SR];  // lse * log2(e); inf: the row adds nothing
-  __shared__ __align__(16) int limit[2][SR];   // last key that the row sees
+  __shared__ __align__(1024) char stage[2][SR * 2 * DK];
+  __shared__ __align__(16) float base[2][SR];
+  __shared__ __align__(16) int limit[2][SR];
+  __shared__ __align__(16) int whole[2][kWaves];
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const WeighItem it = a.weigh[item];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
   const int key0 = it.kv0 + wave * 16 * KT;  // the wave's first key
   const bool any = key0 < it.kv1;
-  // keys
-  bf16x8 k[KT][S::kKSteps];
+  QueryRows<DK, DV, SR> rows;
+  rows.find(a, io, it, head, it.row0);
   int page[KT], place[KT];
 #pragma unroll
   for (int x = 0; x < KT; ++x) page[x] = (int)slot_of(a, it.pg, it.slot, min(key0 + 16 * x + n, it.kv1 - 1), place[x]);
+  rows.load(io, (KLDS char*)stage[0]);
+  bf16x8 k[KT][S::kKSteps];
 #pragma unroll
   for (int x = 0; x < KT; ++x) {
     const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + ((int64_t)page[x] * a.page_size + place[x]) * a.row + (int64_t)head * DK;
 #pragma unroll
     for (int ks = 0; ks < S::kKSteps; ++ks) k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
   }
-  // a stage's rows in pieces of 16 bytes: piece p of row r
-  constexpr int kPieces = DK / 8, kFirst = DV / 8;  // of a row; of them in its first part
-  auto put = [&](int buffer, int row0) {
-    for (int i = threadIdx.x; i < SR * kPieces; i += kThreads) {
-      const int r = i / kPieces, p = i - r * kPieces;
-      const QueryRow q = query_row(a, io, it, head, min(row0 + r, it.row1 - 1));
-      const KGLOBAL uint16_t* x = (const KGLOBAL uint16_t*)io.q + (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK + p * 8;
-      u32x4 w;
-      if (io.q_vec) {
-        w = *(const KGLOBAL u32x4*)x;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
-      }
-      char* to = stage[buffer];
-      if (p < kFirst) to += r * S::kKeyRow + ((p ^ swz<16, S::kKeyRow>(r)) << 4);
-      else to += SR * S::kKeyRow + r * kRest + (((p - kFirst) ^ swz<16, 128>(r)) << 4);
-      *(u32x4*)to = w;
-    }
-    if (threadIdx.x < SR) {
-      const int row = row0 + threadIdx.x;
-      const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
-      const float lse = io.lse[(int64_t)q.token * a.num_q_heads + q.qh];
-      const bool adds = row < it.row1 && lse != -INFINITY;
-      base[buffer][threadIdx.x] = lse * kLog2;
-      limit[buffer][threadIdx.x] = adds ? it.lim0 + q.j * it.lstep : -1;
-    }
-  };
+  rows.note(base[0], limit[0], whole[0], it.kv1 - 1);
+  if (it.row0 + SR < it.row1) rows.find(a, io, it, head, it.row0 + SR);
   float sum[KT];
 #pragma unroll
   for (int x = 0; x < KT; ++x) sum[x] = 0.0f;
-  put(0, it.row0);
   int buffer = 0;
   for (int row0 = it.row0; row0 < it.row1; row0 += SR, buffer ^= 1) {
-    __syncthreads();
-    if (row0 + SR < it.row1) put(buffer ^ 1, row0 + SR);
+    stage_barrier();
+    if (row0 + SR < it.row1) {
+      rows.load(io, (KLDS char*)stage[buffer ^ 1]);
+      rows.note(base[buffer ^ 1], limit[buffer ^ 1], whole[buffer ^ 1], it.kv1 - 1);
+      if (row0 + 2 * SR < it.row1) rows.find(a, io, it, head, row0 + 2 * SR);
+    }
     if (!any) continue;
-    const KLDS char* rows = (const KLDS char*)stage[buffer];
+    const KLDS char* at = (const KLDS char*)stage[buffer];
+    constexpr int kWavesOf = 16 / (SR / kWaves);  // waves that brought 16 rows
 #pragma unroll
     for (int r = 0; r < SR; r += 16) {
+      if (row0 + r >= it.row1) break;
       typename S::Acc s[KT];
 #pragma unroll
       for (int x = 0; x < KT; ++x) s[x] = (typename S::Acc)(0.0f);
 #pragma unroll
       for (int ks = 0; ks < S::kKSteps; ++ks) {
-        const bf16x8 q = S::k_operand(rows + r * S::kKeyRow, rows + SR * S::kKeyRow + r * kRest, 0, ks);
+        const bf16x8 q = S::k_operand(at + r * S::kKeyRow, at + SR * S::kKeyRow + r * S::kRestRow, 0, ks);
 #pragma unroll
         for (int x = 0; x < KT; ++x) s[x] = S::mfma(q, k[x][ks], s[x]);
       }
       const f32x4 b = *(const KLDS f32x4*)&base[buffer][r + 4 * S::group()];
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      const i32x4 lim = *(const KLDS i32x4*)&limit[buffer][r + 4 * S::group()];
+      int all = 1;
 #pragma unroll
-      for (int x = 0; x < KT; ++x) {
-        const int t = key0 + 16 * x + n;
+      for (int w = 0; w < kWavesOf; ++w) all &= whole[buffer][r / 16 * kWavesOf + w];
+      if (__builtin_amdgcn_readfirstlane(all)) {  // every row adds to every key
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
-          sum[x] += t <= lim[i] ? w : 0.0f;
+        for (int x = 0; x < KT; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
+      } else {
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        const i32x4 lim = *(const KLDS i32x4*)&limit[buffer][r + 4 * S::group()];
+#pragma unroll
+        for (int x = 0; x < KT; ++x) {
+          const int t = key0 + 16 * x + n;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
+            sum[x] += t <= lim[i] ? w : 0.0f;
+          }
         }
       }
     }
@@ -242,7 +295,7 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
     e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
-    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 2, 16>), g, b, 0, stream, a, io);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 2, 32>), g, b, 0, stream, a, io);
     else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 32>), g, b, 0, stream, a, io);
     else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 32>), g, b, 0, stream, a, io);
     e = hipGetLastError();
