@@ -7,6 +7,10 @@
 // 32 (or 16) rows of one map, so that a stage's values are brought into LDS once for both maps.
 #include "kamera_attend.h"
 
+#ifndef JVP
+#define JVP 32
+#define JVR 1024
+#endif
 namespace kamera {
 
 namespace {
@@ -30,8 +34,9 @@ template <int D, int TS, int N, int ROWS>
 struct PairRows {
   int row;
   __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int last) {
-    int place;
-    const int t = min(t0 + first + ((int)threadIdx.x & (N - 1)), last);
+    int lane = threadIdx.x, place;
+    asm volatile("" : "+v"(lane));  // (see load)
+    const int t = min(t0 + first + (lane & (N - 1)), last);
     const int page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, t, place)];
     row = page * a.page_size + place;
   }
@@ -39,7 +44,8 @@ struct PairRows {
   __device__ __forceinline__ void load(const StepArgs& a, const uint16_t* k, const uint16_t* v, KLDS char* stage, int first) const {
     constexpr int RK = 1024 / kKeyBytes<D>, LK = 64 / RK, RV = 1024 / kValueBytes<D>, LV = 64 / RV;  // rows of an instruction, lanes of a row
     static_assert(N % RK == 0, "whole instructions");
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // what follows from it is made anew each stage: kept, it would cost the products registers
     KLDS char* values = stage + 2 * TS * kKeyBytes<D>;
 #pragma unroll
     for (int i = 0; i < N; i += RK) {
@@ -104,7 +110,9 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
     }
   }
   const float l = row_sum<32>(st.l);
-  put_state(a, io, it, head, r, st, l);
+  int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
+  asm volatile("" : "+v"(tid));
+  put_state(a, io, it, head, lane_row(a, it, head, it.row0 + (tid >> 7) * 64 + 2 * (tid & 31) + ((tid >> 6) & 1)), st, l);
 }
 
 // ============================================================================
@@ -145,7 +153,9 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   float l = row_sum<ROWS>(st.l);
   static_assert(2 * 64 * S::kBlocks * S::kScores * 4 <= kLds, "two waves' results fit in LDS");
   join_two(st, l, part == 1, map, (f32x4*)(KLDS f32x4*)(lds + map * (kLds / 2)), ml);
-  if (part == 0) put_state(a, io, it, head, r, st, l);
+  int tid = threadIdx.x;  // (as in the wide tile)
+  asm volatile("" : "+v"(tid));
+  if (part == 0) put_state(a, io, it, head, lane_row(a, it, head, it.row0 + 2 * (tid & (ROWS - 1)) + ((tid >> 6) & 1)), st, l);
 }
 
 // One launch for all tiles, the wide ones first.
@@ -187,11 +197,12 @@ __device__ __forceinline__ float widened(T x) {
 }
 
 // PIECES: 16-byte pieces of the two rows that a lane takes
+constexpr int join_waves_of(int wpr) { return wpr > kWaves ? wpr : kWaves; }  // waves of a workgroup
 template <typename T, int WPR, int PIECES>
-__global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
-  constexpr int ROWS = kWaves / WPR;
+__global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
+  constexpr int ROWS = join_waves_of(WPR) / WPR;
   __shared__ float2 weight[ROWS][WPR == 1 ? kWaveSize : kJoinParts];
-  __shared__ f32x4 held[kWaves][PIECES * kWaveSize];
+  __shared__ f32x4 held[join_waves_of(WPR)][PIECES * kWaveSize];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = wave / WPR, seat = wave % WPR;
   const int outs = a.num_q_heads / 2;
   const int64_t task = (int64_t)(blockIdx.y * (uint32_t)kGridRow + blockIdx.x) * ROWS + sub;
@@ -240,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, k
   f32x4 o[PIECES];
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) o[j] = (f32x4)(0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int k = seat; k < n; k += WPR) {
     const float2 w = weight[sub][k];
     const KGLOBAL f32x4* p = parts + row(k) * quads;
@@ -312,8 +323,14 @@ __global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, k
 template <typename T, int WPR>
 hipError_t join(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, hipStream_t stream) {
   const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
-  const dim3 g = grid_of((rows + kWaves / WPR - 1) / (kWaves / WPR)), b(kThreads);
+  constexpr int W = join_waves_of(WPR), ROWS = W / WPR;
+  const dim3 g = grid_of((rows + ROWS - 1) / ROWS), b(W * kWaveSize);
   const int pieces = (a.dv / 2 + kWaveSize - 1) / kWaveSize;
+  if constexpr (WPR > kWaves) {
+    if (pieces <= 1) hipLaunchKernelGGL((diff_join<T, WPR, 1>), g, b, 0, stream, a, io, diff);
+    else hipLaunchKernelGGL((diff_join<T, WPR, 2>), g, b, 0, stream, a, io, diff);
+    return hipGetLastError();
+  }
   if (pieces <= 1) hipLaunchKernelGGL((diff_join<T, WPR, 1>), g, b, 0, stream, a, io, diff);
   else if (pieces <= 2) hipLaunchKernelGGL((diff_join<T, WPR, 2>), g, b, 0, stream, a, io, diff);
   else if (pieces <= 4) hipLaunchKernelGGL((diff_join<T, WPR, 4>), g, b, 0, stream, a, io, diff);
@@ -340,9 +357,11 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_merge == 0) return e;
-  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && (int64_t)a.num_merge * a.num_q_heads < 4096);
-  if (a.dtype == KAMERA_BF16) return wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
-  return wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);
+  const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
+  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > JVP && rows < JVR && a.dv <= 256;
+  if (a.dtype == KAMERA_BF16)
+    return very ? join<uint16_t, 16>(a, io, diff, stream) : wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
+  return very ? join<float, 16>(a, io, diff, stream) : wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);
 }
 
 }  // namespace kamera

@@ -11,6 +11,7 @@ namespace kamera {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWave = 64;
 constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
@@ -33,11 +34,12 @@ __device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s
 // numbers of the same order; the `want`-th highest of the tokens between the first and the last ones is
 // found digit by digit (11, 11 and 10 bits, a count of each digit in LDS), then one pass in the tokens' order
 // writes the numbers of those above it and of the first few equal to it. No order of atomics matters:
-// counts are whole numbers.
+// counts are whole numbers. Lists of up to kSelect * kHeld tokens keep their ranks in registers.
 // ============================================================================
 constexpr int kSelect = 512;   // threads
 constexpr int kDigits = 2048;
 constexpr int kEach = 4;       // tokens of a thread in one turn of the last pass
+constexpr int kHeld = 16;      // ranks of a thread
 
 __device__ __forceinline__ uint32_t rank_of(float x) {
   if (x != x) return 0;
@@ -48,7 +50,6 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 struct List {
   EvictSeq seq;
   const KGLOBAL float* scores;  // of the layer, from the group's first head on
-  int group;
   __device__ __forceinline__ int64_t score_at(const EvictArgs& a, int t) const {
     int place;
     const int64_t page = page_of(a, seq, t, place);
@@ -64,39 +65,40 @@ struct List {
 
 __device__ __forceinline__ int wave_prefix(uint64_t mask) { return __popcll(mask & ((uint64_t(1) << (threadIdx.x & 63)) - 1)); }
 
-__global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
+// HELD: token t = (wave * kHeld + i) * 64 + lane of the list is rank i of its thread; the others are read anew by each pass.
+template <bool HELD>
+__device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, KGLOBAL int32_t* kept, KGLOBAL int32_t* start, int keep) {
   __shared__ uint32_t count[kDigits];
   __shared__ int sums[kSelect / kWave][2];
   __shared__ int found[2];
   __shared__ int gone;
-  const int groups = a.heads / a.together, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int64_t b = block_number();
-  const int si = (int)(b % a.num_seqs);
-  b /= a.num_seqs;
-  const int group = (int)(b % groups), layer = (int)(b / groups);
-  if (layer >= a.layers) return;
-  List l;
-  l.seq = a.seqs[si];
-  l.group = group;
-  l.scores = (const KGLOBAL float*)a.scores + layer * a.scores_stride + (int64_t)group * a.together * a.page_size;
-  const int n = l.seq.num_tokens, keep = min(l.seq.keep, n);
-  KGLOBAL int32_t* kept = (KGLOBAL int32_t*)a.kept + ((int64_t)layer * groups + group) * a.total + l.seq.kept0;
-  KGLOBAL int32_t* start = (KGLOBAL int32_t*)a.starts + ((int64_t)layer * groups + group) * a.num_seqs + si;
-  if (keep == n || keep == 0) {
-    for (int j = tid; j < keep; j += kSelect) kept[j] = j;
-    if (tid == 0) *start = keep;
-    return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = l.seq.num_tokens, lo = l.seq.first, hi = n - l.seq.last;  // ranked: [lo, hi)
+  const int turns = HELD ? (n + kSelect - 1) / kSelect : 0;                // ranks of a thread (its wave's tokens follow each other)
+  uint32_t held[HELD ? kHeld : 1];
+  auto token = [&](int i) { return (wave * turns + i) * kWave + lane; };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      held[i] = 0;
+      if (i < turns && token(i) < hi && token(i) >= lo) held[i] = l.rank(a, token(i));
+    }
   }
-  const int lo = l.seq.first, hi = n - l.seq.last;  // those that are ranked
   int want = keep - l.seq.first - l.seq.last;
   uint32_t border = 0, known = 0;  // bits of the border's rank found so far
   for (int pass = 0; pass < 3 && want > 0; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     for (int i = tid; i < kDigits; i += kSelect) count[i] = 0;
     __syncthreads();
-    for (int t = lo + tid; t < hi; t += kSelect) {
-      const uint32_t r = l.rank(a, t);
+    auto add = [&](uint32_t r) {
       if ((r & known) == border) atomicAdd(&count[(r >> shift) & ((1u << bits) - 1)], 1u);
+    };
+    if constexpr (HELD) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i < turns && token(i) < hi && token(i) >= lo) add(held[i]);
+    } else {
+      for (int t = lo + tid; t < hi; t += kSelect) add(l.rank(a, t));
     }
     __syncthreads();
     // the digit at which the counts from the highest on reach `want`
@@ -131,16 +133,19 @@ __global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
   // tokens that stay, in their order
   if (tid == 0) gone = n;
   int above = 0, equal = 0;  // of the turns before
-  for (int t0 = 0; t0 < n; t0 += kSelect * kEach) {
-    bool hit[kEach], tie[kEach];
-    int at[kEach], tied[kEach], a0 = 0, e0 = 0;
+  constexpr int EACH = HELD ? kHeld : kEach;
+  for (int t0 = 0; t0 < n; t0 += kSelect * EACH) {  // (HELD: once)
+    const int each = HELD ? turns : kEach;
+    bool hit[EACH], tie[EACH];
+    int at[EACH], tied[EACH], a0 = 0, e0 = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int t = t0 + (wave * kEach + i) * kWave + lane;
-      hit[i] = t < n && (t < lo || t >= hi);
+    for (int i = 0; i < EACH; ++i) {
+      const int t = t0 + (wave * each + i) * kWave + lane;
+      const bool there = t < n && (!HELD || i < turns);
+      hit[i] = there && (t < lo || t >= hi);
       tie[i] = false;
-      if (ranked && t >= lo && t < hi) {
-        const uint32_t r = l.rank(a, t);
+      if (ranked && there && t >= lo && t < hi) {
+        const uint32_t r = HELD ? held[HELD ? i : 0] : l.rank(a, t);
         hit[i] = r > border;
         tie[i] = r == border;
       }
@@ -167,13 +172,14 @@ __global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
     }
     int leaves = n;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int t = t0 + (wave * kEach + i) * kWave + lane;
+    for (int i = 0; i < EACH; ++i) {
+      const int t = t0 + (wave * each + i) * kWave + lane;
       const int ties = ebase + tied[i];
       if (hit[i] || (tie[i] && ties < want)) kept[abase + at[i] + min(ties, want)] = t;
-      else if (t < n) leaves = min(leaves, t);
+      else if (t < n && (!HELD || i < turns)) leaves = min(leaves, t);
     }
-    if (leaves < n) atomicMin(&gone, leaves);
+    for (int d = 32; d; d >>= 1) leaves = min(leaves, __shfl_xor(leaves, d, kWave));
+    if (lane == 0 && leaves < n) atomicMin(&gone, leaves);
   }
   __syncthreads();  // (the list is written, and visible to the workgroup)
   const int s0 = min(gone, keep);
@@ -197,6 +203,28 @@ __global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
         if (j < keep) scores[l.score_at(a, j) + (int64_t)h * a.page_size] = x[i];
       }
     }
+}
+
+template <bool HELD>
+__global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
+  const int groups = a.heads / a.together, tid = threadIdx.x;
+  int64_t b = block_number();
+  const int si = (int)(b % a.num_seqs);
+  b /= a.num_seqs;
+  const int group = (int)(b % groups), layer = (int)(b / groups);
+  if (layer >= a.layers) return;
+  List l;
+  l.seq = a.seqs[si];
+  l.scores = (const KGLOBAL float*)a.scores + layer * a.scores_stride + (int64_t)group * a.together * a.page_size;
+  const int n = l.seq.num_tokens, keep = min(l.seq.keep, n);
+  KGLOBAL int32_t* kept = (KGLOBAL int32_t*)a.kept + ((int64_t)layer * groups + group) * a.total + l.seq.kept0;
+  KGLOBAL int32_t* start = (KGLOBAL int32_t*)a.starts + ((int64_t)layer * groups + group) * a.num_seqs + si;
+  if (keep == n || keep == 0) {
+    for (int j = tid; j < keep; j += kSelect) kept[j] = j;
+    if (tid == 0) *start = keep;
+    return;
+  }
+  select_list<HELD>(a, l, kept, start, keep);
 }
 
 // cos/sin of turning back by t positions, formed in fp64 and rounded once
@@ -277,16 +305,72 @@ struct Turned {
   }
 };
 
-// What a launch moves: `tensors` of the pool from tensor0 on, columns from byte `at` of a group on, `units` units
-// of them in slices of `slice`.
+// The same for bf16 bands of 16 * n columns in 16-byte pieces: 8 pairs a unit, in two pieces (NeoX: of either half;
+// GPT-J: side by side).
+struct TurnedPieces {
+  struct Held {
+    u32x4 a, b;
+  };
+  static __device__ __forceinline__ void places(const EvictArgs& a, int unit, int& p, int& i, int& j) {
+    const int units = a.d_rot >> 4, head = unit / units;
+    p = unit - head * units;
+    const int c0 = head * (a.head_bytes / 16);
+    i = c0 + (a.pairing == KAMERA_NEOX ? p : 2 * p);
+    j = a.pairing == KAMERA_NEOX ? i + units : i + 1;
+  }
+  static __device__ __forceinline__ void read(const EvictArgs& a, const KGLOBAL char* row, int unit, Held& x) {
+    int p, i, j;
+    places(a, unit, p, i, j);
+    x.a = ((const KGLOBAL u32x4*)row)[i];
+    x.b = ((const KGLOBAL u32x4*)row)[j];
+  }
+  static __device__ __forceinline__ void write(const EvictArgs& a, KGLOBAL char* row, int unit, const Held& x, int back) {
+    int p, i, j;
+    places(a, unit, p, i, j);
+    const KGLOBAL f32x4* cs = (const KGLOBAL f32x4*)((const KGLOBAL float*)a.phase + (int64_t)back * a.d_rot) + 2 * p;
+    const KGLOBAL f32x4* sn = cs + (a.d_rot >> 3);
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(x.a[e] << 16);
+      f[2 * e + 1] = __uint_as_float(x.a[e] & 0xffff0000u);
+      f[8 + 2 * e] = __uint_as_float(x.b[e] << 16);
+      f[8 + 2 * e + 1] = __uint_as_float(x.b[e] & 0xffff0000u);
+    }
+    const f32x4 c[2] = {cs[0], cs[1]}, s[2] = {sn[0], sn[1]};
+    const bool neox = a.pairing == KAMERA_NEOX;
+    float y[16];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float co = c[q >> 2][q & 3], si = s[q >> 2][q & 3];
+      const float u = neox ? f[q] : f[2 * q], v = neox ? f[8 + q] : f[2 * q + 1];
+      const float yu = u * co - v * si, yv = u * si + v * co;
+      if (neox) {
+        y[q] = yu;
+        y[8 + q] = yv;
+      } else {
+        y[2 * q] = yu;
+        y[2 * q + 1] = yv;
+      }
+    }
+    u32x4 w[2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = (uint32_t)rounded<uint16_t>(y[2 * e]) | ((uint32_t)rounded<uint16_t>(y[2 * e + 1]) << 16);
+    ((KGLOBAL u32x4*)row)[i] = w[0];
+    ((KGLOBAL u32x4*)row)[j] = w[1];
+  }
+};
+
+// A part of what a launch moves: `tensors` of the pool from tensor0 on, columns from byte `at` of a group on, `units`
+// units of them in slices of `slice`; its workgroups.
 struct Move {
   int tensor0, tensors, at, units, slice, slices;
+  int64_t blocks;
 };
 
 template <typename C>
-__global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, Move m) {
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const Move& m, int64_t b) {
   const int groups = a.heads / a.together, tid = threadIdx.x;
-  int64_t b = block_number();
   const int slice = (int)(b % m.slices);
   b /= m.slices;
   const int si = (int)(b % a.num_seqs);
@@ -335,34 +419,48 @@ __global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, Move m) {
 }
 
 template <typename C>
-hipError_t move(const EvictArgs& a, Move m, hipStream_t stream) {
-  m.slice = m.units < 16 ? m.units : 16;
-  m.slices = (m.units + m.slice - 1) / m.slice;
-  const int64_t blocks = (int64_t)a.layers * m.tensors * (a.heads / a.together) * a.num_seqs * m.slices;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (blocks > 0) hipLaunchKernelGGL((evict_move<C>), grid_of(blocks), dim3(kMove), 0, stream, a, m);
+__global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, Move m) {
+  move_rows<C>(a, m, block_number());
+}
+
+// Turned columns and the others, in one launch.
+__global__ __launch_bounds__(kMove) void evict_move_turned(EvictArgs a, Move turned, Move plain0, Move plain1) {
+  int64_t b = block_number();
+  if (b < turned.blocks) {
+    move_rows<TurnedPieces>(a, turned, b);
+  } else if ((b -= turned.blocks) < plain0.blocks) {
+    move_rows<Plain<u32x4>>(a, plain0, b);
+  } else {
+    move_rows<Plain<u32x4>>(a, plain1, b - plain0.blocks);
+  }
+}
+
+Move move_of(const EvictArgs& a, int tensor0, int tensors, int at, int units) {
+  Move m{tensor0, tensors, at, units, units < 16 ? units : 16, 1, 0};
+  if (units > 0) m.slices = (units + m.slice - 1) / m.slice;
+  if (units > 0) m.blocks = (int64_t)a.layers * tensors * (a.heads / a.together) * a.num_seqs * m.slices;
+  return m;
+}
+
+template <typename C>
+hipError_t move(const EvictArgs& a, const Move& m, hipStream_t stream) {
+  if (m.blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  if (m.blocks > 0) hipLaunchKernelGGL((evict_move<C>), grid_of(m.blocks), dim3(kMove), 0, stream, a, m);
   return hipGetLastError();
 }
 
-// columns [at, at + bytes) of every group as they are
+// columns [at, at + bytes) of every group of some tensors, in units of `unit` bytes?
+bool fits(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, int unit) {
+  bool ok = at % unit == 0 && bytes % unit == 0 && a.row_bytes % unit == 0 && a.layer_bytes % unit == 0 && (a.together * a.head_bytes) % unit == 0;
+  for (int t = tensor0; t < tensor0 + tensors; ++t) ok = ok && (uintptr_t)a.pool[t] % unit == 0;
+  return ok;
+}
+
+// those columns as they are
 hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, hipStream_t stream) {
-  if (bytes == 0 || tensors == 0) return hipSuccess;
-  auto fits = [&](int unit) {
-    bool ok = at % unit == 0 && bytes % unit == 0 && a.row_bytes % unit == 0 && a.layer_bytes % unit == 0 && (a.together * a.head_bytes) % unit == 0;
-    for (int t = tensor0; t < tensor0 + tensors; ++t) ok = ok && (uintptr_t)a.pool[t] % unit == 0;
-    return ok;
-  };
-  Move m{tensor0, tensors, at, bytes, 0, 0};
-  if (fits(16)) {
-    m.units = bytes / 16;
-    return move<Plain<u32x4>>(a, m, stream);
-  }
-  if (fits(4)) {
-    m.units = bytes / 4;
-    return move<Plain<uint32_t>>(a, m, stream);
-  }
-  m.units = bytes / 2;
-  return move<Plain<uint16_t>>(a, m, stream);
+  if (fits(a, tensor0, tensors, at, bytes, 16)) return move<Plain<u32x4>>(a, move_of(a, tensor0, tensors, at, bytes / 16), stream);
+  if (fits(a, tensor0, tensors, at, bytes, 4)) return move<Plain<uint32_t>>(a, move_of(a, tensor0, tensors, at, bytes / 4), stream);
+  return move<Plain<uint16_t>>(a, move_of(a, tensor0, tensors, at, bytes / 2), stream);
 }
 
 }  // namespace
@@ -370,7 +468,8 @@ hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int 
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
   const int64_t lists = (int64_t)a.layers * (a.heads / a.together) * a.num_seqs;
   if (lists > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(evict_select, grid_of(lists), dim3(kSelect), 0, stream, a);
+  if (a.longest <= kSelect * kHeld) hipLaunchKernelGGL(evict_select<true>, grid_of(lists), dim3(kSelect), 0, stream, a);
+  else hipLaunchKernelGGL(evict_select<false>, grid_of(lists), dim3(kSelect), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.most_kept == 0) return e;
   const int all = a.together * a.head_bytes;
@@ -379,10 +478,18 @@ hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
   if (phases > 0x7fffffffLL) return hipErrorInvalidValue;
   hipLaunchKernelGGL(evict_phase, grid_of(phases), dim3(256), 0, stream, a);
   e = hipGetLastError();
-  const int es = a.dtype == KAMERA_BF16 ? 2 : 4;
-  if (e == hipSuccess) e = move_plain(a, 0, 1, 0, a.band0 * es, stream);
-  Move m{0, 1, a.band0 * es, a.together * (a.d_rot / 2), 0, 0};
-  if (e == hipSuccess) e = a.dtype == KAMERA_BF16 ? move<Turned<uint16_t>>(a, m, stream) : move<Turned<float>>(a, m, stream);
+  if (e != hipSuccess) return e;
+  const int es = a.dtype == KAMERA_BF16 ? 2 : 4, band = a.band0 * es;
+  if (es == 2 && a.d_rot % 16 == 0 && a.head_bytes % 16 == 0 && band % 16 == 0 && fits(a, 0, a.tensors, 0, all, 16)) {
+    const Move turned = move_of(a, 0, 1, band, a.together * (a.d_rot / 16)), latent = move_of(a, 0, 1, 0, band / 16), values = move_of(a, 1, a.tensors - 1, 0, all / 16);
+    const int64_t blocks = turned.blocks + latent.blocks + values.blocks;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(evict_move_turned, grid_of(blocks), dim3(kMove), 0, stream, a, turned, latent, values);
+    return hipGetLastError();
+  }
+  e = move_plain(a, 0, 1, 0, band, stream);
+  const Move m = move_of(a, 0, 1, band, a.together * (a.d_rot / 2));
+  if (e == hipSuccess) e = es == 2 ? move<Turned<uint16_t>>(a, m, stream) : move<Turned<float>>(a, m, stream);
   if (e == hipSuccess && a.tensors == 2) e = move_plain(a, 1, 1, 0, all, stream);
   return e;
 }

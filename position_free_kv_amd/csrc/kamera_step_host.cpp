@@ -367,7 +367,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 // A run is a segment (a prefix with all its requests' query tokens, or a request's own tokens); an item a
 // tile of its keys and the rows that see any of them. Where that leaves the chip without work for all its
 // workgroups, rows are cut into ranges whose sums are joined (in the order of the ranges).
-constexpr int64_t kWeighSlots = 1024;
+constexpr int64_t kWeighSlots = 2048;
 constexpr int64_t weigh_rows(int kernel) { return kernel == ATTEND_LATENT ? 128 : 512; }  // fewest of a range
 void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
   const Shape h = shape_of(L, s->num_q_heads);

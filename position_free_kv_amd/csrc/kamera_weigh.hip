@@ -296,8 +296,8 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
     if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 2, 32>), g, b, 0, stream, a, io);
-    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 32>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 32>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64>), g, b, 0, stream, a, io);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_weigh_join == 0) return e;
