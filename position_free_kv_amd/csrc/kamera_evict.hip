@@ -34,12 +34,13 @@ __device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s
 // numbers of the same order; the `want`-th highest of the tokens between the first and the last ones is
 // found digit by digit (11, 11 and 10 bits, a count of each digit in LDS), then one pass in the tokens' order
 // writes the numbers of those above it and of the first few equal to it. No order of atomics matters:
-// counts are whole numbers. Lists of up to kSelect * kHeld tokens keep their ranks in registers.
+// counts are whole numbers. Lists of up to kSelect * 16 tokens stay in registers: all scores are read before any
+// is written, so they move in the last pass.
 // ============================================================================
 constexpr int kSelect = 512;   // threads
 constexpr int kDigits = 2048;
 constexpr int kEach = 4;       // tokens of a thread in one turn of the last pass
-constexpr int kHeld = 16;      // ranks of a thread
+constexpr int kHeldFew = 4, kHeldMost = 16;  // scores of a thread
 
 __device__ __forceinline__ uint32_t rank_of(float x) {
   if (x != x) return 0;
@@ -55,18 +56,19 @@ struct List {
     const int64_t page = page_of(a, seq, t, place);
     return page * a.heads * a.page_size + place;
   }
-  __device__ __forceinline__ uint32_t rank(const EvictArgs& a, int t) const {
+  __device__ __forceinline__ float score(const EvictArgs& a, int t) const {
     const KGLOBAL float* p = scores + score_at(a, t);
     float x = p[0];
     for (int h = 1; h < a.together; ++h) x += p[(int64_t)h * a.page_size];
-    return rank_of(x);
+    return x;
   }
+  __device__ __forceinline__ uint32_t rank(const EvictArgs& a, int t) const { return rank_of(score(a, t)); }
 };
 
 __device__ __forceinline__ int wave_prefix(uint64_t mask) { return __popcll(mask & ((uint64_t(1) << (threadIdx.x & 63)) - 1)); }
 
-// HELD: token t = (wave * kHeld + i) * 64 + lane of the list is rank i of its thread; the others are read anew by each pass.
-template <bool HELD>
+// HELD > 0: token (wave * turns + i) * 64 + lane of the list is score i of its thread; 0: every pass reads them anew.
+template <int HELD>
 __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, KGLOBAL int32_t* kept, KGLOBAL int32_t* start, int keep) {
   __shared__ uint32_t count[kDigits];
   __shared__ int sums[kSelect / kWave][2];
@@ -74,14 +76,22 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
   __shared__ int gone;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = l.seq.num_tokens, lo = l.seq.first, hi = n - l.seq.last;  // ranked: [lo, hi)
-  const int turns = HELD ? (n + kSelect - 1) / kSelect : 0;                // ranks of a thread (its wave's tokens follow each other)
-  uint32_t held[HELD ? kHeld : 1];
+  const int turns = HELD ? (n + kSelect - 1) / kSelect : 0;
+  float held[HELD ? HELD : 1];
   auto token = [&](int i) { return (wave * turns + i) * kWave + lane; };
-  if constexpr (HELD) {
+  auto ranked_one = [&](int i) { return i < turns && token(i) < hi && token(i) >= lo; };
+  if constexpr (HELD != 0) {
+    int64_t at[HELD];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      held[i] = 0;
-      if (i < turns && token(i) < hi && token(i) >= lo) held[i] = l.rank(a, token(i));
+    for (int i = 0; i < HELD; ++i) at[i] = l.score_at(a, min(token(min(i, turns - 1)), n - 1));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = l.scores[at[i]];
+    for (int h = 1; h < a.together; ++h) {
+      float x[HELD];
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) x[i] = l.scores[at[i] + (int64_t)h * a.page_size];
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) held[i] += x[i];
     }
   }
   int want = keep - l.seq.first - l.seq.last;
@@ -93,10 +103,10 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
     auto add = [&](uint32_t r) {
       if ((r & known) == border) atomicAdd(&count[(r >> shift) & ((1u << bits) - 1)], 1u);
     };
-    if constexpr (HELD) {
+    if constexpr (HELD != 0) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (i < turns && token(i) < hi && token(i) >= lo) add(held[i]);
+      for (int i = 0; i < HELD; ++i)
+        if (ranked_one(i)) add(rank_of(held[i]));
     } else {
       for (int t = lo + tid; t < hi; t += kSelect) add(l.rank(a, t));
     }
@@ -133,27 +143,33 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
   // tokens that stay, in their order
   if (tid == 0) gone = n;
   int above = 0, equal = 0;  // of the turns before
-  constexpr int EACH = HELD ? kHeld : kEach;
+  const bool with = HELD != 0 && a.together == 1;  // scores move with their tokens here
+  KGLOBAL float* scores = (KGLOBAL float*)(float*)l.scores;
+  constexpr int EACH = HELD ? HELD : kEach;
   for (int t0 = 0; t0 < n; t0 += kSelect * EACH) {  // (HELD: once)
     const int each = HELD ? turns : kEach;
-    bool hit[EACH], tie[EACH];
-    int at[EACH], tied[EACH], a0 = 0, e0 = 0;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
+    // whether the thread's token i is above the border (or stays whatever its score), or equal to it
+    auto judge = [&](int i, bool& hit, bool& tie) {
       const int t = t0 + (wave * each + i) * kWave + lane;
       const bool there = t < n && (!HELD || i < turns);
-      hit[i] = there && (t < lo || t >= hi);
-      tie[i] = false;
+      hit = there && (t < lo || t >= hi);
+      tie = false;
       if (ranked && there && t >= lo && t < hi) {
-        const uint32_t r = HELD ? held[HELD ? i : 0] : l.rank(a, t);
-        hit[i] = r > border;
-        tie[i] = r == border;
+        const uint32_t r = HELD ? rank_of(held[HELD ? i : 0]) : l.rank(a, t);
+        hit = r > border;
+        tie = r == border;
       }
-      const uint64_t h = __ballot(hit[i]), e = __ballot(tie[i]);
-      at[i] = a0 + wave_prefix(h);
-      tied[i] = e0 + wave_prefix(e);
-      a0 += __popcll(h);
-      e0 += __popcll(e);
+    };
+    int a0 = 0, e0 = 0;
+    uint32_t hits = 0, equals = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      bool hit, tie;
+      judge(i, hit, tie);
+      hits |= (uint32_t)hit << i;
+      equals |= (uint32_t)tie << i;
+      a0 += __popcll(__ballot(hit));
+      e0 += __popcll(__ballot(tie));
     }
     __syncthreads();
     if (lane == 0) {
@@ -174,9 +190,17 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const int t = t0 + (wave * each + i) * kWave + lane;
-      const int ties = ebase + tied[i];
-      if (hit[i] || (tie[i] && ties < want)) kept[abase + at[i] + min(ties, want)] = t;
-      else if (t < n && (!HELD || i < turns)) leaves = min(leaves, t);
+      const bool hit = hits >> i & 1, tie = equals >> i & 1;
+      const uint64_t h = __ballot(hit), e = __ballot(tie);
+      const int before = ebase + wave_prefix(e), j = abase + wave_prefix(h) + min(before, want);
+      if (hit || (tie && before < want)) {
+        kept[j] = t;
+        if (with && j != t) scores[l.score_at(a, j)] = held[HELD ? i : 0];
+      } else if (t < n && (!HELD || i < turns)) {
+        leaves = min(leaves, t);
+      }
+      abase += __popcll(h);
+      ebase += __popcll(e);
     }
     for (int d = 32; d; d >>= 1) leaves = min(leaves, __shfl_xor(leaves, d, kWave));
     if (lane == 0 && leaves < n) atomicMin(&gone, leaves);
@@ -184,9 +208,9 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
   __syncthreads();  // (the list is written, and visible to the workgroup)
   const int s0 = min(gone, keep);
   if (tid == 0) *start = s0;
+  if (with) return;
   // The scores move with their tokens: a turn's reads are over before its writes begin, and later turns read
   // from places that earlier ones do not write, as token kept[j] >= j.
-  KGLOBAL float* scores = (KGLOBAL float*)(float*)l.scores;
   for (int h = 0; h < a.together; ++h)
     for (int j0 = s0; j0 < keep; j0 += kSelect * kEach) {
       float x[kEach];
@@ -205,7 +229,7 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
     }
 }
 
-template <bool HELD>
+template <int HELD>
 __global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
   const int groups = a.heads / a.together, tid = threadIdx.x;
   int64_t b = block_number();
@@ -245,14 +269,15 @@ __global__ __launch_bounds__(256) void evict_phase(EvictArgs a) {
 // behind every row written so far (kept[j] >= j, ascending), so no other order is needed.
 // ============================================================================
 constexpr int kMove = 256;  // threads
+constexpr int kSlice = 8;   // units of a slice, at most
 constexpr int kTurn = 8;    // rows of a thread in one turn
 
 // Columns as they are, in pieces of a U.
 template <typename U>
 struct Plain {
   typedef U Held;
-  static __device__ __forceinline__ void read(const EvictArgs&, const KGLOBAL char* row, int unit, Held& x) { x = ((const KGLOBAL U*)row)[unit]; }
-  static __device__ __forceinline__ void write(const EvictArgs&, KGLOBAL char* row, int unit, const Held& x, int) { ((KGLOBAL U*)row)[unit] = x; }
+  static __device__ __forceinline__ void read(const EvictArgs&, const KGLOBAL char* row, int unit, Held& x) { x = __builtin_nontemporal_load((const KGLOBAL U*)row + unit); }
+  static __device__ __forceinline__ void write(const EvictArgs&, KGLOBAL char* row, int unit, const Held& x, int) { __builtin_nontemporal_store(x, (KGLOBAL U*)row + unit); }
 };
 
 template <typename T>
@@ -321,8 +346,8 @@ struct TurnedPieces {
   static __device__ __forceinline__ void read(const EvictArgs& a, const KGLOBAL char* row, int unit, Held& x) {
     int p, i, j;
     places(a, unit, p, i, j);
-    x.a = ((const KGLOBAL u32x4*)row)[i];
-    x.b = ((const KGLOBAL u32x4*)row)[j];
+    x.a = __builtin_nontemporal_load((const KGLOBAL u32x4*)row + i);
+    x.b = __builtin_nontemporal_load((const KGLOBAL u32x4*)row + j);
   }
   static __device__ __forceinline__ void write(const EvictArgs& a, KGLOBAL char* row, int unit, const Held& x, int back) {
     int p, i, j;
@@ -356,8 +381,8 @@ struct TurnedPieces {
     u32x4 w[2];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = (uint32_t)rounded<uint16_t>(y[2 * e]) | ((uint32_t)rounded<uint16_t>(y[2 * e + 1]) << 16);
-    ((KGLOBAL u32x4*)row)[i] = w[0];
-    ((KGLOBAL u32x4*)row)[j] = w[1];
+    __builtin_nontemporal_store(w[0], (KGLOBAL u32x4*)row + i);
+    __builtin_nontemporal_store(w[1], (KGLOBAL u32x4*)row + j);
   }
 };
 
@@ -390,31 +415,49 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const Move& m, int
   const int side = kMove / m.slice;                            // rows side by side
   const int row = tid / m.slice, in = tid - row * m.slice, unit = slice * m.slice + in;
   const bool mine = row < side && in < width;
-  for (int j0 = start; j0 < keep; j0 += side * kTurn) {
-    typename C::Held x[kTurn];
-    int from[kTurn];
+  // A turn's rows are looked up while the turn before is on its way.
+  typename C::Held x[kTurn];
+  int from[kTurn], ahead[kTurn];
+  int64_t src[kTurn], dst[kTurn];
+  auto ask = [&](int j0, int (&f)[kTurn]) {
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) f[i] = kept[min(j0 + i * side + row, keep - 1)];
+  };
+  auto find = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < kTurn; ++i) {
-      const int j = j0 + i * side + row;
-      from[i] = mine && j < keep ? kept[j] : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < kTurn; ++i) {
-      if (from[i] < 0) continue;
       int place;
+      from[i] = ahead[i];
       const int64_t page = page_of(a, seq, from[i], place);
-      C::read(a, pool + (page * a.page_size + place) * a.row_bytes, unit, x[i]);
+      src[i] = (page * a.page_size + place) * a.row_bytes;
+    }
+  };
+  if (start >= keep) return;
+  ask(start, ahead);
+  find(start);
+  for (int j0 = start; j0 < keep; j0 += side * kTurn) {
+    const int next = j0 + side * kTurn;
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i)
+      if (mine && j0 + i * side + row < keep) C::read(a, pool + src[i], unit, x[i]);
+    int back[kTurn];
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      const int j = min(j0 + i * side + row, keep - 1);
+      int place;
+      const int64_t page = page_of(a, seq, j, place);
+      dst[i] = (page * a.page_size + place) * a.row_bytes;
+      back[i] = from[i] - j;
+    }
+    if (next < keep) {
+      ask(next, ahead);
+      find(next);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kTurn; ++i) {
-      if (from[i] < 0) continue;
-      const int j = j0 + i * side + row;
-      int place;
-      const int64_t page = page_of(a, seq, j, place);
-      C::write(a, pool + (page * a.page_size + place) * a.row_bytes, unit, x[i], from[i] - j);
-    }
+    for (int i = 0; i < kTurn; ++i)
+      if (mine && j0 + i * side + row < keep) C::write(a, pool + dst[i], unit, x[i], back[i]);
   }
 }
 
@@ -436,7 +479,7 @@ __global__ __launch_bounds__(kMove) void evict_move_turned(EvictArgs a, Move tur
 }
 
 Move move_of(const EvictArgs& a, int tensor0, int tensors, int at, int units) {
-  Move m{tensor0, tensors, at, units, units < 16 ? units : 16, 1, 0};
+  Move m{tensor0, tensors, at, units, units < kSlice ? units : kSlice, 1, 0};
   if (units > 0) m.slices = (units + m.slice - 1) / m.slice;
   if (units > 0) m.blocks = (int64_t)a.layers * tensors * (a.heads / a.together) * a.num_seqs * m.slices;
   return m;
@@ -468,8 +511,9 @@ hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int 
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
   const int64_t lists = (int64_t)a.layers * (a.heads / a.together) * a.num_seqs;
   if (lists > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (a.longest <= kSelect * kHeld) hipLaunchKernelGGL(evict_select<true>, grid_of(lists), dim3(kSelect), 0, stream, a);
-  else hipLaunchKernelGGL(evict_select<false>, grid_of(lists), dim3(kSelect), 0, stream, a);
+  if (a.longest <= kSelect * kHeldFew) hipLaunchKernelGGL(evict_select<kHeldFew>, grid_of(lists), dim3(kSelect), 0, stream, a);
+  else if (a.longest <= kSelect * kHeldMost) hipLaunchKernelGGL(evict_select<kHeldMost>, grid_of(lists), dim3(kSelect), 0, stream, a);
+  else hipLaunchKernelGGL(evict_select<0>, grid_of(lists), dim3(kSelect), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.most_kept == 0) return e;
   const int all = a.together * a.head_bytes;
