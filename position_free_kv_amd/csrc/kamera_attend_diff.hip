@@ -7,10 +7,6 @@
 // 32 (or 16) rows of one map, so that a stage's values are brought into LDS once for both maps.
 #include "kamera_attend.h"
 
-#ifndef JVP
-#define JVP 32
-#define JVR 1024
-#endif
 namespace kamera {
 
 namespace {
@@ -196,12 +192,27 @@ __device__ __forceinline__ float widened(T x) {
   else return x;
 }
 
+// The maximum or sum of WPR waves' values (all of a workgroup's threads come along)
+template <int WPR, bool MAX>
+__device__ __forceinline__ float2 over_waves(float2 x, float2 (&red)[2][WPR]) {
+  if constexpr (WPR == 1) return x;
+  if ((threadIdx.x & 63) == 0) red[MAX][threadIdx.x / kWaveSize] = x;
+  __syncthreads();
+  x = red[MAX][0];
+  for (int i = 1; i < WPR; ++i) {
+    const float2 y = red[MAX][i];
+    x = MAX ? make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y)) : make_float2(x.x + y.x, x.y + y.y);
+  }
+  return x;
+}
+
 // PIECES: 16-byte pieces of the two rows that a lane takes
 constexpr int join_waves_of(int wpr) { return wpr > kWaves ? wpr : kWaves; }  // waves of a workgroup
 template <typename T, int WPR, int PIECES>
 __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
   constexpr int ROWS = join_waves_of(WPR) / WPR;
   __shared__ float2 weight[ROWS][WPR == 1 ? kWaveSize : kJoinParts];
+  __shared__ float2 red[ROWS][2][WPR];
   __shared__ f32x4 held[join_waves_of(WPR)][PIECES * kWaveSize];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = wave / WPR, seat = wave % WPR;
   const int outs = a.num_q_heads / 2;
@@ -225,25 +236,32 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
       d1 += p[2 * a.dk + c] * p[3 * a.dk + c];
     }
   }
-  float top0 = -INFINITY, top1 = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
+  // every part's maxima and sums become its weights, all parts at once
+  constexpr int MAXP = WPR == 1 ? kWaveSize : kJoinParts, TPR = WPR * kWaveSize, PER = MAXP / TPR;
+  const int tid = threadIdx.x % TPR;
   const KGLOBAL f32x4* stats = (const KGLOBAL f32x4*)a.part_ml;  // (rows of the first map are even)
-  for (int k = lane; k < n; k += kWaveSize) {
-    const f32x4 s = stats[row(k) >> 1];
-    if (s[1] != 0.0f) top0 = fmaxf(top0, s[0]);
-    if (s[3] != 0.0f) top1 = fmaxf(top1, s[2]);
+  f32x4 s[PER];
+  float2 top = make_float2(-INFINITY, -INFINITY), sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    s[e] = (f32x4){-INFINITY, 0.0f, -INFINITY, 0.0f};
+    if (e * TPR + tid < n) s[e] = stats[row(e * TPR + tid) >> 1];
   }
-  top0 = wave_max(top0);
-  top1 = wave_max(top1);
-  for (int k = lane; k < n; k += kWaveSize) {
-    const f32x4 s = stats[row(k) >> 1];
-    const float w0 = s[1] == 0.0f ? 0.0f : s[0] == top0 ? 1.0f : __builtin_amdgcn_exp2f(s[0] - top0);
-    const float w1 = s[3] == 0.0f ? 0.0f : s[2] == top1 ? 1.0f : __builtin_amdgcn_exp2f(s[2] - top1);
-    sum0 += s[1] * w0;
-    sum1 += s[3] * w1;
-    if (k % WPR == seat || WPR == 1) weight[sub][k] = make_float2(w0, w1);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    if (s[e][1] != 0.0f) top.x = fmaxf(top.x, s[e][0]);
+    if (s[e][3] != 0.0f) top.y = fmaxf(top.y, s[e][2]);
   }
-  sum0 = wave_sum(sum0);
-  sum1 = wave_sum(sum1);
+  top = over_waves<WPR, true>(make_float2(wave_max(top.x), wave_max(top.y)), red[sub]);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const float2 w = make_float2(s[e][1] == 0.0f ? 0.0f : s[e][0] == top.x ? 1.0f : __builtin_amdgcn_exp2f(s[e][0] - top.x),
+                                 s[e][3] == 0.0f ? 0.0f : s[e][2] == top.y ? 1.0f : __builtin_amdgcn_exp2f(s[e][2] - top.y));
+    sum.x += s[e][1] * w.x;
+    sum.y += s[e][3] * w.y;
+    if (e * TPR + tid < n) weight[sub][e * TPR + tid] = w;
+  }
+  sum = over_waves<WPR, false>(make_float2(wave_sum(sum.x), wave_sum(sum.y)), red[sub]);
   if (diff.lambdas) lambda += expf(wave_sum(d0)) - expf(wave_sum(d1));
   __syncthreads();
   const int quads = a.dv / 4;  // of a map's row
@@ -269,7 +287,7 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
   for (int j = 0; j < PIECES; ++j) held[wave][j * kWaveSize + lane] = o[j];
   __syncthreads();
   if (seat != 0 || !live) return;
-  const float inv0 = sum0 == 0.0f ? 0.0f : 1.0f / sum0, inv1 = sum1 == 0.0f ? 0.0f : 1.0f / sum1;
+  const float inv0 = sum.x == 0.0f ? 0.0f : 1.0f / sum.x, inv1 = sum.y == 0.0f ? 0.0f : 1.0f / sum.y;
   f32x4 x[(PIECES + 1) / 2];
   float square = 0.0f;
 #pragma unroll
@@ -315,8 +333,8 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
     }
   }
   if (io.lse && lane < 2) {
-    const float sum = lane ? sum1 : sum0, top = lane ? top1 : top0;
-    io.lse[(int64_t)mt.token * a.num_q_heads + 2 * oh + lane] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const float l = lane ? sum.y : sum.x, m = lane ? top.y : top.x;
+    io.lse[(int64_t)mt.token * a.num_q_heads + 2 * oh + lane] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -358,7 +376,7 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
   }
   if (e != hipSuccess || a.num_merge == 0) return e;
   const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
-  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > JVP && rows < JVR && a.dv <= 256;
+  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > 32 && rows < 1024 && a.dv <= 256;
   if (a.dtype == KAMERA_BF16)
     return very ? join<uint16_t, 16>(a, io, diff, stream) : wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
   return very ? join<float, 16>(a, io, diff, stream) : wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);

@@ -143,8 +143,11 @@ hipError_t launch_attend_plain(const StepArgs& a, const AttendIo& io, hipStream_
 hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride,
                                    float* lse, float scale, const kamera_differential& diff, hipStream_t stream);
 
-// Keys of a weighing workgroup: PLAIN 16; on the matrix cores HEADS 256, LATENT 128.
-constexpr int weigh_keys(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 128 : 256; }
+// Keys of a weighing workgroup: PLAIN 16; on the matrix cores HEADS 256, LATENT 64. Items of at most kFewRows rows
+// walk over more of them (matrix cores).
+constexpr int kFewRows = 16;
+constexpr int weigh_keys(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 256; }
+constexpr int weigh_keys_of_few(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 1024; }
 hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_t q_stride, const float* lse, float* scores, float scale,
                              float decay, hipStream_t stream);
 

@@ -441,10 +441,11 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
       w.weigh_join.push_back(WeighJoin{r.part, r.pg, r.slot, r.kv, (int32_t)splits, (int32_t)each, r.lim0, r.lstep, (int32_t)keys});
       w.weigh_longest = std::max(w.weigh_longest, r.kv);
     }
-    for (int64_t kv0 = 0; kv0 < r.kv; kv0 += keys)
+    const int64_t tile = rows <= kFewRows ? weigh_keys_of_few(kernel) : keys;
+    for (int64_t kv0 = 0; kv0 < r.kv; kv0 += tile)
       for (int64_t sp = first_row(r, kv0) / each; sp < splits; ++sp) {
         r.kv0 = (int32_t)kv0;
-        r.kv1 = (int32_t)std::min<int64_t>(kv0 + keys, r.kv);
+        r.kv1 = (int32_t)std::min<int64_t>(kv0 + tile, r.kv);
         r.row0 = (int32_t)std::max(first_row(r, kv0), sp * each);
         r.row1 = (int32_t)std::min(rows, (sp + 1) * each);
         r.split = (int32_t)sp;
@@ -452,7 +453,11 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
       }
   }
   // the longest first: the short ones fill the gaps at the end
-  std::stable_sort(w.weigh.begin(), w.weigh.end(), [](const WeighItem& x, const WeighItem& y) { return x.row1 - x.row0 > y.row1 - y.row0; });
+  auto longer = [](const WeighItem& x, const WeighItem& y) {
+    const int32_t rx = std::max(x.row1 - x.row0, kFewRows), ry = std::max(y.row1 - y.row0, kFewRows);
+    return rx != ry ? rx > ry : x.kv1 - x.kv0 > y.kv1 - y.kv0;
+  };
+  std::stable_sort(w.weigh.begin(), w.weigh.end(), longer);
 }
 
 // What a step's flags ask for, for a pool that the matrix-core kernels take (`matrix`) or any.

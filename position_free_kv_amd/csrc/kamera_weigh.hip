@@ -49,8 +49,11 @@ __device__ __forceinline__ int64_t slot_of(const StepArgs& a, int pg, int slot0,
   return ((const KGLOBAL int32_t*)a.pages)[pg + e];
 }
 
+__device__ __forceinline__ KGLOBAL float* score_at(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head) {
+  return (KGLOBAL float*)io.scores + (page * a.heads + head) * a.page_size + place;
+}
 __device__ __forceinline__ void add_score(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head, float sum) {
-  KGLOBAL float* p = (KGLOBAL float*)io.scores + (page * a.heads + head) * a.page_size + place;
+  KGLOBAL float* p = score_at(a, io, page, place, head);
   *p = io.decay == 0.0f ? sum : io.decay * *p + sum;
 }
 
@@ -166,15 +169,20 @@ struct QueryRows {
   }
 };
 
+template <int DK, int SR>
+struct Stages {
+  __align__(1024) char stage[2][SR * 2 * DK];
+  __align__(16) float base[2][SR];
+  __align__(16) int limit[2][SR];
+  __align__(16) int whole[2][kWaves];
+};
 template <int DK, int DV, int KT, int SR>
-__global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
+__device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, Stages<DK, SR>& lds) {
   typedef State<DK, DV, 16> S;
-  __shared__ __align__(1024) char stage[2][SR * 2 * DK];
-  __shared__ __align__(16) float base[2][SR];
-  __shared__ __align__(16) int limit[2][SR];
-  __shared__ __align__(16) int whole[2][kWaves];
-  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
-  const WeighItem it = a.weigh[item];
+  auto& stage = lds.stage;
+  auto& base = lds.base;
+  auto& limit = lds.limit;
+  auto& whole = lds.whole;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
   const int key0 = it.kv0 + wave * 16 * KT;  // the wave's first key
   const bool any = key0 < it.kv1;
@@ -253,6 +261,113 @@ __global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo 
   }
 }
 
+// ============================================================================
+// At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, a step's keys, their
+// pages' ids and their scores asked for ahead. Bound by reading the keys.
+// ============================================================================
+template <int DK, int DV, int KT>
+__device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head) {
+  typedef State<DK, DV, 16> S;
+  constexpr int STEP = kWaves * 16 * KT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
+  int t = it.kv0 + wave * 16 * KT;
+  if (t >= it.kv1) return;
+  const KGLOBAL uint16_t* keys = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + (int64_t)head * DK;
+  struct Tile {
+    int page[KT], place[KT];
+    float old[KT];
+    bf16x8 k[KT][S::kKSteps];
+  } tile[2];
+  int page[KT], place[KT];  // of the step after the next
+  auto find = [&](int t0) {
+#pragma unroll
+    for (int x = 0; x < KT; ++x) page[x] = (int)slot_of(a, it.pg, it.slot, min(t0 + 16 * x + n, it.kv1 - 1), place[x]);
+  };
+  auto load = [&](Tile& w) {
+#pragma unroll
+    for (int x = 0; x < KT; ++x) {
+      w.page[x] = page[x];
+      w.place[x] = place[x];
+      const KGLOBAL uint16_t* p = keys + ((int64_t)page[x] * a.page_size + place[x]) * a.row;
+#pragma unroll
+      for (int ks = 0; ks < S::kKSteps; ++ks) w.k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
+      w.old[x] = 0.0f;
+      if (io.decay != 0.0f && it.part < 0) w.old[x] = *score_at(a, io, page[x], place[x], head);
+    }
+  };
+  find(t);
+  load(tile[0]);
+  // the rows
+  const QueryRow r = query_row(a, io, it, head, min(it.row0 + n, it.row1 - 1));
+  const KGLOBAL uint16_t* qp = (const KGLOBAL uint16_t*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * DK;
+  bf16x8 q[S::kKSteps];
+#pragma unroll
+  for (int ks = 0; ks < S::kKSteps; ++ks) {
+    u32x4 w;
+    if (io.q_vec) {
+      w = *(const KGLOBAL u32x4*)(qp + S::k_column(ks));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)qp[S::k_column(ks) + 2 * e] | ((uint32_t)qp[S::k_column(ks) + 2 * e + 1] << 16);
+    }
+    q[ks] = __builtin_bit_cast(bf16x8, w);
+  }
+  float base[4];
+  int limit[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = it.row0 + 4 * S::group() + i;
+    const QueryRow y = query_row(a, io, it, head, min(row, it.row1 - 1));
+    const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)y.token * a.num_q_heads + y.qh];
+    base[i] = lse * kLog2;
+    limit[i] = row < it.row1 && lse != -INFINITY ? it.lim0 + y.j * it.lstep : -1;
+  }
+  find(t + STEP);
+  auto work = [&](const Tile& w) {
+#pragma unroll
+    for (int x = 0; x < KT; ++x) {
+      typename S::Acc s = (typename S::Acc)(0.0f);
+#pragma unroll
+      for (int ks = 0; ks < S::kKSteps; ++ks) s = S::mfma(q[ks], w.k[x][ks], s);
+      const int key = t + 16 * x + n;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], io.scale2, -base[i]));
+        sum += key <= limit[i] ? e : 0.0f;
+      }
+      sum = row_sum<16>(sum);
+      if (lane >= 16 || key >= it.kv1) continue;
+      if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + key] = sum;
+      else *score_at(a, io, w.page[x], w.place[x], head) = io.decay == 0.0f ? sum : io.decay * w.old[x] + sum;
+    }
+  };
+#pragma nounroll
+  for (;;) {
+    if (t + STEP < it.kv1) {
+      load(tile[1]);
+      find(t + 2 * STEP);
+    }
+    work(tile[0]);
+    if ((t += STEP) >= it.kv1) break;
+    if (t + STEP < it.kv1) {
+      load(tile[0]);
+      find(t + 2 * STEP);
+    }
+    work(tile[1]);
+    if ((t += STEP) >= it.kv1) break;
+  }
+}
+
+template <int DK, int DV, int KT, int SR, int FEW>
+__global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
+  __shared__ Stages<DK, SR> lds;
+  const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
+  const WeighItem it = a.weigh[item];
+  if (it.row1 - it.row0 <= kFewRows) few_rows<DK, DV, FEW>(a, io, it, head);
+  else many_rows<DK, DV, KT, SR>(a, io, it, head, lds);
+}
+
 // Sums of ranges of rows, joined in their order: a thread a key and head. A range that ends before the first row
 // that sees a tile's keys has none of them.
 __global__ __launch_bounds__(kThreads) void weigh_join(StepArgs a, WeighIo io) {
@@ -295,9 +410,9 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
     e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
-    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 2, 32>), g, b, 0, stream, a, io);
-    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64>), g, b, 0, stream, a, io);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 32, 1>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, 2>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, 4>), g, b, 0, stream, a, io);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_weigh_join == 0) return e;

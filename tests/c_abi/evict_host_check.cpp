@@ -42,7 +42,7 @@ hipError_t launch_step_weigh(const StepArgs& a, int, const void*, int64_t, const
   g_weigh_parts = 0;
   for (int i = 0; i < a.num_weigh; ++i) {
     const WeighItem& it = a.weigh[i];
-    CHECK(it.kv0 >= 0 && it.kv0 < it.kv1 && it.kv1 <= it.kv && it.kv1 - it.kv0 <= keys && it.row0 >= 0 && it.row0 < it.row1 && it.row1 <= (int64_t)it.ntok * G);
+    CHECK(it.kv0 >= 0 && it.kv0 < it.kv1 && it.kv1 <= it.kv && it.kv1 - it.kv0 <= (it.ntok * G <= kFewRows ? weigh_keys_of_few(a.weigh_kernel) : keys) && it.row0 >= 0 && it.row0 < it.row1 && it.row1 <= (int64_t)it.ntok * G);
     for (int t = it.kv0; t < it.kv1; ++t) {
       std::map<int64_t, int> rows;
       for (int row = it.row0; row < it.row1; ++row) {
