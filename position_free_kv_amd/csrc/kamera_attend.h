@@ -128,10 +128,11 @@ __device__ __forceinline__ int key_entry(const StepArgs& a, const AttendRun& run
 // first DV columns of a key (DK if there are fewer) are a row, the others (MLA's rope band) a row of another
 // place. 32 rows: v_mfma_f32_32x32x16_bf16, lane = 32 g + n; 16 rows:
 // v_mfma_f32_16x16x32_bf16, lane = 16 g + n (n: the row; g: the k slots of an operand, 8 each). A step
-// takes 32 keys. Score i of lane (g, n) is that of key slot_key(i).
-template <int DK, int DV, int ROWS>
+// takes 32 keys. Score i of lane (g, n) is that of key slot_key(i). SPLIT: values lie in two arrays that many bytes
+// apart, half of a row in each.
+template <int DK, int DV, int ROWS, int SPLIT = 0>
 struct State {
-  static constexpr int kRow = 2 * DV;
+  static constexpr int kRow = SPLIT ? DV : 2 * DV;
   static constexpr int kKeyRow = 2 * (DK < DV ? DK : DV);
   static constexpr int kRestRow = 2 * DK - kKeyRow;    // 0: no other columns
   static constexpr int kGroups = 64 / ROWS;            // 2 or 4
@@ -204,8 +205,9 @@ struct State {
     const int at = token * kRow + ((piece ^ swz<ROWS, kRow>(token)) << 4) + (lane & 1) * 8;
     constexpr int kSpan = kRow % 256 == 0 ? 256 : 128;  // what the pieces' places are permuted in
     const int c = b * 2 * ROWS;
-    const KLDS char* p = v + ((at ^ (c % kSpan)) + (c / kSpan) * kSpan + u * 16 * kRow);
-    const KLDS char* p2 = v + ((at ^ (c % kSpan) ^ (ROWS == 32 ? 32 : 0)) + (c / kSpan) * kSpan + u * 16 * kRow + next * kRow);
+    const int on = c / kRow * SPLIT + c % kRow / kSpan * kSpan + u * 16 * kRow;
+    const KLDS char* p = v + ((at ^ (c % kSpan)) + on);
+    const KLDS char* p2 = v + ((at ^ (c % kSpan) ^ (ROWS == 32 ? 32 : 0)) + on + next * kRow);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KLDS s16x4*)p);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KLDS s16x4*)p2);
     typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -425,16 +427,16 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // A stage of TS keys, as far as a row of the wave sees: NT x 32 at a time while every row sees them all.
-template <int TS, int NT, int DK, int DV, int ROWS>
-__device__ __forceinline__ void walk(State<DK, DV, ROWS>& st, const bf16x8 (&q)[State<DK, DV, ROWS>::kKSteps], const KLDS char* k,
+template <int TS, int NT, int DK, int DV, int ROWS, int SPLIT>
+__device__ __forceinline__ void walk(State<DK, DV, ROWS, SPLIT>& st, const bf16x8 (&q)[State<DK, DV, ROWS, SPLIT>::kKSteps], const KLDS char* k,
                                      const KLDS char* rest, const KLDS char* v, int t, int end, int end_min, int end_max, float scale2) {
-  typedef State<DK, DV, ROWS> S;
+  typedef State<DK, DV, ROWS, SPLIT> S;
   int s = 0;
 #pragma nounroll
   for (; s < TS && t + s + 32 * NT <= end_min; s += 32 * NT)
-    st.template step<NT, false>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * 2 * DV, t + s, end, scale2);
+    st.template step<NT, false>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * S::kRow, t + s, end, scale2);
 #pragma nounroll
-  for (; s < TS && t + s < end_max; s += 32) st.template step<1, true>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * 2 * DV, t + s, end, scale2);
+  for (; s < TS && t + s < end_max; s += 32) st.template step<1, true>(q, k + s * S::kKeyRow, rest + s * S::kRestRow, v + s * S::kRow, t + s, end, scale2);
 }
 
 // N consecutive columns of a row's result: normalised into the output, or as a partial row.

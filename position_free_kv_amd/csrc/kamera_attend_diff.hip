@@ -17,43 +17,37 @@ dim3 grid_of(int64_t blocks) {
   return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
 }
 
-// Stages lie in one array: keys of the first map, of the second, values.
+// A stage of TS keys lies in four arrays of rows of 2 D bytes, one after the other: keys of the first map, of the
+// second, first halves of the values, second halves. So one place in the pool's rows serves four loads.
 template <int D>
-constexpr int kKeyBytes = 2 * D;
-template <int D>
-constexpr int kValueBytes = 4 * D;
+constexpr int kRowBytes = 2 * D;
 constexpr int kLds = 65536;
 
-// N keys of a stage of TS from `first` on, by one wave. Lane i looks up the pool row of key first + i % N one
-// stage ahead, and the loads take it from there.
+// N keys of a stage of TS from `first` on, by one wave. The page ids are asked for one stage ahead (find) and used only
+// when the stage is loaded: loads return in order, so using them at once would wait for the stage in flight as well.
 template <int D, int TS, int N, int ROWS>
 struct PairRows {
-  int row;
+  static constexpr int RPL = 1024 / kRowBytes<D>, LPR = 64 / RPL, NI = N / RPL;  // rows of an instruction, lanes of a row
+  static_assert(N % RPL == 0, "whole instructions");
+  int page[NI], place[NI];
   __device__ __forceinline__ void find(const StepArgs& a, const AttendRun& run, int t0, int first, int last) {
-    int lane = threadIdx.x, place;
+    int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // (see load)
-    const int t = min(t0 + first + (lane & (N - 1)), last);
-    const int page = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, t, place)];
-    row = page * a.page_size + place;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) page[i] = ((const KGLOBAL int32_t*)a.pages)[key_entry(a, run, min(t0 + first + i * RPL + lane / LPR, last), place[i])];
   }
   // k and v: the layer's rows from the pair's first column on
   __device__ __forceinline__ void load(const StepArgs& a, const uint16_t* k, const uint16_t* v, KLDS char* stage, int first) const {
-    constexpr int RK = 1024 / kKeyBytes<D>, LK = 64 / RK, RV = 1024 / kValueBytes<D>, LV = 64 / RV;  // rows of an instruction, lanes of a row
-    static_assert(N % RK == 0, "whole instructions");
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is made anew each stage: kept, it would cost the products registers
-    KLDS char* values = stage + 2 * TS * kKeyBytes<D>;
 #pragma unroll
-    for (int i = 0; i < N; i += RK) {
-      const int64_t at = (int64_t)__shfl(row, i + lane / LK, kWaveSize) * a.row + ((lane & (LK - 1)) ^ swz<ROWS, kKeyBytes<D>>(first + i + lane / LK)) * 8;
+    for (int i = 0; i < NI; ++i) {
+      const int piece = (lane & (LPR - 1)) ^ swz<ROWS, kRowBytes<D>>(first + i * RPL + lane / LPR);
+      const int64_t at = ((int64_t)page[i] * a.page_size + place[i]) * a.row + piece * 8;
+      KLDS char* to = stage + (first + i * RPL) * kRowBytes<D>;
 #pragma unroll
-      for (int map = 0; map < 2; ++map)
-        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(k + at + map * D), (KLDS void*)(stage + (map * TS + first + i) * kKeyBytes<D>), 16, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < N; i += RV) {
-      const int64_t at = (int64_t)__shfl(row, i + lane / LV, kWaveSize) * a.row + ((lane & (LV - 1)) ^ swz<ROWS, kValueBytes<D>>(first + i + lane / LV)) * 8;
-      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(v + at), (KLDS void*)(values + (first + i) * kValueBytes<D>), 16, 0, 0);
+      for (int x = 0; x < 4; ++x)
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)((x < 2 ? k : v) + at + (x & 1) * D), (KLDS void*)(to + x * TS * kRowBytes<D>), 16, 0, 0);
     }
   }
 };
@@ -64,7 +58,7 @@ struct PairRows {
 template <int D>
 __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds) {
   constexpr int TS = 4096 / D, N = TS / kWaves, NT = TS / 32;
-  typedef State<D, 2 * D, 32> S;
+  typedef State<D, 2 * D, 32, TS * kRowBytes<D>> S;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, map = wave & 1;
   const uint16_t* kp = a.k_pool + io.layer0 + head * 2 * D;
   const uint16_t* vp = a.v_pool + io.layer0 + head * 2 * D;
@@ -84,8 +78,8 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
   S st;
   st.clear();
   auto work = [&](const KLDS char* s, int t) {
-    const KLDS char* k = s + map * TS * kKeyBytes<D>;
-    walk<TS, NT>(st, q, k, k, s + 2 * TS * kKeyBytes<D>, t, r.end, end_min, end_max, io.scale2);
+    const KLDS char* k = s + map * TS * kRowBytes<D>;
+    walk<TS, NT>(st, q, k, k, s + 2 * TS * kRowBytes<D>, t, r.end, end_min, end_max, io.scale2);
   };
   if (any) {
     for (int t = it.kv0;;) {
@@ -119,7 +113,7 @@ template <int D, int ROWS>
 __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds,
                                             float (&ml)[2][kWaves][64]) {
   constexpr int TS = 8192 / D, N = TS / kWaves, HALF = TS / 2;
-  typedef State<D, 2 * D, ROWS> S;
+  typedef State<D, 2 * D, ROWS, TS * kRowBytes<D>> S;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), map = wave & 1, part = wave >> 1;
   const uint16_t* kp = a.k_pool + io.layer0 + head * 2 * D;
   const uint16_t* vp = a.v_pool + io.layer0 + head * 2 * D;
@@ -138,8 +132,8 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   for (int t = it.kv0; t < it.kv1; t += TS) {
     if (t + TS < it.kv1) rows.find(a, it.run, t + TS, first, last);
     stage_barrier();
-    const KLDS char* k = (const KLDS char*)lds + (map * TS + part * HALF) * kKeyBytes<D>;
-    const KLDS char* v = (const KLDS char*)lds + 2 * TS * kKeyBytes<D> + part * HALF * kValueBytes<D>;
+    const KLDS char* k = (const KLDS char*)lds + (map * TS + part * HALF) * kRowBytes<D>;
+    const KLDS char* v = (const KLDS char*)lds + (2 * TS + part * HALF) * kRowBytes<D>;
     walk<HALF, 1>(st, q, k, k, v, t + part * HALF, r.end, end_min, end_max, io.scale2);
     if (t + TS >= it.kv1) break;
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is overwritten
