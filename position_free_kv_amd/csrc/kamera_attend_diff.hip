@@ -40,14 +40,18 @@ struct PairRows {
   __device__ __forceinline__ void load(const StepArgs& a, const uint16_t* k, const uint16_t* v, KLDS char* stage, int first) const {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is made anew each stage: kept, it would cost the products registers
+    const uint32_t row_bytes = 2u * (uint32_t)a.row;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int piece = (lane & (LPR - 1)) ^ swz<ROWS, kRowBytes<D>>(first + i * RPL + lane / LPR);
-      const int64_t at = ((int64_t)page[i] * a.page_size + place[i]) * a.row + piece * 8;
+      int pg = page[i];
+      asm volatile("" : "+v"(pg));  // (the product stays here)
+      const uint32_t row = (uint32_t)(pg * a.page_size + place[i]);  // (below 2^31)
+      const uint32_t piece = (uint32_t)((lane & (LPR - 1)) ^ swz<ROWS, kRowBytes<D>>(first + i * RPL + lane / LPR)) << 4;
+      const uint64_t at = (uint64_t)row * row_bytes + piece;
       KLDS char* to = stage + (first + i * RPL) * kRowBytes<D>;
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)((x < 2 ? k : v) + at + (x & 1) * D), (KLDS void*)(to + x * TS * kRowBytes<D>), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)((const KGLOBAL char*)((x < 2 ? k : v) + (x & 1) * D) + at), (KLDS void*)(to + x * TS * kRowBytes<D>), 16, 0, 0);
     }
   }
 };

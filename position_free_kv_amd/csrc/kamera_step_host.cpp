@@ -113,10 +113,10 @@ constexpr int64_t kShareRows = 96;
 // item, page ids, rows and queries are read one after the other, its results joined and written), of
 // one key of a tile while the chip is full, and of a partial row's column written and read again.
 constexpr double kStartNs = 6000, kPartNs = 0.001;
-double key_ns(int kernel, int tile) {
+double key_ns(int kernel, int tile, int dk) {
   if (kernel == ATTEND_LATENT) return tile == TILE_WIDE ? 60 : 20;
   if (kernel == ATTEND_HEADS) return tile == TILE_WIDE ? 30 : tile == TILE_PAIRS ? 38 : 25;
-  if (kernel == ATTEND_DIFF) return tile == TILE_WIDE ? 55 : 50;
+  if (kernel == ATTEND_DIFF) return (tile == TILE_WIDE ? 49 : 45) * dk / 128;
   return 40;
 }
 
@@ -260,11 +260,11 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     c.keys += tiles * r.kv;
   }
   double whole = 0;  // the launch's time if the places were always full and nothing split
-  for (int k = 0; k < 3; ++k) whole += h.heads * (key_ns(kernel, k) * cls[k].keys + kStartNs * cls[k].tiles) / slots;
+  for (int k = 0; k < 3; ++k) whole += h.heads * (key_ns(kernel, k, h.dk) * cls[k].keys + kStartNs * cls[k].tiles) / slots;
   int64_t chunk_of[3] = {gran, gran, gran};
   for (int k = 0; k < 3; ++k) {
     const Class& c = cls[k];
-    const double per_key = key_ns(kernel, k);
+    const double per_key = key_ns(kernel, k, h.dk);
     const bool alike = c.keys > 0.9 * c.tiles * c.longest;
     double best = 0;
     auto consider = [&](int64_t chunk) {
@@ -295,6 +295,59 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     }
     for (int i = 0; i < fit.coarser && chunk_of[k] < c.longest; ++i) chunk_of[k] *= 2;
   }
+  // Differential attention of many queries: as many wide tiles as fill whole rounds of the places keep their keys
+  // together, and the rest, which would leave most places of a last round empty, are cut into `pieces` that
+  // fill it. (274 tiles of 2 pairs of heads on 512 places: 548 whole ones take two rounds, three pieces each 3.2
+  // rounds of a third.) The rest are the last queries of the last runs.
+  std::vector<int64_t> run_chunk;                                        // keys per item of a run, instead of its class's
+  std::vector<std::pair<int32_t, int32_t>> rest;                        // of a request: its queries from `first` on are run `second`'s
+  if (kernel == ATTEND_DIFF && fit.coarser == 0 && fit.share) {
+    const int tile = tile_rows(kernel, TILE_WIDE);
+    const double places = (double)slots / h.heads;
+    const Class& c = cls[TILE_WIDE];
+    const double rounds = c.tiles / places;
+    if (rounds >= 1) {
+      const double over = rounds - std::floor(rounds);
+      int pieces = 1;
+      double least = over > 0 ? 1 : 0;
+      for (int n = 2; n <= 16 && c.longest >= (int64_t)n * gran; ++n) {
+        const double time = std::ceil(over * n) / n + 0.02 * n;  // (and what the pieces cost beside their keys)
+        if (over > 0 && time < least) {
+          least = time;
+          pieces = n;
+        }
+      }
+      run_chunk.assign(w.runs.size(), 0);
+      rest.assign((size_t)s->num_requests, {0, -1});
+      double left = pieces > 1 ? c.tiles - std::floor(rounds) * places : 0;
+      std::vector<int32_t> request_of(w.runs.size(), -1);
+      for (int i = 0; i < s->num_requests; ++i)
+        if (own_run[(size_t)i] >= 0) request_of[(size_t)own_run[(size_t)i]] = i;
+      const size_t runs = w.runs.size();
+      for (size_t k = runs; k-- > 0;) {
+        AttendRun& r = w.runs[k];
+        if (r.tile != TILE_WIDE) continue;
+        run_chunk[k] = std::max<int64_t>(r.kv, 1);  // whole
+        const int64_t rows = (int64_t)r.ntok * G, piece = (int64_t)round_up((size_t)std::max<int64_t>(ceil_div(r.kv, pieces), 1), (size_t)gran);
+        if (left < 0.5) continue;
+        if (left >= (double)ceil_div(rows, tile) || request_of[k] < 0) {
+          run_chunk[k] = piece;
+          left -= (double)ceil_div(rows, tile);
+          continue;
+        }
+        AttendRun b = r;  // its last queries
+        b.ntok = (int32_t)std::min<int64_t>(r.ntok - 1, (int64_t)std::ceil(left) * tile / G);
+        left = 0;
+        if (b.ntok < 1) continue;
+        r.ntok -= b.ntok;
+        b.tok0 += r.ntok;
+        b.lim0 += r.ntok * r.lstep;
+        rest[(size_t)request_of[k]] = {r.ntok, (int32_t)w.runs.size()};
+        run_chunk.push_back(piece);
+        w.runs.push_back(b);
+      }
+    }
+  }
   int32_t start[4] = {0, 0, 0, 0};  // each class's first item
   for (int c = 0; c < 3; ++c) {
     for (size_t k = 0; k < w.runs.size(); ++k) {
@@ -302,7 +355,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       const int64_t rows = (int64_t)r.ntok * G;
       const int tile = tile_rows(kernel, c);
       if (r.tile != c) continue;
-      const int64_t splits = std::max<int64_t>(ceil_div(r.kv, chunk_of[c]), 1);
+      const int64_t splits = std::max<int64_t>(ceil_div(r.kv, k < run_chunk.size() && run_chunk[k] ? run_chunk[k] : chunk_of[c]), 1);
       const int64_t chunk = (int64_t)round_up((size_t)std::max<int64_t>(ceil_div(r.kv, splits), 1), (size_t)gran);
       const int64_t n = std::max<int64_t>(ceil_div(r.kv, chunk), 1);
       r.splits = (int32_t)n;
@@ -356,7 +409,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
       std::memset(&m, 0, sizeof(m));
       m.token = (int32_t)(tok + j);
       if (sh) part(m, 0, prefix_run[(size_t)q.prefix], listed[(size_t)q.prefix]++);
-      if (run >= 0) part(m, 1, run, j);
+      if (run >= 0 && !rest.empty() && rest[(size_t)i].second >= 0 && j >= rest[(size_t)i].first) part(m, 1, rest[(size_t)i].second, j - rest[(size_t)i].first);
+      else if (run >= 0) part(m, 1, run, j);
       w.max_parts = std::max(w.max_parts, m.splits[0] + m.splits[1]);
       w.merge.push_back(m);
     }

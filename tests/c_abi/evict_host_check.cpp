@@ -276,6 +276,16 @@ void steps(Rng& r) {
   CHECK(least < bytes);
   run_more(many, ws.p, least);
   CHECK(g_weigh_parts == 0);
+  // more wide tiles than a round of places: some runs whole, the last queries of others in pieces
+  for (int extra : {0, 3, 40, 150}) {
+    Steps rounds(KAMERA_GQA, KAMERA_BF16, 128, 8, 128, {300}, {{200, 200}, {330 + extra, 330 + extra}, {5, 1}});
+    rounds.s.flags = KAMERA_STEP_ATTEND | KAMERA_STEP_DIFFERENTIAL | KAMERA_STEP_FIT;
+    const size_t need = rounds.bytes();
+    Buffer w(need);
+    run_more(rounds, w.p, need);
+    rounds.req[1].num_queries -= 20;
+    run_more(rounds, w.p, need);
+  }
   // slots weighed twice
   Steps twice(KAMERA_GQA, KAMERA_F32, 8, 2, 64, {40}, {{40, 1}, {40, 1}});
   twice.s.flags = KAMERA_STEP_WEIGH;
