@@ -56,11 +56,96 @@ struct PairRows {
   }
 };
 
+__device__ __forceinline__ float wave_sum(float x) {
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, kWaveSize);
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ float widened(T x) {
+  if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)x << 16);
+  else return x;
+}
+
+// exp(q1 . k1) - exp(q2 . k2) + lambda_init, by one wave
+__device__ __forceinline__ float lambda_of(const StepArgs& a, const kamera_differential& diff) {
+  if (!diff.lambdas) return diff.lambda_init;
+  const KGLOBAL float* p = (const KGLOBAL float*)diff.lambdas;
+  float d0 = 0.0f, d1 = 0.0f;
+  for (int c = (int)threadIdx.x & 63; c < a.dk; c += kWaveSize) {
+    d0 += p[c] * p[a.dk + c];
+    d1 += p[2 * a.dk + c] * p[3 * a.dk + c];
+  }
+  return expf(wave_sum(d0)) - expf(wave_sum(d1)) + diff.lambda_init;
+}
+// What a row x of `dv` columns is multiplied with, besides the weights, given its sum of squares.
+__device__ __forceinline__ float norm_scale(const kamera_differential& diff, float squares, int dv) {
+  if (!(diff.flags & KAMERA_DIFF_NORM)) return diff.out_scale;
+  const float ms = squares / (float)dv + diff.eps;
+  return ms == 0.0f ? 0.0f : diff.out_scale / sqrtf(ms);  // (zeros stay zeros)
+}
+
+// Results of a run that no other shares: the second map's wave passes its rows on through LDS at `place` (like lanes
+// hold like values), the first map's makes the output. r: the row of the wave's own map. Every wave of the
+// workgroup comes along; idle ones hold nothing.
+template <typename S>
+__device__ __forceinline__ void put_pairs(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, const Lane& r, S& st, float l, int map,
+                                          float lambda, f32x4* place, bool idle) {
+  constexpr int kQuads = S::kScores / 4, ROWS = S::kScores == 16 ? 32 : 16;
+  const int lane = threadIdx.x & 63;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (io.lse && !idle && r.owned && S::group() == 0) io.lse[(int64_t)r.token * a.num_q_heads + r.qh] = l == 0.0f ? -INFINITY : (st.m + log2f(l)) * kLn2;
+  __syncthreads();
+  if (map == 1 && !idle) {
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+        place[(b * kQuads + i) * 64 + lane] = (f32x4){st.o[b][4 * i] * inv, st.o[b][4 * i + 1] * inv, st.o[b][4 * i + 2] * inv, st.o[b][4 * i + 3] * inv};
+  }
+  __syncthreads();
+  if (map == 1 || idle) return;
+  float squares = 0.0f;
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      __builtin_amdgcn_sched_barrier(0);  // (a few values at a time: registers are short)
+      const f32x4 y = place[(b * kQuads + i) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = st.o[b][4 * i + e] * inv - lambda * y[e];
+        st.o[b][4 * i + e] = x;
+        squares += x * x;
+      }
+    }
+  const float scale = norm_scale(diff, row_sum<ROWS>(squares), a.dv);
+  if (!r.owned) return;
+  uint16_t* out = (uint16_t*)io.out + (int64_t)r.token * io.out_stride + (int64_t)(r.qh >> 1) * a.dv;
+  const KGLOBAL uint16_t* weights = (diff.flags & KAMERA_DIFF_NORM) ? (const KGLOBAL uint16_t*)diff.norm_weight : nullptr;
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int c = S::column(b, i);
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = st.o[b][4 * i + e] * scale * (weights ? widened<uint16_t>(weights[c + e]) : 1.0f);
+      if (io.out_vec) {
+        *(KGLOBAL u32x2*)(KGLOBAL void*)(out + c) = (u32x2){pack2(y[0], y[1]), pack2(y[2], y[3])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[c + e] = (uint16_t)pack2(y[e], 0.0f);
+      }
+    }
+}
+
 // ============================================================================
 // Tiles of 128 rows: two waves a map, 32 rows each, share stages of 32 (D = 128) or 64 keys, two in LDS.
 // ============================================================================
 template <int D>
-__device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds) {
+__device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, const AttendItem& it, int head,
+                                          KLDS char* lds) {
   constexpr int TS = 4096 / D, N = TS / kWaves, NT = TS / 32;
   typedef State<D, 2 * D, 32, TS * kRowBytes<D>> S;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, map = wave & 1;
@@ -106,7 +191,10 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
   const float l = row_sum<32>(st.l);
   int tid = threadIdx.x;  // the row again: kept through the loop it would take registers from the products
   asm volatile("" : "+v"(tid));
-  put_state(a, io, it, head, lane_row(a, it, head, it.row0 + (tid >> 7) * 64 + 2 * (tid & 31) + ((tid >> 6) & 1)), st, l);
+  const Lane w = lane_row(a, it, head, it.row0 + (tid >> 7) * 64 + 2 * (tid & 31) + ((tid >> 6) & 1));
+  static_assert(2 * 64 * S::kBlocks * S::kScores * 4 <= kLds, "two waves' results fit in LDS");
+  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_of(a, diff), (f32x4*)(KLDS f32x4*)(lds + (wave >> 1) * (kLds / 2)), false);
+  else put_state(a, io, it, head, w, st, l);
 }
 
 // ============================================================================
@@ -114,8 +202,8 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
 // buffer: the other workgroup of the CU computes while this one loads. The halves are joined at the end.
 // ============================================================================
 template <int D, int ROWS>
-__device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const AttendItem& it, int head, KLDS char* lds,
-                                            float (&ml)[2][kWaves][64]) {
+__device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, const AttendItem& it, int head,
+                                            KLDS char* lds, float (&ml)[2][kWaves][64]) {
   constexpr int TS = 8192 / D, N = TS / kWaves, HALF = TS / 2;
   typedef State<D, 2 * D, ROWS, TS * kRowBytes<D>> S;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), map = wave & 1, part = wave >> 1;
@@ -149,19 +237,21 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   join_two(st, l, part == 1, map, (f32x4*)(KLDS f32x4*)(lds + map * (kLds / 2)), ml);
   int tid = threadIdx.x;  // (as in the wide tile)
   asm volatile("" : "+v"(tid));
-  if (part == 0) put_state(a, io, it, head, lane_row(a, it, head, it.row0 + 2 * (tid & (ROWS - 1)) + ((tid >> 6) & 1)), st, l);
+  const Lane w = lane_row(a, it, head, it.row0 + 2 * (tid & (ROWS - 1)) + ((tid >> 6) & 1));
+  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_of(a, diff), (f32x4*)(KLDS f32x4*)lds, part == 1);
+  else if (part == 0) put_state(a, io, it, head, w, st, l);
 }
 
 // One launch for all tiles, the wide ones first.
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo io) {
+__global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo io, kamera_differential diff) {
   __shared__ __align__(1024) char lds[kLds];
   __shared__ float ml[2][kWaves][64];
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const AttendItem it = a.items[item];
-  if (item < a.num_wide) wide_tile<D>(a, io, it, head, (KLDS char*)lds);
-  else if (item < a.num_wide + a.num_pairs) narrow_tile<D, 32>(a, io, it, head, (KLDS char*)lds, ml);
-  else narrow_tile<D, 16>(a, io, it, head, (KLDS char*)lds, ml);
+  if (item < a.num_wide) wide_tile<D>(a, io, diff, it, head, (KLDS char*)lds);
+  else if (item < a.num_wide + a.num_pairs) narrow_tile<D, 32>(a, io, diff, it, head, (KLDS char*)lds, ml);
+  else narrow_tile<D, 16>(a, io, diff, it, head, (KLDS char*)lds, ml);
 }
 
 // ============================================================================
@@ -171,10 +261,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo 
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
 
-__device__ __forceinline__ float wave_sum(float x) {
-  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, kWaveSize);
-  return x;
-}
 __device__ __forceinline__ float wave_max(float x) {
   for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, kWaveSize));
   return x;
@@ -182,11 +268,6 @@ __device__ __forceinline__ float wave_max(float x) {
 template <typename T>
 __device__ __forceinline__ T narrowed(float x) {
   if constexpr (sizeof(T) == 2) return (T)pack2(x, 0.0f);
-  else return x;
-}
-template <typename T>
-__device__ __forceinline__ float widened(T x) {
-  if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)x << 16);
   else return x;
 }
 
@@ -224,16 +305,6 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
     const int s = k >= mt.splits[0];
     return mt.part[s] + ((int64_t)(s ? k - mt.splits[0] : k) * a.heads + head) * mt.rows[s] + mt.row0[s] + g;
   };
-  // lambda, while the parts' statistics are on their way
-  float lambda = diff.lambda_init;
-  float d0 = 0.0f, d1 = 0.0f;
-  if (diff.lambdas) {
-    const KGLOBAL float* p = (const KGLOBAL float*)diff.lambdas;
-    for (int c = lane; c < a.dk; c += kWaveSize) {
-      d0 += p[c] * p[a.dk + c];
-      d1 += p[2 * a.dk + c] * p[3 * a.dk + c];
-    }
-  }
   // every part's maxima and sums become its weights, all parts at once
   constexpr int MAXP = WPR == 1 ? kWaveSize : kJoinParts, TPR = WPR * kWaveSize, PER = MAXP / TPR;
   const int tid = threadIdx.x % TPR;
@@ -260,7 +331,7 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
     if (e * TPR + tid < n) weight[sub][e * TPR + tid] = w;
   }
   sum = over_waves<WPR, false>(make_float2(wave_sum(sum.x), wave_sum(sum.y)), red[sub]);
-  if (diff.lambdas) lambda += expf(wave_sum(d0)) - expf(wave_sum(d1));
+  const float lambda = lambda_of(a, diff);
   __syncthreads();
   const int quads = a.dv / 4;  // of a map's row
   const KGLOBAL f32x4* parts = (const KGLOBAL f32x4*)a.part_o;
@@ -309,11 +380,7 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
       square += x[j][e] * x[j][e];
     }
   }
-  float scale = diff.out_scale;
-  if (diff.flags & KAMERA_DIFF_NORM) {
-    const float ms = wave_sum(square) / (float)a.dv + diff.eps;
-    scale = ms == 0.0f ? 0.0f : scale / sqrtf(ms);
-  }
+  const float scale = norm_scale(diff, wave_sum(square), a.dv);
   T* out = (T*)io.out + (int64_t)mt.token * io.out_stride + (int64_t)oh * a.dv;
   const T* weights = (diff.flags & KAMERA_DIFF_NORM) ? (const T*)diff.norm_weight : nullptr;
 #pragma unroll
@@ -368,8 +435,8 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
     e = launch_attend_plain(a, io, stream);
   } else if (a.num_items > 0) {
     const dim3 g((unsigned)((int64_t)a.num_items * a.heads)), b(kThreads);
-    if (a.dk == 128) hipLaunchKernelGGL((attend_diff<128>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((attend_diff<64>), g, b, 0, stream, a, io);
+    if (a.dk == 128) hipLaunchKernelGGL((attend_diff<128>), g, b, 0, stream, a, io, diff);
+    else hipLaunchKernelGGL((attend_diff<64>), g, b, 0, stream, a, io, diff);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_merge == 0) return e;

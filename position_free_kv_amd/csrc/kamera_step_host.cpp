@@ -164,7 +164,7 @@ int pick_kernel(const kamera_layout* L, const kamera_pool* pool, bool diff = fal
 void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {
   const Shape h = attend_shape(L, s);
   const int G = h.group;
-  const bool diff = s->flags & KAMERA_STEP_DIFFERENTIAL;  // (its results are always joined: two rows make one)
+  const bool joined = (s->flags & KAMERA_STEP_DIFFERENTIAL) && kernel == ATTEND_PLAIN;  // (a row a wave there: two of them make a result)
   w.runs.clear();
   w.items.clear();
   w.tok.clear();
@@ -231,7 +231,7 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     }
     r.tok0 = (int32_t)tok;
     r.ntok = q.num_queries;
-    r.direct = !shares(q) && !diff;
+    r.direct = !shares(q) && !joined;
     own_run[(size_t)i] = (int32_t)w.runs.size();
     w.runs.push_back(r);
   }
@@ -402,15 +402,19 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   for (int i = 0; i < s->num_requests; tok += s->requests[i++].num_queries) {
     const kamera_request& q = s->requests[i];
     const int run = own_run[(size_t)i];
-    if (run >= 0 && w.runs[(size_t)run].direct) continue;
-    const bool sh = q.num_queries > 0 && shares(q);
+    const bool sh = q.num_queries > 0 && shares(q), cut = !rest.empty() && rest[(size_t)i].second >= 0;
     for (int j = 0; j < q.num_queries; ++j) {
+      const bool later = cut && j >= rest[(size_t)i].first;  // among its last queries, which are another run's
+      const int of = later ? rest[(size_t)i].second : run;
+      if (of >= 0 && w.runs[(size_t)of].direct) {
+        j = cut && !later ? rest[(size_t)i].first - 1 : q.num_queries - 1;  // (all of the run's)
+        continue;
+      }
       MergeToken m;
       std::memset(&m, 0, sizeof(m));
       m.token = (int32_t)(tok + j);
       if (sh) part(m, 0, prefix_run[(size_t)q.prefix], listed[(size_t)q.prefix]++);
-      if (run >= 0 && !rest.empty() && rest[(size_t)i].second >= 0 && j >= rest[(size_t)i].first) part(m, 1, rest[(size_t)i].second, j - rest[(size_t)i].first);
-      else if (run >= 0) part(m, 1, run, j);
+      if (of >= 0) part(m, 1, of, later ? j - rest[(size_t)i].first : j);
       w.max_parts = std::max(w.max_parts, m.splits[0] + m.splits[1]);
       w.merge.push_back(m);
     }

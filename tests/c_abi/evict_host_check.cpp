@@ -22,8 +22,8 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
   CHECK(a.kernel == ATTEND_PLAIN || a.kernel == ATTEND_DIFF);
   for (int i = 0; i < a.num_items; ++i) {
     const AttendRun& run = a.items[i].run;
-    CHECK(!run.direct && run.part0 % 2 == 0);
-    const int64_t parts = run.part0 + (int64_t)run.splits * a.heads * run.ntok * a.group;
+    CHECK(run.part0 % 2 == 0 && !(run.direct && a.kernel == ATTEND_PLAIN));
+    const int64_t parts = run.direct ? 0 : run.part0 + (int64_t)run.splits * a.heads * run.ntok * a.group;
     inside(a.part_ml, (size_t)parts * 8);
     inside(a.part_o, (size_t)(parts * a.dv * 4));
     CHECK((char*)(a.part_ml + parts) <= (char*)a.part_o);
