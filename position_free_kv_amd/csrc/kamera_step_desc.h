@@ -64,13 +64,14 @@ struct alignas(16) WeighItem {
   int32_t tok0, ntok, listed, lim0;
   int32_t lstep, row0, row1, split;
   int64_t part;  // partial sums of the run: part + (split * heads + head) * kv + key; -1: straight to the scores
-  int32_t kv, pad;
+  int32_t kv, fresh;  // keys from `fresh` on are the step's own: their scores start at 0
 };
 static_assert(sizeof(WeighItem) == 64, "weigh record");
 // A run whose rows are cut into `splits` ranges of `rows` rows: its keys' sums are joined from those.
 struct alignas(16) WeighJoin {
   int64_t part;
   int32_t pg, slot, kv, splits;
+  int32_t fresh, pad;
   int32_t rows, lim0, lstep, tile;  // tile: keys of an item (the ranges before the first row that sees any of them hold nothing)
 };
 static_assert(sizeof(WeighJoin) == 48, "weigh join record");

@@ -437,7 +437,7 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
     std::memset(&r, 0, sizeof(r));
     r.pg = pg;
     r.slot = slot;
-    r.kv = kv;
+    r.kv = r.fresh = kv;
     r.lim0 = kv - 1;
     return r;
   };
@@ -482,6 +482,7 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
       r.lim0 = q.num_tokens - q.num_queries;
       r.lstep = 1;
     }
+    if (s->flags & KAMERA_STEP_APPEND) r.fresh = q.num_tokens - q.num_queries;
     runs.push_back(r);
   }
   const int64_t keys = weigh_keys(kernel);
@@ -496,7 +497,7 @@ void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb
     if (splits > 1) {
       r.part = w.weigh_part;
       w.weigh_part += splits * h.heads * r.kv;
-      w.weigh_join.push_back(WeighJoin{r.part, r.pg, r.slot, r.kv, (int32_t)splits, (int32_t)each, r.lim0, r.lstep, (int32_t)keys});
+      w.weigh_join.push_back(WeighJoin{r.part, r.pg, r.slot, r.kv, (int32_t)splits, r.fresh, 0, (int32_t)each, r.lim0, r.lstep, (int32_t)keys});
       w.weigh_longest = std::max(w.weigh_longest, r.kv);
     }
     const int64_t tile = rows <= kFewRows ? weigh_keys_of_few(kernel) : keys;

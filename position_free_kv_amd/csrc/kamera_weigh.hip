@@ -52,9 +52,10 @@ __device__ __forceinline__ int64_t slot_of(const StepArgs& a, int pg, int slot0,
 __device__ __forceinline__ KGLOBAL float* score_at(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head) {
   return (KGLOBAL float*)io.scores + (page * a.heads + head) * a.page_size + place;
 }
-__device__ __forceinline__ void add_score(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head, float sum) {
+// fresh: the token is the step's own
+__device__ __forceinline__ void add_score(const StepArgs& a, const WeighIo& io, int64_t page, int place, int head, float sum, bool fresh) {
   KGLOBAL float* p = score_at(a, io, page, place, head);
-  *p = io.decay == 0.0f ? sum : io.decay * *p + sum;
+  *p = io.decay == 0.0f || fresh ? sum : io.decay * *p + sum;
 }
 
 // ============================================================================
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
   }
   if (lane != 0 || t >= it.kv1) return;
   if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = sum;
-  else add_score(a, io, page, place, head, sum);
+  else add_score(a, io, page, place, head, sum, t >= it.fresh);
 }
 
 // ============================================================================
@@ -257,7 +258,7 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
     const int t = key0 + 16 * x + n;
     if (lane >= 16 || t >= it.kv1) continue;
     if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = total;
-    else add_score(a, io, page[x], place[x], head, total);
+    else add_score(a, io, page[x], place[x], head, total, t >= it.fresh);
   }
 }
 
@@ -339,7 +340,7 @@ __device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, c
       sum = row_sum<16>(sum);
       if (lane >= 16 || key >= it.kv1) continue;
       if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + key] = sum;
-      else *score_at(a, io, w.page[x], w.place[x], head) = io.decay == 0.0f ? sum : io.decay * w.old[x] + sum;
+      else *score_at(a, io, w.page[x], w.place[x], head) = io.decay == 0.0f || key >= it.fresh ? sum : io.decay * w.old[x] + sum;
     }
   };
 #pragma nounroll
@@ -386,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void weigh_join(StepArgs a, WeighIo io) {
   for (int s = (int)(row0 / j.rows); s < j.splits; ++s) sum += p[(int64_t)s * a.heads * j.kv];
   int place;
   const int64_t page = slot_of(a, j.pg, j.slot, t, place);
-  add_score(a, io, page, place, head, sum);
+  add_score(a, io, page, place, head, sum, t >= j.fresh);
 }
 
 template <typename T>

@@ -52,6 +52,8 @@ hipError_t launch_step_weigh(const StepArgs& a, int, const void*, int64_t, const
         CHECK(token >= 0 && token < a.num_tokens);
         if (t <= it.lim0 + j * it.lstep) ++rows[(int64_t)token * G + row - j * G];
       }
+      const bool appends = s->flags & KAMERA_STEP_APPEND;
+      if (!it.listed && it.lstep) CHECK(it.fresh == (appends ? it.lim0 : it.kv));
       if (it.part < 0) {
         CHECK(writers[slot(it.pg, it.slot, t)]++ == 0);
         met[slot(it.pg, it.slot, t)] = rows;
