@@ -1,3 +1,9 @@
+#ifndef LNB
+#define LNB 4
+#endif
+#ifndef HNB
+#define HNB 2
+#endif
 // Weighing (include/kamera_step.h): what each cached token receives of the attention weights of a step's queries.
 // Work list: kamera_step_desc.h.
 //
@@ -105,148 +111,158 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
 // ============================================================================
 // On the matrix cores: S = Q K^T in tiles of 16 rows x 16 keys (v_mfma_f32_16x16x32_bf16). A wave holds
 // 16 KT keys in registers for good; stages of SR query rows go through LDS, laid out as the attention
-// lays out keys, two stages in turn. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
-// row's lse off and adds up the exponentials.
+// lays out keys, NB stages in a ring. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
+// row's lse off and adds up the exponentials. Where the rows lie, their lse and what they see is put into a
+// table first, for up to TABLE rows at a time, so that the ring's loads depend on nothing else.
 // ============================================================================
+template <int DK, int SR, int NB, int TABLE>
+struct Stages {
+  __align__(1024) char stage[NB][SR * 2 * DK];
+  __align__(16) int64_t at[TABLE];   // element of q where the row begins
+  __align__(16) float base[TABLE];   // lse * log2(e)
+  __align__(16) int limit[TABLE];    // last key that the row sees; -1: it adds nothing
+  int whole[TABLE / 16];             // 16 rows that add to all keys
+};
 
-// A wave's share of a stage: PER rows. Lane i looks after row i % PER one stage ahead of its load.
+// A wave's rows of a stage (SR / 4 of them) into LDS, swizzled like keys: the first DV columns (DK if there are fewer),
+// then the others' rows. Always the same number of loads.
 template <int DK, int DV, int SR>
 struct QueryRows {
+  typedef State<DK, DV, 16> S;
   static constexpr int PER = SR / kWaves;
-  int64_t at;   // element of q where the row begins
-  float base;   // lse * log2(e)
-  int limit;    // last key that the row sees; -1: it adds nothing
-  __device__ __forceinline__ void find(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, int row0) {
-    const int wave = threadIdx.x >> 6, row = row0 + wave * PER + ((int)threadIdx.x & (PER - 1));
-    const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
-    at = (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK;
-    const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)q.token * a.num_q_heads + q.qh];
-    base = lse * kLog2;
-    limit = row < it.row1 && lse != -INFINITY ? it.lim0 + q.j * it.lstep : -1;
-  }
-  // the rows' places among the statistics; whole[wave]: every row sees keys up to `last`
-  __device__ __forceinline__ void note(float* bases, int* limits, int* whole, int last) const {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const bool all = __all(limit >= last);
-    if (lane < PER) {
-      bases[wave * PER + lane] = base;
-      limits[wave * PER + lane] = limit;
-    }
-    if (lane == 0) whole[wave] = all;
-  }
-  __device__ __forceinline__ const KGLOBAL uint16_t* row(const WeighIo& io, int i) const {
-    const int lo = __shfl((int)(uint32_t)at, i, 64), hi = __shfl((int)(at >> 32), i, 64);
-    return (const KGLOBAL uint16_t*)io.q + (((int64_t)hi << 32) | (uint32_t)lo);
-  }
-  // the rows into LDS, swizzled like keys: the first DV columns (DK if there are fewer), then the others' rows
-  __device__ __forceinline__ void load(const WeighIo& io, KLDS char* stage) const {
-    typedef State<DK, DV, 16> S;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, first = wave * PER;
-    constexpr int LPR = S::kKeyRow / 16 < 64 ? S::kKeyRow / 16 : 64, RPI = 64 / LPR;  // lanes of a row, rows of an instruction
-    static_assert(S::kKeyRow <= 1024 && PER % RPI == 0, "whole instructions");
-    auto bring = [&](const KGLOBAL uint16_t* x, KLDS char* to) {
-      if (io.q_vec) {
-        __builtin_amdgcn_global_load_lds((const KGLOBAL void*)x, (KLDS void*)to, 16, 0, 0);
-      } else {
-        u32x4 w;
+  static constexpr int LPR = S::kKeyRow / 16 < 64 ? S::kKeyRow / 16 : 64, RPI = 64 / LPR;  // lanes of a row, rows of an instruction
+  static constexpr int kBands = S::kRestRow ? (PER + 7) / 8 : 0;
+  static constexpr int kLoads = PER / RPI + kBands;
+  static_assert(S::kKeyRow <= 1024 && PER % RPI == 0 && (S::kRestRow == 0 || S::kRestRow == 128), "whole instructions");
+  static __device__ __forceinline__ void bring(const WeighIo& io, const KGLOBAL uint16_t* x, KLDS char* to) {
+    if (io.q_vec) {
+      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)x, (KLDS void*)to, 16, 0, 0);
+    } else {
+      u32x4 w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
-        *(KLDS u32x4*)(to + lane * 16) = w;
-      }
-    };
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
+      *(KLDS u32x4*)(to + (threadIdx.x & 63) * 16) = w;
+    }
+  }
+  // at: the table's entries of the stage
+  static __device__ __forceinline__ void load(const WeighIo& io, const int64_t* at, KLDS char* stage) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, first = wave * PER;
+    const KGLOBAL uint16_t* q = (const KGLOBAL uint16_t*)io.q;
 #pragma unroll
     for (int i = 0; i < PER; i += RPI) {
-      const int r = i + lane / LPR;
-      bring(row(io, r) + ((lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(first + r)) * 8, stage + (first + i) * S::kKeyRow);
+      const int r = first + i + lane / LPR;
+      bring(io, q + at[r] + ((lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(r)) * 8, stage + (first + i) * S::kKeyRow);
     }
-    if constexpr (S::kRestRow != 0) {
-      static_assert(S::kRestRow == 128 && PER % 8 == 0, "bands of 8 rows to an instruction");
 #pragma unroll
-      for (int i = 0; i < PER; i += 8) {
-        const int r = i + lane / 8;
-        bring(row(io, r) + DV + ((lane & 7) ^ swz<16, 128>(first + r)) * 8, stage + SR * S::kKeyRow + (first + i) * 128);
-      }
+    for (int i = 0; i < kBands * 8; i += 8) {
+      const int r = first + i + lane / 8;
+      if (PER % 8 == 0 || r < first + PER) bring(io, q + at[r] + DV + ((lane & 7) ^ swz<16, 128>(r)) * 8, stage + SR * S::kKeyRow + (first + i) * 128);
     }
   }
 };
 
-template <int DK, int SR>
-struct Stages {
-  __align__(1024) char stage[2][SR * 2 * DK];
-  __align__(16) float base[2][SR];
-  __align__(16) int limit[2][SR];
-  __align__(16) int whole[2][kWaves];
-};
-template <int DK, int DV, int KT, int SR>
-__device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, Stages<DK, SR>& lds) {
+// vmcnt(n), lgkmcnt(0): all but the last n loads have arrived, LDS reads and writes are done
+template <int N>
+__device__ __forceinline__ void wait_but() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70);
+}
+
+template <int DK, int DV, int KT, int SR, int NB, int TABLE>
+__device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, Stages<DK, SR, NB, TABLE>& lds) {
   typedef State<DK, DV, 16> S;
-  auto& stage = lds.stage;
-  auto& base = lds.base;
-  auto& limit = lds.limit;
-  auto& whole = lds.whole;
+  typedef QueryRows<DK, DV, SR> Q;
+  static_assert(TABLE % SR == 0 && TABLE % kThreads == 0, "whole stages, whole turns of the threads");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
   const int key0 = it.kv0 + wave * 16 * KT;  // the wave's first key
   const bool any = key0 < it.kv1;
-  QueryRows<DK, DV, SR> rows;
-  rows.find(a, io, it, head, it.row0);
   int page[KT], place[KT];
 #pragma unroll
   for (int x = 0; x < KT; ++x) page[x] = (int)slot_of(a, it.pg, it.slot, min(key0 + 16 * x + n, it.kv1 - 1), place[x]);
-  rows.load(io, (KLDS char*)stage[0]);
   bf16x8 k[KT][S::kKSteps];
+  float sum[KT], old[KT];
 #pragma unroll
-  for (int x = 0; x < KT; ++x) {
-    const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + ((int64_t)page[x] * a.page_size + place[x]) * a.row + (int64_t)head * DK;
+  for (int x = 0; x < KT; ++x) sum[x] = old[x] = 0.0f;
+  bool keys = false;
+  for (int chunk = it.row0; chunk < it.row1; chunk += TABLE) {
+    const int rows = min(it.row1 - chunk, TABLE), stages = (rows + SR - 1) / SR;
+    if (chunk > it.row0) __syncthreads();  // (the table has been read)
 #pragma unroll
-    for (int ks = 0; ks < S::kKSteps; ++ks) k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
-  }
-  rows.note(base[0], limit[0], whole[0], it.kv1 - 1);
-  if (it.row0 + SR < it.row1) rows.find(a, io, it, head, it.row0 + SR);
-  float sum[KT];
-#pragma unroll
-  for (int x = 0; x < KT; ++x) sum[x] = 0.0f;
-  int buffer = 0;
-  for (int row0 = it.row0; row0 < it.row1; row0 += SR, buffer ^= 1) {
-    stage_barrier();
-    if (row0 + SR < it.row1) {
-      rows.load(io, (KLDS char*)stage[buffer ^ 1]);
-      rows.note(base[buffer ^ 1], limit[buffer ^ 1], whole[buffer ^ 1], it.kv1 - 1);
-      if (row0 + 2 * SR < it.row1) rows.find(a, io, it, head, row0 + 2 * SR);
+    for (int i = 0; i < TABLE / kThreads; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x, row = chunk + e;
+      if (i * kThreads < rows) {  // (rows behind the last repeat it and add nothing)
+        const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
+        const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)q.token * a.num_q_heads + q.qh];
+        const int limit = row < it.row1 && lse != -INFINITY ? it.lim0 + q.j * it.lstep : -1;
+        const uint64_t all = __ballot(limit >= it.kv1 - 1);
+        lds.at[e] = (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK;
+        lds.base[e] = lse * kLog2;
+        lds.limit[e] = limit;
+        if ((lane & 15) == 0) lds.whole[e / 16] = ((all >> lane) & 0xffff) == 0xffff;
+      }
     }
-    if (!any) continue;
-    const KLDS char* at = (const KLDS char*)stage[buffer];
-    constexpr int kWavesOf = 16 / (SR / kWaves);  // waves that brought 16 rows
+    if (!keys) {  // (asked for behind the table's loads)
+      keys = true;
 #pragma unroll
-    for (int r = 0; r < SR; r += 16) {
-      if (row0 + r >= it.row1) break;
-      typename S::Acc s[KT];
+      for (int x = 0; x < KT; ++x) {
+        const KGLOBAL uint16_t* p = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + ((int64_t)page[x] * a.page_size + place[x]) * a.row + (int64_t)head * DK;
 #pragma unroll
-      for (int x = 0; x < KT; ++x) s[x] = (typename S::Acc)(0.0f);
+        for (int ks = 0; ks < S::kKSteps; ++ks) k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
+        if (io.decay != 0.0f && it.part < 0) old[x] = *score_at(a, io, page[x], place[x], head);
+      }
+    }
+    __syncthreads();
+    auto load = [&](int s) { Q::load(io, lds.at + s * SR, (KLDS char*)lds.stage[s % NB]); };
+    for (int s = 0; s < NB - 1 && s < stages; ++s) load(s);
+    // the keys are waited for here: a first use inside the loop would wait for all loads in each turn
+#pragma unroll
+    for (int x = 0; x < KT; ++x)
 #pragma unroll
       for (int ks = 0; ks < S::kKSteps; ++ks) {
-        const bf16x8 q = S::k_operand(at + r * S::kKeyRow, at + SR * S::kKeyRow + r * S::kRestRow, 0, ks);
-#pragma unroll
-        for (int x = 0; x < KT; ++x) s[x] = S::mfma(q, k[x][ks], s[x]);
+        u32x4 w = __builtin_bit_cast(u32x4, k[x][ks]);
+        asm volatile("" : "+v"(w));
+        k[x][ks] = __builtin_bit_cast(bf16x8, w);
       }
-      const f32x4 b = *(const KLDS f32x4*)&base[buffer][r + 4 * S::group()];
-      int all = 1;
+#pragma nounroll
+    for (int s = 0; s < stages; ++s) {
+      // stage s is here, those after it (NB - 2 of them, unless the last ones are on their way) need not be
+      if (s + NB - 2 < stages) wait_but<Q::kLoads * (NB - 2)>();
+      else wait_but<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (s + NB - 1 < stages) load(s + NB - 1);
+      if (!any) continue;
+      const KLDS char* at = (const KLDS char*)lds.stage[s % NB];
 #pragma unroll
-      for (int w = 0; w < kWavesOf; ++w) all &= whole[buffer][r / 16 * kWavesOf + w];
-      if (__builtin_amdgcn_readfirstlane(all)) {  // every row adds to every key
+      for (int r = 0; r < SR; r += 16) {
+        const int e = s * SR + r;
+        if (e >= rows) break;
+        typename S::Acc c[KT];
 #pragma unroll
-        for (int x = 0; x < KT; ++x)
+        for (int x = 0; x < KT; ++x) c[x] = (typename S::Acc)(0.0f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
-      } else {
-        typedef int i32x4 __attribute__((ext_vector_type(4)));
-        const i32x4 lim = *(const KLDS i32x4*)&limit[buffer][r + 4 * S::group()];
+        for (int ks = 0; ks < S::kKSteps; ++ks) {
+          const bf16x8 q = S::k_operand(at + r * S::kKeyRow, at + SR * S::kKeyRow + r * S::kRestRow, 0, ks);
 #pragma unroll
-        for (int x = 0; x < KT; ++x) {
-          const int t = key0 + 16 * x + n;
+          for (int x = 0; x < KT; ++x) c[x] = S::mfma(q, k[x][ks], c[x]);
+        }
+        const f32x4 b = *(const KLDS f32x4*)&lds.base[e + 4 * S::group()];
+        if (__builtin_amdgcn_readfirstlane(lds.whole[e / 16])) {  // every row adds to every key
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], io.scale2, -b[i]));
-            sum[x] += t <= lim[i] ? w : 0.0f;
+          for (int x = 0; x < KT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(c[x][i], io.scale2, -b[i]));
+        } else {
+          typedef int i32x4 __attribute__((ext_vector_type(4)));
+          const i32x4 lim = *(const KLDS i32x4*)&lds.limit[e + 4 * S::group()];
+#pragma unroll
+          for (int x = 0; x < KT; ++x) {
+            const int t = key0 + 16 * x + n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(c[x][i], io.scale2, -b[i]));
+              sum[x] += t <= lim[i] ? w : 0.0f;
+            }
           }
         }
       }
@@ -258,7 +274,7 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
     const int t = key0 + 16 * x + n;
     if (lane >= 16 || t >= it.kv1) continue;
     if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = total;
-    else add_score(a, io, page[x], place[x], head, total, t >= it.fresh);
+    else *score_at(a, io, page[x], place[x], head) = io.decay == 0.0f || t >= it.fresh ? total : io.decay * old[x] + total;
   }
 }
 
@@ -360,13 +376,13 @@ __device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, c
   }
 }
 
-template <int DK, int DV, int KT, int SR, int FEW>
+template <int DK, int DV, int KT, int SR, int NB, int TABLE, int FEW>
 __global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
-  __shared__ Stages<DK, SR> lds;
+  __shared__ Stages<DK, SR, NB, TABLE> lds;
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const WeighItem it = a.weigh[item];
   if (it.row1 - it.row0 <= kFewRows) few_rows<DK, DV, FEW>(a, io, it, head);
-  else many_rows<DK, DV, KT, SR>(a, io, it, head, lds);
+  else many_rows<DK, DV, KT, SR, NB, TABLE>(a, io, it, head, lds);
 }
 
 // Sums of ranges of rows, joined in their order: a thread a key and head. A range that ends before the first row
@@ -411,9 +427,9 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
     e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
-    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 32, 1>), g, b, 0, stream, a, io);
-    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, 2>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, 4>), g, b, 0, stream, a, io);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 16, LNB, 256, 1>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, HNB, 1024, 2>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, HNB, 1024, 4>), g, b, 0, stream, a, io);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_weigh_join == 0) return e;
