@@ -1,9 +1,3 @@
-#ifndef LNB
-#define LNB 4
-#endif
-#ifndef HNB
-#define HNB 2
-#endif
 // Weighing (include/kamera_step.h): what each cached token receives of the attention weights of a step's queries.
 // Work list: kamera_step_desc.h.
 //
@@ -134,29 +128,38 @@ struct QueryRows {
   static constexpr int kBands = S::kRestRow ? (PER + 7) / 8 : 0;
   static constexpr int kLoads = PER / RPI + kBands;
   static_assert(S::kKeyRow <= 1024 && PER % RPI == 0 && (S::kRestRow == 0 || S::kRestRow == 128), "whole instructions");
-  static __device__ __forceinline__ void bring(const WeighIo& io, const KGLOBAL uint16_t* x, KLDS char* to) {
-    if (io.q_vec) {
-      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)x, (KLDS void*)to, 16, 0, 0);
-    } else {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | ((uint32_t)x[2 * e + 1] << 16);
-      *(KLDS u32x4*)(to + (threadIdx.x & 63) * 16) = w;
-    }
-  }
   // at: the table's entries of the stage
   static __device__ __forceinline__ void load(const WeighIo& io, const int64_t* at, KLDS char* stage) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, first = wave * PER;
-    const KGLOBAL uint16_t* q = (const KGLOBAL uint16_t*)io.q;
+    // (all places first: one wait for LDS instead of one a load)
+    const KGLOBAL uint16_t* x[kLoads];
+    KLDS char* to[kLoads];
+    const bool band = PER % 8 == 0 || lane / 8 < PER;
 #pragma unroll
-    for (int i = 0; i < PER; i += RPI) {
-      const int r = first + i + lane / LPR;
-      bring(io, q + at[r] + ((lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(r)) * 8, stage + (first + i) * S::kKeyRow);
+    for (int i = 0; i < PER / RPI; ++i) {
+      const int r = first + i * RPI + lane / LPR;
+      x[i] = (const KGLOBAL uint16_t*)io.q + at[r] + ((lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(r)) * 8;
+      to[i] = stage + (first + i * RPI) * S::kKeyRow;
     }
 #pragma unroll
-    for (int i = 0; i < kBands * 8; i += 8) {
-      const int r = first + i + lane / 8;
-      if (PER % 8 == 0 || r < first + PER) bring(io, q + at[r] + DV + ((lane & 7) ^ swz<16, 128>(r)) * 8, stage + SR * S::kKeyRow + (first + i) * 128);
+    for (int i = 0; i < kBands; ++i) {
+      const int r = first + (band ? i * 8 + lane / 8 : 0);
+      x[PER / RPI + i] = (const KGLOBAL uint16_t*)io.q + at[r] + DV + ((lane & 7) ^ swz<16, 128>(r)) * 8;
+      to[PER / RPI + i] = stage + SR * S::kKeyRow + (first + i * 8) * 128;
+    }
+    if (io.q_vec) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (i < PER / RPI || band) __builtin_amdgcn_global_load_lds((const KGLOBAL void*)x[i], (KLDS void*)to[i], 16, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (i >= PER / RPI && !band) continue;
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[i][2 * e] | ((uint32_t)x[i][2 * e + 1] << 16);
+        *(KLDS u32x4*)(to[i] + lane * 16) = w;
+      }
     }
   }
 };
@@ -237,14 +240,23 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
       for (int r = 0; r < SR; r += 16) {
         const int e = s * SR + r;
         if (e >= rows) break;
-        typename S::Acc c[KT];
+        constexpr int CHAINS = KT >= 4 ? 1 : 4 / KT;  // products of a tile that do not wait for each other
+        typename S::Acc part[CHAINS][KT], c[KT];
 #pragma unroll
-        for (int x = 0; x < KT; ++x) c[x] = (typename S::Acc)(0.0f);
+        for (int x = 0; x < KT; ++x)
+#pragma unroll
+          for (int y = 0; y < CHAINS; ++y) part[y][x] = (typename S::Acc)(0.0f);
 #pragma unroll
         for (int ks = 0; ks < S::kKSteps; ++ks) {
           const bf16x8 q = S::k_operand(at + r * S::kKeyRow, at + SR * S::kKeyRow + r * S::kRestRow, 0, ks);
 #pragma unroll
-          for (int x = 0; x < KT; ++x) c[x] = S::mfma(q, k[x][ks], c[x]);
+          for (int x = 0; x < KT; ++x) part[ks % CHAINS][x] = S::mfma(q, k[x][ks], part[ks % CHAINS][x]);
+        }
+#pragma unroll
+        for (int x = 0; x < KT; ++x) {
+          c[x] = part[0][x];
+#pragma unroll
+          for (int y = 1; y < CHAINS; ++y) c[x] += part[y][x];
         }
         const f32x4 b = *(const KLDS f32x4*)&lds.base[e + 4 * S::group()];
         if (__builtin_amdgcn_readfirstlane(lds.whole[e / 16])) {  // every row adds to every key
@@ -343,9 +355,13 @@ __device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, c
   auto work = [&](const Tile& w) {
 #pragma unroll
     for (int x = 0; x < KT; ++x) {
-      typename S::Acc s = (typename S::Acc)(0.0f);
+      typename S::Acc s = (typename S::Acc)(0.0f), s1 = s;  // (two chains of products)
 #pragma unroll
-      for (int ks = 0; ks < S::kKSteps; ++ks) s = S::mfma(q[ks], w.k[x][ks], s);
+      for (int ks = 0; ks < S::kKSteps; ks += 2) {
+        s = S::mfma(q[ks], w.k[x][ks], s);
+        s1 = S::mfma(q[ks + 1], w.k[x][ks + 1], s1);
+      }
+      s += s1;
       const int key = t + 16 * x + n;
       float sum = 0.0f;
 #pragma unroll
@@ -427,9 +443,9 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
     e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
-    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 16, LNB, 256, 1>), g, b, 0, stream, a, io);
-    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, HNB, 1024, 2>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, HNB, 1024, 4>), g, b, 0, stream, a, io);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 16, 4, 256, 1>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, 2, 1024, 2>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, 2, 1024, 4>), g, b, 0, stream, a, io);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_weigh_join == 0) return e;
