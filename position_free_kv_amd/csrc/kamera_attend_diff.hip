@@ -5,6 +5,16 @@
 // The "head" of an item is a pair of KV heads: two keys of D columns a token, one value of 2 D columns. Rows
 // of a run alternate between the maps (row = token's number * group + query head of the pair), and a wave takes
 // 32 (or 16) rows of one map, so that a stage's values are brought into LDS once for both maps.
+//
+// Per pair, x = A0 V - lambda A1 V with A_e = softmax(scale q_e K_e^T), one pass over the keys with each map's running
+// maximum and sum; y = x / sqrt(mean x^2 + eps) * weights * out_scale. The maps are combined, and the norm taken, in
+// fp32 from sums in fp32; the weights are rounded to bf16 for the second product alone (at most 2^-8 of each), the output once.
+// A query head and key cost 2 D + 4 D flops, half as much again as plain attention, for the same bytes of the pool.
+//
+// 8 requests with 2481 query tokens over an 8192-token prefix, 28 + 4 heads of 128: 0.95 PFLOP/s in this kernel (463
+// GFLOP in 488 us), 78% of a large library product's rate; bound by the products and the softmax between them, which two
+// waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones, 32 + 8 heads: 66 us and
+// 12.6 in the join; bound by the own tokens' pages and by what a workgroup does before its first key (about 6 us).
 #include "kamera_attend.h"
 
 namespace kamera {
@@ -141,7 +151,12 @@ __device__ __forceinline__ void put_pairs(const StepArgs& a, const AttendIo& io,
 }
 
 // ============================================================================
-// Tiles of 128 rows: two waves a map, 32 rows each, share stages of 32 (D = 128) or 64 keys, two in LDS.
+// Tiles of 128 rows: two waves a map, 32 rows each, share stages of 32 (D = 128) or 64 keys, two in LDS. A wave's 32 rows
+// of 2 D columns of O are 128 registers (D = 128), its queries 32 more: 64 rows would leave one wave a SIMD. One map a wave
+// lets both maps share the values' stage, and LDS feeds 24 products of a stage's 32 keys from 24 KB a wave. Stages of
+// four like arrays, one address for four loads: 689 -> 638 us in the case above; whole tiles for whole rounds of the chip's
+// places (the planner's choice): 638 -> 520; results put out without partial rows where a run has no other: 520 -> 508.
+// A ring of four stages whose loads take their places from a table in LDS: 526 -> 555 (more registers than there are).
 // ============================================================================
 template <int D>
 __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, const AttendItem& it, int head,
@@ -199,7 +214,8 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
 
 // ============================================================================
 // Tiles of up to 64 rows (32: ROWS 16): a wave for each map and half of a stage of 64 (D = 128) or 128 keys. One
-// buffer: the other workgroup of the CU computes while this one loads. The halves are joined at the end.
+// buffer: the other workgroup of the CU computes while this one loads, and twice the bytes are on their way that two
+// buffers of half the size would have. The halves are joined at the end.
 // ============================================================================
 template <int D, int ROWS>
 __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, const AttendItem& it, int head,
@@ -257,7 +273,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo 
 // ============================================================================
 // Join of partial rows: an output row's two maps lie in neighbouring partial rows, 2 dv numbers side by side, which
 // the threads share in 16-byte pieces. WPR waves a row; parts are taken in a fixed order. The maps' normalised
-// rows meet in LDS, and the norm follows.
+// rows meet in LDS, and the norm follows. All parts' statistics are read at once, then their rows, 8 of a wave at a
+// time: bound by two dependent reads when rows are few, by the partial rows' bytes (written and read: 2 dv fp32 a
+// query pair and part) when they are many. 64 tokens of 16 pairs in 18 parts: 12.6 us.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
 
@@ -441,7 +459,11 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
   }
   if (e != hipSuccess || a.num_merge == 0) return e;
   const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
-  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > 32 && rows < 1024 && a.dv <= 256;
+  // Few rows of many parts are shared by 4 or 16 waves each. (4 layers, 32 + 8 heads of 128, whole calls in us with 1, 4
+  // and 16 waves a row: 32 rows 102, 81 and 78, with 64 parts 200, 201 and 147; 128 rows 119, 98 and 95; 512 rows 209, 151
+  // and 164; 1024 rows 240, 206 and 260; 2048 rows 300, 306 and 399. 8 parts and fewer: alike. 16 waves hold rows in
+  // LDS that is made for 256 columns.)
+  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > 8 && rows < 512 && a.dv <= 256;
   if (a.dtype == KAMERA_BF16)
     return very ? join<uint16_t, 16>(a, io, diff, stream) : wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
   return very ? join<float, 16>(a, io, diff, stream) : wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);

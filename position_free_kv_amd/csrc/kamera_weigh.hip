@@ -4,6 +4,14 @@
 // Here the keys stay and the query rows pass by, the other way round than in the attention: a lane's sums
 // belong to its keys, so that nothing is exchanged until the end, and every key's sum is one workgroup's (or a few
 // ranges of rows are joined in their order).
+//
+// score[t] <- decay * score[t] + sum over rows that see t of exp(scale q . k_t - lse): the attention's lse makes the
+// softmax's sum unnecessary, so that each key needs one pass over the rows and no running maximum. Sums are in fp32.
+//
+// 64 requests of one token over 8192 shared and 49300 own tokens, 32 + 8 heads of 128, a layer: 30 us; bound by reading the
+// own keys (3.9 TB/s). 2481 query tokens over 8192 shared and own tokens, 28 + 4 heads: 181 us for 154 GFLOP, 0.85
+// PFLOP/s; bound by exponentials (4 a lane and product tile of 4 instructions) and the products, which take turns. 32 requests
+// of one token, MLA, 16 heads, a layer: 16 us and 4 in the join; bound by the chain item, page, keys, rows.
 #include "kamera_attend.h"
 
 namespace kamera {
@@ -107,7 +115,8 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
 // 16 KT keys in registers for good; stages of SR query rows go through LDS, laid out as the attention
 // lays out keys, NB stages in a ring. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
 // row's lse off and adds up the exponentials. Where the rows lie, their lse and what they see is put into a
-// table first, for up to TABLE rows at a time, so that the ring's loads depend on nothing else.
+// table first, for up to TABLE rows at a time, so that the ring's loads depend on nothing else. (28 + 4 heads as above: two
+// stages of 64 rows 181 us, three 201 to 206: the LDS then holds one workgroup less a CU. MLA, 4 layers: four stages of 16 rows.)
 // ============================================================================
 template <int DK, int SR, int NB, int TABLE>
 struct Stages {
