@@ -46,7 +46,8 @@ __device__ __forceinline__ QueryRow query_row(const StepArgs& a, const WeighIo& 
   QueryRow r;
   r.j = (int)(((uint64_t)(uint32_t)row * a.group_magic) >> a.group_bits);
   const int g = row - r.j * io.rows_of_token;
-  r.token = it.listed ? a.tok[it.tok0 + r.j] : it.tok0 + r.j;
+  r.token = it.tok0 + r.j;
+  if (it.listed) r.token = ((const KGLOBAL int32_t*)a.tok)[r.token];
   r.qh = a.differential ? (head >> 1) * 2 * io.rows_of_token + 2 * g + (head & 1) : head * io.rows_of_token + g;
   return r;
 }
@@ -199,19 +200,23 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
   for (int chunk = it.row0; chunk < it.row1; chunk += TABLE) {
     const int rows = min(it.row1 - chunk, TABLE), stages = (rows + SR - 1) / SR;
     if (chunk > it.row0) __syncthreads();  // (the table has been read)
+    // (rows behind the last repeat it and add nothing; all tokens are asked for, then all lse)
+    constexpr int TURNS = TABLE / kThreads;
+    QueryRow q[TURNS];
+    float lse[TURNS];
 #pragma unroll
-    for (int i = 0; i < TABLE / kThreads; ++i) {
+    for (int i = 0; i < TURNS; ++i) q[i] = query_row(a, io, it, head, min(chunk + i * kThreads + (int)threadIdx.x, it.row1 - 1));
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) lse[i] = ((const KGLOBAL float*)io.lse)[(int64_t)q[i].token * a.num_q_heads + q[i].qh];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
       const int e = i * kThreads + (int)threadIdx.x, row = chunk + e;
-      if (i * kThreads < rows) {  // (rows behind the last repeat it and add nothing)
-        const QueryRow q = query_row(a, io, it, head, min(row, it.row1 - 1));
-        const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)q.token * a.num_q_heads + q.qh];
-        const int limit = row < it.row1 && lse != -INFINITY ? it.lim0 + q.j * it.lstep : -1;
-        const uint64_t all = __ballot(limit >= it.kv1 - 1);
-        lds.at[e] = (int64_t)q.token * io.q_stride + (int64_t)q.qh * DK;
-        lds.base[e] = lse * kLog2;
-        lds.limit[e] = limit;
-        if ((lane & 15) == 0) lds.whole[e / 16] = ((all >> lane) & 0xffff) == 0xffff;
-      }
+      const int limit = row < it.row1 && lse[i] != -INFINITY ? it.lim0 + q[i].j * it.lstep : -1;
+      const uint64_t all = __ballot(limit >= it.kv1 - 1);
+      lds.at[e] = (int64_t)q[i].token * io.q_stride + (int64_t)q[i].qh * DK;
+      lds.base[e] = lse[i] * kLog2;
+      lds.limit[e] = limit;
+      if ((lane & 15) == 0) lds.whole[e / 16] = ((all >> lane) & 0xffff) == 0xffff;
     }
     if (!keys) {  // (asked for behind the table's loads)
       keys = true;
@@ -300,68 +305,80 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
 }
 
 // ============================================================================
-// At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, a step's keys, their
-// pages' ids and their scores asked for ahead. Bound by reading the keys.
+// At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, a step's keys asked for a
+// step ahead and their pages' ids another one before. Bound by reading the keys. In the walk there is nothing but that:
+// no condition on a load (steps behind the last repeat its last key) and no store, so that each wait is for what is
+// needed alone. The sums go to LDS and are added to the scores at the end, which are asked for at the start.
 // ============================================================================
-template <int DK, int DV, int KT>
-__device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head) {
+template <int DK, int DV, int KT, int KEYS>
+__device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, KLDS float* sums) {
   typedef State<DK, DV, 16> S;
-  constexpr int STEP = kWaves * 16 * KT;
+  constexpr int WIDE = 16 * KT, STEP = kWaves * WIDE, EACH = (KEYS / kWaves + 63) / 64;  // keys of a wave's step, of a step; of a lane at the end
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
-  int t = it.kv0 + wave * 16 * KT;
-  if (t >= it.kv1) return;
+  const int t0 = it.kv0 + wave * WIDE, last = it.kv1 - 1;  // the wave's first key
+  if (t0 > last) return;
   const KGLOBAL uint16_t* keys = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + (int64_t)head * DK;
   struct Tile {
-    int page[KT], place[KT];
-    float old[KT];
     bf16x8 k[KT][S::kKSteps];
   } tile[2];
-  int page[KT], place[KT];  // of the step after the next
-  auto find = [&](int t0) {
+  struct Pages {
+    int page[KT], place[KT];
+  } pages[2];
+  auto find = [&](Pages& w, int t) {
 #pragma unroll
-    for (int x = 0; x < KT; ++x) page[x] = (int)slot_of(a, it.pg, it.slot, min(t0 + 16 * x + n, it.kv1 - 1), place[x]);
+    for (int x = 0; x < KT; ++x) w.page[x] = (int)slot_of(a, it.pg, it.slot, min(t + 16 * x + n, last), w.place[x]);
   };
-  auto load = [&](Tile& w) {
+  auto load = [&](Tile& w, const Pages& at) {
 #pragma unroll
     for (int x = 0; x < KT; ++x) {
-      w.page[x] = page[x];
-      w.place[x] = place[x];
-      const KGLOBAL uint16_t* p = keys + ((int64_t)page[x] * a.page_size + place[x]) * a.row;
+      const KGLOBAL uint16_t* p = keys + ((int64_t)at.page[x] * a.page_size + at.place[x]) * a.row;
 #pragma unroll
       for (int ks = 0; ks < S::kKSteps; ++ks) w.k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
-      w.old[x] = 0.0f;
-      if (io.decay != 0.0f && it.part < 0) w.old[x] = *score_at(a, io, page[x], place[x], head);
     }
   };
-  find(t);
-  load(tile[0]);
-  // the rows
+  find(pages[0], t0);
+  find(pages[1], t0 + STEP);
   const QueryRow r = query_row(a, io, it, head, min(it.row0 + n, it.row1 - 1));
+  QueryRow y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = query_row(a, io, it, head, min(it.row0 + 4 * S::group() + i, it.row1 - 1));
+  // the lane's keys at the end: number e of the wave's
+  auto place_of = [&](int e) { return e / WIDE * STEP + wave * WIDE + e % WIDE; };
+  KGLOBAL float* score[EACH];
+  int page[EACH], place[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) page[i] = (int)slot_of(a, it.pg, it.slot, min(it.kv0 + place_of(i * 64 + lane), last), place[i]);
+  load(tile[0], pages[0]);
+  float old[EACH], base[4];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    score[i] = score_at(a, io, page[i], place[i], head);
+    old[i] = *score[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) base[i] = ((const KGLOBAL float*)io.lse)[(int64_t)y[i].token * a.num_q_heads + y[i].qh];
+  // the rows
   const KGLOBAL uint16_t* qp = (const KGLOBAL uint16_t*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * DK;
   bf16x8 q[S::kKSteps];
+  if (io.q_vec) {
 #pragma unroll
-  for (int ks = 0; ks < S::kKSteps; ++ks) {
-    u32x4 w;
-    if (io.q_vec) {
-      w = *(const KGLOBAL u32x4*)(qp + S::k_column(ks));
-    } else {
+    for (int ks = 0; ks < S::kKSteps; ++ks) q[ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(qp + S::k_column(ks)));
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < S::kKSteps; ++ks) {
+      u32x4 w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = (uint32_t)qp[S::k_column(ks) + 2 * e] | ((uint32_t)qp[S::k_column(ks) + 2 * e + 1] << 16);
+      q[ks] = __builtin_bit_cast(bf16x8, w);
     }
-    q[ks] = __builtin_bit_cast(bf16x8, w);
   }
-  float base[4];
   int limit[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = it.row0 + 4 * S::group() + i;
-    const QueryRow y = query_row(a, io, it, head, min(row, it.row1 - 1));
-    const float lse = ((const KGLOBAL float*)io.lse)[(int64_t)y.token * a.num_q_heads + y.qh];
-    base[i] = lse * kLog2;
-    limit[i] = row < it.row1 && lse != -INFINITY ? it.lim0 + y.j * it.lstep : -1;
+    limit[i] = it.row0 + 4 * S::group() + i < it.row1 && base[i] != -INFINITY ? it.lim0 + y[i].j * it.lstep : -1;
+    base[i] *= kLog2;
   }
-  find(t + STEP);
-  auto work = [&](const Tile& w) {
+  auto work = [&](const Tile& w, int t) {
 #pragma unroll
     for (int x = 0; x < KT; ++x) {
       typename S::Acc s = (typename S::Acc)(0.0f), s1 = s;  // (two chains of products)
@@ -378,26 +395,31 @@ __device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, c
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], io.scale2, -base[i]));
         sum += key <= limit[i] ? e : 0.0f;
       }
-      sum = row_sum<16>(sum);
-      if (lane >= 16 || key >= it.kv1) continue;
-      if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + key] = sum;
-      else *score_at(a, io, w.page[x], w.place[x], head) = io.decay == 0.0f || key >= it.fresh ? sum : io.decay * w.old[x] + sum;
+      sums[key - it.kv0] = row_sum<16>(sum);  // (four lanes the same; places behind the last key are there)
     }
   };
+  const int steps = (last - t0) / STEP + 1;
 #pragma nounroll
-  for (;;) {
-    if (t + STEP < it.kv1) {
-      load(tile[1]);
-      find(t + 2 * STEP);
-    }
-    work(tile[0]);
-    if ((t += STEP) >= it.kv1) break;
-    if (t + STEP < it.kv1) {
-      load(tile[0]);
-      find(t + 2 * STEP);
-    }
-    work(tile[1]);
-    if ((t += STEP) >= it.kv1) break;
+  for (int s = 0; s + 1 < steps; s += 2) {
+    const int t = t0 + s * STEP;
+    find(pages[0], t + 2 * STEP);
+    __builtin_amdgcn_sched_barrier(0);
+    load(tile[1], pages[1]);
+    work(tile[0], t);
+    find(pages[1], t + 3 * STEP);
+    __builtin_amdgcn_sched_barrier(0);
+    load(tile[0], pages[0]);
+    work(tile[1], t + STEP);
+  }
+  if (steps & 1) work(tile[0], t0 + (steps - 1) * STEP);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave reads its own sums alone)
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = i * 64 + lane, t = it.kv0 + place_of(e);
+    if (e >= KEYS / kWaves || t > last) continue;
+    const float sum = sums[t - it.kv0];
+    if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = sum;
+    else *score[i] = io.decay == 0.0f || t >= it.fresh ? sum : io.decay * old[i] + sum;
   }
 }
 
@@ -406,8 +428,13 @@ __global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo 
   __shared__ Stages<DK, SR, NB, TABLE> lds;
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const WeighItem it = a.weigh[item];
-  if (it.row1 - it.row0 <= kFewRows) few_rows<DK, DV, FEW>(a, io, it, head);
-  else many_rows<DK, DV, KT, SR, NB, TABLE>(a, io, it, head, lds);
+  constexpr int KEYS = weigh_keys_of_few(DK == DV ? ATTEND_HEADS : ATTEND_LATENT);
+  static_assert(sizeof(lds) >= KEYS * 4 && KEYS % (kWaves * 16 * FEW) == 0, "sums of all keys, whole steps");
+  if (it.row1 - it.row0 > kFewRows) {
+    many_rows<DK, DV, KT, SR, NB, TABLE>(a, io, it, head, lds);
+    __builtin_amdgcn_endpgm();  // (joined by a branch, the other way would wait for all its loads at once, as this one's go to LDS)
+  }
+  few_rows<DK, DV, FEW, KEYS>(a, io, it, head, (KLDS float*)(float*)&lds);
 }
 
 // Sums of ranges of rows, joined in their order: a thread a key and head. A range that ends before the first row
