@@ -149,7 +149,7 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
 // and 143 us, as tiles of more rows 147; MLA, 32 requests, 16 heads, 4 layers: 64, 128 and 256 keys 88, 89 and 103.)
 constexpr int kFewRows = 16;
 constexpr int weigh_keys(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 256; }
-constexpr int weigh_keys_of_few(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 1024; }
+constexpr int weigh_keys_of_few(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 512; }
 hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_t q_stride, const float* lse, float* scores, float scale,
                              float decay, hipStream_t stream);
 

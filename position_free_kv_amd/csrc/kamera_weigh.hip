@@ -305,59 +305,47 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
 }
 
 // ============================================================================
-// At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, a step's keys asked for a
-// step ahead and their pages' ids another one before. Bound by reading the keys. In the walk there is nothing but that:
-// no condition on a load (steps behind the last repeat its last key) and no store, so that each wait is for what is
-// needed alone. The sums go to LDS and are added to the scores at the end, which are asked for at the start.
+// At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, which go straight to LDS in
+// a ring of its own of NB stages. Bound by reading the keys. In the walk there is nothing but that, no other load and
+// no store, so that each wait is for one stage: where the keys lie is put into a table first, the sums go to LDS and
+// are added to the scores at the end, which are asked for at the start. (Keys read into the lanes that multiply them
+// come in 16 bytes a lane and row: 64 requests, 32 + 8 heads, 4.7 TB/s for long tables of their own, by way of LDS FILL.)
 // ============================================================================
-template <int DK, int DV, int KT, int KEYS>
-__device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, KLDS float* sums) {
+template <int DK, int KT, int KEYS, int NB>
+struct Walk {
+  static constexpr int kWide = 16 * KT, kMine = KEYS / kWaves, kStage = kWide * 2 * DK;  // keys of a wave's step, of a wave; bytes of a stage
+  static_assert(kMine % kWide == 0 && (NB > 1 || kMine == kWide), "whole steps, a ring of two where there are more than one");
+  __align__(1024) char stage[kWaves][NB][kStage];
+  uint32_t row[kWaves][kMine];  // of the pool
+  float sum[kWaves][kMine];
+};
+
+template <int DK, int DV, int KT, int KEYS, int NB>
+__device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, const WeighItem& it, int head, Walk<DK, KT, KEYS, NB>& lds) {
   typedef State<DK, DV, 16> S;
-  constexpr int WIDE = 16 * KT, STEP = kWaves * WIDE, EACH = (KEYS / kWaves + 63) / 64;  // keys of a wave's step, of a step; of a lane at the end
+  typedef Walk<DK, KT, KEYS, NB> W;
+  constexpr int WIDE = W::kWide, STEP = kWaves * WIDE, MINE = W::kMine, EACH = (MINE + 63) / 64;
+  constexpr int LPR = S::kKeyRow / 16 < 64 ? S::kKeyRow / 16 : 64, RPI = 64 / LPR, ROWS = WIDE / RPI, BANDS = S::kRestRow ? WIDE / 8 : 0, LOADS = ROWS + BANDS;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
-  const int t0 = it.kv0 + wave * WIDE, last = it.kv1 - 1;  // the wave's first key
-  if (t0 > last) return;
+  const int last = it.kv1 - 1, first = it.kv0 + wave * WIDE;  // the wave's first key
+  if (first > last) return;
   const KGLOBAL uint16_t* keys = (const KGLOBAL uint16_t*)a.k_pool + io.layer0 + (int64_t)head * DK;
-  struct Tile {
-    bf16x8 k[KT][S::kKSteps];
-  } tile[2];
-  struct Pages {
-    int page[KT], place[KT];
-  } pages[2];
-  auto find = [&](Pages& w, int t) {
+  KLDS char* ring = (KLDS char*)lds.stage[wave];
+  KLDS uint32_t* rows = (KLDS uint32_t*)lds.row[wave];
+  KLDS float* sums = (KLDS float*)lds.sum[wave];
+  // the wave's key number e
+  auto key_of = [&](int e) { return first + e / WIDE * STEP + e % WIDE; };
+  int page[EACH], place[EACH];
 #pragma unroll
-    for (int x = 0; x < KT; ++x) w.page[x] = (int)slot_of(a, it.pg, it.slot, min(t + 16 * x + n, last), w.place[x]);
-  };
-  auto load = [&](Tile& w, const Pages& at) {
-#pragma unroll
-    for (int x = 0; x < KT; ++x) {
-      const KGLOBAL uint16_t* p = keys + ((int64_t)at.page[x] * a.page_size + at.place[x]) * a.row;
-#pragma unroll
-      for (int ks = 0; ks < S::kKSteps; ++ks) w.k[x][ks] = __builtin_bit_cast(bf16x8, *(const KGLOBAL u32x4*)(p + S::k_column(ks)));
-    }
-  };
-  find(pages[0], t0);
-  find(pages[1], t0 + STEP);
+  for (int i = 0; i < EACH; ++i) page[i] = (int)slot_of(a, it.pg, it.slot, min(key_of(i * 64 + lane), last), place[i]);
+  // the rows
   const QueryRow r = query_row(a, io, it, head, min(it.row0 + n, it.row1 - 1));
   QueryRow y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = query_row(a, io, it, head, min(it.row0 + 4 * S::group() + i, it.row1 - 1));
-  // the lane's keys at the end: number e of the wave's
-  auto place_of = [&](int e) { return e / WIDE * STEP + wave * WIDE + e % WIDE; };
-  KGLOBAL float* score[EACH];
-  int page[EACH], place[EACH];
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) page[i] = (int)slot_of(a, it.pg, it.slot, min(it.kv0 + place_of(i * 64 + lane), last), place[i]);
-  load(tile[0], pages[0]);
-  float old[EACH], base[4];
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    score[i] = score_at(a, io, page[i], place[i], head);
-    old[i] = *score[i];
-  }
+  float base[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) base[i] = ((const KGLOBAL float*)io.lse)[(int64_t)y[i].token * a.num_q_heads + y[i].qh];
-  // the rows
   const KGLOBAL uint16_t* qp = (const KGLOBAL uint16_t*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * DK;
   bf16x8 q[S::kKSteps];
   if (io.q_vec) {
@@ -372,69 +360,96 @@ __device__ __forceinline__ void few_rows(const StepArgs& a, const WeighIo& io, c
       q[ks] = __builtin_bit_cast(bf16x8, w);
     }
   }
+  KGLOBAL float* score[EACH];
+  float old[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    if (EACH * 64 == MINE || lane < MINE) rows[i * 64 + lane] = (uint32_t)(page[i] * a.page_size + place[i]);  // (below 2^31)
+    score[i] = score_at(a, io, page[i], place[i], head);
+    old[i] = *score[i];
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave reads its own entries alone)
+  auto load = [&](int s) {
+    KLDS char* stage = ring + s % NB * W::kStage;
+    uint32_t at[LOADS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) at[i] = rows[s * WIDE + i * RPI + lane / LPR];
+#pragma unroll
+    for (int i = 0; i < BANDS; ++i) at[ROWS + i] = rows[s * WIDE + i * 8 + lane / 8];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int piece = (lane & (LPR - 1)) ^ swz<16, S::kKeyRow>(i * RPI + lane / LPR);
+      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(keys + (int64_t)at[i] * a.row + piece * 8), (KLDS void*)(stage + i * RPI * S::kKeyRow), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < BANDS; ++i) {
+      const int piece = (lane & 7) ^ swz<16, 128>(i * 8 + lane / 8);
+      __builtin_amdgcn_global_load_lds((const KGLOBAL void*)(keys + (int64_t)at[ROWS + i] * a.row + DV + piece * 8), (KLDS void*)(stage + WIDE * S::kKeyRow + i * 8 * 128), 16, 0, 0);
+    }
+  };
+  const int steps = (last - first) / STEP + 1;
+  load(0);
+  for (int s = 1; s < NB - 1 && s < steps; ++s) load(s);
+  // the rows are waited for here: a first use inside the loop would wait for all loads in each turn
   int limit[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     limit[i] = it.row0 + 4 * S::group() + i < it.row1 && base[i] != -INFINITY ? it.lim0 + y[i].j * it.lstep : -1;
     base[i] *= kLog2;
   }
-  auto work = [&](const Tile& w, int t) {
+#pragma unroll
+  for (int ks = 0; ks < S::kKSteps; ++ks) {
+    u32x4 w = __builtin_bit_cast(u32x4, q[ks]);
+    asm volatile("" : "+v"(w));
+    q[ks] = __builtin_bit_cast(bf16x8, w);
+  }
+#pragma nounroll
+  for (int s = 0; s < steps; ++s) {
+    // stage s is here, those after it (NB - 2 of them, unless the last ones are on their way) need not be
+    if (NB > 2 && s + NB - 2 < steps) wait_but<LOADS * (NB > 2 ? NB - 2 : 0)>();
+    else wait_but<0>();
+    asm volatile("" ::: "memory");
+    if (NB > 1 && s + NB - 1 < steps) load(s + NB - 1);
+    const KLDS char* at = ring + s % NB * W::kStage;
 #pragma unroll
     for (int x = 0; x < KT; ++x) {
-      typename S::Acc s = (typename S::Acc)(0.0f), s1 = s;  // (two chains of products)
+      typename S::Acc c = (typename S::Acc)(0.0f), c1 = c;  // (two chains of products)
 #pragma unroll
       for (int ks = 0; ks < S::kKSteps; ks += 2) {
-        s = S::mfma(q[ks], w.k[x][ks], s);
-        s1 = S::mfma(q[ks + 1], w.k[x][ks + 1], s1);
+        c = S::mfma(q[ks], S::k_operand(at + x * 16 * S::kKeyRow, at + WIDE * S::kKeyRow + x * 16 * S::kRestRow, 0, ks), c);
+        c1 = S::mfma(q[ks + 1], S::k_operand(at + x * 16 * S::kKeyRow, at + WIDE * S::kKeyRow + x * 16 * S::kRestRow, 0, ks + 1), c1);
       }
-      s += s1;
-      const int key = t + 16 * x + n;
+      c += c1;
+      const int key = first + s * STEP + x * 16 + n;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], io.scale2, -base[i]));
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(c[i], io.scale2, -base[i]));
         sum += key <= limit[i] ? e : 0.0f;
       }
-      sums[key - it.kv0] = row_sum<16>(sum);  // (four lanes the same; places behind the last key are there)
+      sums[s * WIDE + x * 16 + n] = row_sum<16>(sum);  // (four lanes the same)
     }
-  };
-  const int steps = (last - t0) / STEP + 1;
-#pragma nounroll
-  for (int s = 0; s + 1 < steps; s += 2) {
-    const int t = t0 + s * STEP;
-    find(pages[0], t + 2 * STEP);
-    __builtin_amdgcn_sched_barrier(0);
-    load(tile[1], pages[1]);
-    work(tile[0], t);
-    find(pages[1], t + 3 * STEP);
-    __builtin_amdgcn_sched_barrier(0);
-    load(tile[0], pages[0]);
-    work(tile[1], t + STEP);
   }
-  if (steps & 1) work(tile[0], t0 + (steps - 1) * STEP);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave reads its own sums alone)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
-    const int e = i * 64 + lane, t = it.kv0 + place_of(e);
-    if (e >= KEYS / kWaves || t > last) continue;
-    const float sum = sums[t - it.kv0];
+    const int e = i * 64 + lane, t = key_of(e);
+    if ((EACH * 64 != MINE && e >= MINE) || t > last) continue;
+    const float sum = sums[e];
     if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = sum;
     else *score[i] = io.decay == 0.0f || t >= it.fresh ? sum : io.decay * old[i] + sum;
   }
 }
 
-template <int DK, int DV, int KT, int SR, int NB, int TABLE, int FEW>
+template <int DK, int DV, int KT, int SR, int NB, int TABLE, int FEW_KT, int FEW_NB>
 __global__ __launch_bounds__(kThreads, 2) void weigh_matrix(StepArgs a, WeighIo io) {
-  __shared__ Stages<DK, SR, NB, TABLE> lds;
+  typedef Stages<DK, SR, NB, TABLE> Many;
+  typedef Walk<DK, FEW_KT, weigh_keys_of_few(DK == DV ? ATTEND_HEADS : ATTEND_LATENT), FEW_NB> Few;
+  __shared__ __align__(1024) char lds[sizeof(Many) > sizeof(Few) ? sizeof(Many) : sizeof(Few)];
   const int item = blockIdx.x / a.heads, head = blockIdx.x - item * a.heads;
   const WeighItem it = a.weigh[item];
-  constexpr int KEYS = weigh_keys_of_few(DK == DV ? ATTEND_HEADS : ATTEND_LATENT);
-  static_assert(sizeof(lds) >= KEYS * 4 && KEYS % (kWaves * 16 * FEW) == 0, "sums of all keys, whole steps");
-  if (it.row1 - it.row0 > kFewRows) {
-    many_rows<DK, DV, KT, SR, NB, TABLE>(a, io, it, head, lds);
-    __builtin_amdgcn_endpgm();  // (joined by a branch, the other way would wait for all its loads at once, as this one's go to LDS)
-  }
-  few_rows<DK, DV, FEW, KEYS>(a, io, it, head, (KLDS float*)(float*)&lds);
+  if (it.row1 - it.row0 <= kFewRows) few_rows<DK, DV>(a, io, it, head, *(Few*)lds);
+  else many_rows<DK, DV, KT, SR, NB, TABLE>(a, io, it, head, *(Many*)lds);
 }
 
 // Sums of ranges of rows, joined in their order: a thread a key and head. A range that ends before the first row
@@ -479,9 +494,9 @@ hipError_t launch_step_weigh(const StepArgs& a, int layer, const void* q, int64_
     e = a.dtype == KAMERA_BF16 ? plain<uint16_t>(a, io, stream) : plain<float>(a, io, stream);
   } else {
     const dim3 g((unsigned)((int64_t)a.num_weigh * a.heads)), b(kThreads);
-    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 16, 4, 256, 1>), g, b, 0, stream, a, io);
-    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, 2, 1024, 2>), g, b, 0, stream, a, io);
-    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, 2, 1024, 4>), g, b, 0, stream, a, io);
+    if (a.weigh_kernel == ATTEND_LATENT) hipLaunchKernelGGL((weigh_matrix<576, 512, 1, 16, 4, 256, 1, 1>), g, b, 0, stream, a, io);
+    else if (a.dk == 128) hipLaunchKernelGGL((weigh_matrix<128, 128, 4, 64, 2, 1024, 1, 3>), g, b, 0, stream, a, io);
+    else hipLaunchKernelGGL((weigh_matrix<64, 64, 4, 64, 2, 1024, 2, 3>), g, b, 0, stream, a, io);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.num_weigh_join == 0) return e;
