@@ -227,11 +227,11 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   const uint16_t* vp = a.v_pool + io.layer0 + head * 2 * D;
   const int first = wave * N, last = it.kv1 - 1;
   PairRows<D, TS, N, ROWS> rows;
-  if (it.kv1 > it.kv0) {
-    rows.find(a, it.run, it.kv0, first, last);
-    rows.load(a, kp, vp, lds, first);
-  }
-  const Lane r = lane_row(a, it, head, it.row0 + 2 * S::row() + map);
+  const bool any = it.kv1 > it.kv0;
+  if (any) rows.find(a, it.run, it.kv0, first, last);
+  Lane r = lane_row(a, it, head, it.row0 + 2 * S::row() + map);
+  asm volatile("" : "+v"(r.token));  // (here: behind the stage's loads it would wait for them, and the queries after it)
+  if (any) rows.load(a, kp, vp, lds, first);
   const int end_min = __builtin_amdgcn_readfirstlane(r.end), end_max = __builtin_amdgcn_readlane(r.end, ROWS - 1);
   bf16x8 q[S::kKSteps];
   S::load_q(io, r, q);
