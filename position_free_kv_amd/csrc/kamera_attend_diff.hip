@@ -15,6 +15,8 @@
 // GFLOP in 488 us), 78% of a large library product's rate; bound by the products and the softmax between them, which two
 // waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones, 32 + 8 heads: 66 us and
 // 12.6 in the join; bound by the own tokens' pages and by what a workgroup does before its first key (about 6 us).
+#include <type_traits>
+
 #include "kamera_attend.h"
 
 namespace kamera {
@@ -76,16 +78,19 @@ __device__ __forceinline__ float widened(T x) {
   else return x;
 }
 
-// exp(q1 . k1) - exp(q2 . k2) + lambda_init, by one wave
-__device__ __forceinline__ float lambda_of(const StepArgs& a, const kamera_differential& diff) {
-  if (!diff.lambdas) return diff.lambda_init;
+// exp(q1 . k1) - exp(q2 . k2) + lambda_init, by one wave: its lanes' shares of the products, and what they make
+__device__ __forceinline__ float2 lambda_products(const StepArgs& a, const kamera_differential& diff) {
+  float2 d = make_float2(0.0f, 0.0f);
+  if (!diff.lambdas) return d;
   const KGLOBAL float* p = (const KGLOBAL float*)diff.lambdas;
-  float d0 = 0.0f, d1 = 0.0f;
   for (int c = (int)threadIdx.x & 63; c < a.dk; c += kWaveSize) {
-    d0 += p[c] * p[a.dk + c];
-    d1 += p[2 * a.dk + c] * p[3 * a.dk + c];
+    d.x += p[c] * p[a.dk + c];
+    d.y += p[2 * a.dk + c] * p[3 * a.dk + c];
   }
-  return expf(wave_sum(d0)) - expf(wave_sum(d1)) + diff.lambda_init;
+  return d;
+}
+__device__ __forceinline__ float lambda_from(const kamera_differential& diff, float2 d) {
+  return diff.lambdas ? expf(wave_sum(d.x)) - expf(wave_sum(d.y)) + diff.lambda_init : diff.lambda_init;
 }
 // What a row x of `dv` columns is multiplied with, besides the weights, given its sum of squares.
 __device__ __forceinline__ float norm_scale(const kamera_differential& diff, float squares, int dv) {
@@ -208,7 +213,7 @@ __device__ __forceinline__ void wide_tile(const StepArgs& a, const AttendIo& io,
   asm volatile("" : "+v"(tid));
   const Lane w = lane_row(a, it, head, it.row0 + (tid >> 7) * 64 + 2 * (tid & 31) + ((tid >> 6) & 1));
   static_assert(2 * 64 * S::kBlocks * S::kScores * 4 <= kLds, "two waves' results fit in LDS");
-  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_of(a, diff), (f32x4*)(KLDS f32x4*)(lds + (wave >> 1) * (kLds / 2)), false);
+  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_from(diff, lambda_products(a, diff)), (f32x4*)(KLDS f32x4*)(lds + (wave >> 1) * (kLds / 2)), false);
   else put_state(a, io, it, head, w, st, l);
 }
 
@@ -254,7 +259,7 @@ __device__ __forceinline__ void narrow_tile(const StepArgs& a, const AttendIo& i
   int tid = threadIdx.x;  // (as in the wide tile)
   asm volatile("" : "+v"(tid));
   const Lane w = lane_row(a, it, head, it.row0 + 2 * (tid & (ROWS - 1)) + ((tid >> 6) & 1));
-  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_of(a, diff), (f32x4*)(KLDS f32x4*)lds, part == 1);
+  if (it.run.direct) put_pairs(a, io, diff, w, st, l, map, lambda_from(diff, lambda_products(a, diff)), (f32x4*)(KLDS f32x4*)lds, part == 1);
   else if (part == 0) put_state(a, io, it, head, w, st, l);
 }
 
@@ -274,8 +279,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo 
 // Join of partial rows: an output row's two maps lie in neighbouring partial rows, 2 dv numbers side by side, which
 // the threads share in 16-byte pieces. WPR waves a row; parts are taken in a fixed order. The maps' normalised
 // rows meet in LDS, and the norm follows. All parts' statistics are read at once, then their rows, 8 of a wave at a
-// time: bound by two dependent reads when rows are few, by the partial rows' bytes (written and read: 2 dv fp32 a
-// query pair and part) when they are many. 64 tokens of 16 pairs in 18 parts: 12.6 us.
+// time and none under a condition (a load under one is waited for before the next: 4 layers of 2 requests over 2000
+// tokens 81 us that way, 69 this way). Bound by three dependent reads when rows are few, by the partial rows' bytes
+// (written and read: 2 dv fp32 a query pair and part) when they are many. 64 tokens of 16 pairs in 18 parts: 12.6 us.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
 
@@ -304,21 +310,22 @@ __device__ __forceinline__ float2 over_waves(float2 x, float2 (&red)[2][WPR]) {
 }
 
 // PIECES: 16-byte pieces of the two rows that a lane takes
-constexpr int join_waves_of(int wpr) { return wpr > kWaves ? wpr : kWaves; }  // waves of a workgroup
 template <typename T, int WPR, int PIECES>
-__global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
-  constexpr int ROWS = join_waves_of(WPR) / WPR;
+__global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, kamera_differential diff) {
+  constexpr int ROWS = kWaves / WPR;
   __shared__ float2 weight[ROWS][WPR == 1 ? kWaveSize : kJoinParts];
   __shared__ float2 red[ROWS][2][WPR];
-  __shared__ f32x4 held[join_waves_of(WPR)][PIECES * kWaveSize];
+  __shared__ f32x4 held[kWaves][PIECES * kWaveSize];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = wave / WPR, seat = wave % WPR;
   const int outs = a.num_q_heads / 2;
   const int64_t task = (int64_t)(blockIdx.y * (uint32_t)kGridRow + blockIdx.x) * ROWS + sub;
   const bool live = task < (int64_t)a.num_merge * outs;
   const int64_t i = live ? task / outs : 0;
   const int oh = (int)(task % outs), head = 2 * oh / a.group, g = 2 * oh % a.group;
+  const int quads = a.dv / 4;  // of a map's row
   const MergeToken mt = a.merge[i];
-  const int n = mt.splits[0] + mt.splits[1];
+  const float2 products = lambda_products(a, diff);
+  const int n = mt.splits[0] + mt.splits[1];  // (one at least)
   auto row = [&](int k) {  // of the first map; the second's is the next
     const int s = k >= mt.splits[0];
     return mt.part[s] + ((int64_t)(s ? k - mt.splits[0] : k) * a.heads + head) * mt.rows[s] + mt.row0[s] + g;
@@ -329,13 +336,24 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
   const KGLOBAL f32x4* stats = (const KGLOBAL f32x4*)a.part_ml;  // (rows of the first map are even)
   f32x4 s[PER];
   float2 top = make_float2(-INFINITY, -INFINITY), sum = make_float2(0.0f, 0.0f);
+  // (places behind the last part read it again: a load under a condition is waited for before the next one)
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    s[e] = (f32x4){-INFINITY, 0.0f, -INFINITY, 0.0f};
-    if (e * TPR + tid < n) s[e] = stats[row(e * TPR + tid) >> 1];
+  for (int e = 0; e < PER; ++e) s[e] = stats[row(min(e * TPR + tid, n - 1)) >> 1];
+  const T* weights = (diff.flags & KAMERA_DIFF_NORM) ? (const T*)diff.norm_weight : nullptr;
+  float gain[(PIECES + 1) / 2][4];
+#pragma unroll
+  for (int j = 0; j < (PIECES + 1) / 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gain[j][e] = 1.0f;
+  if (weights) {
+#pragma unroll
+    for (int j = 0; j < (PIECES + 1) / 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) gain[j][e] = widened<T>(((const KGLOBAL T*)weights)[4 * min(j * kWaveSize + lane, quads - 1) + e]);
   }
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
+    if (e * TPR + tid >= n) s[e] = (f32x4){-INFINITY, 0.0f, -INFINITY, 0.0f};
     if (s[e][1] != 0.0f) top.x = fmaxf(top.x, s[e][0]);
     if (s[e][3] != 0.0f) top.y = fmaxf(top.y, s[e][2]);
   }
@@ -349,27 +367,40 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
     if (e * TPR + tid < n) weight[sub][e * TPR + tid] = w;
   }
   sum = over_waves<WPR, false>(make_float2(wave_sum(sum.x), wave_sum(sum.y)), red[sub]);
-  const float lambda = lambda_of(a, diff);
+  const float lambda = lambda_from(diff, products);
   __syncthreads();
-  const int quads = a.dv / 4;  // of a map's row
   const KGLOBAL f32x4* parts = (const KGLOBAL f32x4*)a.part_o;
   f32x4 o[PIECES];
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) o[j] = (f32x4)(0.0f);
-#pragma unroll 8
-  for (int k = seat; k < n; k += WPR) {
-    const float2 w = weight[sub][k];
-    const KGLOBAL f32x4* p = parts + row(k) * quads;
+  // COUNT parts from k on: their rows are asked for together, then weighed
+  int k = seat;
+  auto take = [&](auto count) {
+    constexpr int COUNT = decltype(count)::value;
+    f32x4 x[COUNT][PIECES];
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) {
-      const int f = j * kWaveSize + lane;
-      if (f >= 2 * quads) continue;
-      const f32x4 x = p[f];
-      const float wf = f < quads ? w.x : w.y;
+    for (int i = 0; i < COUNT; ++i) {
+      const KGLOBAL f32x4* p = parts + row(k + i * WPR) * quads;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] += x[e] * wf;  // (an empty part's row is 0)
+      for (int j = 0; j < PIECES; ++j) x[i][j] = p[min(j * kWaveSize + lane, 2 * quads - 1)];
     }
-  }
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const float2 w = weight[sub][k + i * WPR];
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        const float wf = j * kWaveSize + lane < quads ? w.x : w.y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] += x[i][j][e] * wf;  // (an empty part's row is 0)
+      }
+    }
+    k += COUNT * WPR;
+  };
+  constexpr int MOST = PIECES <= 2 ? 8 : 16 / PIECES;
+  while (k + (MOST - 1) * WPR < n) take(std::integral_constant<int, MOST>());
+  if (MOST > 4 && k + 3 * WPR < n) take(std::integral_constant<int, 4>());
+  if (MOST > 2 && k + WPR < n) take(std::integral_constant<int, 2>());
+  if (k < n) take(std::integral_constant<int, 1>());
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) held[wave][j * kWaveSize + lane] = o[j];
   __syncthreads();
@@ -400,14 +431,13 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
   }
   const float scale = norm_scale(diff, wave_sum(square), a.dv);
   T* out = (T*)io.out + (int64_t)mt.token * io.out_stride + (int64_t)oh * a.dv;
-  const T* weights = (diff.flags & KAMERA_DIFF_NORM) ? (const T*)diff.norm_weight : nullptr;
 #pragma unroll
   for (int j = 0; j < (PIECES + 1) / 2; ++j) {
     const int c = j * kWaveSize + lane;
     if (c >= quads) continue;
     float y[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = x[j][e] * scale * (weights ? widened<T>(weights[4 * c + e]) : 1.0f);
+    for (int e = 0; e < 4; ++e) y[e] = x[j][e] * scale * gain[j][e];
     if (sizeof(T) == 2 && io.out_vec) {
       *(KGLOBAL u32x2*)(KGLOBAL void*)(out + 4 * c) = (u32x2){pack2(y[0], y[1]), pack2(y[2], y[3])};
     } else {
@@ -424,14 +454,9 @@ __global__ __launch_bounds__(kWaveSize * join_waves_of(WPR)) void diff_join(Step
 template <typename T, int WPR>
 hipError_t join(const StepArgs& a, const AttendIo& io, const kamera_differential& diff, hipStream_t stream) {
   const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
-  constexpr int W = join_waves_of(WPR), ROWS = W / WPR;
-  const dim3 g = grid_of((rows + ROWS - 1) / ROWS), b(W * kWaveSize);
+  constexpr int ROWS = kWaves / WPR;
+  const dim3 g = grid_of((rows + ROWS - 1) / ROWS), b(kThreads);
   const int pieces = (a.dv / 2 + kWaveSize - 1) / kWaveSize;
-  if constexpr (WPR > kWaves) {
-    if (pieces <= 1) hipLaunchKernelGGL((diff_join<T, WPR, 1>), g, b, 0, stream, a, io, diff);
-    else hipLaunchKernelGGL((diff_join<T, WPR, 2>), g, b, 0, stream, a, io, diff);
-    return hipGetLastError();
-  }
   if (pieces <= 1) hipLaunchKernelGGL((diff_join<T, WPR, 1>), g, b, 0, stream, a, io, diff);
   else if (pieces <= 2) hipLaunchKernelGGL((diff_join<T, WPR, 2>), g, b, 0, stream, a, io, diff);
   else if (pieces <= 4) hipLaunchKernelGGL((diff_join<T, WPR, 4>), g, b, 0, stream, a, io, diff);
@@ -459,14 +484,12 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
   }
   if (e != hipSuccess || a.num_merge == 0) return e;
   const int64_t rows = (int64_t)a.num_merge * (a.num_q_heads / 2);
-  // Few rows of many parts are shared by 4 or 16 waves each. (4 layers, 32 + 8 heads of 128, whole calls in us with 1, 4
-  // and 16 waves a row: 32 rows 102, 81 and 78, with 64 parts 200, 201 and 147; 128 rows 119, 98 and 95; 512 rows 209, 151
-  // and 164; 1024 rows 240, 206 and 260; 2048 rows 300, 306 and 399. 8 parts and fewer: alike. 16 waves hold rows in
-  // LDS that is made for 256 columns.)
-  const bool wide = a.max_parts > kWaveSize || (a.max_parts > 8 && rows < 2048), very = a.max_parts > 8 && rows < 512 && a.dv <= 256;
-  if (a.dtype == KAMERA_BF16)
-    return very ? join<uint16_t, 16>(a, io, diff, stream) : wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
-  return very ? join<float, 16>(a, io, diff, stream) : wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);
+  // Few rows are shared by 4 waves each. (4 layers, 32 + 8 heads of 128, whole calls in us with 1 and 4 waves a row: 32
+  // rows 71 and 66, with 18 parts 86 and 69; 512 rows 175 and 165; 1024 rows 209 and 216; 2048 rows 298 and 320. 16
+  // waves: 32 rows 75, 512 rows 189.)
+  const bool wide = a.max_parts > kWaveSize || rows < 1024;
+  if (a.dtype == KAMERA_BF16) return wide ? join<uint16_t, kWaves>(a, io, diff, stream) : join<uint16_t, 1>(a, io, diff, stream);
+  return wide ? join<float, kWaves>(a, io, diff, stream) : join<float, 1>(a, io, diff, stream);
 }
 
 }  // namespace kamera
