@@ -466,11 +466,21 @@ __global__ __launch_bounds__(kThreads) void weigh_join(StepArgs a, WeighIo io) {
   const int kv0 = t / j.tile * j.tile;
   const int64_t row0 = j.lstep && kv0 > j.lim0 ? (int64_t)(kv0 - j.lim0) * io.rows_of_token : 0;
   const KGLOBAL float* p = (const KGLOBAL float*)a.weigh_part + j.part + (int64_t)head * j.kv + t;
-  float sum = 0.0f;
-  for (int s = (int)(row0 / j.rows); s < j.splits; ++s) sum += p[(int64_t)s * a.heads * j.kv];
   int place;
   const int64_t page = slot_of(a, j.pg, j.slot, t, place);
-  add_score(a, io, page, place, head, sum, t >= j.fresh);
+  KGLOBAL float* score = score_at(a, io, page, place, head);
+  const float old = *score;
+  const int64_t stride = (int64_t)a.heads * j.kv;
+  float sum = 0.0f;
+  constexpr int kAtOnce = 8;
+  for (int s = (int)(row0 / j.rows); s < j.splits; s += kAtOnce) {  // (places behind the last range read it again)
+    float x[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) x[i] = p[min(s + i, j.splits - 1) * stride];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) sum += s + i < j.splits ? x[i] : 0.0f;
+  }
+  *score = io.decay == 0.0f || t >= j.fresh ? sum : io.decay * old + sum;
 }
 
 template <typename T>
