@@ -428,8 +428,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
 // A run is a segment (a prefix with all its requests' query tokens, or a request's own tokens); an item a
 // tile of its keys and the rows that see any of them. Where that leaves the chip without work for all its
 // workgroups, rows are cut into ranges whose sums are joined (in the order of the ranges).
-// (8 requests with 2481 query tokens over 8192 shared ones, 28 + 4 heads: ranges for 2048 workgroups 228 us, for 512 and
-// 1024 250 to 289. MLA, 32 requests, 16 heads, 4 layers: ranges of at least 64, 128, 192 and 256 rows 112, 85, 96 and 102.)
+// (8 requests with 2481 query tokens over 8192 shared ones, 28 + 4 heads: ranges for 760 workgroups 200 us, for 1536 to 4608
+// 177 to 182. MLA, 32 requests, 16 heads, 4 layers: ranges of at least 64, 128, 192 and 256 rows 112, 85, 96 and 102.)
 constexpr int64_t kWeighSlots = 2048;
 constexpr int64_t weigh_rows(int kernel) { return kernel == ATTEND_LATENT ? 128 : 512; }  // fewest of a range
 void plan_weights(const kamera_layout* L, const kamera_step* s, const Tables& tb, int kernel, Fit fit, Work& w) {

@@ -8,10 +8,11 @@
 // score[t] <- decay * score[t] + sum over rows that see t of exp(scale q . k_t - lse): the attention's lse makes the
 // softmax's sum unnecessary, so that each key needs one pass over the rows and no running maximum. Sums are in fp32.
 //
-// 64 requests of one token over 8192 shared and 49300 own tokens, 32 + 8 heads of 128, a layer: 30 us; bound by reading the
-// own keys (3.9 TB/s). 2481 query tokens over 8192 shared and own tokens, 28 + 4 heads: 181 us for 154 GFLOP, 0.85
-// PFLOP/s; bound by exponentials (4 a lane and product tile of 4 instructions) and the products, which take turns. 32 requests
-// of one token, MLA, 16 heads, a layer: 16 us and 4 in the join; bound by the chain item, page, keys, rows.
+// 64 requests of one token over 8192 shared and 49300 own tokens, 32 + 8 heads of 128, a layer: 27 us; bound by reading the
+// own keys (118 MB, 4.4 TB/s; longer ones 4.8). 2481 query tokens over 8192 shared and own tokens, 28 + 4 heads: 180 us
+// for 154 GFLOP, 0.86 PFLOP/s; bound by the products and the exponentials, which take about the same time and overlap
+// in part (without branches between a stage's tiles: 182). 32 requests of one token, MLA, 16 heads, a layer: 15 us
+// and 4 in the join; bound by dependent reads: item, tokens, lse, query rows.
 #include "kamera_attend.h"
 
 namespace kamera {
@@ -117,7 +118,8 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
 // lays out keys, NB stages in a ring. Lane 16 g + n gets the scores of key n and rows 4 g .. 4 g + 3, takes the
 // row's lse off and adds up the exponentials. Where the rows lie, their lse and what they see is put into a
 // table first, for up to TABLE rows at a time, so that the ring's loads depend on nothing else. (28 + 4 heads as above: two
-// stages of 64 rows 181 us, three 201 to 206: the LDS then holds one workgroup less a CU. MLA, 4 layers: four stages of 16 rows.)
+// stages of 64 rows 181 us, three 201 to 206: the LDS then holds one workgroup less a CU. MLA: four stages of 16 rows, with
+// the table 88 us, without it 91.)
 // ============================================================================
 template <int DK, int SR, int NB, int TABLE>
 struct Stages {
@@ -308,8 +310,9 @@ __device__ __forceinline__ void many_rows(const StepArgs& a, const WeighIo& io, 
 // At most 16 rows: they stay in registers, and each wave walks over 16 KT keys at a time, which go straight to LDS in
 // a ring of its own of NB stages. Bound by reading the keys. In the walk there is nothing but that, no other load and
 // no store, so that each wait is for one stage: where the keys lie is put into a table first, the sums go to LDS and
-// are added to the scores at the end, which are asked for at the start. (Keys read into the lanes that multiply them
-// come in 16 bytes a lane and row: 64 requests, 32 + 8 heads, 4.7 TB/s for long tables of their own, by way of LDS FILL.)
+// are added to the scores at the end, which are asked for at the start. (64 requests, 32 + 8 heads, 4 layers: keys into
+// the lanes that multiply them, 16 bytes a lane and row, with a store and conditions in the walk 131 us, without them
+// 125, by way of LDS 115. Two stages ahead and 3 workgroups a CU 115, three and 2 123.)
 // ============================================================================
 template <int DK, int KT, int KEYS, int NB>
 struct Walk {
