@@ -109,8 +109,10 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
     };
     if constexpr (HELD != 0) {
 #pragma unroll
-      for (int i = 0; i < HELD; ++i)
+      for (int i = 0; i < HELD; ++i) {
+        if (i >= turns) break;
         if (ranked_one(i)) add(rank_of(held[i]));
+      }
     } else {
       for (int t = lo + tid; t < hi; t += kSelect) add(l.rank(a, t));
     }
@@ -168,6 +170,7 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
     uint32_t hits = 0, equals = 0;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
+      if (HELD && i >= turns) break;
       bool hit, tie;
       judge(i, hit, tie);
       hits |= (uint32_t)hit << i;
@@ -193,6 +196,7 @@ __device__ __forceinline__ void select_list(const EvictArgs& a, const List& l, K
     int leaves = n;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
+      if (HELD && i >= turns) break;
       const int t = t0 + (wave * each + i) * kWave + lane;
       const bool hit = hits >> i & 1, tie = equals >> i & 1;
       const uint64_t h = __ballot(hit), e = __ballot(tie);
