@@ -626,3 +626,59 @@ def test_diff_of_more_tiles_than_places():
     themselves, runs that are joined, and a request that is both."""
     c = Case(layers=1, heads=128, kv_heads=8, head_dim=64, prefixes=[300], requests=[(0, 200, 200), (0, 333, 333), (0, 5, 1)])
     eu.check_diff(c, Params(c), scale_of(c))
+
+
+@pytest.mark.parametrize("heads,dim,dtype", [(400, 64, BF16), (300, 128, BF16), (400, 64, F32)])
+def test_more_heads_of_a_pair_than_rows_of_a_tile(heads, dim, dtype):
+    """A token's rows fill several tiles; whole rounds of them do not end between tokens."""
+    c = Case(dtype=dtype, layers=1, heads=heads, kv_heads=2, head_dim=dim, prefixes=[70], requests=[(0, 30, 1), (0, 150, 130), (0, 60, 59), (-1, 9, 9)])
+    eu.check_diff(c, Params(c), scale_of(c))
+    eu.check_weigh(c, scale_of(c), diff=True)
+
+
+@pytest.mark.parametrize("family,heads,kv,dim", [(GQA, 1, 1, 64), (GQA, 1, 1, 128), (GQA, 2, 2, 64), (MLA, 1, 1, 64)])
+def test_weigh_ranges_that_end_in_a_few_rows(family, heads, kv, dim):
+    """4100 rows in ranges of 512 (latent ones: 128) leave a last range of 4, whose sums are joined like the others'."""
+    more = dict(heads=heads, kv_heads=kv, head_dim=dim) if family == GQA else dict(family=MLA, heads=heads, latent=512, rope=dim)
+    c = Case(layers=1, prefixes=[300], requests=[(0, 4100, 4100)], **more)
+    eu.check_weigh(c, scale_of(c))
+
+
+def test_two_callers_at_once():
+    """Threads with a stream, workspaces and pools of their own."""
+    import threading
+    cases = [Case(head_dim=128, heads=8, kv_heads=2, prefixes=[500], requests=[(0, 30 + i, 1) for i in range(9)] + [(0, 200, 150)], seed=i) for i in range(3)]
+    params = [Params(c, seed=i) for i, c in enumerate(cases)]
+    lse = [torch.stack([eu.own_lse(c, layer, scale_of(c)) for layer in range(c.layers)]) for c in cases]
+    caches = [[Cache(seqs=SEQS + [(3000, 1000 + i, 5, 7)], reanchor=True, seed=i) for _ in range(4)] for i in range(3)]
+
+    def work(i, turn, stream):
+        scores = eu.new_scores(cases[i])
+        with torch.cuda.stream(stream):
+            out = eu.attend_diff(cases[i], params[i], scale_of(cases[i]), stream=stream)
+            eu.weigh(cases[i], lse[i], scores, scale_of(cases[i]), 0.5, stream=stream)
+            cache = caches[i][turn]
+            cache.run(stream=stream)
+            stream.synchronize()
+        return (*out, scores, cache.kept, cache.scores_flat, *cache.flat)
+
+    alone = [work(i, 0, torch.cuda.Stream()) for i in range(3)]
+    got, failed = {}, []
+
+    def caller(i, stream):
+        try:
+            for turn in range(1, 4):
+                got[i, turn] = work(i, turn, stream)
+        except BaseException as e:  # (shown by the test's own thread)
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=caller, args=(i, torch.cuda.Stream())) for i in range(3)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for (i, _), results in got.items():
+        assert all(torch.equal(a, b) for a, b in zip(alone[i], results))
