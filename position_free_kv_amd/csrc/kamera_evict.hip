@@ -35,8 +35,9 @@ __device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s
 // found digit by digit (11, 11 and 10 bits, a count of each digit in LDS), then one pass in the tokens' order
 // writes the numbers of those above it and of the first few equal to it. No order of atomics matters:
 // counts are whole numbers. Lists of up to kSelect * 16 tokens stay in registers: all scores are read before any
-// is written, so they move in the last pass. Bound by the passes' waits and the counts in LDS: 28 layers x 4 heads of
-// 1500 tokens in 10.5 us, 12 x 8 x 16 lists of 1000 to 8000 in 68.
+// is written, so they move in the last pass. Bound by the waits between the passes (with 4 copies of the counts against
+// conflicts 71 instead of 67 us): 28 layers x 4 heads of
+// 1500 tokens in 9.3 us, 12 x 8 x 16 lists of 1000 to 8000 in 56 (67 with turns behind the list's end).
 // 4, 16 or no scores of a thread held, whole calls in us (28 layers, 4 heads): 1500 tokens 45, 52 and 49; 2100 tokens
 // -, 64 and 63; 4000 -, 104 and 109; 8000 -, 190 and 211.
 // ============================================================================
