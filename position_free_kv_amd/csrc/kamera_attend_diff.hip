@@ -11,10 +11,10 @@
 // fp32 from sums in fp32; the weights are rounded to bf16 for the second product alone (at most 2^-8 of each), the output once.
 // A query head and key cost 2 D + 4 D flops, half as much again as plain attention, for the same bytes of the pool.
 //
-// 8 requests with 2481 query tokens over an 8192-token prefix, 28 + 4 heads of 128: 0.95 PFLOP/s in this kernel (463
-// GFLOP in 488 us), 78% of a large library product's rate; bound by the products and the softmax between them, which two
-// waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones, 32 + 8 heads: 66 us and
-// 12.6 in the join; bound by the own tokens' pages and by what a workgroup does before its first key (about 6 us).
+// 8 requests with 2481 query tokens over an 8192-token prefix, 28 + 4 heads of 128: 0.93 PFLOP/s in this kernel (463
+// GFLOP in 500 us), 76% of a large library product's rate; bound by the products and the softmax between them, which two
+// waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones, 32 + 8 heads: 62 us and
+// 12 in the join; bound by the own tokens' pages and by what a workgroup does before its first key (about 6 us).
 #include <type_traits>
 
 #include "kamera_attend.h"
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_diff(StepArgs a, AttendIo 
 // rows meet in LDS, and the norm follows. All parts' statistics are read at once, then their rows, 8 of a wave at a
 // time and none under a condition (a load under one is waited for before the next: 4 layers of 2 requests over 2000
 // tokens 81 us that way, 69 this way). Bound by three dependent reads when rows are few, by the partial rows' bytes
-// (written and read: 2 dv fp32 a query pair and part) when they are many. 64 tokens of 16 pairs in 18 parts: 12.6 us.
+// (written and read: 2 dv fp32 a query pair and part) when they are many. 64 tokens of 16 pairs in 18 parts: 12 us.
 // ============================================================================
 constexpr int kJoinParts = 2 * kMaxSplits;
 
