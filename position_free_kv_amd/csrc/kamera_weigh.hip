@@ -69,7 +69,10 @@ __device__ __forceinline__ void add_score(const StepArgs& a, const WeighIo& io, 
 }
 
 // ============================================================================
-// Any layout: 16 lanes a key, 16 keys a workgroup, every lane VEC * NJ of its columns; the rows one after the other.
+// Any layout: 16 lanes a key, 16 keys a workgroup, every lane NJ of its columns; ROWS rows at a time, all of them asked for
+// before the first is used, and no read under a condition. Bound by their reads' latency. (fp32, whole calls in us with a row
+// at a time and conditions, and so: 23 query tokens of 5 requests over 300 shared ones, 8 + 2 heads of 64, 63 and 36; MLA, 32
+// requests, 16 heads, 2 layers, 3398 and 984 (1030 a row at a time).)
 // ============================================================================
 template <typename T>
 __device__ __forceinline__ float widened(T x) {
@@ -77,7 +80,7 @@ __device__ __forceinline__ float widened(T x) {
   else return x;
 }
 
-template <typename T, int NJ>
+template <typename T, int NJ, int ROWS>
 __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) {
   const uint32_t block = block_number();
   const int item = (int)(block / (uint32_t)a.heads), head = (int)(block - (uint32_t)item * (uint32_t)a.heads);
@@ -91,21 +94,37 @@ __global__ __launch_bounds__(kThreads) void weigh_plain(StepArgs a, WeighIo io) 
 #pragma unroll
   for (int i = 0; i < NJ; ++i) {
     const int d = i * 16 + lane;
-    k[i] = d < a.dk ? widened<T>(kp[d]) : 0.0f;
+    k[i] = widened<T>(kp[min(d, a.dk - 1)]);
   }
   float sum = 0.0f;
-  for (int row = it.row0; row < it.row1; ++row) {
-    const QueryRow r = query_row(a, io, it, head, row);
-    const KGLOBAL T* qp = (const KGLOBAL T*)io.q + (int64_t)r.token * io.q_stride + (int64_t)r.qh * a.dk;
-    const float lse = io.lse[(int64_t)r.token * a.num_q_heads + r.qh];
-    float s = 0.0f;
+  for (int row = it.row0; row < it.row1; row += ROWS) {
+    // (rows behind the last and columns behind a row's end are read again and not used)
+    QueryRow r[ROWS];
+    float lse[ROWS], s[ROWS];
+    T x[ROWS][NJ];
 #pragma unroll
-    for (int i = 0; i < NJ; ++i) {
-      const int d = i * 16 + lane;
-      if (d < a.dk) s += widened<T>(qp[d]) * k[i];
+    for (int y = 0; y < ROWS; ++y) r[y] = query_row(a, io, it, head, min(row + y, it.row1 - 1));
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+      const KGLOBAL T* qp = (const KGLOBAL T*)io.q + (int64_t)r[y].token * io.q_stride + (int64_t)r[y].qh * a.dk;
+      lse[y] = ((const KGLOBAL float*)io.lse)[(int64_t)r[y].token * a.num_q_heads + r[y].qh];
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) x[y][i] = qp[min(i * 16 + lane, a.dk - 1)];
     }
-    for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d, 16);
-    if (t <= it.lim0 + r.j * it.lstep && lse != -INFINITY) sum += exp2f(s * io.scale2 - lse * kLog2);
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+      s[y] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) s[y] += i * 16 + lane < a.dk ? widened<T>(x[y][i]) * k[i] : 0.0f;
+    }
+    for (int d = 8; d; d >>= 1)
+#pragma unroll
+      for (int y = 0; y < ROWS; ++y) s[y] += __shfl_xor(s[y], d, 16);
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+      const float w = exp2f(s[y] * io.scale2 - lse[y] * kLog2);
+      sum += row + y < it.row1 && t <= it.lim0 + r[y].j * it.lstep && lse[y] != -INFINITY ? w : 0.0f;
+    }
   }
   if (lane != 0 || t >= it.kv1) return;
   if (it.part >= 0) a.weigh_part[it.part + ((int64_t)it.split * a.heads + head) * it.kv + t] = sum;
@@ -489,9 +508,9 @@ __global__ __launch_bounds__(kThreads) void weigh_join(StepArgs a, WeighIo io) {
 template <typename T>
 hipError_t plain(const StepArgs& a, const WeighIo& io, hipStream_t stream) {
   const dim3 g = grid_of((int64_t)a.num_weigh * a.heads), b(kThreads);
-  if (a.dk <= 128) hipLaunchKernelGGL((weigh_plain<T, 8>), g, b, 0, stream, a, io);
-  else if (a.dk <= 640) hipLaunchKernelGGL((weigh_plain<T, 40>), g, b, 0, stream, a, io);
-  else hipLaunchKernelGGL((weigh_plain<T, 64>), g, b, 0, stream, a, io);
+  if (a.dk <= 128) hipLaunchKernelGGL((weigh_plain<T, 8, 8>), g, b, 0, stream, a, io);
+  else if (a.dk <= 640) hipLaunchKernelGGL((weigh_plain<T, 40, 2>), g, b, 0, stream, a, io);
+  else hipLaunchKernelGGL((weigh_plain<T, 64, 1>), g, b, 0, stream, a, io);
   return hipGetLastError();
 }
 
