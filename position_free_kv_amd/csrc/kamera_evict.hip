@@ -2,7 +2,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "kamera_step_desc.h"
+#include "kamera_evict_moves.h"
 
 namespace kamera {
 
@@ -14,11 +14,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWave = 64;
-constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
 dim3 grid_of(int64_t blocks) {
-  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+  return blocks <= kEvictGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kEvictGridRow, (unsigned)(evict_grid(blocks) / kEvictGridRow));
 }
-__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
+__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kEvictGridRow + blockIdx.x; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Page and place in it of token t of a sequence.
@@ -285,7 +284,6 @@ __global__ __launch_bounds__(256) void evict_phase(EvictArgs a) {
 // whole call. Slices of 64, 256 and 512 bytes, turns of 2, 4 and 16 rows, and cached stores were all slower.
 // ============================================================================
 constexpr int kMove = 256;  // threads
-constexpr int kSlice = 8;   // units of a slice, at most
 constexpr int kTurn = 8;    // rows of a thread in one turn
 
 // Columns as they are, in pieces of a U.
@@ -402,24 +400,12 @@ struct TurnedPieces {
   }
 };
 
-// A part of what a launch moves: `tensors` of the pool from tensor0 on, columns from byte `at` of a group on, `units`
-// units of them in slices of `slice`; its workgroups.
-struct Move {
-  int tensor0, tensors, at, units, slice, slices;
-  int64_t blocks;
-};
-
 template <typename C>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, const Move& m, int64_t b) {
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictMove& m, int64_t b) {
+  EvictTask task;
+  if (!evict_task(a, m, b, task)) return;
   const int groups = a.heads / a.together, tid = threadIdx.x;
-  const int slice = (int)(b % m.slices);
-  b /= m.slices;
-  const int si = (int)(b % a.num_seqs);
-  b /= a.num_seqs;
-  const int group = (int)(b % groups);
-  b /= groups;
-  const int tensor = m.tensor0 + (int)(b % m.tensors), layer = (int)(b / m.tensors);
-  if (layer >= a.layers) return;
+  const int slice = task.slice, si = task.seq, group = task.group, tensor = task.tensor, layer = task.layer;
   const EvictSeq seq = a.seqs[si];
   const int keep = min(seq.keep, seq.num_tokens);
   if (keep == seq.num_tokens) return;
@@ -478,31 +464,21 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const Move& m, int
 }
 
 template <typename C>
-__global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, Move m) {
+__global__ __launch_bounds__(kMove) void evict_move(EvictArgs a, EvictMove m) {
   move_rows<C>(a, m, block_number());
 }
 
 // Turned columns and the others, in one launch.
-__global__ __launch_bounds__(kMove) void evict_move_turned(EvictArgs a, Move turned, Move plain0, Move plain1) {
+__global__ __launch_bounds__(kMove) void evict_move_turned(EvictArgs a, EvictMoves m) {
   int64_t b = block_number();
-  if (b < turned.blocks) {
-    move_rows<TurnedPieces>(a, turned, b);
-  } else if ((b -= turned.blocks) < plain0.blocks) {
-    move_rows<Plain<u32x4>>(a, plain0, b);
-  } else {
-    move_rows<Plain<u32x4>>(a, plain1, b - plain0.blocks);
-  }
-}
-
-Move move_of(const EvictArgs& a, int tensor0, int tensors, int at, int units) {
-  Move m{tensor0, tensors, at, units, units < kSlice ? units : kSlice, 1, 0};
-  if (units > 0) m.slices = (units + m.slice - 1) / m.slice;
-  if (units > 0) m.blocks = (int64_t)a.layers * tensors * (a.heads / a.together) * a.num_seqs * m.slices;
-  return m;
+  const int part = evict_part(m, b);
+  if (part == 0) move_rows<TurnedPieces>(a, m.turned, b);
+  else if (part == 1) move_rows<Plain<u32x4>>(a, m.plain0, b);
+  else if (part == 2) move_rows<Plain<u32x4>>(a, m.plain1, b);
 }
 
 template <typename C>
-hipError_t move(const EvictArgs& a, const Move& m, hipStream_t stream) {
+hipError_t move(const EvictArgs& a, const EvictMove& m, hipStream_t stream) {
   if (m.blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   if (m.blocks > 0) hipLaunchKernelGGL((evict_move<C>), grid_of(m.blocks), dim3(kMove), 0, stream, a, m);
   return hipGetLastError();
@@ -517,9 +493,9 @@ bool fits(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, int u
 
 // those columns as they are
 hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, hipStream_t stream) {
-  if (fits(a, tensor0, tensors, at, bytes, 16)) return move<Plain<u32x4>>(a, move_of(a, tensor0, tensors, at, bytes / 16), stream);
-  if (fits(a, tensor0, tensors, at, bytes, 4)) return move<Plain<uint32_t>>(a, move_of(a, tensor0, tensors, at, bytes / 4), stream);
-  return move<Plain<uint16_t>>(a, move_of(a, tensor0, tensors, at, bytes / 2), stream);
+  if (fits(a, tensor0, tensors, at, bytes, 16)) return move<Plain<u32x4>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 16), stream);
+  if (fits(a, tensor0, tensors, at, bytes, 4)) return move<Plain<uint32_t>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 4), stream);
+  return move<Plain<uint16_t>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 2), stream);
 }
 
 }  // namespace
@@ -541,14 +517,14 @@ hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int es = a.dtype == KAMERA_BF16 ? 2 : 4, band = a.band0 * es;
   if (es == 2 && a.d_rot % 16 == 0 && a.head_bytes % 16 == 0 && band % 16 == 0 && fits(a, 0, a.tensors, 0, all, 16)) {
-    const Move turned = move_of(a, 0, 1, band, a.together * (a.d_rot / 16)), latent = move_of(a, 0, 1, 0, band / 16), values = move_of(a, 1, a.tensors - 1, 0, all / 16);
-    const int64_t blocks = turned.blocks + latent.blocks + values.blocks;
+    const EvictMoves m = evict_moves_turned(a);
+    const int64_t blocks = m.turned.blocks + m.plain0.blocks + m.plain1.blocks;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(evict_move_turned, grid_of(blocks), dim3(kMove), 0, stream, a, turned, latent, values);
+    hipLaunchKernelGGL(evict_move_turned, grid_of(blocks), dim3(kMove), 0, stream, a, m);
     return hipGetLastError();
   }
   e = move_plain(a, 0, 1, 0, band, stream);
-  const Move m = move_of(a, 0, 1, band, a.together * (a.d_rot / 2));
+  const EvictMove m = evict_move_of(a, 0, 1, band, a.together * (a.d_rot / 2));
   if (e == hipSuccess) e = es == 2 ? move<Turned<uint16_t>>(a, m, stream) : move<Turned<float>>(a, m, stream);
   if (e == hipSuccess && a.tensors == 2) e = move_plain(a, 1, 1, 0, all, stream);
   return e;

@@ -1,0 +1,67 @@
+// How the rows that an eviction moves are shared out to workgroups (kernels: kamera_evict.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "kamera_step_desc.h"
+
+namespace kamera {
+
+// A launch of up to this many workgroups lies along one dimension of its grid; more are rounded up to whole rows of it.
+constexpr int64_t kEvictGridRow = int64_t(1) << 22;
+constexpr int64_t evict_grid(int64_t blocks) {
+  return blocks <= kEvictGridRow ? blocks : (blocks + kEvictGridRow - 1) / kEvictGridRow * kEvictGridRow;
+}
+
+constexpr int kSlice = 8;  // units of a slice, at most
+
+// A part of what a launch moves: `tensors` of the pool from tensor0 on, columns from byte `at` of a group on, `units`
+// units of them in slices of `slice`; its workgroups.
+struct EvictMove {
+  int tensor0, tensors, at, units, slice, slices;
+  int64_t blocks;
+};
+
+inline EvictMove evict_move_of(const EvictArgs& a, int tensor0, int tensors, int at, int units) {
+  EvictMove m{tensor0, tensors, at, units, units < kSlice ? units : kSlice, 1, 0};
+  if (units > 0) m.slices = (units + m.slice - 1) / m.slice;
+  if (units > 0) m.blocks = (int64_t)a.layers * tensors * (a.heads / a.together) * a.num_seqs * m.slices;
+  return m;
+}
+
+// What workgroup b of a move walks over: a list's rows, in a slice of their columns of one tensor. false: the move has no
+// workgroup of that number (a grid's surplus, or a move of nothing, which may have no tensors to divide by).
+struct EvictTask {
+  int slice, seq, group, tensor, layer;
+};
+__host__ __device__ inline bool evict_task(const EvictArgs& a, const EvictMove& m, int64_t b, EvictTask& t) {
+  if (b >= m.blocks) return false;
+  const int groups = a.heads / a.together;
+  t.slice = (int)(b % m.slices);
+  b /= m.slices;
+  t.seq = (int)(b % a.num_seqs);
+  b /= a.num_seqs;
+  t.group = (int)(b % groups);
+  b /= groups;
+  t.tensor = m.tensor0 + (int)(b % m.tensors);
+  t.layer = (int)(b / m.tensors);
+  return true;
+}
+
+// Turned columns and the others, in one launch: their workgroups one after the other, then the grid's surplus. Number b of
+// the launch becomes its number in a move: 0, 1 or 2; 3: it has no work.
+struct EvictMoves {
+  EvictMove turned, plain0, plain1;
+};
+__host__ __device__ inline int evict_part(const EvictMoves& m, int64_t& b) {
+  if (b < m.turned.blocks) return 0;
+  if ((b -= m.turned.blocks) < m.plain0.blocks) return 1;
+  return (b -= m.plain0.blocks) < m.plain1.blocks ? 2 : 3;
+}
+inline EvictMoves evict_moves_turned(const EvictArgs& a) {
+  const int es = a.dtype == KAMERA_BF16 ? 2 : 4, band = a.band0 * es;
+  return EvictMoves{evict_move_of(a, 0, 1, band, a.together * (a.d_rot / 16)), evict_move_of(a, 0, 1, 0, band / 16),
+                    evict_move_of(a, 1, a.tensors - 1, 0, a.together * a.head_bytes / 16)};
+}
+
+}  // namespace kamera

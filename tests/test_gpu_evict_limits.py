@@ -1,0 +1,53 @@
+"""Limits of eviction, weighing and differential attention on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+from position_free_kv_amd import abi, step
+from tests.step_util import E32, HALF
+
+pytestmark = pytest.mark.gpu
+
+GQA, MLA, BF16, F32 = abi.GQA, abi.MLA, abi.BF16, abi.F32
+
+
+def test_evict_more_than_2_22_workgroups():
+    """466 layers of 1001 sequences, 9 slices of a latent row: 3890 workgroups more than a row of the grid, whose second
+    row has 4.2 million without work. Two tokens each, of which one stays."""
+    layers, seqs, latent, rope, base = 466, 1001, 512, 64, 1e4
+    pages, F = seqs + 1, latent + rope
+    lay = abi.make_layout(MLA, BF16, layers, latent_dim=latent, rope_dim=rope, rope_base=base, page_size=2)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rows = torch.empty(layers, pages, 2, F, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    scores = torch.rand(layers, pages, 1, 2, generator=gen, device="cuda")
+    was, old = rows.clone(), scores.clone()
+    order = np.random.default_rng(0).permutation(pages)[:seqs].astype(np.int32)
+    e = step.Eviction(block_tables=order.reshape(seqs, 1), num_tokens=2, keep=1, flags=step.REANCHOR)
+    kept = torch.full((layers, 1, seqs), -1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(step.evict_workspace_bytes(lay, e), dtype=torch.uint8, device="cuda")
+    step.evict(lay, abi.make_pool(rows, None, pages), e, scores, ws, kept=kept)
+    torch.cuda.synchronize()
+    at = torch.from_numpy(order.astype(np.int64)).cuda()
+    stays = (old[:, at, 0, 1] > old[:, at, 0, 0]).int()
+    assert torch.equal(kept[:, 0], stays)
+    want = old.clone()
+    want[:, at, 0, 0] = old[:, at, 0].amax(-1)
+    assert torch.equal(scores, want)
+    spare = torch.ones(pages, dtype=torch.bool, device="cuda")
+    spare[at] = False
+    assert torch.equal(rows[:, spare].view(torch.int16), was[:, spare].view(torch.int16))
+    assert torch.equal(rows[:, at, 1].view(torch.int16), was[:, at, 1].view(torch.int16))
+    theta = base ** (-torch.arange(rope // 2, dtype=torch.float64, device="cuda") * 2 / rope)
+    c, s = theta.cos(), (-theta).sin()
+    for part in range(0, layers, 50):
+        l = slice(part, part + 50)
+        moved = stays[l].bool()
+        got, stay, from1 = rows[l, at, 0], was[l, at, 0], was[l, at, 1]
+        assert torch.equal(got[~moved].view(torch.int16), stay[~moved].view(torch.int16))
+        got, from1 = got[moved], from1[moved]
+        assert torch.equal(got[:, :latent].view(torch.int16), from1[:, :latent].view(torch.int16))
+        a, b = (from1[:, latent + i * rope // 2:latent + (i + 1) * rope // 2].double() for i in range(2))
+        y = torch.cat([a * c - b * s, a * s + b * c], 1)
+        terms = torch.cat([(a * c).abs() + (b * s).abs(), (a * s).abs() + (b * c).abs()], 1)
+        # cos and sin rounded once, two products and a sum in fp32, one rounding
+        assert ((got[:, latent:].double() - y).abs() <= 4 * E32 * terms + HALF[BF16] * y.abs() * (1 + 2 ** -6) + 1e-38).all()
