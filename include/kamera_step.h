@@ -232,7 +232,8 @@ enum {
  * columns and scores move to the sequence's first `keep` slots, in their order; what lies behind them is left as it
  * was. (The caller then lowers the request's num_tokens; with REANCHOR position0 + token stays the
  * position of every token.) Pool slots of different sequences must be distinct (KAMERA_E_OVERLAP). Moved bits are unchanged
- * but for turned keys, computed in fp32 (cos/sin rounded once from fp64) and rounded once. */
+ * but for turned keys, computed in fp32 (cos/sin rounded once from fp64) and rounded once. More layers, heads and sequences
+ * than one launch takes (2^31 workgroups) are refused (KAMERA_E_SHAPE) before anything is changed. */
 typedef struct kamera_eviction {
   const kamera_evict_seq* seqs; /* HOST [num_seqs]                                                 */
   float* scores;                /* device fp32: layer l's (as kamera_step_weigh's) at scores + l * scores_stride */

@@ -18,7 +18,6 @@ dim3 grid_of(int64_t blocks) {
   return blocks <= kEvictGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kEvictGridRow, (unsigned)(evict_grid(blocks) / kEvictGridRow));
 }
 __device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kEvictGridRow + blockIdx.x; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Page and place in it of token t of a sequence.
 __device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s, int t, int& place) {
@@ -260,9 +259,9 @@ __global__ __launch_bounds__(kSelect) void evict_select(EvictArgs a) {
 }
 
 // cos/sin of turning back by t positions, formed in fp64 and rounded once
-__global__ __launch_bounds__(256) void evict_phase(EvictArgs a) {
+__global__ __launch_bounds__(kEvictPhases) void evict_phase(EvictArgs a) {
   const int half = a.d_rot >> 1;
-  const int64_t i = (int64_t)block_number() * 256 + threadIdx.x, t = i / half;
+  const int64_t i = (int64_t)block_number() * kEvictPhases + threadIdx.x, t = i / half;
   if (t >= a.shifts) return;
   const int p = (int)(i - t * half);
   double s, c;
@@ -478,55 +477,34 @@ __global__ __launch_bounds__(kMove) void evict_move_turned(EvictArgs a, EvictMov
 }
 
 template <typename C>
-hipError_t move(const EvictArgs& a, const EvictMove& m, hipStream_t stream) {
-  if (m.blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+void move(const EvictArgs& a, const EvictMove& m, hipStream_t stream) {
   if (m.blocks > 0) hipLaunchKernelGGL((evict_move<C>), grid_of(m.blocks), dim3(kMove), 0, stream, a, m);
-  return hipGetLastError();
-}
-
-// columns [at, at + bytes) of every group of some tensors, in units of `unit` bytes?
-bool fits(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, int unit) {
-  bool ok = at % unit == 0 && bytes % unit == 0 && a.row_bytes % unit == 0 && a.layer_bytes % unit == 0 && (a.together * a.head_bytes) % unit == 0;
-  for (int t = tensor0; t < tensor0 + tensors; ++t) ok = ok && (uintptr_t)a.pool[t] % unit == 0;
-  return ok;
-}
-
-// those columns as they are
-hipError_t move_plain(const EvictArgs& a, int tensor0, int tensors, int at, int bytes, hipStream_t stream) {
-  if (fits(a, tensor0, tensors, at, bytes, 16)) return move<Plain<u32x4>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 16), stream);
-  if (fits(a, tensor0, tensors, at, bytes, 4)) return move<Plain<uint32_t>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 4), stream);
-  return move<Plain<uint16_t>>(a, evict_move_of(a, tensor0, tensors, at, bytes / 2), stream);
 }
 
 }  // namespace
 
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream) {
-  const int64_t lists = (int64_t)a.layers * (a.heads / a.together) * a.num_seqs;
-  if (lists > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (a.longest <= kSelect * kHeldFew) hipLaunchKernelGGL(evict_select<kHeldFew>, grid_of(lists), dim3(kSelect), 0, stream, a);
-  else if (a.longest <= kSelect * kHeldMost) hipLaunchKernelGGL(evict_select<kHeldMost>, grid_of(lists), dim3(kSelect), 0, stream, a);
-  else hipLaunchKernelGGL(evict_select<0>, grid_of(lists), dim3(kSelect), 0, stream, a);
+  const EvictLaunches l = evict_launches(a);
+  if (a.longest <= kSelect * kHeldFew) hipLaunchKernelGGL(evict_select<kHeldFew>, grid_of(l.lists), dim3(kSelect), 0, stream, a);
+  else if (a.longest <= kSelect * kHeldMost) hipLaunchKernelGGL(evict_select<kHeldMost>, grid_of(l.lists), dim3(kSelect), 0, stream, a);
+  else hipLaunchKernelGGL(evict_select<0>, grid_of(l.lists), dim3(kSelect), 0, stream, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.most_kept == 0) return e;
-  const int all = a.together * a.head_bytes;
-  if (!a.phase) return move_plain(a, 0, a.tensors, 0, all, stream);
-  const int64_t phases = ceil_div((int64_t)a.shifts * (a.d_rot / 2), 256);
-  if (phases > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(evict_phase, grid_of(phases), dim3(256), 0, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int es = a.dtype == KAMERA_BF16 ? 2 : 4, band = a.band0 * es;
-  if (es == 2 && a.d_rot % 16 == 0 && a.head_bytes % 16 == 0 && band % 16 == 0 && fits(a, 0, a.tensors, 0, all, 16)) {
-    const EvictMoves m = evict_moves_turned(a);
-    const int64_t blocks = m.turned.blocks + m.plain0.blocks + m.plain1.blocks;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(evict_move_turned, grid_of(blocks), dim3(kMove), 0, stream, a, m);
-    return hipGetLastError();
+  if (e == hipSuccess && l.phases > 0) {
+    hipLaunchKernelGGL(evict_phase, grid_of(l.phases), dim3(kEvictPhases), 0, stream, a);
+    e = hipGetLastError();
   }
-  e = move_plain(a, 0, 1, 0, band, stream);
-  const EvictMove m = evict_move_of(a, 0, 1, band, a.together * (a.d_rot / 2));
-  if (e == hipSuccess) e = es == 2 ? move<Turned<uint16_t>>(a, m, stream) : move<Turned<float>>(a, m, stream);
-  if (e == hipSuccess && a.tensors == 2) e = move_plain(a, 1, 1, 0, all, stream);
+  if (e == hipSuccess && l.together) {
+    hipLaunchKernelGGL(evict_move_turned, grid_of(l.moves.turned.blocks + l.moves.plain0.blocks + l.moves.plain1.blocks), dim3(kMove), 0, stream, a, l.moves);
+    e = hipGetLastError();
+  }
+  for (int i = 0; i < l.parts && e == hipSuccess; ++i) {
+    if (l.columns[i] == EVICT_BY_16) move<Plain<u32x4>>(a, l.part[i], stream);
+    else if (l.columns[i] == EVICT_BY_4) move<Plain<uint32_t>>(a, l.part[i], stream);
+    else if (l.columns[i] == EVICT_BY_2) move<Plain<uint16_t>>(a, l.part[i], stream);
+    else if (a.dtype == KAMERA_BF16) move<Turned<uint16_t>>(a, l.part[i], stream);
+    else move<Turned<float>>(a, l.part[i], stream);
+    e = hipGetLastError();
+  }
   return e;
 }
 

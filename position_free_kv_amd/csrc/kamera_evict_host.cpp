@@ -2,6 +2,7 @@
 // with the other operators' (kamera_step_host.cpp); an eviction, like a list of page copies, has none.
 #include <hip/hip_runtime.h>
 
+#include "kamera_evict_moves.h"
 #include "kamera_step_host.h"
 
 using namespace kamera;
@@ -153,6 +154,7 @@ kamera_status evict(const kamera_layout* L, const kamera_pool* pool, const kamer
   a.shifts = n.shifts;
   a.longest = n.longest;
   a.most_kept = n.most_kept;
+  if (evict_largest(evict_launches(a)) >= int64_t(1) << 31) return host_fail(KAMERA_E_SHAPE, "too many layers, heads and sequences for one call");
   st = host_stage(blob.data(), f.upload, ws, stream);
   if (st != KAMERA_OK) return st;
   const hipError_t err = launch_evict(a, stream);

@@ -208,6 +208,7 @@ struct EvictArgs {
   int32_t d_rot, band0, pairing, shifts;          // band0: first rotated column of a head
   int32_t longest, most_kept;                     // most tokens, and most kept tokens, of a sequence that loses some
 };
+// (kamera_evict_moves.h: the largest launch has fewer than 2^31 workgroups)
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream);
 
 }  // namespace kamera

@@ -39,6 +39,9 @@ EvictArgs args_of(const Shape& s) {
   a.dtype = s.dtype;
   a.d_rot = gqa ? s.dim : s.rope;
   a.band0 = gqa ? 0 : s.latent;
+  a.most_kept = 1;
+  a.shifts = 2;
+  a.phase = reinterpret_cast<float*>(uintptr_t(1) << 40);
   return a;
 }
 
@@ -65,7 +68,7 @@ struct Met {
 
 void turned(const Shape& s) {
   const EvictArgs a = args_of(s);
-  const EvictMoves m = evict_moves_turned(a);
+  const EvictMoves m = evict_launches(a).moves;
   Met met[3] = {Met(a, m.turned), Met(a, m.plain0), Met(a, m.plain1)};
   const int64_t blocks = m.turned.blocks + m.plain0.blocks + m.plain1.blocks;
   CHECK(evict_grid(blocks) >= blocks);

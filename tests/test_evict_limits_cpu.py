@@ -3,11 +3,26 @@ import os
 import subprocess
 import tempfile
 
+import numpy as np
 import pytest
+
+from position_free_kv_amd import abi, step
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "position_free_kv_amd", "csrc")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
+FAKE = 0x10_0000_0000
+
+
+def _gpu_present() -> bool:
+    try:
+        import torch
+        return torch.cuda.device_count() > 0
+    except Exception:  # noqa: BLE001
+        return False
+
+
+pytestmark = pytest.mark.skipif(_gpu_present(), reason="fake device addresses")
 
 
 def compiled_and_run(check: str, *sources: str) -> None:
@@ -25,3 +40,17 @@ def compiled_and_run(check: str, *sources: str) -> None:
 
 def test_every_workgroup_of_a_move_has_work_of_its_own_or_none():
     compiled_and_run("evict_moves_check.cpp")
+
+
+@pytest.mark.parametrize("family,layers,seqs,keep,flags,fits", [
+    (abi.MLA, 1 << 20, 2047, 0, 0, True), (abi.MLA, 1 << 20, 2048, 0, 0, False),                    # lists
+    (abi.GQA, 1 << 15, 1023, 1, 0, True), (abi.GQA, 1 << 15, 1024, 1, 0, False),                    # 64 workgroups each that move rows
+    (abi.MLA, 1 << 18, 910, 1, step.REANCHOR, True), (abi.MLA, 1 << 18, 911, 1, step.REANCHOR, False)])  # 9 each
+def test_evictions_of_more_than_one_launch_are_refused(family, layers, seqs, keep, flags, fits):
+    """Before anything is enqueued: scores that have moved without their rows could not be put right."""
+    kind = dict(num_kv_heads=8, head_dim=256) if family == abi.GQA else dict(latent_dim=512, rope_dim=64)
+    lay = abi.make_layout(family, abi.BF16, layers, page_size=2, **kind)
+    e = step.Eviction(block_tables=np.arange(seqs, dtype=np.int32).reshape(seqs, 1), num_tokens=2, keep=keep, flags=flags)
+    with pytest.raises(abi.KameraError) as err:
+        step.evict(lay, abi.make_pool(FAKE, FAKE if family == abi.GQA else None, seqs), e, FAKE, (FAKE, 1 << 50))
+    assert err.value.name == ("KAMERA_E_HIP" if fits else "KAMERA_E_SHAPE")
