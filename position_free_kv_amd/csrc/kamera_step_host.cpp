@@ -301,7 +301,10 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
   // together, and the rest, which would leave most places of a last round empty, are cut into `pieces` that
   // fill it. (274 tiles of 2 pairs of heads on 512 places: 548 whole ones take two rounds, three pieces each 3.2
   // rounds of a third.) The rest are the last queries of the last runs. (8 requests, 2481 query tokens, 28 + 4 heads: 638 us
-  // without this, 520 with it.)
+  // without this, 520 with it.) Only where a whole tile of the longest run takes no longer than kWhole even shares of
+  // the launch: a long request among short ones would be the last workgroup alone. (Requests of 250 to 500 queries, the
+  // longest taking 0.9 shares: whole 682 us, in ranges 721; 1.1 shares: 644 and 647; 1.2: 715 and 632; 7.3, one of 120000
+  // tokens among 7 of 1000: 5337 and 1044.)
   std::vector<int64_t> run_chunk;                                        // keys per item of a run, instead of its class's
   std::vector<std::pair<int32_t, int32_t>> rest;                        // of a request: its queries from `first` on are run `second`'s
   if (kernel == ATTEND_DIFF && fit.coarser == 0 && fit.share) {
@@ -309,7 +312,8 @@ void plan_attention(const kamera_layout* L, const kamera_step* s, const Tables& 
     const double places = (double)slots / h.heads;
     const Class& c = cls[TILE_WIDE];
     const double rounds = c.tiles / places;
-    if (rounds >= 1) {
+    constexpr double kWhole = 1.1;
+    if (rounds >= 1 && kStartNs + key_ns(kernel, TILE_WIDE, h.dk) * c.longest <= kWhole * whole) {
       const double over = rounds - std::floor(rounds);
       int pieces = 1;
       double least = over > 0 ? 1 : 0;

@@ -54,3 +54,7 @@ def test_evictions_of_more_than_one_launch_are_refused(family, layers, seqs, kee
     with pytest.raises(abi.KameraError) as err:
         step.evict(lay, abi.make_pool(FAKE, FAKE if family == abi.GQA else None, seqs), e, FAKE, (FAKE, 1 << 50))
     assert err.value.name == ("KAMERA_E_HIP" if fits else "KAMERA_E_SHAPE")
+
+
+def test_long_requests_among_short_ones_are_shared_out():
+    compiled_and_run("diff_plan_check.cpp", "kamera_step_host.cpp", "kamera_evict_host.cpp")

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 from position_free_kv_amd import abi, step
-from tests.step_util import E32, HALF
+from tests import evict_util as eu
+from tests.evict_util import Params
+from tests.step_util import E32, HALF, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +53,13 @@ def test_evict_more_than_2_22_workgroups():
         terms = torch.cat([(a * c).abs() + (b * s).abs(), (a * s).abs() + (b * c).abs()], 1)
         # cos and sin rounded once, two products and a sum in fp32, one rounding
         assert ((got[:, latent:].double() - y).abs() <= 4 * E32 * terms + HALF[BF16] * y.abs() * (1 + 2 ** -6) + 1e-38).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("place", [0, 7])
+def test_diff_of_a_long_request_among_short_ones(dim, place):
+    """More wide tiles than places, whose keys are cut into ranges throughout."""
+    requests = [(0, 150, 130)] * 8
+    requests[place] = (0, 4000, 130)
+    c = Case(layers=1, heads=128, kv_heads=8, head_dim=dim, prefixes=[60], requests=requests, seed=place)
+    eu.check_diff(c, Params(c), 1.0 / float(np.sqrt(dim)))
