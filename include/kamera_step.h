@@ -245,7 +245,10 @@ typedef struct kamera_eviction {
   uint32_t flags;               /* KAMERA_EVICT_REANCHOR                                           */
   int32_t reserved;             /* must be 0                                                       */
 } kamera_eviction;
-/* Bytes of device workspace of an eviction (256-byte aligned; 0 if the arguments are invalid). The tables are
+/* Bytes of device workspace of an eviction (256-byte aligned; 0 if the arguments are invalid). They also serve every smaller
+ * one: of some of its sequences, each of at most as many tokens that keeps at most as many, of the same layout, flags and
+ * heads_together (asked for with `kept`, those with it only). With REANCHOR most of them are cosines and sines, fp32, of as
+ * many positions as the longest sequence has tokens. The tables are
  * staged, so the call cannot be recorded in a captured graph (KAMERA_E_UNSUPPORTED). */
 size_t kamera_evict_workspace_bytes(const kamera_layout* layout, const kamera_eviction* eviction);
 kamera_status kamera_evict(const kamera_layout* layout, const kamera_pool* pool, const kamera_eviction* eviction,

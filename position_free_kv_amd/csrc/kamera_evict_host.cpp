@@ -15,6 +15,9 @@ struct EvictOffsets {
 struct EvictCounts {
   int64_t tokens = 0, entries = 0, kept = 0;
   int32_t longest = 0, most_kept = 0, shifts = 0;  // of the sequences that lose tokens
+  // What the workspace has room for, so that one for longer sequences serves shorter ones: table entries wherever the
+  // tokens begin in a page, and shifts (tokens that leave a sequence, and 0) however many stay
+  int64_t room_entries = 0, room_shifts = 0;
 };
 
 int kv_heads(const kamera_layout* L) { return L->family == KAMERA_GQA ? L->num_kv_heads : 1; }
@@ -40,6 +43,8 @@ kamera_status check_eviction(const kamera_layout* L, const kamera_eviction* e, E
     if (s.slot0 < 0 || s.slot0 >= P) return host_fail(KAMERA_E_PAGE, "sequence %d: slot0 must be in [0, page_size)", i);
     if ((int64_t)s.slot0 + s.num_tokens >= kMaxSlot) return host_fail(KAMERA_E_SHAPE, "sequence %d: too many tokens", i);
     n.entries += table_entries(s.slot0, s.num_tokens, P);
+    n.room_entries += table_entries(P - 1, s.num_tokens, P);
+    n.room_shifts = std::max<int64_t>(n.room_shifts, (int64_t)s.num_tokens + 1);
     n.tokens += s.num_tokens;
     n.kept += std::min(s.keep, s.num_tokens);
     if (s.keep >= s.num_tokens) continue;
@@ -64,11 +69,11 @@ EvictOffsets carve(const kamera_layout* L, const kamera_eviction* e, const Evict
   const bool turn = e->flags & KAMERA_EVICT_REANCHOR;
   const int64_t lists = (int64_t)L->num_layers * (kv_heads(L) / e->heads_together);
   f.seqs = take((size_t)e->num_seqs * sizeof(EvictSeq));
-  f.pages = take((size_t)n.entries * 4);
+  f.pages = take((size_t)n.room_entries * 4);
   f.theta = take(turn ? (size_t)rotary(L) / 2 * 8 : 0);
   f.upload = at;
   f.starts = take((size_t)(lists * e->num_seqs) * 4);
-  f.phase = take(turn ? (size_t)n.shifts * rotary(L) * 4 : 0);
+  f.phase = take(turn ? (size_t)n.room_shifts * rotary(L) * 4 : 0);
   f.kept = take(e->kept ? 0 : (size_t)(lists * n.kept) * 4);
   f.total = std::max<size_t>(at, kAlign);
   return f;

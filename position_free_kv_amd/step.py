@@ -398,7 +398,8 @@ class Eviction:
 
 
 def evict_workspace_bytes(layout: Layout, eviction: Eviction) -> int:
-    """Bytes that an eviction needs (those for longer sequences that keep at least as much serve shorter ones too)."""
+    """Bytes that an eviction needs. Those for longer sequences that keep at least as much serve shorter ones, and fewer of them, too
+    (of the same layout, flags and heads_together)."""
     return int(_lib().kamera_evict_workspace_bytes(ctypes.byref(layout), ctypes.byref(eviction.c)))
 
 

@@ -58,3 +58,36 @@ def test_evictions_of_more_than_one_launch_are_refused(family, layers, seqs, kee
 
 def test_long_requests_among_short_ones_are_shared_out():
     compiled_and_run("diff_plan_check.cpp", "kamera_step_host.cpp", "kamera_evict_host.cpp")
+
+
+@pytest.mark.parametrize("flags", [0, step.REANCHOR])
+@pytest.mark.parametrize("family,page", [(abi.GQA, 1), (abi.GQA, 16), (abi.MLA, 3), (abi.MLA, 64)])
+def test_a_workspace_serves_shorter_evictions(family, page, flags):
+    """Of some of the sequences, each of at most as many tokens that keeps at most as many, wherever they begin in a page."""
+    kind = dict(num_kv_heads=2, head_dim=128) if family == abi.GQA else dict(latent_dim=512, rope_dim=64)
+    lay = abi.make_layout(family, abi.BF16, 2, page_size=page, **kind)
+    rng = np.random.default_rng(page)
+
+    def eviction(n, keep):
+        slot0 = rng.integers(0, page, n.size)
+        entries = -(-(slot0 + n) // page)
+        tables = np.split(np.arange(entries.sum(), dtype=np.int32), np.cumsum(entries)[:-1])
+        return step.Eviction(block_tables=tables, num_tokens=n, keep=keep, slot0=slot0, flags=flags)
+
+    pool = abi.make_pool(FAKE, FAKE if family == abi.GQA else None, 1 << 20)
+    cases = [([1100], [1090], [1000], [100]), ([2000], [2000], [1000], [100]), ([8000], [7900], [4000], [500]), ([1600], [1600], [1599], [1599])]
+    for _ in range(60):
+        seqs = int(rng.integers(1, 12))
+        n = np.exp(rng.uniform(0, np.log(9000), seqs)).astype(np.int64)
+        keep = np.exp(rng.uniform(0, np.log(9000), seqs)).astype(np.int64)
+        some = rng.random(seqs) < 0.7
+        some[rng.integers(seqs)] = True
+        cases.append((n, keep, rng.integers(1, n[some] + 1), rng.integers(0, keep[some] + 1)))
+    for n, keep, less, stay in cases:
+        large, small = eviction(np.asarray(n), keep), eviction(np.asarray(less), stay)
+        room = step.evict_workspace_bytes(lay, large)
+        assert 0 < step.evict_workspace_bytes(lay, small) <= room, (n, keep, less, stay)
+        try:
+            step.evict(lay, pool, small, FAKE, (FAKE, room))
+        except abi.KameraError as e:  # (staging needs a GPU)
+            assert e.name == "KAMERA_E_HIP", e
