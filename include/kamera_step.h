@@ -201,8 +201,8 @@ kamera_status kamera_step_attend_diff(const kamera_step_plan* plan, int32_t laye
  * wrote, scale its scale. scores: fp32, of this layer, in pages like the pool's: score of KV head h (MLA:
  * 0) at slot o of page p at [(p * heads + h) * page_size + o]. Every token of a request with queries and of
  * its prefix is met once, a shared prefix by the sum over all its requests' queries; the scores of other
- * slots are not touched. decay 0: scores are not read. In a step of KAMERA_STEP_APPEND too the query tokens are
- * new, and their scores start at 0 whatever their slots held before. Sums are fp32, in an order that the plan fixes. A row
+ * slots are not touched. decay 0: what the scores held has no effect. In a step of KAMERA_STEP_APPEND too the query
+ * tokens are new, and their scores start at 0 whatever their slots held before. Sums are fp32, in an order that the plan fixes. A row
  * whose lse is -inf adds nothing; otherwise infinities and NaN that a row sees act as in the formula,
  * what it does not see has no effect. The plan's workspace holds partial sums, so launches of one plan
  * belong on one stream at a time. */

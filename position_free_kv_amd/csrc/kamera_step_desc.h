@@ -140,7 +140,7 @@ hipError_t launch_attend_heads(const StepArgs& a, const AttendIo& io, hipStream_
 hipError_t launch_attend_latent(const StepArgs& a, const AttendIo& io, hipStream_t stream);
 // partial rows by the plain kernel (kamera_step.hip), which differential attention joins by itself
 hipError_t launch_attend_plain(const StepArgs& a, const AttendIo& io, hipStream_t stream);
-// Differential attention; a: the step's arguments for pairs of KV heads (differential_args)
+// Differential attention; a: the step's arguments with half the heads, pairs of KV heads, of twice the group and value width
 hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride,
                                    float* lse, float scale, const kamera_differential& diff, hipStream_t stream);
 
