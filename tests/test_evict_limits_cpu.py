@@ -91,3 +91,7 @@ def test_a_workspace_serves_shorter_evictions(family, page, flags):
             step.evict(lay, pool, small, FAKE, (FAKE, room))
         except abi.KameraError as e:  # (staging needs a GPU)
             assert e.name == "KAMERA_E_HIP", e
+
+
+def test_rows_are_left_whole_in_small_workspaces():
+    compiled_and_run("weigh_plan_check.cpp", "kamera_step_host.cpp", "kamera_evict_host.cpp")

@@ -63,3 +63,32 @@ def test_diff_of_a_long_request_among_short_ones(dim, place):
     requests[place] = (0, 4000, 130)
     c = Case(layers=1, heads=128, kv_heads=8, head_dim=dim, prefixes=[60], requests=requests, seed=place)
     eu.check_diff(c, Params(c), 1.0 / float(np.sqrt(dim)))
+
+
+@pytest.mark.parametrize("kind", [dict(heads=14, kv_heads=1, head_dim=64), dict(heads=14, kv_heads=1, head_dim=80), dict(dtype=F32, heads=14, kv_heads=1, head_dim=64),
+                                  dict(family=MLA, heads=16, latent=512, rope=64), dict(family=MLA, dtype=F32, heads=16, latent=512, rope=64)])
+def test_weigh_in_less_workspace(kind):
+    """Rows in ranges, and whole in the least workspace that is taken: within the same bounds."""
+    c = Case(layers=1, prefixes=[300], requests=[(0, 200, 180), (0, 700, 120), (-1, 30, 90)], **kind)
+    scale = 1.0 / float(np.sqrt(c.dk))
+    s = c.step(step.WEIGH | step.FIT)
+    ws = c.workspace(s)
+    lse, before = eu.own_lse(c, 0, scale), eu.new_scores(c)
+    want, tol = eu.expect_weigh(c, 0, lse, before[0], scale, 1.0)
+    results, least = [], 0
+    for part in (1.0, 0.5, 0.0):
+        least = max(int(ws.numel() * part) // 256 * 256, 256)
+        while True:  # the first size from there on that is taken
+            try:
+                plan = step.upload(c.lay, s, c.pool, (ws.data_ptr(), least))
+                break
+            except abi.KameraError as e:
+                assert e.name == "KAMERA_E_WORKSPACE"
+                least += 256
+        assert least <= ws.numel()
+        scores = before.clone()
+        step.weigh(plan, 0, c.q[0], lse, scores[0], scale)
+        torch.cuda.synchronize()
+        assert (np.abs(eu.host(scores[0]) - want) <= tol).all()
+        results.append(scores)
+    assert least < ws.numel() and not torch.equal(results[0], results[-1])  # other sums, other roundings
