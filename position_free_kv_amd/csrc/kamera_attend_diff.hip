@@ -18,16 +18,13 @@
 #include <type_traits>
 
 #include "kamera_attend.h"
+#include "kamera_grid.h"
 
 namespace kamera {
 
 namespace {
 
 constexpr int kWaveSize = 64;
-constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
-dim3 grid_of(int64_t blocks) {
-  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
-}
 
 // A stage of TS keys lies in four arrays of rows of 2 D bytes, one after the other: keys of the first map, of the
 // second, first halves of the values, second halves. So one place in the pool's rows serves four loads.
@@ -318,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void diff_join(StepArgs a, AttendIo io, k
   __shared__ f32x4 held[kWaves][PIECES * kWaveSize];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = wave / WPR, seat = wave % WPR;
   const int outs = a.num_q_heads / 2;
-  const int64_t task = (int64_t)(blockIdx.y * (uint32_t)kGridRow + blockIdx.x) * ROWS + sub;
+  const int64_t task = (int64_t)block_number() * ROWS + sub;
   const bool live = task < (int64_t)a.num_merge * outs;
   const int64_t i = live ? task / outs : 0;
   const int oh = (int)(task % outs), head = 2 * oh / a.group, g = 2 * oh % a.group;

@@ -14,10 +14,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWave = 64;
-dim3 grid_of(int64_t blocks) {
-  return blocks <= kEvictGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kEvictGridRow, (unsigned)(evict_grid(blocks) / kEvictGridRow));
-}
-__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kEvictGridRow + blockIdx.x; }
 
 // Page and place in it of token t of a sequence.
 __device__ __forceinline__ int64_t page_of(const EvictArgs& a, const EvictSeq& s, int t, int& place) {

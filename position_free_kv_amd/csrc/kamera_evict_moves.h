@@ -3,15 +3,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include "kamera_grid.h"
 #include "kamera_step_desc.h"
 
 namespace kamera {
-
-// A launch of up to this many workgroups lies along one dimension of its grid; more are rounded up to whole rows of it.
-constexpr int64_t kEvictGridRow = int64_t(1) << 22;
-constexpr int64_t evict_grid(int64_t blocks) {
-  return blocks <= kEvictGridRow ? blocks : (blocks + kEvictGridRow - 1) / kEvictGridRow * kEvictGridRow;
-}
 
 constexpr int kSlice = 8;  // units of a slice, at most
 

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kamera_grid.h"
 #include "kamera_step_desc.h"
 
 namespace kamera {
@@ -20,14 +21,6 @@ constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-
-// Workgroups of a launch, in rows of kGridRow along the grid's second dimension: the runtime takes fewer
-// than 2^32 threads along the first. The last row may have some to spare.
-constexpr int64_t kGridRow = int64_t(1) << 22;
-dim3 grid_of(int64_t blocks, unsigned z = 1) {
-  return blocks <= kGridRow ? dim3((unsigned)blocks, 1, z) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow), z);
-}
-__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
 
 // Element types by their storage: uint16_t holds bf16 bits, float itself.
 template <typename T>

@@ -14,16 +14,11 @@
 // in part (without branches between a stage's tiles the whole call took 183 instead of 181). 32 requests of one token, MLA, 16 heads, a layer: 15 us
 // and 4 in the join; bound by dependent reads: item, tokens, lse, query rows.
 #include "kamera_attend.h"
+#include "kamera_grid.h"
 
 namespace kamera {
 
 namespace {
-
-constexpr int64_t kGridRow = int64_t(1) << 22;  // (as kamera_step.hip's grids)
-dim3 grid_of(int64_t blocks) {
-  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
-}
-__device__ __forceinline__ uint32_t block_number() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
 
 struct WeighIo {
   const void* q;

@@ -71,8 +71,8 @@ void turned(const Shape& s) {
   const EvictMoves m = evict_launches(a).moves;
   Met met[3] = {Met(a, m.turned), Met(a, m.plain0), Met(a, m.plain1)};
   const int64_t blocks = m.turned.blocks + m.plain0.blocks + m.plain1.blocks;
-  CHECK(evict_grid(blocks) >= blocks);
-  for (int64_t n = 0; n < evict_grid(blocks); ++n) {
+  CHECK(grid_blocks(blocks) >= blocks);
+  for (int64_t n = 0; n < grid_blocks(blocks); ++n) {
     int64_t b = n;
     const int part = evict_part(m, b);
     if (part < 3) met[part](b);
@@ -84,7 +84,7 @@ void plain(const Shape& s, int tensor0, int tensors, int units) {
   const EvictArgs a = args_of(s);
   const EvictMove m = evict_move_of(a, tensor0, tensors, 0, units);
   Met met(a, m);
-  for (int64_t b = 0; b < evict_grid(m.blocks); ++b) met(b);
+  for (int64_t b = 0; b < grid_blocks(m.blocks); ++b) met(b);
   met.all();
 }
 
