@@ -161,7 +161,7 @@ kamera_status kamera_step_append(const kamera_step_plan* plan, int32_t layer, co
  * the second product in bf16. Values of unseen tokens and unused slots are not read into any
  * result, whatever they hold. Infinities and NaN that a query sees act as in the formula (0 * inf
  * is NaN; with a scale of 0, keys that are not finite give unspecified results), but a query all
- * of whose scores are -inf has sum 0, output 0 and lse -inf. Results are the same bits on every
+ * of whose scores are -inf has sum 0, output 0 (NaN where it sees a value that is not finite) and lse -inf. Results are the same bits on every
  * run of a step (KAMERA_STEP_FIT: in a workspace of the same size). The plan's workspace holds
  * the partial results, so launches of one plan belong on one stream at a time. */
 kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, const void* q, int64_t q_stride,
@@ -178,7 +178,7 @@ kamera_status kamera_step_attend(const kamera_step_plan* plan, int32_t layer, co
  *     out = x / sqrt(mean(x^2) + eps) * norm_weight * out_scale   (KAMERA_DIFF_NORM; else x * out_scale)
  * q [N][num_q_heads][head_dim], out [N][num_q_heads / 2][2 head_dim], element type the layout's,
  * strides in elements between tokens, 0: packed. lse (fp32 [N][num_q_heads], packed, may be NULL) as
- * kamera_step_attend's, of each map. A map all of whose scores are -inf, or that sees nothing, is 0, and
+ * kamera_step_attend's, of each map. A map all of whose scores are -inf, or that sees nothing, is 0 (as there), and
  * a row of zeros stays zero under the norm, whatever eps. Everything else as kamera_step_attend:
  * fp32 but for the probabilities, one rounding at the end, unseen tokens not read into any result. */
 enum { KAMERA_DIFF_NORM = 1u };

@@ -154,7 +154,8 @@ __device__ __forceinline__ void put_pairs(const StepArgs& a, const AttendIo& io,
 
 // ============================================================================
 // Tiles of 128 rows: two waves a map, 32 rows each, share stages of 32 (D = 128) or 64 keys, two in LDS. A wave's 32 rows
-// of 2 D columns of O are 128 registers (D = 128), its queries 32 more: 64 rows would leave one wave a SIMD. One map a wave
+// of 2 D columns of O are 128 registers (D = 128), its queries 32 more: 64 rows would leave one wave a SIMD. (All 256 are taken
+// and 52 spilled, none among a stage's products; D = 64 takes 204.) One map a wave
 // lets both maps share the values' stage, and LDS feeds 24 products of a stage's 32 keys from 24 KB a wave. Stages of
 // four like arrays, one address for four loads: 689 -> 638 us in the case above; whole tiles for whole rounds of the chip's
 // places (the planner's choice): 638 -> 520; results put out without partial rows where a run has no other: 520 -> 508.

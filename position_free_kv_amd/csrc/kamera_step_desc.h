@@ -145,8 +145,8 @@ hipError_t launch_step_attend_diff(const StepArgs& a, int layer, const void* q, 
                                    float* lse, float scale, const kamera_differential& diff, hipStream_t stream);
 
 // Keys of a weighing workgroup: PLAIN 16; on the matrix cores HEADS 256, LATENT 64. Items of at most kFewRows rows
-// walk over more of them (matrix cores). (64 requests of one token, 32 + 8 heads, 4 layers: 256 and 512 keys 117 and 116 us,
-// 1024 116 but 194 instead of 179 for many rows, whose workgroups then find less LDS; as tiles of many rows 147. MLA, 32
+// walk over more of them (matrix cores). (64 requests of one token, 32 + 8 heads, 4 layers: 256, 512 and 1024 keys 116.4, 115
+// and 116.6 us, 1024 186 instead of 177 for many rows, whose workgroups then find less LDS; as tiles of many rows 147. MLA, 32
 // requests, 16 heads, 4 layers: 64, 128 and 256 keys 88, 89 and 103.)
 constexpr int kFewRows = 16;
 constexpr int weigh_keys(int kernel) { return kernel == ATTEND_PLAIN ? 16 : kernel == ATTEND_LATENT ? 64 : 256; }
