@@ -12,9 +12,10 @@
 // A query head and key cost 2 D + 4 D flops, half as much again as plain attention, for the same bytes of the pool.
 //
 // 8 requests with 2481 query tokens over an 8192-token prefix, 28 + 4 heads of 128: 0.93 PFLOP/s in this kernel (463
-// GFLOP in 500 us), 76% of a large library product's rate; bound by the products and the softmax between them, which two
-// waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones, 32 + 8 heads: 62 us and
-// 12 in the join; bound by the own tokens' pages and by what a workgroup does before its first key (about 6 us).
+// GFLOP in 500 us; 0.8 on a slower machine), 76% of a large library product's rate; bound by the products and the
+// softmax between them, which two waves a SIMD take in turn. 64 requests of one token over 8192 shared and 49300 own ones,
+// 32 + 8 heads: 62 us and 12 in the join; bound by the own tokens' pages and by what a workgroup does before its first
+// key (about 6 us).
 #include <type_traits>
 
 #include "kamera_attend.h"

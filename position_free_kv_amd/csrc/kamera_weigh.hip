@@ -9,10 +9,11 @@
 // softmax's sum unnecessary, so that each key needs one pass over the rows and no running maximum. Sums are in fp32.
 //
 // 64 requests of one token over 8192 shared and 49300 own tokens, 32 + 8 heads of 128, a layer: 27 us; bound by reading the
-// own keys (118 MB, 4.4 TB/s; longer ones 4.8, in whole rounds of workgroups and in broken ones alike). 2481 query tokens over 8192 shared and own tokens, 28 + 4 heads: 166 us
-// for 154 GFLOP, 0.93 PFLOP/s; bound by the products and the exponentials, which take about the same time and overlap
-// in part (without branches between a stage's tiles the whole call took 183 instead of 181). 32 requests of one token, MLA, 16 heads, a layer: 15 us
-// and 4 in the join; bound by dependent reads: item, tokens, lse, query rows.
+// own keys (118 MB, 4.4 TB/s; longer ones 4.8, in whole rounds of workgroups and in broken ones alike). 2481 query
+// tokens over 8192 shared and own tokens, 28 + 4 heads: 166 us for 154 GFLOP, 0.93 PFLOP/s (0.8 on a slower machine); bound by
+// the products and the exponentials, which take about the same time and overlap in part (without branches between a stage's
+// tiles the whole call took 183 instead of 181). 32 requests of one token, MLA, 16 heads, a layer: 15 us and 4 in the join;
+// bound by dependent reads: item, tokens, lse, query rows.
 #include "kamera_attend.h"
 #include "kamera_grid.h"
 
